@@ -21,6 +21,8 @@ __all__ = [
     "forward_splitkv_noalloc", "backward", "bwd_workspace_size", "quantize_e4m3",
     "forward_e4m3", "e4m3_bytes", "quantize_qkv_e4m3", "attention_unfused",
     "unfused_workspace_size", "unfused_intermediates",
+    "CacheE4M3", "cache_alloc_e4m3", "cache_slots", "cache_append_e4m3", "cache_forward_e4m3",
+    "cache_forward_workspace_size",
     "check_errors", "status_string", "library_path", "load_library", "SYMBOLS",
 ]
 
@@ -53,6 +55,12 @@ SYMBOLS = {
     "fa_attn_unfused": (_c.c_int, [_c.c_void_p] * 5 + [_c.c_int] * 4 +
                         [_c.c_float, _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "fa_attn_unfused_workspace_size": (_c.c_size_t, [_c.c_int] * 4),
+    "fa_cache_slots": (_c.c_int, [_c.c_void_p] * 9 + [_c.c_int] * 5 + [_c.c_void_p]),
+    "fa_cache_append_e4m3": (_c.c_int, [_c.c_void_p] * 2 + [_c.c_longlong] * 2 + [_c.c_void_p] * 5 +
+                             [_c.c_int] * 5 + [_c.c_void_p]),
+    "fa_cache_fwd_e4m3": (_c.c_int, [_c.c_void_p, _c.c_longlong] + [_c.c_void_p] * 9 + [_c.c_int] * 8 +
+                          [_c.c_float, _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "fa_cache_fwd_e4m3_workspace_size": (_c.c_size_t, [_c.c_int]),
     "fa_check_errors": (_c.c_int, [_c.c_void_p]),
     "fa_selftest_wait_timeout": (_c.c_int, [_c.c_uint, _c.c_void_p]),
     "fa_status_string": (_c.c_char_p, [_c.c_int]),
@@ -62,7 +70,7 @@ SYMBOLS = {
 }
 
 STATUS = {0: "FA_OK", -1: "FA_ERR_INVALID_ARG", -2: "FA_ERR_UNSUPPORTED",
-          -3: "FA_ERR_MISALIGNED", -4: "FA_ERR_CUDA", -5: "FA_ERR_TIMEOUT"}
+          -3: "FA_ERR_MISALIGNED", -4: "FA_ERR_CUDA", -5: "FA_ERR_TIMEOUT", -6: "FA_ERR_INDEX"}
 
 _lock = threading.Lock()
 _lib = None
@@ -111,7 +119,7 @@ def _raise(status: int, where: str):
     detail = ""
     if status == -4:
         detail = f"cudaError {lib.fa_get_last_cuda_error()}"
-    elif status == -5:
+    elif status in (-5, -6):
         rec = (ctypes.c_uint * 4)()
         lib.fa_get_last_error_record(rec)
         detail = f"record code={rec[0]} site={rec[1]} block={rec[2]} tile={rec[3]}"
@@ -156,7 +164,8 @@ def splitkv_num_splits(B, H, N, causal=False) -> int:
 
 def check_errors(stream=None) -> None:
     """Synchronise the stream and raise FAError if a device-side bounded wait
-    expired since the last check."""
+    expired, or a cache call met an index out of range, since the last
+    check."""
     st = load_library().fa_check_errors(_stream_handle(stream))
     if st != 0:
         _raise(st, "fa_check_errors")
@@ -463,3 +472,7 @@ def forward_host(q, k, v, scale=None, causal=False, stream=None, staging=None, o
     if st != 0:
         _raise(st, "fa_check_errors")
     return o, lse
+
+
+from .cache import (CacheE4M3, cache_alloc_e4m3, cache_append_e4m3, cache_forward_e4m3,  # noqa: E402
+                    cache_forward_workspace_size, cache_slots)

@@ -19,6 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(OUT_DIR, "libfa_fwd.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
+UNITS = ("fa_fwd.cu", "fa_cache.cu")
 
 
 def _sources():
@@ -53,20 +54,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(OUT_DIR, exist_ok=True)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [
-        _nvcc(), ARCH, "-std=c++17", "-O3", "-lineinfo", "-shared",
-        "-Xcompiler", "-fPIC", "-Xptxas", "-v",
-        "-I", INCLUDE, "-I", CSRC,
-        "-o", tmp, os.path.join(CSRC, "fa_fwd.cu"),
-    ]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    flags = [ARCH, "-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
+    jobs = []  # one nvcc per translation unit, at the same time
+    for unit in UNITS:
+        obj = os.path.join(OUT_DIR, f"{unit}.{os.getpid()}.o")
+        cmd = [_nvcc(), *flags, "-Xptxas", "-v", "-c", "-o", obj, os.path.join(CSRC, unit)]
+        jobs.append((cmd, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    report, failed = "", False
+    for cmd, _, proc in jobs:
+        out = proc.communicate()[0]
+        report += " ".join(cmd) + "\n" + out
+        failed = failed or proc.returncode != 0
+    objs = [obj for _, obj, _ in jobs]
+    if not failed:
+        cmd = [_nvcc(), ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        report += " ".join(cmd) + "\n" + res.stdout + res.stderr
+        failed = res.returncode != 0
+    for obj in objs:
+        if os.path.exists(obj):
+            os.remove(obj)
     with open(os.path.join(OUT_DIR, "ptxas_report.txt"), "w") as f:
-        f.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+        f.write(report)
+    if failed:
+        raise RuntimeError("nvcc failed:\n" + report)
     os.replace(tmp, LIB_PATH)
     if verbose:
-        print(res.stderr)
+        print(report)
     return LIB_PATH
 
 

@@ -1,0 +1,229 @@
+"""The 8-bit key/value cache: from prompts to single tokens.
+
+A serving step is three calls, all on the device and without a
+synchronisation, so that a step can be captured into a CUDA graph:
+
+    cu, slots, lens, used = cache_slots(table, lens, new, free, used, P, T)
+    cache_append_e4m3(k, v, cache, slots)             # per layer
+    o, lse = cache_forward_e4m3(q, cache, table, lens, cu)
+
+``include/fa_fwd.h`` says what each does with every input.
+"""
+from __future__ import annotations
+
+import math
+from typing import NamedTuple
+
+import torch
+
+__all__ = ["CacheE4M3", "cache_alloc_e4m3", "cache_slots", "cache_append_e4m3", "cache_forward_e4m3",
+           "cache_forward_workspace_size"]
+
+_I32, _I64, _F32, _U8, _BF16 = torch.int32, torch.int64, torch.float32, torch.uint8, torch.bfloat16
+
+
+class CacheE4M3(NamedTuple):
+    """A pool of cache blocks: codes uint8 [blocks, Hkv, P, d], scales fp32
+    [blocks, Hkv], of K and of V."""
+    k8: torch.Tensor
+    v8: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def _lib():
+    from . import load_library
+    return load_library()
+
+
+def _done(status, where):
+    if status != 0:
+        from . import _raise
+        _raise(status, where)
+
+
+def _check(name, t, dtype, shape, device):
+    """A contiguous CUDA tensor of this type; ``shape`` has None where any size will do."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    s = t.shape
+    if len(s) != len(shape) or any(b is not None and a != b for a, b in zip(s, shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(s)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _check_rows(name, t, heads, d, device):
+    """bf16 [T, heads, d], heads and d contiguous, any stride between tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != _BF16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
+        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {d}], got {tuple(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _check_cache(cache):
+    k8 = cache.k8
+    if not isinstance(k8, torch.Tensor) or k8.dim() != 4:
+        raise ValueError("cache.k8 must be a uint8 [blocks, heads, block_tokens, d] tensor")
+    if not k8.is_cuda:
+        raise ValueError("the cache must be CUDA tensors")
+    dev, shape = k8.device, k8.shape
+    _check("cache.k8", k8, _U8, shape, dev)
+    _check("cache.v8", cache.v8, _U8, shape, dev)
+    _check("cache.k_scale", cache.k_scale, _F32, shape[:2], dev)
+    _check("cache.v_scale", cache.v_scale, _F32, shape[:2], dev)
+    return dev, shape
+
+
+def _call(device, stream, fn, *args):
+    """``fn`` with ``device`` current and on ``stream`` (default: the current
+    one), so that what it allocates belongs to that stream."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return fn(torch._C._cuda_getCurrentRawStream(device.index), *args)
+    with torch.cuda.device(device):
+        if stream is None:
+            return fn(torch.cuda.current_stream().cuda_stream, *args)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            return fn(stream.cuda_stream, *args)
+
+
+def cache_alloc_e4m3(num_blocks, heads_kv, block_tokens, d, device=None):
+    """An empty cache: codes 0, scales 0 (a block gets its scale with its
+    first rows)."""
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    shape = (num_blocks, heads_kv, block_tokens, d)
+    return CacheE4M3(torch.zeros(shape, dtype=_U8, device=device), torch.zeros(shape, dtype=_U8, device=device),
+                     torch.zeros(shape[:2], dtype=_F32, device=device),
+                     torch.zeros(shape[:2], dtype=_F32, device=device))
+
+
+def cache_slots(block_table, seq_lens, new_lens, free_blocks, free_used, block_tokens, num_tokens, stream=None):
+    """Grant blocks for each request's new tokens and map them to slots.
+
+    block_table int32 [R, max_blocks] (written in place), seq_lens and
+    new_lens int32 [R], free_blocks int32 [F] with the first free_used (int32
+    [1]) of them gone, num_tokens the length of the slot map.  Returns
+    (cu_new int32 [R + 1], slot_map int64 [num_tokens], seq_lens_out int32
+    [R], free_used_out int32 [1]).  A request that cannot be served keeps its
+    length and gets slots of -1; slots behind the last request's are -1."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 [R, max_blocks] tensor")
+    dev = block_table.device
+    if dev.type != "cuda":
+        raise ValueError("block_table must be a CUDA tensor")
+    R, M = block_table.shape
+    _check("block_table", block_table, _I32, (R, M), dev)
+    _check("seq_lens", seq_lens, _I32, (R,), dev)
+    _check("new_lens", new_lens, _I32, (R,), dev)
+    _check("free_blocks", free_blocks, _I32, (None,), dev)
+    _check("free_used", free_used, _I32, (1,), dev)
+    if num_tokens < 0:
+        raise ValueError(f"num_tokens must not be negative, got {num_tokens}")
+    return _call(dev, stream, _slots, block_table, seq_lens, new_lens, free_blocks, free_used, R, M,
+                 int(block_tokens), int(num_tokens))
+
+
+def _slots(handle, table, seq_lens, new_lens, free, used, R, M, P, T):
+    dev = table.device
+    cu = torch.empty(R + 1, dtype=_I32, device=dev)
+    slots = torch.empty(T, dtype=_I64, device=dev)
+    lens = torch.empty(R, dtype=_I32, device=dev)
+    gone = torch.empty(1, dtype=_I32, device=dev)
+    _done(_lib().fa_cache_slots(table.data_ptr(), seq_lens.data_ptr(), new_lens.data_ptr(), free.data_ptr(),
+                                used.data_ptr(), cu.data_ptr(), slots.data_ptr(), lens.data_ptr(), gone.data_ptr(),
+                                R, M, free.shape[0], P, T, handle), "fa_cache_slots")
+    return cu, slots, lens, gone
+
+
+def cache_append_e4m3(k, v, cache, slot_map, stream=None):
+    """Write new K and V rows (bf16 [T, Hkv, d], any stride between tokens)
+    into the cache at the slots of ``slot_map`` (int64 [T], -1: skip), each
+    run of rows in a block with the block's scale, which grows to fit."""
+    dev, (blocks, H, P, d) = _check_cache(cache)
+    _check_rows("k", k, H, d, dev)
+    _check_rows("v", v, H, d, dev)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"k has {T} rows, v {v.shape[0]}")
+    _check("slot_map", slot_map, _I64, (T,), dev)
+    if T:
+        _call(dev, stream, _append, k, v, cache, slot_map, T, H, d, blocks, P)
+
+
+def _append(handle, k, v, cache, slot_map, T, H, d, blocks, P):
+    _done(_lib().fa_cache_append_e4m3(
+        k.data_ptr(), v.data_ptr(), k.stride(0) if T > 1 else H * d, v.stride(0) if T > 1 else H * d,
+        cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
+        slot_map.data_ptr(), T, H, d, blocks, P, handle), "fa_cache_append_e4m3")
+
+
+_ws_bytes = {}
+
+
+def cache_forward_workspace_size(d, device=None) -> int:
+    """Workspace bytes of ``cache_forward_e4m3`` on ``device`` (default: the
+    current one), whatever the batch."""
+    index = torch.cuda.current_device() if device is None else torch.device(device).index
+    n = _ws_bytes.get((index, d))
+    if n is None:
+        with torch.cuda.device(index):
+            n = int(_lib().fa_cache_fwd_e4m3_workspace_size(int(d)))
+        if n:
+            _ws_bytes[index, d] = n
+    return n
+
+
+def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal=True, workspace=None, stream=None):
+    """Attention of each request's newest tokens over its cached keys.
+
+    q bf16 [T, Hq, d] (any stride between tokens), Hq a multiple of the
+    cache's heads; request r's rows are cu_q[r] .. cu_q[r + 1] (cu_q int32
+    [R + 1]), its last ones of seq_lens[r] (int32 [R]) cached tokens, whose
+    blocks are block_table[r] (int32 [R, max_blocks]).  Returns (o bf16 [T,
+    Hq, d], lse fp32 [T, Hq]); rows behind cu_q[R] are not written.
+    ``workspace`` (a CUDA tensor of cache_forward_workspace_size(d) bytes) may
+    be passed to reuse memory; calls that may overlap need one each."""
+    dev, (blocks, H, P, d) = _check_cache(cache)
+    _check_rows("q", q, None, d, dev)
+    T, Hq, _ = q.shape
+    if Hq == 0 or H == 0 or Hq % H:
+        raise ValueError(f"{Hq} query heads do not share {H} kv heads evenly")
+    _check("block_table", block_table, _I32, (None, None), dev)
+    R, M = block_table.shape
+    _check("seq_lens", seq_lens, _I32, (R,), dev)
+    _check("cu_q", cu_q, _I32, (R + 1,), dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    return _call(dev, stream, _forward, q, cache, block_table, seq_lens, cu_q, float(scale), int(bool(causal)),
+                 workspace, R, T, Hq, H, d, blocks, P, M)
+
+
+def _forward(handle, q, cache, table, seq_lens, cu_q, scale, causal, ws, R, T, Hq, H, d, blocks, P, M):
+    dev = q.device
+    o = torch.empty((T, Hq, d), dtype=_BF16, device=dev)
+    lse = torch.empty((T, Hq), dtype=_F32, device=dev)
+    if ws is None:
+        ws = torch.empty(cache_forward_workspace_size(d, dev), dtype=_U8, device=dev)
+    _done(_lib().fa_cache_fwd_e4m3(
+        q.data_ptr(), q.stride(0) if T > 1 else Hq * d, cache.k8.data_ptr(), cache.v8.data_ptr(),
+        cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
+        o.data_ptr(), lse.data_ptr(), R, T, Hq, H, d, blocks, P, M, scale, causal, ws.data_ptr(),
+        ws.numel() * ws.element_size(), handle), "fa_cache_fwd_e4m3")
+    return o, lse

@@ -1,0 +1,299 @@
+// C ABI of the 8-bit key/value cache (declared in include/fa_fwd.h): argument
+// validation and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "fa_cache.cuh"
+#include "fa_cache_fwd.cuh"
+#include "fa_fwd.h"
+#include "fa_host.h"
+
+namespace fa {
+namespace {
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+// log2 of the tokens per block, -1 where it is none of 16, 32, 64, 128.
+int block_shift(int P) { return P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : P == 128 ? 7 : -1; }
+
+// Sizes of a cache that fits 2^31 code rows of 128 bytes (the tensor maps'
+// coordinates are 32-bit).
+int check_cache(int Hkv, int d, int blocks, int P) {
+  if (Hkv <= 0 || blocks <= 0) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || block_shift(P) < 0 || Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  const long long bh = static_cast<long long>(blocks) * Hkv;
+  if (bh > 0x7fffffffLL || static_cast<long long>(blocks) * P > (1ll << 40)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// ------------------------------------------------------------------- slots
+
+int cache_slots(const SlotArgs& a, int P, cudaStream_t s) {
+  if (a.R < 0 || a.T < 0 || a.F < 0 || a.M <= 0) return FA_ERR_INVALID_ARG;
+  if (block_shift(P) < 0) return FA_ERR_UNSUPPORTED;
+  if (!a.free_used || !a.cu_new || !a.free_used_out) return FA_ERR_INVALID_ARG;
+  if (a.R > 0 && (!a.table || !a.seq_lens || !a.new_lens || !a.seq_lens_out)) return FA_ERR_INVALID_ARG;
+  if ((a.T > 0 && !a.slot_map) || (a.F > 0 && !a.free_blocks)) return FA_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(a.table), static_cast<const void*>(a.seq_lens),
+                        static_cast<const void*>(a.new_lens), static_cast<const void*>(a.free_blocks),
+                        static_cast<const void*>(a.free_used), static_cast<const void*>(a.cu_new),
+                        static_cast<const void*>(a.seq_lens_out), static_cast<const void*>(a.free_used_out)})
+    if (misaligned(p, 4)) return FA_ERR_MISALIGNED;
+  if (misaligned(a.slot_map, 8)) return FA_ERR_MISALIGNED;
+  const size_t r = static_cast<size_t>(a.R);
+  const Range ins[] = {{a.seq_lens, 4 * r}, {a.new_lens, 4 * r}, {a.free_blocks, 4 * static_cast<size_t>(a.F)},
+                       {a.free_used, 4}};
+  const Range outs[] = {{a.table, 4 * r * a.M}, {a.cu_new, 4 * (r + 1)}, {a.slot_map, 8 * static_cast<size_t>(a.T)},
+                        {a.seq_lens_out, 4 * r}, {a.free_used_out, 4}};
+  for (int i = 0; i < 5; ++i) {
+    for (const Range& in : ins)
+      if (host::overlap(outs[i].p, outs[i].n, in.p, in.n)) return FA_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 5; ++j)
+      if (host::overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return FA_ERR_INVALID_ARG;
+  }
+  host::Device dev;
+  const int st = host::device(&dev);
+  if (st != FA_OK) return st;
+  long long grid = (static_cast<long long>(a.T) + slots::kThreads - 1) / slots::kThreads;
+  grid = grid < 1 ? 1 : (grid > 2 * dev.sms ? 2 * dev.sms : grid);
+  fa_cache_slots_kernel<<<static_cast<unsigned>(grid), slots::kThreads, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : host::fail(e);
+}
+
+// ------------------------------------------------------------------ append
+
+template <int D>
+void launch_append(const AppendArgs& a, dim3 grid, cudaStream_t s) {
+  const int nv = ((1 << a.sh) * D) / (8 * app::kThreads);  // 1 .. 16
+  if (nv == 16) fa_cache_append_kernel<D, 16><<<grid, app::kThreads, 0, s>>>(a);
+  else if (nv == 8) fa_cache_append_kernel<D, 8><<<grid, app::kThreads, 0, s>>>(a);
+  else if (nv == 4) fa_cache_append_kernel<D, 4><<<grid, app::kThreads, 0, s>>>(a);
+  else if (nv == 2) fa_cache_append_kernel<D, 2><<<grid, app::kThreads, 0, s>>>(a);
+  else fa_cache_append_kernel<D, 1><<<grid, app::kThreads, 0, s>>>(a);
+}
+
+int cache_append(const void* k, const void* v, long long k_stride, long long v_stride, void* k8, void* v8,
+                 float* ks, float* vs, const long long* slot_map, int T, int Hkv, int d, int blocks, int P,
+                 cudaStream_t s) {
+  int st = check_cache(Hkv, d, blocks, P);
+  if (st != FA_OK) return st;
+  if (T < 0) return FA_ERR_INVALID_ARG;
+  if (T == 0) return FA_OK;
+  if (!k || !v || !k8 || !v8 || !ks || !vs || !slot_map) return FA_ERR_INVALID_ARG;
+  const long long row = static_cast<long long>(Hkv) * d;
+  if (T > 1 && (k_stride < row || v_stride < row)) return FA_ERR_INVALID_ARG;
+  if ((k_stride | v_stride) & 7) return FA_ERR_MISALIGNED;
+  if (k_stride > (1ll << 40) || v_stride > (1ll << 40)) return FA_ERR_UNSUPPORTED;
+  for (const void* p : {k, v, static_cast<const void*>(k8), static_cast<const void*>(v8)})
+    if (misaligned(p, 16)) return FA_ERR_MISALIGNED;
+  if (misaligned(ks, 4) || misaligned(vs, 4) || misaligned(slot_map, 8)) return FA_ERR_MISALIGNED;
+  const size_t nx = 2 * static_cast<size_t>(row), nc = static_cast<size_t>(blocks) * P * row;
+  const size_t nk = static_cast<size_t>(T - 1) * k_stride * 2 + nx, nv = static_cast<size_t>(T - 1) * v_stride * 2 + nx;
+  const size_t ns = static_cast<size_t>(blocks) * Hkv * 4;
+  const Range outs[] = {{k8, nc}, {v8, nc}, {ks, ns}, {vs, ns}};
+  const Range ins[] = {{k, nk}, {v, nv}, {slot_map, 8 * static_cast<size_t>(T)}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Range& in : ins)
+      if (host::overlap(outs[i].p, outs[i].n, in.p, in.n)) return FA_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 4; ++j)
+      if (host::overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return FA_ERR_INVALID_ARG;
+  }
+  host::Device dev;
+  if ((st = host::device(&dev)) != FA_OK) return st;
+  AppendArgs a{};
+  a.x[0] = static_cast<const __nv_bfloat16*>(k);
+  a.x[1] = static_cast<const __nv_bfloat16*>(v);
+  a.stride[0] = k_stride;
+  a.stride[1] = v_stride;
+  a.codes[0] = static_cast<uint8_t*>(k8);
+  a.codes[1] = static_cast<uint8_t*>(v8);
+  a.scale[0] = ks;
+  a.scale[1] = vs;
+  a.slot_map = slot_map;
+  a.slots = static_cast<long long>(blocks) * P;
+  a.T = T;
+  a.Hkv = Hkv;
+  a.sh = block_shift(P);
+  a.err = dev.index_err;
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(T) + app::kChunk - 1) / app::kChunk),
+                  static_cast<unsigned>(Hkv), 2);
+  if (d == 128) launch_append<128>(a, grid, s);
+  else launch_append<64>(a, grid, s);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : host::fail(e);
+}
+
+// ----------------------------------------------------------------- forward
+
+// Workspace: the CTAs' marks, then two partials of `rows` query rows per CTA.
+constexpr int kMaxGrid = 256;
+size_t partial_bytes(int sms, int rows, int d) { return static_cast<size_t>(2) * sms * rows * (d + 1) * 4; }
+size_t marks_bytes(int sms) { return static_cast<size_t>(sms) * 32; }
+
+size_t cache_fwd_workspace(int d) {
+  if (d != 64 && d != 128) return 0;
+  host::Device dev;
+  if (host::device(&dev) != FA_OK) return 0;
+  return marks_bytes(dev.sms) + partial_bytes(dev.sms, dec::kRows, d);
+}
+
+std::mutex g_cache_mu;
+bool g_cache_ready[64][2] = {};
+
+template <int D>
+int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, char* ws, const host::Device& dev,
+                     cudaStream_t s) {
+  using Ly = dec::Layout<D>;
+  auto kernel = fa_cache_fwd_kernel<D>;
+  auto merge = fa_cache_merge_kernel<D, dec::kRows>;
+  cudaError_t e = cudaSuccess;
+  {
+    std::lock_guard<std::mutex> lock(g_cache_mu);
+    bool& ready = g_cache_ready[dev.dev][D == 128];
+    if (!ready) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::kAlloc);
+      if (e != cudaSuccess) return host::fail(e);
+      ready = true;
+    }
+  }
+  const int grid = dev.sms < kMaxGrid ? dev.sms : kMaxGrid;
+  a.desc = reinterpret_cast<int4*>(ws);
+  a.cont = reinterpret_cast<int*>(ws + static_cast<size_t>(dev.sms) * 16);
+  a.part_o = reinterpret_cast<float*>(ws + marks_bytes(dev.sms));
+  a.part_l = a.part_o + static_cast<size_t>(2) * grid * dec::kRows * D;
+  CUtensorMap mk, mv;
+  const cuuint64_t rows = static_cast<cuuint64_t>(P) * D / 128;
+  const cuuint64_t bh = static_cast<cuuint64_t>(a.blocks) * a.Hkv;
+  const cuuint32_t box = static_cast<cuuint32_t>((P < dec::kKeys ? P : dec::kKeys) * D / 128);
+  int st = host::tensor_map(&mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, k8, 128, rows, bh, 128, rows * 128, 128, box);
+  if (st != FA_OK) return st;
+  st = host::tensor_map(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, v8, 128, rows, bh, 128, rows * 128, 128, box);
+  if (st != FA_OK) return st;
+  kernel<<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return host::fail(e);
+  // A unit of one tile is never split: nothing to merge.
+  if (static_cast<long long>(a.M) * P <= dec::kKeys) return FA_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, merge, static_cast<const CacheFwdArgs&>(a), grid);
+  return e == cudaSuccess ? FA_OK : host::fail(e);
+}
+
+int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8, const float* ks, const float* vs,
+              const int* table, const int* seq_lens, const int* cu_q, void* o, float* lse, int R, int T, int Hq,
+              int Hkv, int d, int blocks, int P, int M, float scale, int causal, void* ws, size_t ws_bytes,
+              cudaStream_t s) {
+  int st = check_cache(Hkv, d, blocks, P);
+  if (st != FA_OK) return st;
+  if (R < 0 || T < 0 || Hq <= 0 || M <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * Hq > 0x7fffffffLL || static_cast<long long>(M) * P > 0x7fffff00LL)
+    return FA_ERR_UNSUPPORTED;
+  if (T == 0 || R == 0) return FA_OK;
+  if (!q || !k8 || !v8 || !ks || !vs || !table || !seq_lens || !cu_q || !o || !lse || !ws) return FA_ERR_INVALID_ARG;
+  const long long row = static_cast<long long>(Hq) * d;
+  if (T > 1 && q_stride < row) return FA_ERR_INVALID_ARG;
+  if (q_stride & 7) return FA_ERR_MISALIGNED;
+  if (q_stride > (1ll << 40)) return FA_ERR_UNSUPPORTED;
+  for (const void* p : {q, k8, v8, static_cast<const void*>(o), static_cast<const void*>(ws)})
+    if (misaligned(p, 16)) return FA_ERR_MISALIGNED;
+  for (const void* p : {static_cast<const void*>(ks), static_cast<const void*>(vs), static_cast<const void*>(table),
+                        static_cast<const void*>(seq_lens), static_cast<const void*>(cu_q),
+                        static_cast<const void*>(lse)})
+    if (misaligned(p, 4)) return FA_ERR_MISALIGNED;
+  host::Device dev;
+  if ((st = host::device(&dev)) != FA_OK) return st;
+  const size_t need = cache_fwd_workspace(d);
+  if (need == 0) return FA_ERR_UNSUPPORTED;
+  if (ws_bytes < need) return FA_ERR_INVALID_ARG;
+  const size_t nc = static_cast<size_t>(blocks) * P * Hkv * d, ns = static_cast<size_t>(blocks) * Hkv * 4;
+  const size_t nq = (static_cast<size_t>(T - 1) * q_stride + row) * 2, no = static_cast<size_t>(T) * row * 2;
+  const Range ins[] = {{q, nq}, {k8, nc}, {v8, nc}, {ks, ns}, {vs, ns},
+                       {table, static_cast<size_t>(R) * M * 4}, {seq_lens, static_cast<size_t>(R) * 4},
+                       {cu_q, (static_cast<size_t>(R) + 1) * 4}};
+  const Range outs[] = {{o, no}, {lse, static_cast<size_t>(T) * Hq * 4}, {ws, need}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& in : ins)
+      if (host::overlap(outs[i].p, outs[i].n, in.p, in.n)) return FA_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 3; ++j)
+      if (host::overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return FA_ERR_INVALID_ARG;
+  }
+  CacheFwdArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.ks = ks;
+  a.vs = vs;
+  a.table = table;
+  a.seq_lens = seq_lens;
+  a.cu_q = cu_q;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.R = R;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.g = Hq / Hkv;
+  a.sh = block_shift(P);
+  a.M = M;
+  a.blocks = blocks;
+  a.causal = causal;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.err = dev.err;
+  a.index_err = dev.index_err;
+  a.timeout_ns = 2000ull * 1000 * 1000;
+  char* w = static_cast<char*>(ws);
+  return d == 128 ? launch_cache_fwd<128>(a, k8, v8, P, w, dev, s) : launch_cache_fwd<64>(a, k8, v8, P, w, dev, s);
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+int fa_cache_slots(int* block_table, const int* seq_lens, const int* new_lens, const int* free_blocks,
+                   const int* free_used, int* cu_new, long long* slot_map, int* seq_lens_out, int* free_used_out,
+                   int R, int max_blocks, int num_free, int block_tokens, int num_tokens, void* stream) {
+  fa::SlotArgs a{block_table, seq_lens, new_lens, free_blocks, free_used, cu_new, slot_map, seq_lens_out,
+                 free_used_out, R, max_blocks, num_free, fa::block_shift(block_tokens), num_tokens};
+  return fa::cache_slots(a, block_tokens, static_cast<cudaStream_t>(stream));
+}
+
+int fa_cache_append_e4m3(const void* k, const void* v, long long k_stride, long long v_stride, void* k8, void* v8,
+                         float* k_scale, float* v_scale, const long long* slot_map, int T, int Hkv, int d,
+                         int num_blocks, int block_tokens, void* stream) {
+  return fa::cache_append(k, v, k_stride, v_stride, k8, v8, k_scale, v_scale, slot_map, T, Hkv, d, num_blocks,
+                          block_tokens, static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_cache_fwd_e4m3_workspace_size(int d) { return fa::cache_fwd_workspace(d); }
+
+int fa_cache_fwd_e4m3(const void* q, long long q_stride, const void* k8, const void* v8, const float* k_scale,
+                      const float* v_scale, const int* block_table, const int* seq_lens, const int* cu_q, void* o,
+                      float* lse, int R, int T, int Hq, int Hkv, int d, int num_blocks, int block_tokens,
+                      int max_blocks, float scale, int causal, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  return fa::cache_fwd(q, q_stride, k8, v8, k_scale, v_scale, block_table, seq_lens, cu_q, o, lse, R, T, Hq, Hkv, d,
+                       num_blocks, block_tokens, max_blocks, scale, causal, workspace, workspace_bytes,
+                       static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

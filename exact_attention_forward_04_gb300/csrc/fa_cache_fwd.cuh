@@ -1,0 +1,767 @@
+// Attention over the 8-bit key/value cache, few query rows per kv head
+// (decode, drafted tokens): the cache is streamed once and bounds the time.
+//
+//   s_ij = scale * q_i . k_j,  L_i = ln sum_j exp(s_ij),  O_i = sum_j exp(s_ij - L_i) v_j
+//
+// over the visible keys j of query i.  The rows of one (request, kv head) are
+// its new tokens times the Hq / Hkv query heads that share the kv head, in
+// tiles of 16; a work unit is one such tile over all of the request's keys.
+//
+// Work.  The keys of every unit are cut into tiles of 32, and the tiles of
+// all units, in order, into one equal range per CTA (one CTA per SM), so any
+// mix of lengths fills the GPU evenly.  A CTA covers whole units and at most
+// two pieces of units, which it leaves as normalised partials with their
+// logsumexp; a second, dependent kernel merges those per row in CTA order.
+//
+// A CTA.  One producer warp walks the range: it reads block tables and
+// scales, publishes one descriptor per unit piece, and moves the tiles (32
+// keys of K and of V as codes) through a ring of TMA loads.  Eight warps take
+// the tiles in turn, each with a softmax of its own; at the end of a piece
+// they merge through shared memory.  In a warp a tile goes
+//   codes -> f16 (exact) -> S = Q K^T -> P -> O += P V
+// by m16n8k16 f16 products with 16 rows per tile: each warp reads its own
+// keys straight from shared memory in the product's operand layout, which a
+// choice of which key and which head-dim index each lane takes makes 16-byte
+// reads without bank conflicts (Tok below).  tcgen05 would need the codes
+// converted in shared memory first: twice the traffic of the conversion for
+// rows that fill an eighth of its 128.
+//
+// Numbers.  A query row is divided by the power of two of its largest element
+// and held in f16, three bits more than its bf16 has: exact but for elements
+// below 2^-17 of the row's largest, whose error is at most 2^-25 of it.  Sums
+// are fp32.  The row keeps two references: m, the largest s (log2 units), for
+// l = sum 2^(s - m); and E, the largest s + floor(log2 v_scale), for the
+// output's weights 2^(14 + s - E) v_scale, which lie below 2^15 and are
+// rounded to f16 (11 bits), so that neither a block of small values nor one
+// of zeros costs the others precision.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "fa_cache.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+namespace dec {
+
+constexpr int kWarps = 8;                    // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);  // and the producer
+constexpr int kRows = 16;                    // query rows of a unit
+constexpr int kKeys = 32;                    // keys of a tile
+constexpr int kSegs = 4;                     // unit pieces in flight
+constexpr int kUnitCost = 3;                 // a piece's fixed cost, in tiles
+constexpr int kMinCost = 12;                 // least cost of a CTA's range
+constexpr float kInit = -1e30f;              // references before the first key
+
+enum : unsigned { kSiteStageFull = 501, kSiteStageEmpty = 502, kSiteSegFull = 503, kSiteSegEmpty = 504,
+                  kSiteMergeW = 505, kSiteMergeR = 506 };
+
+struct Seg {
+  int r, h, row0;      // request, kv head, first row of the tile
+  int nv;              // rows of the tile that exist
+  int c0, n, len;      // the request's first query row, new tokens, cached tokens
+  int t0, nt;          // first key tile of the piece and their number (0: end)
+  int mode;            // 0: the whole unit; 1: leaves a partial in slot
+  int slot, base;      // base: ring position of the first tile
+};
+
+template <int D>
+struct Layout {
+  static constexpr int kHalf = kKeys * D;       // codes of K (or V) of a tile
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = 131072 / kStage;
+  static constexpr int kMerge = kStages * kStage;
+  static constexpr int kStats = kMerge + kWarps * kRows * D * 4;  // float4 [warps][rows]
+  static constexpr int kScales = kStats + kWarps * kRows * 16;    // float4 [stages]
+  static constexpr int kValid = kScales + kStages * 16;           // int [stages]
+  static constexpr int kSeg = kValid + kStages * 4;
+  static constexpr int kBar = (kSeg + kSegs * static_cast<int>(sizeof(Seg)) + 15) & ~15;
+  static constexpr int kFull = kBar;                    // [stages]
+  static constexpr int kEmpty = kFull + 8 * kStages;    // [stages]
+  static constexpr int kSegFull = kEmpty + 8 * kStages; // [segs]
+  static constexpr int kSegEmpty = kSegFull + 8 * kSegs;
+  static constexpr int kMergeW = kSegEmpty + 8 * kSegs;
+  static constexpr int kMergeR = kMergeW + 8;
+  static constexpr int kAbort = kMergeR + 8;
+  static constexpr int kScan = kAbort + 8;              // long long [33]
+  static constexpr int kStart = kScan + 33 * 8;         // long long rem, int r
+  static constexpr int kBytes = kStart + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+};
+
+// Which key of a 32-key tile is column n (0..7) of score tile j (0..3), and
+// where its bytes lie.  TMA stores 128-byte rows with the 16-byte chunks of
+// row y XORed by y & 7.  A K read takes, over eight lanes (n = 2i, 2i+1; four
+// chunks each), a V read columns 2t of four t and two (d = 128) adjacent
+// chunks: both touch all 32 banks once for the row orders 0 2 5 7 (even
+// columns) and 4 6 1 3 (odd), as rows 2i and 2i+1 differ in bit 2 and the four
+// rows of a V read in bits 1-2.  At d = 64 a row holds two keys, the columns
+// 2i and 2i+1, and the two orders belong to score tiles 2j and 2j+1.
+template <int D>
+__device__ __forceinline__ int tok(int j, int n) {
+  if constexpr (D == 128) {
+    return 8 * j + ((0x37156240u >> (4 * n)) & 7u);
+  } else {
+    const uint32_t rows = (j & 1) ? 0x3164u : 0x7520u;
+    return 16 * (j >> 1) + 2 * static_cast<int>((rows >> (4 * (n >> 1))) & 7u) + (n & 1);
+  }
+}
+// Byte offset of 16-byte chunk c of key `t`.
+template <int D>
+__device__ __forceinline__ uint32_t code_at(int t, int c) {
+  const int row = D == 128 ? t : t >> 1;
+  const int ch = D == 128 ? c : (t & 1) * 4 + c;
+  return static_cast<uint32_t>(row * 128 + ((ch ^ (row & 7)) << 4));
+}
+
+// Waits for a phase for at most `timeout_ns`, whether or not the CTA is
+// giving up: for copies in flight that must not outlive it.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 <= timeout_ns) {
+  }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Four E4M3 codes to two pairs of f16 (exact).
+__device__ __forceinline__ void e4m3_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(c));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// floor(log2 x) of a normal positive x (smaller ones: -127).
+__device__ __forceinline__ float floor_log2(float x) {
+  return static_cast<float>(static_cast<int>((__float_as_uint(x) >> 23) & 0xffu) - 127);
+}
+
+// The power of two just below a row's largest |element| (as fp32 bits), kept
+// where both it and its reciprocal are normal.
+__device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23) - 127;
+  return max(-120, min(120, e));
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+}  // namespace dec
+
+struct CacheFwdArgs {
+  const __nv_bfloat16* q;  // [T][Hq][D] with a token stride
+  long long q_stride;
+  const float* ks;         // [blocks][Hkv]
+  const float* vs;
+  const int* table;        // [R][M]
+  const int* seq_lens;     // [R]
+  const int* cu_q;         // [R + 1]
+  __nv_bfloat16* o;        // [T][Hq][D]
+  float* lse;              // [T][Hq]
+  float* part_o;           // [2 grid][rows][D]
+  float* part_l;           // [2 grid][rows], log2 units
+  int4* desc;              // [grid]: the unit begun and not finished by each CTA
+  int* cont;               // [grid]: 1, 2: holds (the end of) a unit begun before it
+  int R, T, Hq, Hkv, g, sh, M, blocks, causal;
+  float scale_log2;        // scale * log2(e)
+  DevError* err;
+  DevError* index_err;
+  unsigned long long timeout_ns;
+};
+
+namespace dec {
+
+struct Req {
+  int c0, n, len, nrt, kt;
+};
+// A request's rows and keys, with what is out of range cut off.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ Req request(const CacheFwdArgs& a, int r) {
+  Req q;
+  const int c0 = a.cu_q[r], c1 = a.cu_q[r + 1], len = a.seq_lens[r];
+  q.c0 = max(0, min(a.T, c0));
+  q.n = max(0, min(a.T, c1) - q.c0);
+  const long long cap = static_cast<long long>(a.M) << a.sh;
+  q.len = static_cast<int>(max(0ll, min(cap, static_cast<long long>(len))));
+  q.nrt = static_cast<int>((static_cast<long long>(q.n) * a.g + ROWS - 1) / ROWS);
+  q.kt = max(1, (q.len + KEYS - 1) / KEYS);
+  return q;
+}
+__device__ __forceinline__ long long cost_of(const CacheFwdArgs& a, const Req& q) {
+  return static_cast<long long>(a.Hkv) * q.nrt * (q.kt + kUnitCost);
+}
+
+}  // namespace dec
+
+template <int D>
+__global__ void __launch_bounds__(dec::kThreads, 1)
+    fa_cache_fwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ CacheFwdArgs a) {
+  using namespace dec;
+  using Ly = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  griddep_launch_dependents();  // the merge's CTAs may line up; they wait for this grid
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Ly::kAbort);
+  Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
+  float4* s_scales = reinterpret_cast<float4*>(sm + Ly::kScales);
+  int* s_valid = reinterpret_cast<int*>(sm + Ly::kValid);
+  if (tid == 0) {
+    for (int i = 0; i < Ly::kStages; ++i) {
+      mbar_init(base + Ly::kFull + 8 * i, 1);
+      mbar_init(base + Ly::kEmpty + 8 * i, 1);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(base + Ly::kSegFull + 8 * i, 1);
+      mbar_init(base + Ly::kSegEmpty + 8 * i, kWarps);
+    }
+    mbar_init(base + Ly::kMergeW, kWarps);
+    mbar_init(base + Ly::kMergeR, kWarps);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    a.cont[blockIdx.x] = 0;
+  }
+
+  // this CTA's range of the total cost, and the request that it starts in
+  const int per = (a.R + kThreads - 1) / kThreads;
+  const int ra = min(a.R, tid * per), rb = min(a.R, ra + per);
+  long long mine = 0, total;
+  for (int r = ra; r < rb; ++r) {
+    mine += cost_of(a, request<kRows, kKeys>(a, r));
+    if (blockIdx.x == 0) {
+      const int len = a.seq_lens[r], c0 = a.cu_q[r], c1 = a.cu_q[r + 1];
+      if (len < 0 || len > (static_cast<long long>(a.M) << a.sh)) record_index_error(a.index_err, kSiteFwdLen, r);
+      if (c0 < 0 || c1 < c0 || c1 > a.T) record_index_error(a.index_err, kSiteFwdRows, r);
+    }
+  }
+  const long long before = cta_scan(mine, reinterpret_cast<long long*>(sm + Ly::kScan), total) - mine;
+  const long long want = (total + kMinCost - 1) / kMinCost;
+  const int parts = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, want)));
+  if (static_cast<int>(blockIdx.x) >= parts) return;
+  const long long x0 = total * blockIdx.x / parts, x1 = total * (blockIdx.x + 1) / parts;
+  if (x0 >= x1) return;
+  if (before <= x0 && x0 < before + mine) {
+    long long x = before;
+    int r = ra;
+    for (;; ++r) {
+      const long long c = cost_of(a, request<kRows, kKeys>(a, r));
+      if (x0 < x + c) break;  // ends: this thread's requests hold x0
+      x += c;
+    }
+    *reinterpret_cast<long long*>(sm + Ly::kStart) = x0 - x;
+    *reinterpret_cast<int*>(sm + Ly::kStart + 8) = r;
+  }
+  __syncthreads();
+  const WaitCtx wc{abort_flag, a.err, a.timeout_ns};
+  auto full = [&](int s) { return base + Ly::kFull + 8 * s; };
+  auto empty = [&](int s) { return base + Ly::kEmpty + 8 * s; };
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    long long x = x0, rem = *reinterpret_cast<long long*>(sm + Ly::kStart);
+    int r = *reinterpret_cast<int*>(sm + Ly::kStart + 8);
+    int pos = 0, nseg = 0;  // ring positions used, pieces published
+    int held = -1;          // first request of the 32 in the lanes' registers
+    Req mineq{};
+    const int P = 1 << a.sh;
+    const int boxes = P < kKeys ? 2 : 1;
+    const uint32_t box_bytes = static_cast<uint32_t>(Ly::kHalf / boxes);
+    bool ok = true;
+    while (ok && x < x1) {
+      if (held < 0 || r >= held + 32) {
+        held = r;
+        if (r + lane < a.R) mineq = request<kRows, kKeys>(a, r + lane);
+      }
+      Req q;
+      q.c0 = __shfl_sync(0xffffffffu, mineq.c0, r - held);
+      q.n = __shfl_sync(0xffffffffu, mineq.n, r - held);
+      q.len = __shfl_sync(0xffffffffu, mineq.len, r - held);
+      q.nrt = __shfl_sync(0xffffffffu, mineq.nrt, r - held);
+      q.kt = __shfl_sync(0xffffffffu, mineq.kt, r - held);
+      const long long cost = cost_of(a, q);
+      const int unit = q.kt + kUnitCost;
+      while (ok && rem < cost && x < x1) {
+        const int u = static_cast<int>(rem / unit);
+        const int y = static_cast<int>(rem - static_cast<long long>(u) * unit);
+        const int take = static_cast<int>(min(static_cast<long long>(unit - y), x1 - x));
+        const int t0 = max(0, y - kUnitCost), t1 = max(0, y + take - kUnitCost);
+        x += take;
+        rem += take;
+        if (t1 <= t0) continue;
+        const int h = u / q.nrt, rt = u - h * q.nrt;
+        // publish the piece
+        const int si = nseg % kSegs;
+        if (nseg >= kSegs)
+          ok = mbar_wait(base + Ly::kSegEmpty + 8 * si, ((nseg / kSegs) - 1) & 1, wc, kSiteSegEmpty, nseg);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const bool begins = t0 == 0, ends = t1 == q.kt;
+        if (lane == 0) {
+          Seg s;
+          s.r = r;
+          s.h = h;
+          s.row0 = rt * kRows;
+          s.nv = min(kRows, q.n * a.g - s.row0);
+          s.c0 = q.c0;
+          s.n = q.n;
+          s.len = q.len;
+          s.t0 = t0;
+          s.nt = t1 - t0;
+          s.mode = begins && ends ? 0 : 1;
+          s.slot = 2 * blockIdx.x + (begins ? 1 : 0);
+          s.base = pos;
+          segs[si] = s;
+          mbar_arrive(base + Ly::kSegFull + 8 * si);
+          if (begins && !ends) a.desc[blockIdx.x] = make_int4(r, h, rt, s.nv);
+          if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
+        }
+        ++nseg;
+        // its tiles, 32 at a time: a lane fetches one tile's blocks and scales
+        const int* row = a.table + static_cast<long long>(r) * a.M;
+        for (int b = t0; ok && b < t1; b += 32) {
+          const int tile = b + lane;
+          int blk[2] = {-1, -1};
+          float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};
+          if (tile < t1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int key = tile * kKeys + i * 16;
+              if (i < boxes && key < q.len) {
+                blk[i] = row[key >> a.sh];
+                if (blk[i] < 0 || blk[i] >= a.blocks) {
+                  record_index_error(a.index_err, kSiteFwdBlock, r);
+                  blk[i] = -1;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (blk[i] >= 0) {
+                const long long bh = static_cast<long long>(blk[i]) * a.Hkv + h;
+                ks[i] = a.ks[bh];
+                vs[i] = a.vs[bh];
+              }
+            if (boxes == 1) { ks[1] = ks[0]; vs[1] = vs[0]; }
+          }
+          const int cnt = min(32, t1 - b);
+          for (int i = 0; i < cnt; ++i) {
+            const int st = pos % Ly::kStages, round = pos / Ly::kStages;
+            if (round > 0) ok = mbar_wait(empty(st), (round - 1) & 1, wc, kSiteStageEmpty, pos);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            if (lane == i) {
+              const int valid = boxes == 1 ? (blk[0] >= 0 ? 3 : 0)
+                                           : (blk[0] >= 0 ? 1 : 0) | (blk[1] >= 0 ? 2 : 0);
+              s_scales[st] = make_float4(ks[0], ks[1], vs[0], vs[1]);
+              s_valid[st] = valid;
+              const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
+              const uint32_t nbox = (blk[0] >= 0 ? 1u : 0u) + (blk[1] >= 0 ? 1u : 0u);
+              if (nbox == 0) {
+                mbar_arrive(full(st));
+              } else {
+                mbar_arrive_expect_tx(full(st), nbox * 2 * box_bytes);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (blk[j] >= 0) {
+                    const int y = ((tile * kKeys) & (P - 1)) * D / 128;
+                    const int bh = blk[j] * a.Hkv + h;
+                    tma_load_3d(kb + j * box_bytes, &tmK, full(st), 0, boxes == 1 ? y : 0, bh);
+                    tma_load_3d(vb + j * box_bytes, &tmV, full(st), 0, boxes == 1 ? y : 0, bh);
+                  }
+              }
+            }
+            __syncwarp();
+            ++pos;
+          }
+        }
+      }
+      ++r;
+      rem = 0;
+    }
+    // the end, also after a wait that gave up (the others then stop by the flag)
+    if (ok) {
+      const int si = nseg % kSegs;
+      if (nseg >= kSegs)
+        ok = mbar_wait(base + Ly::kSegEmpty + 8 * si, ((nseg / kSegs) - 1) & 1, wc, kSiteSegEmpty, nseg);
+      if (lane == 0 && ok) {
+        segs[si].nt = 0;
+        mbar_arrive(base + Ly::kSegFull + 8 * si);
+      }
+    }
+    // every load issued has landed before this warp exits, also where the
+    // consumers gave up
+    for (int p = max(0, pos - Ly::kStages); p < pos; ++p)
+      mbar_drain(full(p % Ly::kStages), (p / Ly::kStages) & 1, a.timeout_ns);
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g4 = lane >> 2, t4 = lane & 3;
+  constexpr int kK = D / 16;   // score products per 8 keys
+  constexpr int kN = D / 8;    // output tiles of 8 columns
+  float* merge = reinterpret_cast<float*>(sm + Ly::kMerge);
+  float4* stats = reinterpret_cast<float4*>(sm + Ly::kStats);
+  for (int ns = 0;; ++ns) {
+    const int si = ns % kSegs;
+    bool ok = mbar_wait(base + Ly::kSegFull + 8 * si, (ns / kSegs) & 1, wc, kSiteSegFull, ns);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    const Seg& s = segs[si];
+    if (s.nt == 0) return;
+
+    float o[kN][4];
+    float m[2] = {kInit, kInit}, E[2] = {kInit, kInit}, l[2] = {0.f, 0.f};
+    if (warp < s.nt) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      // Q rows g4 and g4 + 8 in operand layout: product kk takes, in lane t4,
+      // the four elements 4 (kk % 4) .. + 3 of chunk t4 + 4 (kk / 4)
+      uint32_t qa[kK][4];
+      float c[2];     // scale of the scores of each row
+      int lim[2];     // keys visible to it
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int row = s.row0 + g4 + 8 * y;
+        const bool real = g4 + 8 * y < s.nv;
+        const int tk = row / a.g;
+        const __nv_bfloat16* src =
+            a.q + (s.c0 + tk) * a.q_stride + static_cast<long long>(s.h * a.g + row - tk * a.g) * D;
+        uint4 w[D / 32];  // 2 vectors of 8 per chunk
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+          w[e] = real ? __ldg(reinterpret_cast<const uint4*>(src + (t4 + 4 * (e >> 1)) * 16 + (e & 1) * 8))
+                      : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t am = 0;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) am = amax2(w[e].x, amax2(w[e].y, amax2(w[e].z, amax2(w[e].w, am))));
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        const int ex = row_exponent(am << 16);
+        const float inv = pow2i(-ex);
+        c[y] = a.scale_log2 * pow2i(ex);
+        lim[y] = !real ? 0 : (a.causal ? min(s.len, s.len - s.n + tk + 1) : s.len);
+#pragma unroll
+        for (int kk = 0; kk < kK; ++kk) {
+          const uint4 v = w[2 * (kk >> 2) + ((kk & 3) >> 1)];
+          const uint32_t p0 = (kk & 1) ? v.z : v.x, p1 = (kk & 1) ? v.w : v.y;
+          qa[kk][y] = pack_f16(__uint_as_float(p0 << 16) * inv, __uint_as_float(p0 & 0xffff0000u) * inv);
+          qa[kk][2 + y] = pack_f16(__uint_as_float(p1 << 16) * inv, __uint_as_float(p1 & 0xffff0000u) * inv);
+        }
+      }
+      // keys visible to every real row of the tile
+      const int all = a.causal ? min(s.len, s.len - s.n + s.row0 / a.g + 1) : s.len;
+
+      for (int k = warp; k < s.nt; k += kWarps) {
+        const int p = s.base + k, st = p % Ly::kStages;
+        ok = mbar_wait(full(st), (p / Ly::kStages) & 1, wc, kSiteStageFull, p);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
+        const float4 sc = s_scales[st];
+        const int valid = s_valid[st];
+        const int key0 = (s.t0 + k) * kKeys;
+        const bool careful = key0 + kKeys > all || valid != 3;
+        // scores in log2 units
+        float x[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[j][e] = 0.f;
+          const int t = tok<D>(j, g4);
+#pragma unroll
+          for (int hc = 0; hc < D / 64; ++hc) {
+            const uint4 w = lds128(kb + code_at<D>(t, t4 + 4 * hc));
+            const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t b0, b1;
+              e4m3_to_f16(wd[e], b0, b1);
+              mma16816(x[j], qa[4 * hc + e], b0, b1);
+            }
+          }
+        }
+        float gm[2][2];  // largest score of each row in each group of 16 keys
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) {
+          const float k2 = gr ? sc.y : sc.x;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float f = c[y] * k2;
+#pragma unroll
+            for (int j = 2 * gr; j < 2 * gr + 2; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) x[j][2 * y + e] *= f;
+          }
+        }
+        if (careful) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int t = tok<D>(j, 2 * t4 + e);
+              const bool there = (valid >> (t >> 4)) & 1;
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (!there || key0 + t >= lim[y]) x[j][2 * y + e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            gm[gr][y] = quad_max(fmaxf(fmaxf(x[2 * gr][2 * y], x[2 * gr][2 * y + 1]),
+                                       fmaxf(x[2 * gr + 1][2 * y], x[2 * gr + 1][2 * y + 1])));
+        const float lv[2] = {floor_log2(sc.z), floor_log2(sc.w)};
+        float wgt[2][2], up[2];
+        bool grew = false;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float m1 = fmaxf(m[y], fmaxf(gm[0][y], gm[1][y]));
+          const float E1 = fmaxf(E[y], fmaxf(gm[0][y] + lv[0], gm[1][y] + lv[1]));
+          l[y] *= ex2(m[y] - m1);
+          up[y] = ex2(E[y] - E1);
+          grew = grew || E1 > E[y];
+          m[y] = m1;
+          E[y] = E1;
+          const float f = ex2(fminf(m1 - E1 + 14.f, 120.f));
+          wgt[0][y] = f * sc.z;
+          wgt[1][y] = f * sc.w;
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            o[i][0] *= up[0];
+            o[i][1] *= up[0];
+            o[i][2] *= up[1];
+            o[i][3] *= up[1];
+          }
+        }
+        uint32_t pa[2][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float p0 = ex2(x[j][2 * y] - m[y]), p1 = ex2(x[j][2 * y + 1] - m[y]);
+            l[y] += p0 + p1;
+            pa[j >> 1][2 * (j & 1) + y] = pack_f16(p0 * wgt[j >> 1][y], p1 * wgt[j >> 1][y]);
+          }
+        // O += P V: lane g4 takes output columns g4 D/8 .. of the keys 2 t4, 2 t4 + 1
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          uint32_t w[4][D / 32];  // keys: score tile 2 ks (even, odd column), 2 ks + 1
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = tok<D>(2 * ks + (e >> 1), 2 * t4 + (e & 1));
+            if constexpr (D == 128) {
+              const uint4 v = lds128(vb + code_at<D>(t, g4));
+              w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
+            } else {
+              const uint2 v = lds64(vb + code_at<D>(t, g4 >> 1) + (g4 & 1) * 8);
+              w[e][0] = v.x; w[e][1] = v.y;
+            }
+            // what lies behind the last token may be anything, NaN too
+            if (careful && (key0 + t >= s.len || !((valid >> (t >> 4)) & 1))) {
+#pragma unroll
+              for (int f = 0; f < D / 32; ++f) w[e][f] = 0u;
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < D / 32; ++f) {
+            uint32_t b0[4], b1[4];
+            e4m3_to_f16(__byte_perm(w[0][f], w[1][f], 0x5140), b0[0], b0[1]);
+            e4m3_to_f16(__byte_perm(w[0][f], w[1][f], 0x7362), b0[2], b0[3]);
+            e4m3_to_f16(__byte_perm(w[2][f], w[3][f], 0x5140), b1[0], b1[1]);
+            e4m3_to_f16(__byte_perm(w[2][f], w[3][f], 0x7362), b1[2], b1[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mma16816(o[4 * f + e], pa[ks], b0[e], b1[e]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(st));
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+      }
+    }
+
+    // merge of the warps.  The buffer is free once every warp has read the
+    // piece before.
+    if (ns > 0) {
+      ok = mbar_wait(base + Ly::kMergeR, (ns - 1) & 1, wc, kSiteMergeR, ns);
+      if (!__all_sync(0xffffffffu, ok)) return;
+    }
+    // Lane (g4, t4) holds columns (2 t4 + e) D/8 + i of rows g4 (+ 8) in
+    // o[i][e (+ 2)]; 16-byte chunks are XORed so that the eight lanes of a
+    // store fall on different banks.
+    auto chunk_at = [](int row, int ch) {
+      const int sw = D == 128 ? ((ch >> 3) & 3) | ((row & 1) << 2) : ((ch >> 3) & 1) | ((row & 1) << 1);
+      return ch ^ sw;
+    };
+    if (warp < s.nt) {
+      float* mw = merge + warp * kRows * D;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int row = g4 + 8 * y;
+        if (row < s.nv) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < kN; i += 4) {
+              const int ch = ((2 * t4 + e) * (D / 8) + i) >> 2;
+              *reinterpret_cast<float4*>(mw + row * D + 4 * chunk_at(row, ch)) =
+                  make_float4(o[i][2 * y + e], o[i + 1][2 * y + e], o[i + 2][2 * y + e], o[i + 3][2 * y + e]);
+            }
+          if (t4 == 0) stats[warp * kRows + row] = make_float4(m[y], l[y], E[y], 0.f);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(base + Ly::kMergeW);
+    ok = mbar_wait(base + Ly::kMergeW, ns & 1, wc, kSiteMergeW, ns);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    const int nw = min(kWarps, s.nt);
+    for (int it = tid; it < s.nv * (D / 4); it += 32 * kWarps) {
+      const int row = it / (D / 4), ch = it % (D / 4);
+      float M = kInit, Em = kInit;
+      for (int w = 0; w < nw; ++w) {
+        const float4 q = stats[w * kRows + row];
+        M = fmaxf(M, q.x);
+        Em = fmaxf(Em, q.z);
+      }
+      float L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < nw; ++w) {
+        const float4 q = stats[w * kRows + row];
+        const float f = ex2(q.z - Em);
+        const float4 v = *reinterpret_cast<const float4*>(merge + (w * kRows + row) * D + 4 * chunk_at(row, ch));
+        L += q.y * ex2(q.x - M);
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+      // a row without a visible key: O = 0, L = -inf
+      const float fin = L == 0.f ? 0.f : ex2(Em - M - 14.f) / L;
+      const float lg = L == 0.f ? -INFINITY : M + log2f(L);
+      acc.x *= fin;
+      acc.y *= fin;
+      acc.z *= fin;
+      acc.w *= fin;
+      if (s.mode == 0) {
+        const int rr = s.row0 + row, tk = rr / a.g;
+        const long long at = static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
+        *reinterpret_cast<uint2*>(a.o + at * D + 4 * ch) =
+            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+        if (ch == 0) a.lse[at] = lg * 0.6931471805599453f;
+      } else {
+        const long long at = static_cast<long long>(s.slot) * kRows + row;
+        *reinterpret_cast<float4*>(a.part_o + at * D + 4 * ch) = acc;
+        if (ch == 0) a.part_l[at] = lg;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(base + Ly::kMergeR);
+      mbar_arrive(base + Ly::kSegEmpty + 8 * si);
+    }
+  }
+}
+
+// Merges the partials of each unit that more than one CTA worked on, in CTA
+// order: L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s.  One CTA per CTA of
+// the forward: it takes the unit that one began and did not finish.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) fa_cache_merge_kernel(const __grid_constant__ CacheFwdArgs a, int grid) {
+  __shared__ int s_end;
+  __shared__ int s_n;
+  __shared__ int s_slot[257];
+  griddep_wait();
+  const int4 d = a.desc[blockIdx.x];
+  if (d.x < 0) return;
+  const int c = blockIdx.x, tid = threadIdx.x;
+  if (tid == 0) {
+    s_end = grid;
+    s_n = 0;
+  }
+  __syncthreads();
+  // the unit ends in the first CTA behind this one that says so; CTAs in
+  // between may have had nothing to do
+  const int at = c + 1 + tid;
+  const int mark = at < grid ? a.cont[at] : 0;
+  if (mark == 2) atomicMin(&s_end, at);
+  __syncthreads();
+  const bool part = mark != 0 && at <= s_end;
+  const uint32_t bal = __ballot_sync(0xffffffffu, part);
+  __shared__ int s_cnt[8];
+  if ((tid & 31) == 0) s_cnt[tid >> 5] = __popc(bal);
+  __syncthreads();
+  int off = 1;
+  for (int w = 0; w < (tid >> 5); ++w) off += s_cnt[w];
+  if (part) s_slot[off + __popc(bal & ((1u << (tid & 31)) - 1u))] = 2 * at;
+  if (tid == 0) s_slot[0] = 2 * c + 1;
+  if (tid == 255) s_n = off + __popc(bal);
+  __syncthreads();
+  const int n = s_n;
+  const int n0 = max(0, min(a.T, a.cu_q[d.x]));
+  for (int it = tid; it < d.w * (D / 4); it += 256) {
+    const int row = it / (D / 4), ch = it % (D / 4);
+    float M = -INFINITY;
+    for (int i = 0; i < n; ++i) M = fmaxf(M, a.part_l[static_cast<long long>(s_slot[i]) * ROWS + row]);
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; ++i) {
+      const long long p = static_cast<long long>(s_slot[i]) * ROWS + row;
+      const float l = a.part_l[p];
+      const float f = l == -INFINITY ? 0.f : ex2(l - M);
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + p * D + 4 * ch);
+      L += f;
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int rr = d.z * ROWS + row, tk = rr / a.g;
+    const long long to = static_cast<long long>(n0 + tk) * a.Hq + d.y * a.g + (rr - tk * a.g);
+    *reinterpret_cast<uint2*>(a.o + to * D + 4 * ch) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (ch == 0) a.lse[to] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace fa

@@ -14,11 +14,13 @@
 #include "fa_fp8.cuh"
 #include "fa_fwd.h"
 #include "fa_fwd_pair.cuh"
+#include "fa_host.h"
 #include "fa_unfused.cuh"
 
 namespace fa {
 
 __device__ DevError g_dev_error;
+__device__ DevError g_index_error;  // first block, slot or length outside its range
 
 // Fixed scratch of the no-allocation split entry point: part of the module
 // image, so it exists on every device the library is loaded on and costs no
@@ -293,6 +295,7 @@ struct DeviceInfo {
   int pair_clusters[16] = {};
   bool unf_ready[4] = {};
   DevError* err = nullptr;         // this device's copy of g_dev_error
+  DevError* index_err = nullptr;   // and of g_index_error
   void* noalloc_scratch = nullptr;  // this device's copy of g_noalloc_scratch
   int sms = 0;                      // multiprocessors (set by the backward's first launch)
   int prep_per_sm[2] = {};          // resident blocks per SM of the backward's statistics kernel (d 64, 128)
@@ -315,6 +318,8 @@ int current_device(int* dev_out, DeviceInfo** info) {
     if (!di.err) {
       DevError* p = nullptr;
       e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_dev_error);
+      if (e != cudaSuccess) return cuda_fail(e);
+      e = cudaGetSymbolAddress(reinterpret_cast<void**>(&di.index_err), g_index_error);
       if (e != cudaSuccess) return cuda_fail(e);
       di.err = p;
     }
@@ -1128,6 +1133,29 @@ int fwd_e4m3(const void* q8, const void* k8, const void* vt8, const float* dsq, 
 }
 
 }  // namespace
+
+// For the library's other translation unit (fa_host.h).
+namespace host {
+int fail(cudaError_t e) { return cuda_fail(e); }
+bool overlap(const void* a, size_t na, const void* b, size_t nb) { return overlaps(a, na, b, nb); }
+int tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, cuuint64_t d0, cuuint64_t d1,
+               cuuint64_t d2, cuuint64_t stride1, cuuint64_t stride2, cuuint32_t box0, cuuint32_t box1) {
+  return encode_3d(map, dtype, base, d0, d1, d2, stride1, stride2, box0, box1);
+}
+int device(Device* out) {
+  int dev = 0;
+  DeviceInfo* di = nullptr;
+  const int st = current_device(&dev, &di);
+  if (st != FA_OK) return st;
+  std::lock_guard<std::mutex> lock(g_setup_mu);
+  if (di->sms == 0) {
+    const cudaError_t e = cudaDeviceGetAttribute(&di->sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  *out = Device{dev, di->sms, di->err, di->index_err};
+  return FA_OK;
+}
+}  // namespace host
 }  // namespace fa
 
 extern "C" {
@@ -1278,6 +1306,18 @@ int fa_check_errors(void* stream) {
     if (e != cudaSuccess) return fa::cuda_fail(e);
     return FA_ERR_TIMEOUT;
   }
+  e = cudaMemcpyFromSymbol(&rec, fa::g_index_error, sizeof(rec));
+  if (e != cudaSuccess) return fa::cuda_fail(e);
+  if (rec.code != 0) {
+    fa::t_last_record[0] = rec.code;
+    fa::t_last_record[1] = rec.site;
+    fa::t_last_record[2] = rec.block;
+    fa::t_last_record[3] = rec.tile;
+    const fa::DevError zero = {0, 0, 0, 0};
+    e = cudaMemcpyToSymbol(fa::g_index_error, &zero, sizeof(zero));
+    if (e != cudaSuccess) return fa::cuda_fail(e);
+    return FA_ERR_INDEX;
+  }
   return FA_OK;
 }
 
@@ -1289,6 +1329,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_MISALIGNED: return "FA_ERR_MISALIGNED";
     case FA_ERR_CUDA: return "FA_ERR_CUDA";
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
+    case FA_ERR_INDEX: return "FA_ERR_INDEX";
     default: return "FA_ERR_UNKNOWN";
   }
 }

@@ -45,7 +45,9 @@ typedef enum {
                               in fa_bwd and fa_fwd_e4m3 */
   FA_ERR_MISALIGNED = -3,  /* a pointer is not 16-byte aligned (lse: 4-byte) */
   FA_ERR_CUDA = -4,        /* a CUDA runtime/driver call failed; see fa_get_last_cuda_error */
-  FA_ERR_TIMEOUT = -5      /* a bounded device-side wait expired (see fa_check_errors) */
+  FA_ERR_TIMEOUT = -5,     /* a bounded device-side wait expired (see fa_check_errors) */
+  FA_ERR_INDEX = -6        /* a slot, block or length on the device was out of range
+                              (see fa_check_errors) */
 } fa_status;
 
 /*
@@ -332,10 +334,141 @@ int fa_attn_unfused(const void* q, const void* k, const void* v, void* o, float*
 size_t fa_attn_unfused_workspace_size(int B, int H, int N, int d);
 
 /*
+ * The 8-bit key/value cache: what attention needs from a prompt to its last
+ * token.  The cache is a pool of blocks of P tokens, P one of 16, 32, 64, 128:
+ *   k8, v8           : E4M3 codes [num_blocks][Hkv][P][d], 16-byte aligned;
+ *   k_scale, v_scale : fp32 [num_blocks][Hkv]: the value a code stands for is
+ *                      E4M3(code) * scale of its block and head.
+ * d is 64 or 128 and num_blocks * Hkv at most 2^31 - 1.  A request of `len`
+ * cached tokens keeps token i in block table[i / P] at offset i % P; the
+ * block's number times P plus the offset is the token's slot.  Requests come
+ * as a batch of R: block_table int32 [R][max_blocks], seq_lens int32 [R], and
+ * rows of new tokens one request behind the other, request r's from cu[r] to
+ * cu[r + 1].
+ *
+ * Lengths, tables and slots are device memory and are checked there: a value
+ * out of range is never used as an address.  What each call does with it is
+ * said below; where that loses a token, fa_check_errors reports FA_ERR_INDEX
+ * and the record's site and work item say which check (601 a slot of an
+ * append, item: token; 611 a block, 612 a length, 613 row offsets of a
+ * forward, item: request).
+ *
+ * Calls take any state of these arrays, so they can be captured into a graph
+ * and replayed on new lengths.
+ */
+
+/*
+ * fa_cache_slots — grants blocks to requests and gives every new token its
+ * slot, on the device:
+ *   held_r = ceil(seq_lens[r] / P), need_r = ceil((seq_lens[r] + new_lens[r]) / P) - held_r
+ *   block_table[r][held_r + i] = the next entries of free_blocks, in the order
+ *     of the requests, from free_blocks[*free_used] on     (written in place)
+ *   cu_new[r]       = new_lens[0] + ... + new_lens[r - 1], r = 0 .. R
+ *   slot_map[cu_new[r] + i] = slot of token seq_lens[r] + i of request r
+ *   seq_lens_out[r] = seq_lens[r] + new_lens[r]
+ *   *free_used_out  = *free_used + the number of blocks granted
+ * A request that cannot be served is left as it is: its blocks would exceed
+ * max_blocks, its tokens num_tokens, or the free blocks do not last for it.
+ * Its slots are -1, its seq_lens_out is seq_lens[r], and it takes no block (a
+ * request that needs no block is served even when none are left).  Slots
+ * behind cu_new[R] are -1, and so are those in a held block whose table entry
+ * is negative.  Negative lengths count as 0.
+ *   free_blocks : int32 [num_free], distinct blocks in use by no request.
+ *   free_used   : int32 [1], how many of them are gone already.
+ *   slot_map    : int64 [num_tokens].  cu_new: int32 [R + 1].
+ *   R, num_free, num_tokens >= 0; max_blocks >= 1.  Arrays of no element may
+ *   be NULL.
+ * Errors: NULL, a negative count, outputs that overlap inputs or one another:
+ * FA_ERR_INVALID_ARG; block_tokens not 16, 32, 64 or 128: FA_ERR_UNSUPPORTED;
+ * int32 arrays not 4-byte or slot_map not 8-byte aligned: FA_ERR_MISALIGNED.
+ * Enqueues one kernel.
+ */
+int fa_cache_slots(int* block_table, const int* seq_lens, const int* new_lens, const int* free_blocks,
+                   const int* free_used, int* cu_new, long long* slot_map, int* seq_lens_out,
+                   int* free_used_out, int R, int max_blocks, int num_free, int block_tokens,
+                   int num_tokens, void* stream);
+
+/*
+ * fa_cache_append_e4m3 — writes T new K and V rows into the cache at their
+ * slots.  A run is a longest stretch of consecutive rows in consecutive slots
+ * of one block.  For each run, each head and K and V apart:
+ *   a = max |x| over the run; e = the smallest integer with a <= 448 * 2^e,
+ *     kept within [-100, 120]
+ *   scale = 2^e where the run starts at offset 0 of its block (a new block),
+ *     else the larger of 2^e and the block's scale; if that grew, the codes
+ *     of the block's rows before the run become E4M3(value * old / new)
+ *   code = E4M3(x / scale)
+ * with E4M3 rounding to nearest even.  Rows behind the run are left as they
+ * were.  Scales are powers of two, so a code that stays within E4M3's normal
+ * range keeps its exact value when its block's scale grows.
+ *   k, v     : bf16, row t of head h at k + t * k_stride + h * d (elements), so
+ *              that a slice of a projection's output can be given as it is;
+ *              16-byte aligned, strides multiples of 8 and at least Hkv * d
+ *              (of no matter for T = 1).  Finite: a NaN or infinity leaves its
+ *              run's codes and scale unspecified.
+ *   slot_map : int64 [T].  -1: the row is skipped; any other value outside
+ *              [0, num_blocks * P) is reported (FA_ERR_INDEX) and skipped.
+ *              Two runs of one call must not lie in one block (their writes
+ *              of its scale would race: that block's contents are then
+ *              unspecified); fa_cache_slots gives no such map while its free
+ *              blocks are distinct.
+ *   T >= 0 (0: nothing to do).  Hkv <= 65535.
+ * Errors: NULL, a negative or zero size, a short stride, or a cache array that
+ * overlaps another array: FA_ERR_INVALID_ARG; d, P or sizes out of range:
+ * FA_ERR_UNSUPPORTED; alignment: FA_ERR_MISALIGNED.  Enqueues one kernel.
+ */
+int fa_cache_append_e4m3(const void* k, const void* v, long long k_stride, long long v_stride, void* k8,
+                         void* v8, float* k_scale, float* v_scale, const long long* slot_map, int T,
+                         int Hkv, int d, int num_blocks, int block_tokens, void* stream);
+
+/*
+ * fa_cache_fwd_e4m3 — attention of each request's newest tokens over its
+ * cached keys, themselves among them (append first).  Request r has
+ * n = cu_q[r + 1] - cu_q[r] query rows, the tokens len - n .. len - 1 of its
+ * len = seq_lens[r]: one when decoding, several of a draft, all of a prompt.
+ * Query head h reads kv head h / (Hq / Hkv).  With x_i the query row of token
+ * position i and k_j, v_j the cached values:
+ *   s_ij = scale * x_i . k_j,  L_i = ln sum_j exp(s_ij),  O_i = sum_j exp(s_ij - L_i) v_j
+ * over j < len and, if causal, j <= i.  A row without a visible key gets O = 0
+ * and L = -inf; rows from cu_q[R] on are left as they were.
+ *   q    : bf16, row t of head h at q + t * q_stride + h * d (elements),
+ *          16-byte aligned, q_stride a multiple of 8 and at least Hq * d (of
+ *          no matter for T = 1).
+ *   o    : bf16 [T][Hq][d], 16-byte aligned.  lse: fp32 [T][Hq].
+ *   cu_q : int32 [R + 1], ascending from 0 on; R, T >= 0 (0: nothing to do).
+ *   Hq a multiple of Hkv; T * Hq and max_blocks * P below 2^31.
+ *   scale: finite.  causal: 0 or 1.
+ *   What lies in the cache at and behind a request's len may be anything.
+ *   Lengths above max_blocks * P, negative ones and row offsets outside
+ *   [0, T] are cut off to the range and reported (FA_ERR_INDEX); the keys of a
+ *   block outside [0, num_blocks) count as not visible and it is reported.
+ *   workspace: at least fa_cache_fwd_e4m3_workspace_size(d) bytes, 16-byte
+ *          aligned.  Contents on entry are ignored.  Calls that may run at
+ *          the same time need one each.
+ * O and L are those of the exact attention over the cached values, up to the
+ * rounding of the softmax weights to f16 in the product with V.  Results do
+ * not depend on the order in which blocks run, and are the same from call to
+ * call.  Errors as above, and Hq % Hkv != 0, a missing or short workspace, or
+ * an output that overlaps an input or another output: FA_ERR_INVALID_ARG.
+ * Enqueues one kernel, and a second that merges the parts of requests whose
+ * keys were split (launched as a programmatic dependent of the first).
+ */
+int fa_cache_fwd_e4m3(const void* q, long long q_stride, const void* k8, const void* v8,
+                      const float* k_scale, const float* v_scale, const int* block_table,
+                      const int* seq_lens, const int* cu_q, void* o, float* lse, int R, int T, int Hq,
+                      int Hkv, int d, int num_blocks, int block_tokens, int max_blocks, float scale,
+                      int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fa_cache_fwd_e4m3 on the current device, whatever the
+ * batch; 0 for an unsupported d. */
+size_t fa_cache_fwd_e4m3_workspace_size(int d);
+
+/*
  * fa_check_errors — synchronise `stream`, then report and clear the device
  * error record: FA_ERR_TIMEOUT if a bounded wait expired in any kernel since
- * the last check (the outputs of that call are then invalid), FA_ERR_CUDA if
- * the synchronisation failed, else FA_OK.
+ * the last check (the outputs of that call are then invalid), FA_ERR_INDEX if
+ * a cache call met an index out of range (it did what its own text says),
+ * FA_ERR_CUDA if the synchronisation failed, else FA_OK.
  */
 int fa_check_errors(void* stream);
 
@@ -358,9 +491,9 @@ const char* fa_status_string(int status);
 int fa_get_last_cuda_error(void);
 
 /*
- * The device error record behind the most recent FA_ERR_TIMEOUT returned by
- * fa_check_errors on this thread: out4[0] = code (1 = bounded wait expired),
- * out4[1] = wait site, out4[2] = CTA index, out4[3] = work item.  All zero if
+ * The device error record behind the most recent FA_ERR_TIMEOUT or
+ * FA_ERR_INDEX returned by fa_check_errors on this thread: out4[0] = code (1),
+ * out4[1] = site, out4[2] = CTA index, out4[3] = work item.  All zero if
  * none.  FA_ERR_INVALID_ARG if out4 is NULL.
  */
 int fa_get_last_error_record(unsigned int* out4);

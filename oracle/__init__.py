@@ -35,3 +35,10 @@ from .fp8 import (  # noqa: F401
     quantize_e4m3,
     transpose_keys_last,
 )
+from .cache import (  # noqa: F401
+    attention_cache,
+    block_scale,
+    cache_append,
+    cache_slots,
+    cache_values,
+)
