@@ -154,7 +154,7 @@ def test_oracle_slots_by_hand():
 
 
 def test_oracle_scale_is_the_smallest_power_of_two():
-    for a in (1e-30, 0.3, 1.75, 1.7578125, 447.0, 448.0, 449.0, 1e6, 3e38):
+    for a in (1e-25, 0.3, 1.75, 1.7578125, 447.0, 448.0, 449.0, 1e6, 3e38):
         s = oracle.block_scale(a)
         assert a <= 448 * s and a > 224 * s
     assert oracle.block_scale(0.0) == 2.0 ** -100 and oracle.block_scale(1e-37) == 2.0 ** -100
