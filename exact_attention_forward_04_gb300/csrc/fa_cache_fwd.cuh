@@ -49,6 +49,8 @@ constexpr int kThreads = 32 * (kWarps + 1);  // and the producer
 constexpr int kRows = 16;                    // query rows of a unit
 constexpr int kKeys = 32;                    // keys of a tile
 constexpr int kSegs = 4;                     // unit pieces in flight
+constexpr int kMeta = 64;                    // tiles whose blocks and scales are held
+constexpr int kIssue = 8;                    // lanes that issue loads
 constexpr int kUnitCost = 3;                 // a piece's fixed cost, in tiles
 constexpr int kMinCost = 12;                 // least cost of a CTA's range
 constexpr float kInit = -1e30f;              // references before the first key
@@ -72,9 +74,9 @@ struct Layout {
   static constexpr int kStages = 131072 / kStage;
   static constexpr int kMerge = kStages * kStage;
   static constexpr int kStats = kMerge + kWarps * kRows * D * 4;  // float4 [warps][rows]
-  static constexpr int kScales = kStats + kWarps * kRows * 16;    // float4 [stages]
-  static constexpr int kValid = kScales + kStages * 16;           // int [stages]
-  static constexpr int kSeg = kValid + kStages * 4;
+  static constexpr int kScales = kStats + kWarps * kRows * 16;    // float4 [meta]
+  static constexpr int kBlk = kScales + kMeta * 16;               // int2 [meta]
+  static constexpr int kSeg = kBlk + kMeta * 8;
   static constexpr int kBar = (kSeg + kSegs * static_cast<int>(sizeof(Seg)) + 15) & ~15;
   static constexpr int kFull = kBar;                    // [stages]
   static constexpr int kEmpty = kFull + 8 * kStages;    // [stages]
@@ -114,11 +116,10 @@ __device__ __forceinline__ uint32_t code_at(int t, int c) {
   return static_cast<uint32_t>(row * 128 + ((ch ^ (row & 7)) << 4));
 }
 
-// Waits for a phase for at most `timeout_ns`, whether or not the CTA is
+// Waits for a phase until the time `end` at most, whether or not the CTA is
 // giving up: for copies in flight that must not outlive it.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 <= timeout_ns) {
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t end) {
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() < end) {
   }
 }
 
@@ -149,8 +150,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Ly::kAbort);
   Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
   float4* s_scales = reinterpret_cast<float4*>(sm + Ly::kScales);
-  int* s_valid = reinterpret_cast<int*>(sm + Ly::kValid);
+  int2* s_blk = reinterpret_cast<int2*>(sm + Ly::kBlk);
   if (tid == 0) {
     for (int i = 0; i < Ly::kStages; ++i) {
       mbar_init(base + Ly::kFull + 8 * i, 1);
@@ -296,11 +296,11 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
     long long x = x0, rem = *reinterpret_cast<long long*>(sm + Ly::kStart);
     int r = *reinterpret_cast<int*>(sm + Ly::kStart + 8);
     int pos = 0, nseg = 0;  // ring positions used, pieces published
+    int issued = 0;         // positions up to this lane's last load
     int held = -1;          // first request of the 32 in the lanes' registers
     Req mineq{};
     const int P = 1 << a.sh;
     const int boxes = P < kKeys ? 2 : 1;
-    const uint32_t box_bytes = static_cast<uint32_t>(Ly::kHalf / boxes);
     bool ok = true;
     while (ok && x < x1) {
       if (held < 0 || r >= held + 32) {
@@ -350,7 +350,10 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
           if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
         }
         ++nseg;
-        // its tiles, 32 at a time: a lane fetches one tile's blocks and scales
+        // its tiles, 32 at a time: a lane fetches one tile's blocks and scales,
+        // then one lane issues the loads.  An entry is reused 64 tiles later:
+        // before the first of these 32 tiles was issued, all but the last
+        // ring's worth (at most 32) had been consumed.
         const int* row = a.table + static_cast<long long>(r) * a.M;
         for (int b = t0; ok && b < t1; b += 32) {
           const int tile = b + lane;
@@ -376,36 +379,45 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
                 vs[i] = a.vs[bh];
               }
             if (boxes == 1) { ks[1] = ks[0]; vs[1] = vs[0]; }
+            const int at = (pos + lane) % kMeta;
+            s_scales[at] = make_float4(ks[0], ks[1], vs[0], vs[1]);
+            s_blk[at] = make_int2(blk[0], boxes == 1 ? blk[0] : blk[1]);
           }
+          __syncwarp();
           const int cnt = min(32, t1 - b);
-          for (int i = 0; i < cnt; ++i) {
-            const int st = pos % Ly::kStages, round = pos / Ly::kStages;
-            if (round > 0) ok = mbar_wait(empty(st), (round - 1) & 1, wc, kSiteStageEmpty, pos);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            if (lane == i) {
-              const int valid = boxes == 1 ? (blk[0] >= 0 ? 3 : 0)
-                                           : (blk[0] >= 0 ? 1 : 0) | (blk[1] >= 0 ? 2 : 0);
-              s_scales[st] = make_float4(ks[0], ks[1], vs[0], vs[1]);
-              s_valid[st] = valid;
+          if (lane < kIssue) {
+            for (int i = lane; i < cnt; i += kIssue) {
+              const int p = pos + i, st = p % Ly::kStages, round = p / Ly::kStages;
+              if (round > 0 && !mbar_wait(empty(st), (round - 1) & 1, wc, kSiteStageEmpty, p)) { ok = false; break; }
+              issued = p + 1;
+              const int2 bl = s_blk[p % kMeta];
               const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
-              const uint32_t nbox = (blk[0] >= 0 ? 1u : 0u) + (blk[1] >= 0 ? 1u : 0u);
-              if (nbox == 0) {
-                mbar_arrive(full(st));
+              if (boxes == 1) {
+                if (bl.x >= 0) {
+                  const int y = (((b + i) * kKeys) & (P - 1)) * D / 128;
+                  const int bh = bl.x * a.Hkv + h;
+                  mbar_arrive_expect_tx(full(st), Ly::kStage);
+                  tma_load_3d(kb, &tmK, full(st), 0, y, bh);
+                  tma_load_3d(vb, &tmV, full(st), 0, y, bh);
+                } else {
+                  mbar_arrive(full(st));
+                }
               } else {
-                mbar_arrive_expect_tx(full(st), nbox * 2 * box_bytes);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  if (blk[j] >= 0) {
-                    const int y = ((tile * kKeys) & (P - 1)) * D / 128;
-                    const int bh = blk[j] * a.Hkv + h;
-                    tma_load_3d(kb + j * box_bytes, &tmK, full(st), 0, boxes == 1 ? y : 0, bh);
-                    tma_load_3d(vb + j * box_bytes, &tmV, full(st), 0, boxes == 1 ? y : 0, bh);
-                  }
+                const uint32_t nbox = (bl.x >= 0 ? 1u : 0u) + (bl.y >= 0 ? 1u : 0u);
+                mbar_arrive_expect_tx(full(st), nbox * Ly::kHalf);
+                if (bl.x >= 0) {
+                  tma_load_3d(kb, &tmK, full(st), 0, 0, bl.x * a.Hkv + h);
+                  tma_load_3d(vb, &tmV, full(st), 0, 0, bl.x * a.Hkv + h);
+                }
+                if (bl.y >= 0) {
+                  tma_load_3d(kb + Ly::kHalf / 2, &tmK, full(st), 0, 0, bl.y * a.Hkv + h);
+                  tma_load_3d(vb + Ly::kHalf / 2, &tmV, full(st), 0, 0, bl.y * a.Hkv + h);
+                }
               }
             }
-            __syncwarp();
-            ++pos;
           }
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) pos += cnt;
         }
       }
       ++r;
@@ -423,8 +435,12 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
     }
     // every load issued has landed before this warp exits, also where the
     // consumers gave up
-    for (int p = max(0, pos - Ly::kStages); p < pos; ++p)
-      mbar_drain(full(p % Ly::kStages), (p / Ly::kStages) & 1, a.timeout_ns);
+    issued = __reduce_max_sync(0xffffffffu, issued);
+    if (lane == 0) {
+      const uint64_t end = globaltimer_ns() + a.timeout_ns;
+      for (int p = max(0, issued - Ly::kStages); p < issued; ++p)
+        mbar_drain(full(p % Ly::kStages), (p / Ly::kStages) & 1, end);
+    }
     return;
   }
 
@@ -490,28 +506,41 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
         ok = mbar_wait(full(st), (p / Ly::kStages) & 1, wc, kSiteStageFull, p);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
-        const float4 sc = s_scales[st];
-        const int valid = s_valid[st];
+        const float4 sc = s_scales[p % kMeta];
+        const int2 bl = s_blk[p % kMeta];
+        const int valid = (bl.x >= 0 ? 1 : 0) | (bl.y >= 0 ? 2 : 0);
         const int key0 = (s.t0 + k) * kKeys;
         const bool careful = key0 + kKeys > all || valid != 3;
         // scores in log2 units
         float x[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[j][e] = 0.f;
-          const int t = tok<D>(j, g4);
+        // two score tiles at a time: two chains of dependent products
 #pragma unroll
-          for (int hc = 0; hc < D / 64; ++hc) {
-            const uint4 w = lds128(kb + code_at<D>(t, t4 + 4 * hc));
-            const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+        for (int j = 0; j < 4; j += 2) {
+          uint32_t w[2][D / 16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t b0, b1;
-              e4m3_to_f16(wd[e], b0, b1);
-              mma16816(x[j], qa[4 * hc + e], b0, b1);
+          for (int f = 0; f < 2; ++f) {
+            const int t = tok<D>(j + f, g4);
+#pragma unroll
+            for (int hc = 0; hc < D / 64; ++hc) {
+              const uint4 v = lds128(kb + code_at<D>(t, t4 + 4 * hc));
+              w[f][4 * hc] = v.x;
+              w[f][4 * hc + 1] = v.y;
+              w[f][4 * hc + 2] = v.z;
+              w[f][4 * hc + 3] = v.w;
             }
           }
+#pragma unroll
+          for (int e = 0; e < kK; ++e)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              uint32_t b0, b1;
+              e4m3_to_f16(w[f][e], b0, b1);
+              mma16816(x[j + f], qa[e], b0, b1);
+            }
         }
         float gm[2][2];  // largest score of each row in each group of 16 keys
 #pragma unroll
