@@ -172,20 +172,10 @@ def _append(handle, k, v, cache, slot_map, T, H, d, blocks, P):
         slot_map.data_ptr(), T, H, d, blocks, P, handle), "fa_cache_append_e4m3")
 
 
-_ws_bytes = {}
-
-
-def cache_forward_workspace_size(d, device=None) -> int:
-    """Workspace bytes of ``cache_forward_e4m3`` on ``device`` (default: the
-    current one), whatever the batch."""
-    index = torch.cuda.current_device() if device is None else torch.device(device).index
-    n = _ws_bytes.get((index, d))
-    if n is None:
-        with torch.cuda.device(index):
-            n = int(_lib().fa_cache_fwd_e4m3_workspace_size(int(d)))
-        if n:
-            _ws_bytes[index, d] = n
-    return n
+def cache_forward_workspace_size(R, T, heads, heads_kv, d) -> int:
+    """Workspace bytes of ``cache_forward_e4m3`` on the current device for R
+    requests and T query rows (0: none needed, or sizes it does not take)."""
+    return int(_lib().fa_cache_fwd_e4m3_workspace_size(int(R), int(T), int(heads), int(heads_kv), int(d)))
 
 
 def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal=True, workspace=None, stream=None):
@@ -196,8 +186,8 @@ def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal
     [R + 1]), its last ones of seq_lens[r] (int32 [R]) cached tokens, whose
     blocks are block_table[r] (int32 [R, max_blocks]).  Returns (o bf16 [T,
     Hq, d], lse fp32 [T, Hq]); rows behind cu_q[R] are not written.
-    ``workspace`` (a CUDA tensor of cache_forward_workspace_size(d) bytes) may
-    be passed to reuse memory; calls that may overlap need one each."""
+    ``workspace`` (a CUDA tensor of cache_forward_workspace_size bytes) may be
+    passed to reuse memory; calls that may overlap need one each."""
     dev, (blocks, H, P, d) = _check_cache(cache)
     _check_rows("q", q, None, d, dev)
     T, Hq, _ = q.shape
@@ -220,7 +210,7 @@ def _forward(handle, q, cache, table, seq_lens, cu_q, scale, causal, ws, R, T, H
     o = torch.empty((T, Hq, d), dtype=_BF16, device=dev)
     lse = torch.empty((T, Hq), dtype=_F32, device=dev)
     if ws is None:
-        ws = torch.empty(cache_forward_workspace_size(d, dev), dtype=_U8, device=dev)
+        ws = torch.empty(_lib().fa_cache_fwd_e4m3_workspace_size(R, T, Hq, H, d), dtype=_U8, device=dev)
     _done(_lib().fa_cache_fwd_e4m3(
         q.data_ptr(), q.stride(0) if T > 1 else Hq * d, cache.k8.data_ptr(), cache.v8.data_ptr(),
         cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),

@@ -9,6 +9,7 @@
 
 #include "fa_cache.cuh"
 #include "fa_cache_fwd.cuh"
+#include "fa_cache_prompt.cuh"
 #include "fa_fwd.h"
 #include "fa_host.h"
 
@@ -135,57 +136,46 @@ int cache_append(const void* k, const void* v, long long k_stride, long long v_s
 
 // ----------------------------------------------------------------- forward
 
-// Workspace: the CTAs' marks, then two partials of `rows` query rows per CTA.
+// Which kernel: the few-row one while a request has 48 rows per kv head or
+// fewer on average (tokens times the query heads of a kv head): it reads the
+// keys again for every 16 of them, the other pays for 128.  16 requests of 2-5
+// drafted tokens, 8 heads sharing (27 rows): 45 us against 74.
+bool many_rows(int R, int T, int g) {
+  return static_cast<long long>(T) * g > 48ll * R;
+}
+
+// Workspace: the CTAs' marks, then two partials of a unit's query rows per CTA.
 constexpr int kMaxGrid = 256;
-size_t partial_bytes(int sms, int rows, int d) { return static_cast<size_t>(2) * sms * rows * (d + 1) * 4; }
 size_t marks_bytes(int sms) { return static_cast<size_t>(sms) * 32; }
 
-size_t cache_fwd_workspace(int d) {
-  if (d != 64 && d != 128) return 0;
+size_t cache_fwd_workspace(int R, int T, int Hq, int Hkv, int d) {
+  if ((d != 64 && d != 128) || R <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
   host::Device dev;
   if (host::device(&dev) != FA_OK) return 0;
-  return marks_bytes(dev.sms) + partial_bytes(dev.sms, dec::kRows, d);
+  const int rows = many_rows(R, T, Hq / Hkv) ? prm::kRows : dec::kRows;
+  return marks_bytes(dev.sms) + static_cast<size_t>(2) * dev.sms * rows * (d + 1) * 4;
 }
 
 std::mutex g_cache_mu;
-bool g_cache_ready[64][2] = {};
+bool g_cache_ready[64][2][3] = {};
 
-template <int D>
-int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, char* ws, const host::Device& dev,
-                     cudaStream_t s) {
-  using Ly = dec::Layout<D>;
-  auto kernel = fa_cache_fwd_kernel<D>;
-  auto merge = fa_cache_merge_kernel<D, dec::kRows>;
-  cudaError_t e = cudaSuccess;
-  {
-    std::lock_guard<std::mutex> lock(g_cache_mu);
-    bool& ready = g_cache_ready[dev.dev][D == 128];
-    if (!ready) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::kAlloc);
-      if (e != cudaSuccess) return host::fail(e);
-      ready = true;
-    }
+// Dynamic shared memory of a kernel, set once per device.
+template <typename K>
+int ready(K kernel, int bytes, bool& done) {
+  std::lock_guard<std::mutex> lock(g_cache_mu);
+  if (!done) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return host::fail(e);
+    done = true;
   }
-  const int grid = dev.sms < kMaxGrid ? dev.sms : kMaxGrid;
-  a.desc = reinterpret_cast<int4*>(ws);
-  a.cont = reinterpret_cast<int*>(ws + static_cast<size_t>(dev.sms) * 16);
-  a.part_o = reinterpret_cast<float*>(ws + marks_bytes(dev.sms));
-  a.part_l = a.part_o + static_cast<size_t>(2) * grid * dec::kRows * D;
-  CUtensorMap mk, mv;
-  const cuuint64_t rows = static_cast<cuuint64_t>(P) * D / 128;
-  const cuuint64_t bh = static_cast<cuuint64_t>(a.blocks) * a.Hkv;
-  const cuuint32_t box = static_cast<cuuint32_t>((P < dec::kKeys ? P : dec::kKeys) * D / 128);
-  int st = host::tensor_map(&mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, k8, 128, rows, bh, 128, rows * 128, 128, box);
-  if (st != FA_OK) return st;
-  st = host::tensor_map(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, v8, 128, rows, bh, 128, rows * 128, 128, box);
-  if (st != FA_OK) return st;
-  kernel<<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return host::fail(e);
-  // A unit of one tile is never split: nothing to merge.
-  if (static_cast<long long>(a.M) * P <= dec::kKeys) return FA_OK;
+  return FA_OK;
+}
+
+// The merge as a programmatic dependent of the kernel before it.
+template <int D, int ROWS>
+int launch_merge(const CacheFwdArgs& a, int grid, int split, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.gridDim = dim3(grid, split, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -193,8 +183,53 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, merge, static_cast<const CacheFwdArgs&>(a), grid);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_cache_merge_kernel<D, ROWS>, a, grid);
   return e == cudaSuccess ? FA_OK : host::fail(e);
+}
+
+template <int D>
+int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, char* ws, const host::Device& dev,
+                     cudaStream_t s) {
+  const int grid = dev.sms < kMaxGrid ? dev.sms : kMaxGrid;
+  const bool many = many_rows(a.R, a.T, a.g);
+  a.desc = reinterpret_cast<int4*>(ws);
+  a.cont = reinterpret_cast<int*>(ws + static_cast<size_t>(dev.sms) * 16);
+  a.part_o = reinterpret_cast<float*>(ws + marks_bytes(dev.sms));
+  a.part_l = a.part_o + static_cast<size_t>(2) * grid * (many ? prm::kRows : dec::kRows) * D;
+  bool* set = g_cache_ready[dev.dev][D == 128];
+  int st = FA_OK;
+  if (many) {
+    using Ly = prm::Layout<D>;
+    const uint8_t* kc = static_cast<const uint8_t*>(k8);
+    const uint8_t* vc = static_cast<const uint8_t*>(v8);
+    if (P == 16) {
+      if ((st = ready(fa_cache_prompt_kernel<D, 16>, Ly::kAlloc, set[1])) != FA_OK) return st;
+      fa_cache_prompt_kernel<D, 16><<<grid, prm::kThreads, Ly::kAlloc, s>>>(kc, vc, a);
+    } else {
+      if ((st = ready(fa_cache_prompt_kernel<D, 32>, Ly::kAlloc, set[2])) != FA_OK) return st;
+      fa_cache_prompt_kernel<D, 32><<<grid, prm::kThreads, Ly::kAlloc, s>>>(kc, vc, a);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return host::fail(e);
+    // a unit of one tile is never split: nothing to merge
+    if (static_cast<long long>(a.M) * P <= prm::kKeys) return FA_OK;
+    return launch_merge<D, prm::kRows>(a, grid, 4, s);
+  }
+  using Ly = dec::Layout<D>;
+  if ((st = ready(fa_cache_fwd_kernel<D>, Ly::kAlloc, set[0])) != FA_OK) return st;
+  CUtensorMap mk, mv;
+  const cuuint64_t rows = static_cast<cuuint64_t>(P) * D / 128;
+  const cuuint64_t bh = static_cast<cuuint64_t>(a.blocks) * a.Hkv;
+  const cuuint32_t box = static_cast<cuuint32_t>((P < dec::kKeys ? P : dec::kKeys) * D / 128);
+  st = host::tensor_map(&mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, k8, 128, rows, bh, 128, rows * 128, 128, box);
+  if (st != FA_OK) return st;
+  st = host::tensor_map(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, v8, 128, rows, bh, 128, rows * 128, 128, box);
+  if (st != FA_OK) return st;
+  fa_cache_fwd_kernel<D><<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return host::fail(e);
+  if (static_cast<long long>(a.M) * P <= dec::kKeys) return FA_OK;
+  return launch_merge<D, dec::kRows>(a, grid, 1, s);
 }
 
 int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8, const float* ks, const float* vs,
@@ -222,7 +257,7 @@ int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8,
     if (misaligned(p, 4)) return FA_ERR_MISALIGNED;
   host::Device dev;
   if ((st = host::device(&dev)) != FA_OK) return st;
-  const size_t need = cache_fwd_workspace(d);
+  const size_t need = cache_fwd_workspace(R, T, Hq, Hkv, d);
   if (need == 0) return FA_ERR_UNSUPPORTED;
   if (ws_bytes < need) return FA_ERR_INVALID_ARG;
   const size_t nc = static_cast<size_t>(blocks) * P * Hkv * d, ns = static_cast<size_t>(blocks) * Hkv * 4;
@@ -284,7 +319,9 @@ int fa_cache_append_e4m3(const void* k, const void* v, long long k_stride, long 
                           block_tokens, static_cast<cudaStream_t>(stream));
 }
 
-size_t fa_cache_fwd_e4m3_workspace_size(int d) { return fa::cache_fwd_workspace(d); }
+size_t fa_cache_fwd_e4m3_workspace_size(int R, int T, int Hq, int Hkv, int d) {
+  return fa::cache_fwd_workspace(R, T, Hq, Hkv, d);
+}
 
 int fa_cache_fwd_e4m3(const void* q, long long q_stride, const void* k8, const void* v8, const float* k_scale,
                       const float* v_scale, const int* block_table, const int* seq_lens, const int* cu_q, void* o,

@@ -33,7 +33,8 @@
 // l = sum 2^(s - m); and E, the largest s + floor(log2 v_scale), for the
 // output's weights 2^(14 + s - E) v_scale, which lie below 2^15 and are
 // rounded to f16 (11 bits), so that neither a block of small values nor one
-// of zeros costs the others precision.
+// of zeros costs the others precision.  E is kept as its distance from m:
+// beside a large m a sum with log2 v_scale would be lost.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -215,6 +216,12 @@ __device__ __forceinline__ Req request(const CacheFwdArgs& a, int r) {
   q.kt = max(1, (q.len + KEYS - 1) / KEYS);
   return q;
 }
+// Reports what request() cuts off.
+__device__ __forceinline__ void check_request(const CacheFwdArgs& a, int r) {
+  const int len = a.seq_lens[r], c0 = a.cu_q[r], c1 = a.cu_q[r + 1];
+  if (len < 0 || len > (static_cast<long long>(a.M) << a.sh)) record_index_error(a.index_err, kSiteFwdLen, r);
+  if (c0 < 0 || c1 < c0 || c1 > a.T) record_index_error(a.index_err, kSiteFwdRows, r);
+}
 __device__ __forceinline__ long long cost_of(const CacheFwdArgs& a, const Req& q) {
   return static_cast<long long>(a.Hkv) * q.nrt * (q.kt + kUnitCost);
 }
@@ -263,11 +270,7 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
   long long mine = 0, total;
   for (int r = ra; r < rb; ++r) {
     mine += cost_of(a, request<kRows, kKeys>(a, r));
-    if (blockIdx.x == 0) {
-      const int len = a.seq_lens[r], c0 = a.cu_q[r], c1 = a.cu_q[r + 1];
-      if (len < 0 || len > (static_cast<long long>(a.M) << a.sh)) record_index_error(a.index_err, kSiteFwdLen, r);
-      if (c0 < 0 || c1 < c0 || c1 > a.T) record_index_error(a.index_err, kSiteFwdRows, r);
-    }
+    if (blockIdx.x == 0) check_request(a, r);
   }
   const long long before = cta_scan(mine, reinterpret_cast<long long*>(sm + Ly::kScan), total) - mine;
   const long long want = (total + kMinCost - 1) / kMinCost;
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
     if (s.nt == 0) return;
 
     float o[kN][4];
-    float m[2] = {kInit, kInit}, E[2] = {kInit, kInit}, l[2] = {0.f, 0.f};
+    float m[2] = {kInit, kInit}, E[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // E: the second reference less m
     if (warp < s.nt) {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
@@ -578,14 +581,14 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
         bool grew = false;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float m1 = fmaxf(m[y], fmaxf(gm[0][y], gm[1][y]));
-          const float E1 = fmaxf(E[y], fmaxf(gm[0][y] + lv[0], gm[1][y] + lv[1]));
-          l[y] *= ex2(m[y] - m1);
-          up[y] = ex2(E[y] - E1);
-          grew = grew || E1 > E[y];
+          const float m1 = fmaxf(m[y], fmaxf(gm[0][y], gm[1][y])), dm = m[y] - m1;
+          const float E1 = fmaxf(E[y] + dm, fmaxf(gm[0][y] - m1 + lv[0], gm[1][y] - m1 + lv[1]));
+          l[y] *= ex2(dm);
+          up[y] = ex2(E[y] + dm - E1);
+          grew = grew || up[y] != 1.f;
           m[y] = m1;
           E[y] = E1;
-          const float f = ex2(fminf(m1 - E1 + 14.f, 120.f));
+          const float f = ex2(fminf(14.f - E1, 120.f));
           wgt[0][y] = f * sc.z;
           wgt[1][y] = f * sc.w;
         }
@@ -686,17 +689,17 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
     const int nw = min(kWarps, s.nt);
     for (int it = tid; it < s.nv * (D / 4); it += 32 * kWarps) {
       const int row = it / (D / 4), ch = it % (D / 4);
-      float M = kInit, Em = kInit;
+      float M = kInit, Em = -INFINITY;
+      for (int w = 0; w < nw; ++w) M = fmaxf(M, stats[w * kRows + row].x);
       for (int w = 0; w < nw; ++w) {
         const float4 q = stats[w * kRows + row];
-        M = fmaxf(M, q.x);
-        Em = fmaxf(Em, q.z);
+        Em = fmaxf(Em, q.z + (q.x - M));
       }
       float L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int w = 0; w < nw; ++w) {
         const float4 q = stats[w * kRows + row];
-        const float f = ex2(q.z - Em);
+        const float f = ex2(q.z + (q.x - M) - Em);
         const float4 v = *reinterpret_cast<const float4*>(merge + (w * kRows + row) * D + 4 * chunk_at(row, ch));
         L += q.y * ex2(q.x - M);
         acc.x += f * v.x;
@@ -705,7 +708,7 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
         acc.w += f * v.w;
       }
       // a row without a visible key: O = 0, L = -inf
-      const float fin = L == 0.f ? 0.f : ex2(Em - M - 14.f) / L;
+      const float fin = L == 0.f ? 0.f : ex2(Em - 14.f) / L;
       const float lg = L == 0.f ? -INFINITY : M + log2f(L);
       acc.x *= fin;
       acc.y *= fin;
@@ -732,8 +735,9 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
 }
 
 // Merges the partials of each unit that more than one CTA worked on, in CTA
-// order: L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s.  One CTA per CTA of
-// the forward: it takes the unit that one began and did not finish.
+// order: L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s.  One CTA (or more, in
+// y, for large units) per CTA of the forward: it takes the unit that one began
+// and did not finish.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(256) fa_cache_merge_kernel(const __grid_constant__ CacheFwdArgs a, int grid) {
   __shared__ int s_end;
@@ -767,7 +771,7 @@ __global__ void __launch_bounds__(256) fa_cache_merge_kernel(const __grid_consta
   __syncthreads();
   const int n = s_n;
   const int n0 = max(0, min(a.T, a.cu_q[d.x]));
-  for (int it = tid; it < d.w * (D / 4); it += 256) {
+  for (int it = blockIdx.y * 256 + tid; it < d.w * (D / 4); it += 256 * gridDim.y) {
     const int row = it / (D / 4), ch = it % (D / 4);
     float M = -INFINITY;
     for (int i = 0; i < n; ++i) M = fmaxf(M, a.part_l[static_cast<long long>(s_slot[i]) * ROWS + row]);

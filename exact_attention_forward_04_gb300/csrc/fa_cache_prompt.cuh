@@ -1,0 +1,780 @@
+// Attention over the 8-bit key/value cache, many query rows per kv head
+// (prompts, chunks of them): bound by the tensor cores.
+//
+// The rows of one (request, kv head), new tokens times the query heads that
+// share the kv head, come in tiles of 256: two halves of 128 rows, A and B,
+// each a single-SM tcgen05 tile with a softmax warpgroup of its own, over the
+// same keys in tiles of 128.  As in the few-row kernel (fa_cache_fwd.cuh) the
+// key tiles of all units, in order, are cut into one equal range per CTA, and
+// units that more than one CTA works on leave partials for the merge; here
+// a unit's number of key tiles follows its last row's position.
+//
+// tcgen05 has no product of f16 with E4M3, and rounding Q and P to 8 bits
+// would cost what the cache saved.  So four warps turn the codes into f16
+// (exact) on their way to shared memory: they copy the next tiles' codes to a
+// buffer while the present ones are multiplied, and write them out in the
+// 128-byte-swizzled layout that the products read, K as K-major and V as
+// MN-major operand.  256 rows share that work: per key tile about 250
+// instructions of each of these warps against 2048 cycles of tensor pipe at
+// d = 128.
+//
+// TMEM (512 columns): S of A [0,128) and B [128,256) in fp32, P over the
+// first 64 columns of each as f16 pairs; O of A [256,384) and B [384,512).
+// One thread issues, for key tile j (after S_A(0), S_B(0)),
+//   PV_A(j), S_A(j+1), PV_B(j), S_B(j+1)
+// so that one half's softmax runs under the other half's products.  S(j+1)
+// overwrites P(j), which PV(j) before it reads: products issued by one thread
+// to the same tensor pipe run in order.
+//
+// Warps: 0-3 softmax and epilogue of A, 4-7 of B, 8-11 codes to f16 (and Q),
+// 12 issues the products, 13 walks the range.
+//
+// Softmax: as in the few-row kernel a row has two references, m for l = sum
+// 2^(s - m) and E for the weights 2^(10 + s - E) v_scale of the product, both
+// moved only when a tile exceeds one by more than 4 (so the weights stay below
+// 2^15; O is rescaled then).  The exponentials give the weights directly,
+// log2 v_scale being in their argument, and l takes each block's sum times
+// the inverse of what its weights carry.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "fa_cache_fwd.cuh"
+#include "sm103_ptx.cuh"
+#include "tmem_ldst.cuh"
+
+namespace fa {
+
+namespace prm {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 256;       // query rows of a unit
+constexpr int kHalf = 128;
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kSegs = 4;
+constexpr int kUnitCost = 3;     // a piece's fixed cost, in tiles
+constexpr int kMinCost = 6;      // least cost of a CTA's range
+constexpr float kLazy = 4.f;     // log2 a reference may be exceeded by
+constexpr float kBias = 10.f;    // log2 the weights are scaled by
+constexpr float kInit = -1e30f;
+constexpr float kTiny = 1.17549435e-38f;
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for B
+
+enum : unsigned { kSiteSegFull = 521, kSiteSegEmpty = 522, kSiteQFull = 523, kSiteQEmpty = 524, kSiteKFull = 525,
+                  kSiteKEmpty = 526, kSiteVFull = 527, kSiteVEmpty = 528, kSiteS = 529, kSiteP = 530, kSitePV = 531,
+                  kSiteScales = 532 };
+
+template <int D>
+struct Layout {
+  static constexpr int kQHalf = kHalf * D * 2;   // one half's rows, f16
+  static constexpr int kTile = kKeys * D * 2;    // K or V, f16
+  static constexpr int kQ = 0;
+  static constexpr int kK = 2 * kQHalf;          // [2]
+  static constexpr int kV = kK + 2 * kTile;      // [2]
+  static constexpr int kRaw = kV + 2 * kTile;                 // codes of the next tiles of K and V
+  static constexpr int kScan = kRaw;                          // before the first: long long [33]
+  static constexpr int kRowScale = kRaw + 2 * kKeys * D;      // float [256]
+  static constexpr int kKs = kRowScale + kRows * 4;        // float [4][8]: K scale, -1: no block
+  static constexpr int kLv = kKs + 4 * 8 * 4;                 // float [4][8]: log2 of the V scale
+  static constexpr int kSeg = kLv + 4 * 8 * 4;
+  static constexpr int kBar = (kSeg + kSegs * static_cast<int>(sizeof(dec::Seg)) + 15) & ~15;
+  static constexpr int kSegFull = kBar;
+  static constexpr int kSegEmpty = kSegFull + 8 * kSegs;
+  static constexpr int kQFull = kSegEmpty + 8 * kSegs;
+  static constexpr int kQEmpty = kQFull + 8;
+  static constexpr int kKFull = kQEmpty + 8;      // [2]
+  static constexpr int kKEmpty = kKFull + 16;
+  static constexpr int kVFull = kKEmpty + 16;
+  static constexpr int kVEmpty = kVFull + 16;
+  static constexpr int kSFull = kVEmpty + 16;     // [2] A, B
+  static constexpr int kPFull = kSFull + 16;
+  static constexpr int kPvDone = kPFull + 16;
+  static constexpr int kScales = kPvDone + 16;    // [4]
+  static constexpr int kFin = kScales + 32;
+  static constexpr int kTmemSlot = kFin + 8;
+  static constexpr int kAbort = kTmemSlot + 8;
+  static constexpr int kStart = (kAbort + 8 + 15) & ~15;  // int4
+  static constexpr int kBytes = kStart + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
+};
+
+// sum of floor((a i + b) / m) over i < n, all >= 0 (the Euclid-like sum).
+__device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    if (a >= m) {
+      s += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      s += n * (b / m);
+      b %= m;
+    }
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// Key tiles of row tile rt: up to its last row's position.
+__device__ __forceinline__ int tiles_of(const CacheFwdArgs& a, const dec::Req& q, int rt) {
+  int seen = q.len;
+  if (a.causal && q.n <= q.len) {
+    const unsigned last = min(static_cast<unsigned>(rt) * kRows + kRows, static_cast<unsigned>(q.n) * a.g) - 1;
+    seen = q.len - q.n + static_cast<int>(last / a.g) + 1;
+  }
+  return max(1, (seen + kKeys - 1) / kKeys);
+}
+// Cost of the row tiles before rt (< nrt): all of them full, so tile i sees
+// base + floor((256 (i + 1) - 1) / g) + 1 keys, base = len - n, and has
+// floor((256 i + 255 + g (base + 128)) / (128 g)) key tiles.
+__device__ __forceinline__ long long cost_before(const CacheFwdArgs& a, const dec::Req& q, int rt) {
+  if (!(a.causal && q.n <= q.len)) return static_cast<long long>(rt) * (tiles_of(a, q, 0) + kUnitCost);
+  const long long base = q.len - q.n;
+  return floor_sum(rt, static_cast<long long>(kKeys) * a.g, kRows, a.g * (base + kKeys) + kRows - 1) +
+         static_cast<long long>(rt) * kUnitCost;
+}
+__device__ __forceinline__ long long head_cost(const CacheFwdArgs& a, const dec::Req& q) {
+  return q.nrt == 0 ? 0 : cost_before(a, q, q.nrt - 1) + tiles_of(a, q, q.nrt - 1) + kUnitCost;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N) : "memory");
+}
+
+// kind::f16 with f16 A and B (format 0), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Sixteen codes to sixteen f16, two 16-byte pieces.
+__device__ __forceinline__ void codes16(uint4 c, uint4& lo, uint4& hi) {
+  dec::e4m3_to_f16(c.x, lo.x, lo.y);
+  dec::e4m3_to_f16(c.y, lo.z, lo.w);
+  dec::e4m3_to_f16(c.z, hi.x, hi.y);
+  dec::e4m3_to_f16(c.w, hi.z, hi.w);
+}
+
+// 16 bytes from global to shared memory, or zeros; for the thread that waits
+// for its own copies.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but this thread's latest group of copies are done.
+__device__ __forceinline__ void copies_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&r)[32], int lo, int hi) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = lo; i < hi; i += 2) m = fmax3(m, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+  return m;
+}
+
+}  // namespace prm
+
+// GROUP: keys that share a block for certain, 16 (P = 16) or 32.
+template <int D, int GROUP>
+__global__ void __launch_bounds__(prm::kThreads, 1)
+    fa_cache_prompt_kernel(const uint8_t* __restrict__ k8, const uint8_t* __restrict__ v8,
+                           const __grid_constant__ CacheFwdArgs a) {
+  using namespace prm;
+  using dec::Req;
+  using dec::Seg;
+  using Ly = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  griddep_launch_dependents();
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Ly::kAbort);
+  Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
+  if (tid == 0) {
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(base + Ly::kSegFull + 8 * i, 1);
+      mbar_init(base + Ly::kSegEmpty + 8 * i, 13);  // 8 softmax warps, 4 converters, the issuer
+    }
+    mbar_init(base + Ly::kQFull, 4);
+    mbar_init(base + Ly::kQEmpty, 9);  // the products' reads, and each softmax warp's of the row scales
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(base + Ly::kKFull + 8 * i, 4);
+      mbar_init(base + Ly::kKEmpty + 8 * i, 1);
+      mbar_init(base + Ly::kVFull + 8 * i, 4);
+      mbar_init(base + Ly::kVEmpty + 8 * i, 1);
+      mbar_init(base + Ly::kSFull + 8 * i, 1);
+      mbar_init(base + Ly::kPFull + 8 * i, 4);
+      mbar_init(base + Ly::kPvDone + 8 * i, 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(base + Ly::kScales + 8 * i, 1);
+    mbar_init(base + Ly::kFin, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    a.cont[blockIdx.x] = 0;
+  }
+
+  const int per = (a.R + kThreads - 1) / kThreads;
+  const int ra = min(a.R, tid * per), rb = min(a.R, ra + per);
+  long long mine = 0, total;
+  for (int r = ra; r < rb; ++r) {
+    mine += a.Hkv * head_cost(a, dec::request<kRows, kKeys>(a, r));
+    if (blockIdx.x == 0) dec::check_request(a, r);
+  }
+  const long long before = cta_scan(mine, reinterpret_cast<long long*>(sm + Ly::kScan), total) - mine;
+  const long long want = (total + kMinCost - 1) / kMinCost;
+  const int parts = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, want)));
+  if (static_cast<int>(blockIdx.x) >= parts) return;
+  const long long x0 = total * blockIdx.x / parts, x1 = total * (blockIdx.x + 1) / parts;
+  if (x0 >= x1) return;
+  if (before <= x0 && x0 < before + mine) {
+    long long x = before;
+    int r = ra;
+    for (;; ++r) {
+      const long long c = a.Hkv * head_cost(a, dec::request<kRows, kKeys>(a, r));
+      if (x0 < x + c) break;  // ends: this thread's requests hold x0
+      x += c;
+    }
+    // and the kv head, the row tile and the place in it
+    const Req q = dec::request<kRows, kKeys>(a, r);
+    const long long per_head = head_cost(a, q);
+    const int h = static_cast<int>((x0 - x) / per_head);
+    const long long y = x0 - x - h * per_head;
+    int lo = 0, hi = q.nrt;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cost_before(a, q, mid) <= y) lo = mid; else hi = mid;
+    }
+    *reinterpret_cast<int4*>(sm + Ly::kStart) = make_int4(r, h, lo, static_cast<int>(y - cost_before(a, q, lo)));
+  }
+  if (warp == 12) {
+    tmem_alloc(base + Ly::kTmemSlot, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + Ly::kTmemSlot);
+  auto wait = [&](int at, uint32_t parity, unsigned site, int item) {
+    return mbar_wait(base + at, parity & 1u, WaitCtx{abort_flag, a.err, a.timeout_ns}, site, item);
+  };
+
+  if (warp >= 12) {
+    reg_dec<64>();
+    if (warp == 13 && lane == 0) {
+      // ------------------------------------------------------- the walker
+      const int4 at = *reinterpret_cast<const int4*>(sm + Ly::kStart);
+      int r = at.x, h = at.y, rt = at.z, y = at.w;
+      long long left = x1 - x0;
+      int nseg = 0;
+      bool ok = true;
+      Req q = dec::request<kRows, kKeys>(a, r);
+      while (left > 0) {
+        if (rt >= q.nrt) {  // the next kv head, the next request with rows
+          rt = 0;
+          if (++h == a.Hkv) {
+            h = 0;
+            do q = dec::request<kRows, kKeys>(a, ++r); while (q.nrt == 0);  // ends: cost is left
+          }
+        }
+        const int kt = tiles_of(a, q, rt);
+        const int take = static_cast<int>(min(static_cast<long long>(kt + kUnitCost - y), left));
+        const int t0 = max(0, y - kUnitCost), t1 = max(0, y + take - kUnitCost);
+        left -= take;
+        if (t1 > t0) {
+          const int si = nseg % kSegs;
+          if (nseg >= kSegs && !wait(Ly::kSegEmpty + 8 * si, nseg / kSegs - 1, kSiteSegEmpty, nseg)) {
+            ok = false;
+            break;
+          }
+          const bool begins = t0 == 0, ends = t1 == kt;
+          Seg* s = segs + si;
+          s->r = r;
+          s->h = h;
+          s->row0 = rt * kRows;
+          s->nv = min(kRows, q.n * a.g - rt * kRows);
+          s->c0 = q.c0;
+          s->n = q.n;
+          s->len = q.len;
+          s->t0 = t0;
+          s->nt = t1 - t0;
+          s->mode = begins && ends ? 0 : 1;
+          s->slot = 2 * blockIdx.x + (begins ? 1 : 0);
+          s->base = 0;
+          mbar_arrive(base + Ly::kSegFull + 8 * si);
+          if (begins && !ends) a.desc[blockIdx.x] = make_int4(r, h, rt, min(kRows, q.n * a.g - rt * kRows));
+          if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
+          ++nseg;
+        }
+        ++rt;
+        y = 0;
+      }
+      if (ok) {
+        const int si = nseg % kSegs;
+        if (nseg < kSegs || wait(Ly::kSegEmpty + 8 * si, nseg / kSegs - 1, kSiteSegEmpty, nseg)) {
+          segs[si].nt = 0;
+          mbar_arrive(base + Ly::kSegFull + 8 * si);
+        }
+      }
+    } else if (warp == 12 && lane == 0) {
+      // ------------------------------------------------------- the issuer
+      constexpr uint32_t idS = idesc_f16_f32(kHalf, kKeys, false), idPV = idesc_f16_f32(kHalf, D, true);
+      // operand descriptors (sw128_desc) by their low word; the high word,
+      // stride 1024 and the swizzle, is the same for all
+      constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+      auto desc = [](uint32_t lo) { return (static_cast<uint64_t>(kHi) << 32) | lo; };
+      auto low = [](uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); };
+      int jt = 0, cnt_a = 0, cnt_b = 0;
+      auto issue_s = [&](int x, int st) {
+        const uint32_t q = low(base + Ly::kQ + x * Ly::kQHalf, 16), k = low(base + Ly::kK + st * Ly::kTile, 16);
+        const uint32_t d = tmem + kColS + x * kHalf;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = static_cast<uint32_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+          mma_ss(d, desc(q + off), desc(k + off), idS, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(base + Ly::kSFull + 8 * x);
+      };
+      for (int ns = 0;; ++ns) {
+        const int si = ns % kSegs;
+        if (!wait(Ly::kSegFull + 8 * si, ns / kSegs, kSiteSegFull, ns)) break;
+        const int nt = segs[si].nt;
+        const int halves = segs[si].nv > kHalf ? 2 : 1;
+        if (nt == 0) break;
+        bool ok = wait(Ly::kQFull, ns, kSiteQFull, ns);
+        // j = -1: the first scores only
+#pragma unroll 1
+        for (int j = -1; ok && j < nt; ++j) {
+          const int st = (jt - 1) & 1, nx = jt & 1;  // stages of tile j and of the next, jt
+          const bool more = j + 1 < nt;
+          if (more) ok = wait(Ly::kKFull + 8 * nx, jt >> 1, kSiteKFull, jt);
+          if (ok && j >= 0) ok = wait(Ly::kVFull + 8 * st, (jt - 1) >> 1, kSiteVFull, jt);
+#pragma unroll 1
+          for (int x = 0; ok && x < halves; ++x) {
+            if (j >= 0) {
+              ok = wait(Ly::kPFull + 8 * x, x ? cnt_b++ : cnt_a++, kSiteP, jt);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t v = low(base + Ly::kV + st * Ly::kTile, 16384);
+              const uint32_t d = tmem + kColO + x * kHalf, p = tmem + kColS + x * kHalf;
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_ts(d, p + 8 * kk, desc(v + static_cast<uint32_t>(kk * 128)), idPV, j == 0 && kk == 0 ? 0u : 1u);
+              tc_commit(base + Ly::kPvDone + 8 * x);
+            }
+            if (more) {
+              tc_fence_after();
+              issue_s(x, nx);
+            }
+          }
+          if (!ok) break;
+          if (j >= 0) tc_commit(base + Ly::kVEmpty + 8 * st);
+          if (more) {
+            tc_commit(base + Ly::kKEmpty + 8 * nx);
+            if (j + 2 == nt) tc_commit(base + Ly::kQEmpty);  // the last read of Q
+            ++jt;
+          }
+        }
+        if (!ok) break;
+        mbar_arrive(base + Ly::kSegEmpty + 8 * si);
+      }
+      // nothing that reads shared or tensor memory outlives the CTA
+      tc_commit(base + Ly::kFin);
+      dec::mbar_drain(base + Ly::kFin, 0, globaltimer_ns() + a.timeout_ns);
+    }
+  } else if (warp >= 8) {
+    reg_dec<80>();
+    // ------------------------------------------- codes and queries to f16
+    constexpr int kChunks = D / 16;                 // 16-code chunks of a row
+    constexpr int kPer = kKeys * kChunks / 128;     // per thread and tile
+    const int cw = warp - 8, ct = tid - 256;
+    const int c16 = ct % kChunks, row_lo = ct / kChunks;
+    constexpr int kStep = 128 / kChunks;            // rows between a thread's chunks
+    const int P1 = (1 << a.sh) - 1;
+    int jt = 0;
+    for (int ns = 0;; ++ns) {
+      const int si = ns % kSegs;
+      bool ok = wait(Ly::kSegFull + 8 * si, ns / kSegs, kSiteSegFull, ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const Seg& s = segs[si];
+      const int nt = s.nt;
+      if (nt == 0) break;
+      const int h = s.h, len = s.len, t0 = s.t0;
+      const int* table = a.table + static_cast<long long>(s.r) * a.M;
+      // block of 16-key group `lane` (< 8) of tile j, -1: none
+      auto blocks_of = [&](int j) {
+        int b = -1;
+        const int key = (t0 + j) * kKeys + lane * 16;
+        if (lane < 8 && j < nt && key < len) {
+          b = table[key >> a.sh];
+          if (b < 0 || b >= a.blocks) {
+            if (cw == 0) record_index_error(a.index_err, kSiteFwdBlock, s.r);
+            b = -1;
+          }
+        }
+        return b;
+      };
+      // a thread's chunk i of tile j: its row's place in the cache, if any
+      auto place = [&](int ids, int j, int i, bool& real) {
+        const int row = row_lo + kStep * i, key = (t0 + j) * kKeys + row;
+        const int b = __shfl_sync(0xffffffffu, ids, row >> 4);
+        real = b >= 0 && key < len;
+        return real ? ((static_cast<long long>(b) * a.Hkv + h) << a.sh) * D + (key & P1) * D + c16 * 16 : 0ll;
+      };
+      // codes wait in buffers that only the thread that copied them reads
+      const uint32_t raw_k = base + Ly::kRaw + ct * 16, raw_v = raw_k + kKeys * D;
+      auto fetch = [&](uint32_t to, const uint8_t* codes, int ids, int j) {
+        if (j < nt) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            bool real;
+            const long long at = place(ids, j, i, real);
+            copy16(to + i * 2048, codes + at, real);
+          }
+        }
+        copies_group();
+      };
+      auto put = [&](uint32_t at, int i, uint4 codes) {
+        const int row = row_lo + kStep * i;
+        uint4 lo, hi;
+        codes16(codes, lo, hi);
+        const uint32_t to = at + (c16 >> 2) * 16384 + row * 128;
+        const int p = (c16 & 3) * 2;
+        // eight lanes of a store on different banks: the upper half of a
+        // 128-wide row writes its second piece first
+        const bool swap = D == 128 && (c16 & 4);
+        sts128(to + (((p + (swap ? 1 : 0)) ^ (row & 7)) << 4), swap ? hi : lo);
+        sts128(to + (((p + (swap ? 0 : 1)) ^ (row & 7)) << 4), swap ? lo : hi);
+      };
+      int ids = blocks_of(0), ids_next = blocks_of(1);
+
+      // Q: the bf16 rows copied to where they go, then, each by the threads
+      // that copied it, divided by a power of two of its own and made f16
+      ok = ns == 0 || wait(Ly::kQEmpty, ns - 1, kSiteQEmpty, ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      {
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes per row (8 elements each), rows per warp
+        const int col = lane % kLanes;
+        const uint32_t to = base + Ly::kQ + (col >> 3) * 16384;
+        const int rows = s.nv > kHalf ? kRows : kHalf;
+        auto spot = [&](int row) {
+          return to + (row >> 7) * Ly::kQHalf + (row & 127) * 128 + (((col & 7) ^ (row & 7)) << 4);
+        };
+#pragma unroll 4
+        for (int row = cw * kAt + lane / kLanes; row < rows; row += 4 * kAt) {
+          const int rr = s.row0 + row, tk = rr / a.g;
+          const bool real = row < s.nv;
+          const long long at = (s.c0 + tk) * a.q_stride + static_cast<long long>(h * a.g + rr - tk * a.g) * D + col * 8;
+          copy16(spot(row), a.q + (real ? at : 0), real);
+        }
+        copies_group();
+        fetch(raw_k, k8, ids, 0);
+        fetch(raw_v, v8, ids, 0);
+        copies_done();
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll 4
+        for (int row = cw * kAt + lane / kLanes; row < rows; row += 4 * kAt) {
+          const uint4 w = dec::lds128(spot(row));
+          uint32_t am = amax2(w.x, amax2(w.y, amax2(w.z, amax2(w.w, 0u))));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+          const int ex = dec::row_exponent(am << 16);
+          const float inv = dec::pow2i(-ex);
+          auto two16 = [&](uint32_t v) {
+            v ^= flip;
+            return dec::pack_f16(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
+          };
+          sts128(spot(row), make_uint4(two16(w.x), two16(w.y), two16(w.z), two16(w.w)));
+          if (col == 0)
+            reinterpret_cast<float*>(sm + Ly::kRowScale)[row] = fmaxf(fabsf(a.scale_log2) * dec::pow2i(ex), kTiny);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + Ly::kQFull);
+
+      for (int j = 0; j < nt; ++j, ++jt) {
+        const int st = jt & 1;
+        float ks = -1.f, lv = 0.f;
+        if (cw == 0 && lane < 8 && ids >= 0) {
+          const long long bh = static_cast<long long>(ids) * a.Hkv + h;
+          ks = a.ks[bh];
+          lv = log2f(a.vs[bh]);
+        }
+        const int ids_after = blocks_of(j + 2);
+        // K
+        if (jt >= 2) {
+          ok = wait(Ly::kKEmpty + 8 * st, (jt >> 1) - 1, kSiteKEmpty, jt);
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        copies_but_one();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) put(base + Ly::kK + st * Ly::kTile, i, dec::lds128(raw_k + i * 2048));
+        fetch(raw_k, k8, ids_next, j + 1);
+        if (cw == 0) {
+          if (lane < 8) {
+            reinterpret_cast<float*>(sm + Ly::kKs)[(jt & 3) * 8 + lane] = ks;
+            reinterpret_cast<float*>(sm + Ly::kLv)[(jt & 3) * 8 + lane] = fmaxf(lv, -200.f);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(base + Ly::kScales + 8 * (jt & 3));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(base + Ly::kKFull + 8 * st);
+        // V
+        if (jt >= 2) {
+          ok = wait(Ly::kVEmpty + 8 * st, (jt >> 1) - 1, kSiteVEmpty, jt);
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        copies_but_one();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) put(base + Ly::kV + st * Ly::kTile, i, dec::lds128(raw_v + i * 2048));
+        fetch(raw_v, v8, ids_next, j + 1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(base + Ly::kVFull + 8 * st);
+        ids = ids_next;
+        ids_next = ids_after;
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
+    }
+    copies_done();  // none outlives the CTA, also where a wait gave up
+  } else {
+    reg_inc<184>();
+    // ------------------------------------------------ softmax and epilogue
+    const int x = warp >> 2;  // half
+    const int row = tid;      // of the unit: 128 x + TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + kColS + x * kHalf, tO = tmem + lane_off + kColO + x * kHalf;
+    constexpr int kGroups = kKeys / GROUP, kIn = GROUP == 16 ? 2 : 1;  // groups of a tile, of a 32-key chunk
+    int cnt = 0, jt = 0;  // tiles of this half, tiles of the CTA
+    for (int ns = 0;; ++ns) {
+      const int si = ns % kSegs;
+      bool ok = wait(Ly::kSegFull + 8 * si, ns / kSegs, kSiteSegFull, ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const Seg& s = segs[si];
+      const int nt = s.nt;
+      if (nt == 0) break;
+      // no wait is left out for a piece without rows in this half: a phase
+      // that a warp never saw could pass for a later one of the same parity
+      ok = wait(Ly::kQFull, ns, kSiteQFull, ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const float c = lds_f32(base + Ly::kRowScale + 4 * row);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + Ly::kQEmpty);
+      if (x == 1 && s.nv <= kHalf) {
+        jt += nt;
+        if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
+        continue;
+      }
+      // keys visible to this row, and to every row of this warp
+      const int lim = a.causal ? min(s.len, s.len - s.n + (s.row0 + row) / a.g + 1) : s.len;
+      const int all = __reduce_min_sync(0xffffffffu, lim);
+      float m = kInit, e = 0.f, l = 0.f;  // e: the second reference less the first
+      for (int j = 0; j < nt; ++j, ++jt, ++cnt) {
+        // (the scales of a tile are never replaced before its scores are read)
+        ok = wait(Ly::kSFull + 8 * x, cnt, kSiteS, jt) && wait(Ly::kScales + 8 * (jt & 3), jt >> 2, kSiteScales, jt);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        uint32_t v[4][32];
+        float mx[4];  // of each 32 keys
+        // scales of 16-key group i
+        const uint32_t tile_scales = base + Ly::kKs + (jt & 3) * 32;
+        auto ks_at = [&](int i) { return lds_f32(tile_scales + 4 * i); };
+        auto lv_at = [&](int i) { return lds_f32(tile_scales + (Ly::kLv - Ly::kKs) + 4 * i); };
+        const int key0 = (s.t0 + j) * kKeys;
+        bool careful = key0 + kKeys > all;
+        // read twice, so that they are not held beside the scores
+        auto k_of = [&](int g) { return fmaxf(c * ks_at(g * (8 / kGroups)), kTiny); };
+        auto lv_of = [&](int g) { return lv_at(g * (8 / kGroups)); };
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) careful = careful | (ks_at(g * (8 / kGroups)) < 0.f);
+        if constexpr (GROUP == 32) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ldred_max32(tS + 32 * q, v[q], mx[q]);
+          tmem_ldred_wait32(v[0], mx[0]);
+          tmem_ldred_dep32(v[1], mx[1]);
+          tmem_ldred_dep32(v[2], mx[2]);
+          tmem_ldred_dep32(v[3], mx[3]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, v[q]);
+          tmem_ld_wait32(v[0]);
+          tmem_ld_dep32(v[1]);
+          tmem_ld_dep32(v[2]);
+          tmem_ld_dep32(v[3]);
+        }
+        if (careful) {
+          constexpr uint32_t kNegInf = 0xff800000u;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            // keys of the group below this are visible
+            const int end = ks_at(q) < 0.f ? 0 : lim - (key0 + 16 * q);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e >= end) v[q >> 1][(q & 1) * 16 + e] = kNegInf;
+          }
+        }
+        // the tile's references, eb relative to mb
+        float mb = kInit, eb = -INFINITY;
+        auto see = [&](int g, float top) {
+          const float t = top * k_of(g), m1 = fmaxf(mb, t);
+          eb = fmaxf(eb + (mb - m1), t - m1 + lv_of(g));
+          mb = m1;
+        };
+        if (careful || GROUP == 16) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < kIn; ++i) see(q * kIn + i, max32(v[q], i * GROUP, (i + 1) * GROUP));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) see(q, mx[q]);
+        }
+        const bool bump = mb > m + kLazy || eb + (mb - m) > e + kLazy;
+        float up = 1.f;
+        if (bump) {
+          const float m1 = fmaxf(m, mb), e1 = fmaxf(e + (m - m1), eb + (mb - m1));
+          l *= ex2(m - m1);
+          up = ex2(e + (m - m1) - e1);
+          m = m1;
+          e = e1;
+        }
+        if (__any_sync(0xffffffffu, bump) && j > 0) {
+          // (where this wait gives up the loop ends below: leaving it here
+          // costs registers)
+          ok = __all_sync(0xffffffffu, wait(Ly::kPvDone + 8 * x, cnt - 1, kSitePV, jt));
+          tc_fence_after();
+          // a few columns at a time, beside the scores in registers
+#pragma unroll 1
+          for (int q = 0; q < D / 8; ++q) {
+            uint32_t o[8];
+            tmem_ld8(tO + 8 * q, o);
+            tmem_ld_wait8(o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * up);
+            tmem_st8(tO + 8 * q, o);
+          }
+        }
+        // The exponent is one fused product and sum, whose product is not
+        // rounded as m's was: above 2^17 (log2 units) that difference counts,
+        // and the scores are reduced in two steps instead.
+        const bool far = __any_sync(0xffffffffu, fabsf(m) > 131072.f && m != kInit);
+        if (far) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[q][i] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(v[q][i]), k_of(q * kIn + i / GROUP)), m));
+        }
+        float sums = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < kIn; ++i) {
+            const int g = q * kIn + i;
+            // 2^lw: what the weights of this group carry beside 2^(s - m).
+            // Below 2^-60 they are 0 in f16 whatever it is.
+            const float up_g = fminf(fmaxf(lv_of(g) + kBias - e, -60.f), 120.f);
+            const float fk = far ? 1.f : k_of(g), nm = far ? up_g : up_g - m;
+            const uint64_t f2 = f2_pack(fk, fk);
+            const uint64_t n2 = f2_pack(nm, nm);
+            uint64_t sum = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int y = i * GROUP; y < (i + 1) * GROUP; y += 2) {
+              float a0, a1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[q][y]), __uint_as_float(v[q][y + 1])), f2, n2), a0, a1);
+              a0 = ex2(a0);
+              a1 = ex2(a1);
+              sum = f2_add(sum, f2_pack(a0, a1));
+              w[y >> 1] = dec::pack_f16(a0, a1);
+            }
+            float s0, s1;
+            f2_unpack(sum, s0, s1);
+            sums = fmaf(s0 + s1, ex2(-up_g), sums);
+          }
+          tmem_st16(tS + 16 * q, w);
+        }
+        l += sums;
+        tmem_st_wait();
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(base + Ly::kPFull + 8 * x);
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ok = wait(Ly::kPvDone + 8 * x, cnt - 1, kSitePV, jt);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const bool real = row < s.nv;
+      const float inv = l == 0.f ? 0.f : ex2(e - kBias) / l;
+      const float lg = l == 0.f ? -INFINITY : m + log2f(l);
+      const int rr = s.row0 + row, tk = rr / a.g;
+      const long long at = static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
+      const long long pat = static_cast<long long>(s.slot) * kRows + row;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * q, o);
+        tmem_ld_wait32(o);
+        if (real) {
+          if (s.mode == 0) {
+            uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + 32 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(
+                  pack_bf16(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv),
+                  pack_bf16(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv),
+                  pack_bf16(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv),
+                  pack_bf16(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + pat * D + 32 * q);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                   __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+          }
+        }
+      }
+      if (real) {
+        if (s.mode == 0) a.lse[at] = lg * 0.6931471805599453f;
+        else a.part_l[pat] = lg;
+      }
+      tc_fence_before();  // O has been read: the next piece's first product may overwrite it
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace fa

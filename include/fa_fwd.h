@@ -442,8 +442,8 @@ int fa_cache_append_e4m3(const void* k, const void* v, long long k_stride, long 
  *   Lengths above max_blocks * P, negative ones and row offsets outside
  *   [0, T] are cut off to the range and reported (FA_ERR_INDEX); the keys of a
  *   block outside [0, num_blocks) count as not visible and it is reported.
- *   workspace: at least fa_cache_fwd_e4m3_workspace_size(d) bytes, 16-byte
- *          aligned.  Contents on entry are ignored.  Calls that may run at
+ *   workspace: at least fa_cache_fwd_e4m3_workspace_size(R, T, Hq, Hkv, d)
+ *          bytes, 16-byte aligned.  Contents on entry are ignored.  Calls that may run at
  *          the same time need one each.
  * O and L are those of the exact attention over the cached values, up to the
  * rounding of the softmax weights to f16 in the product with V.  Results do
@@ -459,9 +459,10 @@ int fa_cache_fwd_e4m3(const void* q, long long q_stride, const void* k8, const v
                       int Hkv, int d, int num_blocks, int block_tokens, int max_blocks, float scale,
                       int causal, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of fa_cache_fwd_e4m3 on the current device, whatever the
- * batch; 0 for an unsupported d. */
-size_t fa_cache_fwd_e4m3_workspace_size(int d);
+/* Workspace bytes of fa_cache_fwd_e4m3 on the current device for these sizes
+ * (about 2.5 MB, 40 MB for batches of prompts); 0 for sizes it has no work for
+ * or does not take. */
+size_t fa_cache_fwd_e4m3_workspace_size(int R, int T, int Hq, int Hkv, int d);
 
 /*
  * fa_check_errors — synchronise `stream`, then report and clear the device

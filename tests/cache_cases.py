@@ -62,14 +62,15 @@ def forward_bounds(O, L, A, S, W, d):
     rounding of a weight, half of 2^-10 relative; the sums and divisions below
     2^-18 in all; then bf16, half of 2^-7 of the result.  A weight times its V
     scale is at most w = max p_j scale_j and is rounded as 2^14 times a number
-    in which w lies in [1, 2): below f16's smallest normal number its rounding
-    is off by up to half of f16's smallest step, 2^-25, that is by 2^-39 w, and
-    moves the result by 2^-39 w |V code value| for that key: 2^-39 W in all
-    (which counts where the heaviest keys are 0 in a column).
+    in which w lies in [1, 2), or with many rows as 2^10 times one in which it
+    lies in [1, 2^5): below f16's smallest normal number its rounding is off by
+    up to half of f16's smallest step, 2^-25, that is by 2^-35 w, and moves the
+    result by 2^-35 w |V code value| for that key: 2^-35 W in all (which counts
+    where the heaviest keys are 0 in a column).
     L: eps, the logarithm's and the last product's rounding."""
     u = 2.0 ** -24
     eps = (2 * d + 8) * u * S + 2.0 ** -21
-    bO = (2 * eps[..., None] + 2.0 ** -11 + 2.0 ** -18) * A + 2.0 ** -39 * W
+    bO = (2 * eps[..., None] + 2.0 ** -11 + 2.0 ** -18) * A + 2.0 ** -35 * W
     bO = bO + 2.0 ** -8 * (O.abs() + bO) + 1e-30
     bL = eps + 2.0 ** -20 + 4 * u * L.abs()
     return bO, bL

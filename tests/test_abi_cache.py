@@ -90,8 +90,9 @@ def test_forward_refusals(lib, kw, want):
     assert _fwd(lib, **kw) == want
 
 
-def test_forward_workspace_of_an_unsupported_head_dim(lib):
-    assert lib.fa_cache_fwd_e4m3_workspace_size(96) == 0
+def test_forward_workspace_of_sizes_not_taken(lib):
+    for bad in ((4, 9, 6, 3, 96), (0, 9, 6, 3, 128), (4, 0, 6, 3, 128), (4, 9, 7, 3, 128), (4, 9, 6, 0, 64)):
+        assert lib.fa_cache_fwd_e4m3_workspace_size(*bad) == 0, bad
 
 
 def test_status_string(lib):

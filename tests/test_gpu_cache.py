@@ -239,6 +239,34 @@ def test_forward_drafts_and_prompts(d, causal, g):
     _forward_case(lens, new, 32, 2, g, d, causal=causal, seed=g)
 
 
+@pytest.mark.parametrize("P", (16, 32, 64, 128))
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("g", (1, 4, 7))
+def test_forward_prompts(P, d, g):
+    """Tens of rows and more per kv head: whole prompts and chunks behind a
+    prefix, one half of a row tile and both, lengths around the key tiles."""
+    lens, new = [127, 128, 129, 300, 40, 1, 260], [127, 60, 129, 33, 1, 1, 70]
+    _forward_case(lens, new, P, 1, g, d, seed=g)
+
+
+@pytest.mark.parametrize("d", (64, 128))
+def test_forward_prompts_not_causal_and_negative_scale(d):
+    _forward_case([200, 90], [70, 90], 32, 2, 4, d, causal=False, seed=3)
+    _forward_case([200, 90], [70, 90], 64, 1, 4, d, scale=-0.15, seed=4)
+    _forward_case([200, 90], [70, 90], 16, 1, 4, d, scale=0.0, seed=5)
+
+
+@pytest.mark.parametrize("P", (16, 64))
+def test_forward_prompt_behind_a_long_prefix(P):
+    """Many key tiles, units split over CTAs, references that keep rising."""
+    _forward_case([2600], [150], P, 2, 2, 64, sigma=4.0, seed=6)
+    _forward_case([1900, 5], [40, 5], P, 1, 8, 128, sigma=6.0, seed=7)
+
+
+def test_forward_prompts_longer_than_what_is_cached():
+    _forward_case([5, 0, 130], [100, 40, 140], 32, 1, 4, 64, seed=8)
+
+
 def test_forward_one_long_request():
     """One unit over all SMs, merged."""
     _forward_case([9001], [1], 64, 1, 4, 128, seed=2)
@@ -267,7 +295,8 @@ def test_forward_peaky_rows():
 
 
 @pytest.mark.parametrize("d", (64, 128))
-def test_forward_blocks_of_very_different_scale(d):
+@pytest.mark.parametrize("rows", (1, 20))
+def test_forward_blocks_of_very_different_scale(d, rows):
     """V blocks of zeros with the smallest scale beside large ones; the
     weights of small blocks stay exact where the large ones' vanish."""
     P, lens = 16, [96, 64]
@@ -280,23 +309,25 @@ def test_forward_blocks_of_very_different_scale(d):
     vs[table[1, 2].item()] = 2.0 ** -100
     vs[table[0, 3].item()] = 2.0 ** 40
     k8[table[0, 3].item()] = k8[table[0, 3].item()] | 0x80  # its scores are far below the others'
-    q = torch.full((2, 2, d), 1.0, dtype=torch.bfloat16)
+    cu = [0, rows, 2 * rows]
+    q = torch.full((2 * rows, 2, d), 1.0, dtype=torch.bfloat16)
     k8[table[0, 1].item()] &= 0x7F
     ks[table[0, 1].item()] = 1.0
     ks[table[0, 3].item()] = 4.0
     cache = fa.CacheE4M3(*(t.to(DEV) for t in (k8, v8, ks, vs)))
-    o, lse = fa.cache_forward_e4m3(q.to(DEV), cache, table.to(DEV), i32(lens), i32([0, 1, 2]))
+    o, lse = fa.cache_forward_e4m3(q.to(DEV), cache, table.to(DEV), i32(lens), i32(cu))
     fa.check_errors()
-    assert_forward(o, lse, q, (k8, v8, ks, vs), table, lens, [0, 1, 2], 1 / math.sqrt(d), True)
+    assert_forward(o, lse, q, (k8, v8, ks, vs), table, lens, cu, 1 / math.sqrt(d), True)
 
 
-def test_forward_query_magnitudes():
+@pytest.mark.parametrize("g", (2, 34))
+def test_forward_query_magnitudes(g):
     """Rows of any magnitude, zeros, and elements far below a row's largest."""
     lens, P, d = [60, 60, 60, 60], 32, 64
     table, blocks = make_tables(lens, P, seed=1)
     k8, ks = make_codes(blocks, 1, P, d, 2)
     v8, vs = make_codes(blocks, 1, P, d, 3)
-    q = torch.randn(4, 2, d, generator=torch.Generator().manual_seed(4))
+    q = torch.randn(4, g, d, generator=torch.Generator().manual_seed(4))
     q[0] *= 2.0 ** -130
     q[1] = 0
     q[2] *= torch.exp2(-torch.arange(d).float())
@@ -318,7 +349,7 @@ def test_forward_strided_queries_untouched_rows_and_repeatability():
     cache = fa.CacheE4M3(*(t.to(DEV) for t in (k8, v8, ks, vs)))
     big = torch.randn(6, 12, d, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).to(DEV)
     q = big[:, 2:6]
-    ws = torch.full((fa.cache_forward_workspace_size(d),), 0xFF, dtype=torch.uint8, device=DEV)
+    ws = torch.full((fa.cache_forward_workspace_size(3, 6, 4, 2, d),), 0xFF, dtype=torch.uint8, device=DEV)
     o, lse = fa.cache_forward_e4m3(q, cache, table.to(DEV), i32(lens), i32([0, 2, 3, 3]), workspace=ws)
     assert_forward(o[:3], lse[:3], q[:3].cpu(), (k8, v8, ks, vs), table, lens, [0, 2, 3, 3], d ** -0.5, True)
     lib = fa.load_library()
