@@ -157,7 +157,7 @@ size_t cache_fwd_workspace(int R, int T, int Hq, int Hkv, int d) {
 }
 
 std::mutex g_cache_mu;
-bool g_cache_ready[64][2][3] = {};
+bool g_cache_ready[64][2][5] = {};
 
 // Dynamic shared memory of a kernel, set once per device.
 template <typename K>
@@ -202,13 +202,14 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
     using Ly = prm::Layout<D>;
     const uint8_t* kc = static_cast<const uint8_t*>(k8);
     const uint8_t* vc = static_cast<const uint8_t*>(v8);
-    if (P == 16) {
-      if ((st = ready(fa_cache_prompt_kernel<D, 16>, Ly::kAlloc, set[1])) != FA_OK) return st;
-      fa_cache_prompt_kernel<D, 16><<<grid, prm::kThreads, Ly::kAlloc, s>>>(kc, vc, a);
-    } else {
-      if ((st = ready(fa_cache_prompt_kernel<D, 32>, Ly::kAlloc, set[2])) != FA_OK) return st;
-      fa_cache_prompt_kernel<D, 32><<<grid, prm::kThreads, Ly::kAlloc, s>>>(kc, vc, a);
-    }
+    auto launch = [&](auto kernel, bool& done) {
+      if ((st = ready(kernel, Ly::kAlloc, done)) == FA_OK) kernel<<<grid, prm::kThreads, Ly::kAlloc, s>>>(kc, vc, a);
+    };
+    if (P == 16) launch(fa_cache_prompt_kernel<D, 16>, set[1]);
+    else if (P == 32) launch(fa_cache_prompt_kernel<D, 32>, set[2]);
+    else if (P == 64) launch(fa_cache_prompt_kernel<D, 64>, set[3]);
+    else launch(fa_cache_prompt_kernel<D, 128>, set[4]);
+    if (st != FA_OK) return st;
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return host::fail(e);
     // a unit of one tile is never split: nothing to merge

@@ -194,7 +194,7 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32], int lo, int hi) 
 
 }  // namespace prm
 
-// GROUP: keys that share a block for certain, 16 (P = 16) or 32.
+// GROUP: tokens of a block, P: keys that share their scales.
 template <int D, int GROUP>
 __global__ void __launch_bounds__(prm::kThreads, 1)
     fa_cache_prompt_kernel(const uint8_t* __restrict__ k8, const uint8_t* __restrict__ v8,
@@ -406,12 +406,28 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
   } else if (warp >= 8) {
     reg_dec<80>();
     // ------------------------------------------- codes and queries to f16
-    constexpr int kChunks = D / 16;                 // 16-code chunks of a row
-    constexpr int kPer = kKeys * kChunks / 128;     // per thread and tile
+    // A thread turns 16 codes of a row into two 16-byte pieces, of rows kStep
+    // apart.  Eight lanes hold four chunks of two rows: their pieces 0 2 4 6,
+    // XORed with the row's low bits, fall on different banks.
+    constexpr int kPer = kKeys * D / 16 / 128;      // per thread and tile
+    constexpr int kStep = kKeys / kPer;
     const int cw = warp - 8, ct = tid - 256;
-    const int c16 = ct % kChunks, row_lo = ct / kChunks;
-    constexpr int kStep = 128 / kChunks;            // rows between a thread's chunks
+    const int c16 = (lane & 3) + (D == 128 ? 4 * (cw & 1) : 0);
+    const int row_lo = (lane >> 2) + 8 * (D == 128 ? cw >> 1 : cw);
+    const uint32_t piece = static_cast<uint32_t>((c16 >> 2) * 16384 + row_lo * 128 +
+                                                 ((((c16 & 3) * 2) ^ (row_lo & 7)) << 4));
     const int P1 = (1 << a.sh) - 1;
+    // codes wait in buffers that only the thread that copied them reads
+    const uint32_t raw_k = base + Ly::kRaw + ct * 16, raw_v = raw_k + kKeys * D;
+    auto put = [&](uint32_t to, uint32_t from) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        uint4 lo, hi;
+        codes16(dec::lds128(from + i * 2048), lo, hi);
+        sts128(to + piece + i * (kStep * 128), lo);
+        sts128((to + piece + i * (kStep * 128)) ^ 16u, hi);
+      }
+    };
     int jt = 0;
     for (int ns = 0;; ++ns) {
       const int si = ns % kSegs;
@@ -422,7 +438,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       if (nt == 0) break;
       const int h = s.h, len = s.len, t0 = s.t0;
       const int* table = a.table + static_cast<long long>(s.r) * a.M;
-      // block of 16-key group `lane` (< 8) of tile j, -1: none
+      // block and head of 16-key group `lane` (< 8) of tile j, -1: none
       auto blocks_of = [&](int j) {
         int b = -1;
         const int key = (t0 + j) * kKeys + lane * 16;
@@ -431,41 +447,26 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           if (b < 0 || b >= a.blocks) {
             if (cw == 0) record_index_error(a.index_err, kSiteFwdBlock, s.r);
             b = -1;
+          } else {
+            b = b * a.Hkv + h;
           }
         }
         return b;
       };
-      // a thread's chunk i of tile j: its row's place in the cache, if any
-      auto place = [&](int ids, int j, int i, bool& real) {
-        const int row = row_lo + kStep * i, key = (t0 + j) * kKeys + row;
-        const int b = __shfl_sync(0xffffffffu, ids, row >> 4);
-        real = b >= 0 && key < len;
-        return real ? ((static_cast<long long>(b) * a.Hkv + h) << a.sh) * D + (key & P1) * D + c16 * 16 : 0ll;
-      };
-      // codes wait in buffers that only the thread that copied them reads
-      const uint32_t raw_k = base + Ly::kRaw + ct * 16, raw_v = raw_k + kKeys * D;
+      // this thread's chunks of tile j, zeros where there is no token
       auto fetch = [&](uint32_t to, const uint8_t* codes, int ids, int j) {
         if (j < nt) {
+          const int last = len - (t0 + j) * kKeys - row_lo;
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
-            bool real;
-            const long long at = place(ids, j, i, real);
-            copy16(to + i * 2048, codes + at, real);
+            const int b = __shfl_sync(0xffffffffu, ids, (row_lo + kStep * i) >> 4);
+            const bool real = b >= 0 && kStep * i < last;
+            const uint8_t* from = codes + c16 * 16 + static_cast<long long>(real ? b : 0) * (D << a.sh) +
+                                  ((row_lo + kStep * i) & P1) * D;
+            copy16(to + i * 2048, from, real);
           }
         }
         copies_group();
-      };
-      auto put = [&](uint32_t at, int i, uint4 codes) {
-        const int row = row_lo + kStep * i;
-        uint4 lo, hi;
-        codes16(codes, lo, hi);
-        const uint32_t to = at + (c16 >> 2) * 16384 + row * 128;
-        const int p = (c16 & 3) * 2;
-        // eight lanes of a store on different banks: the upper half of a
-        // 128-wide row writes its second piece first
-        const bool swap = D == 128 && (c16 & 4);
-        sts128(to + (((p + (swap ? 1 : 0)) ^ (row & 7)) << 4), swap ? hi : lo);
-        sts128(to + (((p + (swap ? 0 : 1)) ^ (row & 7)) << 4), swap ? lo : hi);
       };
       int ids = blocks_of(0), ids_next = blocks_of(1);
 
@@ -518,9 +519,8 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         const int st = jt & 1;
         float ks = -1.f, lv = 0.f;
         if (cw == 0 && lane < 8 && ids >= 0) {
-          const long long bh = static_cast<long long>(ids) * a.Hkv + h;
-          ks = a.ks[bh];
-          lv = log2f(a.vs[bh]);
+          ks = a.ks[ids];
+          lv = log2f(a.vs[ids]);
         }
         const int ids_after = blocks_of(j + 2);
         // K
@@ -529,8 +529,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           if (!__all_sync(0xffffffffu, ok)) break;
         }
         copies_but_one();
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) put(base + Ly::kK + st * Ly::kTile, i, dec::lds128(raw_k + i * 2048));
+        put(base + Ly::kK + st * Ly::kTile, raw_k);
         fetch(raw_k, k8, ids_next, j + 1);
         if (cw == 0) {
           if (lane < 8) {
@@ -549,8 +548,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           if (!__all_sync(0xffffffffu, ok)) break;
         }
         copies_but_one();
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) put(base + Ly::kV + st * Ly::kTile, i, dec::lds128(raw_v + i * 2048));
+        put(base + Ly::kV + st * Ly::kTile, raw_v);
         fetch(raw_v, v8, ids_next, j + 1);
         fence_proxy_async_smem();
         __syncwarp();
@@ -569,7 +567,9 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
     const int row = tid;      // of the unit: 128 x + TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + kColS + x * kHalf, tO = tmem + lane_off + kColO + x * kHalf;
-    constexpr int kGroups = kKeys / GROUP, kIn = GROUP == 16 ? 2 : 1;  // groups of a tile, of a 32-key chunk
+    constexpr int kGroups = kKeys / GROUP;          // groups of a tile
+    constexpr int kIn = GROUP == 16 ? 2 : 1;        // of a 32-key chunk
+    constexpr int kStepG = 8 / kGroups;             // a group's place among the scales
     int cnt = 0, jt = 0;  // tiles of this half, tiles of the CTA
     for (int ns = 0;; ++ns) {
       const int si = ns % kSegs;
@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       const int lim = a.causal ? min(s.len, s.len - s.n + (s.row0 + row) / a.g + 1) : s.len;
       const int all = __reduce_min_sync(0xffffffffu, lim);
       float m = kInit, e = 0.f, l = 0.f;  // e: the second reference less the first
+      bool far = false;
       for (int j = 0; j < nt; ++j, ++jt, ++cnt) {
         // (the scales of a tile are never replaced before its scores are read)
         ok = wait(Ly::kSFull + 8 * x, cnt, kSiteS, jt) && wait(Ly::kScales + 8 * (jt & 3), jt >> 2, kSiteScales, jt);
@@ -608,11 +609,11 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         const int key0 = (s.t0 + j) * kKeys;
         bool careful = key0 + kKeys > all;
         // read twice, so that they are not held beside the scores
-        auto k_of = [&](int g) { return fmaxf(c * ks_at(g * (8 / kGroups)), kTiny); };
-        auto lv_of = [&](int g) { return lv_at(g * (8 / kGroups)); };
+        auto k_of = [&](int g) { return fmaxf(c * ks_at(g * kStepG), kTiny); };
+        auto lv_of = [&](int g) { return lv_at(g * kStepG); };
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) careful = careful | (ks_at(g * (8 / kGroups)) < 0.f);
-        if constexpr (GROUP == 32) {
+        for (int g = 0; g < kGroups; ++g) careful = careful | (ks_at(g * kStepG) < 0.f);
+        if constexpr (GROUP >= 32) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ldred_max32(tS + 32 * q, v[q], mx[q]);
           tmem_ldred_wait32(v[0], mx[0]);
@@ -645,14 +646,23 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           eb = fmaxf(eb + (mb - m1), t - m1 + lv_of(g));
           mb = m1;
         };
-        if (careful || GROUP == 16) {
+        if constexpr (GROUP == 16) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < kIn; ++i) see(q * kIn + i, max32(v[q], i * GROUP, (i + 1) * GROUP));
+          for (int g = 0; g < 8; ++g) see(g, max32(v[g >> 1], (g & 1) * 16, (g & 1) * 16 + 16));
         } else {
+          if (careful) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) see(q, mx[q]);
+            for (int q = 0; q < 4; ++q) mx[q] = max32(v[q], 0, 32);
+          }
+          if constexpr (GROUP == 32) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) see(g, mx[g]);
+          } else if constexpr (GROUP == 64) {
+            see(0, fmaxf(mx[0], mx[1]));
+            see(1, fmaxf(mx[2], mx[3]));
+          } else {
+            see(0, fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]));
+          }
         }
         const bool bump = mb > m + kLazy || eb + (mb - m) > e + kLazy;
         float up = 1.f;
@@ -663,61 +673,66 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           m = m1;
           e = e1;
         }
-        if (__any_sync(0xffffffffu, bump) && j > 0) {
-          // (where this wait gives up the loop ends below: leaving it here
-          // costs registers)
-          ok = __all_sync(0xffffffffu, wait(Ly::kPvDone + 8 * x, cnt - 1, kSitePV, jt));
-          tc_fence_after();
-          // a few columns at a time, beside the scores in registers
+        if (__any_sync(0xffffffffu, bump)) {
+          // The exponent is one fused product and sum, whose product is not
+          // rounded as m's was: above 2^17 (log2 units) that difference
+          // counts, and the scores are reduced in two steps instead.
+          far = __any_sync(0xffffffffu, fabsf(m) > 131072.f && m != kInit);
+          if (j > 0) {
+            // (where this wait gives up the loop ends below: leaving it here
+            // costs registers)
+            ok = __all_sync(0xffffffffu, wait(Ly::kPvDone + 8 * x, cnt - 1, kSitePV, jt));
+            tc_fence_after();
+            // a few columns at a time, beside the scores in registers
 #pragma unroll 1
-          for (int q = 0; q < D / 8; ++q) {
-            uint32_t o[8];
-            tmem_ld8(tO + 8 * q, o);
-            tmem_ld_wait8(o);
+            for (int q = 0; q < D / 8; ++q) {
+              uint32_t o[8];
+              tmem_ld8(tO + 8 * q, o);
+              tmem_ld_wait8(o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * up);
-            tmem_st8(tO + 8 * q, o);
+              for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * up);
+              tmem_st8(tO + 8 * q, o);
+            }
           }
         }
-        // The exponent is one fused product and sum, whose product is not
-        // rounded as m's was: above 2^17 (log2 units) that difference counts,
-        // and the scores are reduced in two steps instead.
-        const bool far = __any_sync(0xffffffffu, fabsf(m) > 131072.f && m != kInit);
         if (far) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              v[q][i] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(v[q][i]), k_of(q * kIn + i / GROUP)), m));
+              v[q][i] = __float_as_uint(
+                  __fsub_rn(__fmul_rn(__uint_as_float(v[q][i]), k_of((32 * q + i) / GROUP)), m));
         }
         float sums = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w[16];
+        for (int g = 0; g < kGroups; ++g) {
+          // 2^up_g: what the weights of this group carry beside 2^(s - m).
+          // Below 2^-60 they are 0 in f16 whatever it is.
+          const float up_g = fminf(fmaxf(lv_of(g) + kBias - e, -60.f), 120.f);
+          const float fk = far ? 1.f : k_of(g), nm = far ? up_g : up_g - m;
+          const uint64_t f2 = f2_pack(fk, fk), n2 = f2_pack(nm, nm);
+          uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < kIn; ++i) {
-            const int g = q * kIn + i;
-            // 2^lw: what the weights of this group carry beside 2^(s - m).
-            // Below 2^-60 they are 0 in f16 whatever it is.
-            const float up_g = fminf(fmaxf(lv_of(g) + kBias - e, -60.f), 120.f);
-            const float fk = far ? 1.f : k_of(g), nm = far ? up_g : up_g - m;
-            const uint64_t f2 = f2_pack(fk, fk);
-            const uint64_t n2 = f2_pack(nm, nm);
-            uint64_t sum = f2_pack(0.f, 0.f);
+          for (int q = 0; q < (GROUP + 31) / 32; ++q) {
+            const int ch = g * GROUP / 32 + q, lo = (g * GROUP) % 32;
+            constexpr int n = GROUP < 32 ? GROUP : 32;
+            uint32_t w[n / 2];
 #pragma unroll
-            for (int y = i * GROUP; y < (i + 1) * GROUP; y += 2) {
+            for (int y = 0; y < n; y += 2) {
               float a0, a1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[q][y]), __uint_as_float(v[q][y + 1])), f2, n2), a0, a1);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[ch][lo + y]), __uint_as_float(v[ch][lo + y + 1])), f2, n2), a0,
+                        a1);
               a0 = ex2(a0);
               a1 = ex2(a1);
-              sum = f2_add(sum, f2_pack(a0, a1));
+              sum[(y >> 1) & 1] = f2_add(sum[(y >> 1) & 1], f2_pack(a0, a1));
               w[y >> 1] = dec::pack_f16(a0, a1);
             }
-            float s0, s1;
-            f2_unpack(sum, s0, s1);
-            sums = fmaf(s0 + s1, ex2(-up_g), sums);
+            if constexpr (GROUP < 32) tmem_st8(tS + 8 * g, w);
+            else tmem_st16(tS + 16 * ch, w);
           }
-          tmem_st16(tS + 16 * q, w);
+          float s0, s1;
+          f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+          sums = fmaf(s0 + s1, ex2(-up_g), sums);
         }
         l += sums;
         tmem_st_wait();
