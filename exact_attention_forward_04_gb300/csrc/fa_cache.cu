@@ -200,10 +200,15 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
   int st = FA_OK;
   if (many) {
     using Ly = prm::Layout<D>;
-    const uint8_t* kc = static_cast<const uint8_t*>(k8);
+    // a key per 128-byte row, zeros behind the codes at d = 64
+    CUtensorMap mk;
+    st = host::tensor_map(&mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, k8, D, static_cast<cuuint64_t>(P),
+                          static_cast<cuuint64_t>(a.blocks) * a.Hkv, D, static_cast<cuuint64_t>(P) * D, 128,
+                          static_cast<cuuint32_t>(P));
+    if (st != FA_OK) return st;
     const uint8_t* vc = static_cast<const uint8_t*>(v8);
     auto launch = [&](auto kernel, bool& done) {
-      if ((st = ready(kernel, Ly::kAlloc, done)) == FA_OK) kernel<<<grid, prm::kThreads, Ly::kAlloc, s>>>(kc, vc, a);
+      if ((st = ready(kernel, Ly::kAlloc, done)) == FA_OK) kernel<<<grid, prm::kThreads, Ly::kAlloc, s>>>(mk, vc, a);
     };
     if (P == 16) launch(fa_cache_prompt_kernel<D, 16>, set[1]);
     else if (P == 32) launch(fa_cache_prompt_kernel<D, 32>, set[2]);

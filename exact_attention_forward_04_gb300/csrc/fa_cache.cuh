@@ -231,9 +231,8 @@ __device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32_t w1, float inv) 
                      __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv);
 }
 
-// Four codes times `ratio` (a power of two below 1), rounded to nearest even.
-__device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
-  float f[4];
+// Four codes' values.
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t c, float (&f)[4]) {
   asm("{\n\t.reg .b16 lo, hi, a, b, c, d;\n\t.reg .b32 x, y;\n\t"
       "mov.b32 {lo, hi}, %4;\n\t"
       "cvt.rn.f16x2.e4m3x2 x, lo;\n\t"
@@ -246,6 +245,11 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
       "cvt.f32.f16 %3, d;\n}"
       : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
       : "r"(c));
+}
+// Four codes times `ratio` (a power of two below 1), rounded to nearest even.
+__device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
+  float f[4];
+  e4m3x4_to_f32(c, f);
   return pack_e4m3x4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
 }
 

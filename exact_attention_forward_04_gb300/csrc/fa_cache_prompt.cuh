@@ -9,14 +9,17 @@
 // units that more than one CTA works on leave partials for the merge; here
 // a unit's number of key tiles follows its last row's position.
 //
-// tcgen05 has no product of f16 with E4M3, and rounding Q and P to 8 bits
-// would cost what the cache saved.  So four warps turn the codes into f16
-// (exact) on their way to shared memory: they copy the next tiles' codes to a
-// buffer while the present ones are multiplied, and write them out in the
-// 128-byte-swizzled layout that the products read, K as K-major and V as
-// MN-major operand.  256 rows share that work: per key tile about 250
-// instructions of each of these warps against 2048 cycles of tensor pipe at
-// d = 128.
+// Products.  S is taken in 8 bits: a query row, divided by a power of two of
+// its own, is the sum of two E4M3 numbers per element, the rounded value and
+// the rest (bf16 has 8 significant bits, E4M3 four: exact down to 2^-9 of the
+// row's largest element, and off by at most 2^-17 of that below), so that
+//   S = Q_hi K^T + Q_lo K^T
+// costs what one f16 product would, and K goes from the cache to the tensor
+// cores as it is.  P stays f16, as two parts of it would cost the softmax more
+// than they save; tcgen05 has no product of f16 with E4M3, so four warps turn
+// V's codes into f16 (exact) on their way: bulk copies bring the next tile's
+// to a buffer, as the blocks hold them, and these warps write them out in the
+// 128-byte-swizzled layout of an MN-major operand.
 //
 // TMEM (512 columns): S of A [0,128) and B [128,256) in fp32, P over the
 // first 64 columns of each as f16 pairs; O of A [256,384) and B [384,512).
@@ -27,7 +30,7 @@
 // to the same tensor pipe run in order.
 //
 // Warps: 0-3 softmax and epilogue of A, 4-7 of B, 8-11 codes to f16 (and Q),
-// 12 issues the products, 13 walks the range.
+// 12 issues the products, 13 walks the range, 14 loads.
 //
 // Softmax: as in the few-row kernel a row has two references, m for l = sum
 // 2^(s - m) and E for the weights 2^(10 + s - E) v_scale of the product, both
@@ -61,21 +64,25 @@ constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for B
 
 enum : unsigned { kSiteSegFull = 521, kSiteSegEmpty = 522, kSiteQFull = 523, kSiteQEmpty = 524, kSiteKFull = 525,
                   kSiteKEmpty = 526, kSiteVFull = 527, kSiteVEmpty = 528, kSiteS = 529, kSiteP = 530, kSitePV = 531,
-                  kSiteScales = 532 };
+                  kSiteScales = 532, kSiteRawFull = 533, kSiteRawEmpty = 534 };
 
 template <int D>
 struct Layout {
-  static constexpr int kQHalf = kHalf * D * 2;   // one half's rows, f16
-  static constexpr int kTile = kKeys * D * 2;    // K or V, f16
+  static constexpr int kPart = kHalf * 128;      // one half's rows, high or low parts (d = 64: half of each row used)
+  static constexpr int kQHalf = 2 * kPart;
+  static constexpr int kKTile = kKeys * 128;     // K codes, rows as for Q
+  static constexpr int kVTile = kKeys * D * 2;   // V, f16
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kQHalf;          // [2]
-  static constexpr int kV = kK + 2 * kTile;      // [2]
-  static constexpr int kRaw = kV + 2 * kTile;                 // codes of the next tiles of K and V
+  static constexpr int kV = kK + 2 * kKTile;     // [2]
+  static constexpr int kStaged = kV + 2 * kVTile;             // bf16 rows of one half of Q
+  static constexpr int kRaw = kStaged + kHalf * D * 2;        // codes of the next tile of V
   static constexpr int kScan = kRaw;                          // before the first: long long [33]
-  static constexpr int kRowScale = kRaw + 2 * kKeys * D;      // float [256]
+  static constexpr int kRowScale = kRaw + kKeys * D;          // float [256]
   static constexpr int kKs = kRowScale + kRows * 4;        // float [4][8]: K scale, -1: no block
   static constexpr int kLv = kKs + 4 * 8 * 4;                 // float [4][8]: log2 of the V scale
-  static constexpr int kSeg = kLv + 4 * 8 * 4;
+  static constexpr int kClean = kLv + 4 * 8 * 4;              // int [4]: every key of the tile is one to see
+  static constexpr int kSeg = kClean + 4 * 4;
   static constexpr int kBar = (kSeg + kSegs * static_cast<int>(sizeof(dec::Seg)) + 15) & ~15;
   static constexpr int kSegFull = kBar;
   static constexpr int kSegEmpty = kSegFull + 8 * kSegs;
@@ -89,7 +96,9 @@ struct Layout {
   static constexpr int kPFull = kSFull + 16;
   static constexpr int kPvDone = kPFull + 16;
   static constexpr int kScales = kPvDone + 16;    // [4]
-  static constexpr int kFin = kScales + 32;
+  static constexpr int kRawFull = kScales + 32;
+  static constexpr int kRawEmpty = kRawFull + 8;
+  static constexpr int kFin = kRawEmpty + 8;
   static constexpr int kTmemSlot = kFin + 8;
   static constexpr int kAbort = kTmemSlot + 8;
   static constexpr int kStart = (kAbort + 8 + 15) & ~15;  // int4
@@ -170,13 +179,24 @@ __device__ __forceinline__ void codes16(uint4 c, uint4& lo, uint4& hi) {
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copies_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but this thread's latest group of copies are done.
-__device__ __forceinline__ void copies_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void sts64(uint32_t at, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(v.x), "r"(v.y) : "memory");
+}
+
+// Four bf16 times `inv` as the sum of two E4M3 numbers each.
+__device__ __forceinline__ void split4(uint32_t w0, uint32_t w1, float inv, uint32_t& hi, uint32_t& lo) {
+  const float f[4] = {__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
+                      __uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xffff0000u) * inv};
+  hi = pack_e4m3x4(f[0], f[1], f[2], f[3]);
+  float g[4];
+  e4m3x4_to_f32(hi, g);
+  lo = pack_e4m3x4(f[0] - g[0], f[1] - g[1], f[2] - g[2], f[3] - g[3]);
 }
 
 __device__ __forceinline__ float lds_f32(uint32_t at) {
@@ -197,7 +217,7 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32], int lo, int hi) 
 // GROUP: tokens of a block, P: keys that share their scales.
 template <int D, int GROUP>
 __global__ void __launch_bounds__(prm::kThreads, 1)
-    fa_cache_prompt_kernel(const uint8_t* __restrict__ k8, const uint8_t* __restrict__ v8,
+    fa_cache_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const uint8_t* __restrict__ v8,
                            const __grid_constant__ CacheFwdArgs a) {
   using namespace prm;
   using dec::Req;
@@ -215,12 +235,12 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(base + Ly::kSegFull + 8 * i, 1);
-      mbar_init(base + Ly::kSegEmpty + 8 * i, 13);  // 8 softmax warps, 4 converters, the issuer
+      mbar_init(base + Ly::kSegEmpty + 8 * i, 14);  // 8 softmax warps, 4 converters, issuer, loader
     }
     mbar_init(base + Ly::kQFull, 4);
     mbar_init(base + Ly::kQEmpty, 9);  // the products' reads, and each softmax warp's of the row scales
     for (int i = 0; i < 2; ++i) {
-      mbar_init(base + Ly::kKFull + 8 * i, 4);
+      mbar_init(base + Ly::kKFull + 8 * i, 1);
       mbar_init(base + Ly::kKEmpty + 8 * i, 1);
       mbar_init(base + Ly::kVFull + 8 * i, 4);
       mbar_init(base + Ly::kVEmpty + 8 * i, 1);
@@ -228,6 +248,8 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       mbar_init(base + Ly::kPFull + 8 * i, 4);
       mbar_init(base + Ly::kPvDone + 8 * i, 1);
     }
+    mbar_init(base + Ly::kRawFull, 1);
+    mbar_init(base + Ly::kRawEmpty, 4);
     for (int i = 0; i < 4; ++i) mbar_init(base + Ly::kScales + 8 * i, 1);
     mbar_init(base + Ly::kFin, 1);
     *abort_flag = 0;
@@ -337,9 +359,86 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           mbar_arrive(base + Ly::kSegFull + 8 * si);
         }
       }
+    } else if (warp == 14) {
+      // ------------------------------------------------------- the loader
+      // Codes of a tile's blocks, as they lie, into the raw buffers; its
+      // scales, fetched while the tile before is converted.
+      const int unit = min(1 << a.sh, kKeys);  // tokens that lie together
+      fence_proxy_async_smem();  // the scan's use of the raw buffer
+      if (lane == 0) prefetch_tensormap(&tmK);
+      int jt = 0;
+      bool ok = true;
+      for (int ns = 0;; ++ns) {
+        const int si = ns % kSegs;
+        ok = __all_sync(0xffffffffu, wait(Ly::kSegFull + 8 * si, ns / kSegs, kSiteSegFull, ns));
+        if (!ok) break;
+        const Seg& s = segs[si];
+        const int nt = s.nt, h = s.h, len = s.len, t0 = s.t0;
+        if (nt == 0) break;
+        const int* table = a.table + static_cast<long long>(s.r) * a.M;
+        // block of this lane's 16 keys (8 lanes) in tile j; -1: none, -2: no keys
+        auto block_of = [&](int j) {
+          const int key = (t0 + j) * kKeys + lane * 16;
+          return lane < 8 && j < nt && key < len ? table[key >> a.sh] : -2;
+        };
+        int next = block_of(0);
+        for (int j = 0; j < nt; ++j, ++jt) {
+          const int b = next;
+          const bool real = b >= 0 && b < a.blocks;
+          if (b != -2 && !real) record_index_error(a.index_err, kSiteFwdBlock, s.r);
+          const long long bh = static_cast<long long>(b) * a.Hkv + h;
+          float ks = -1.f, lv = 0.f;
+          if (real) {
+            ks = a.ks[bh];
+            lv = a.vs[bh];
+          }
+          next = block_of(j + 1);
+          const bool issue = real && ((lane * 16) & (unit - 1)) == 0;
+          const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, issue)) * unit * D);
+          const bool clean = __popc(__ballot_sync(0xffffffffu, real)) == 8 && (t0 + j + 1) * kKeys <= len;
+          const int st = jt & 1, in_block = ((t0 + j) * kKeys + lane * 16) & ((1 << a.sh) - 1);
+          ok = jt < 2 || wait(Ly::kKEmpty + 8 * st, (jt >> 1) - 1, kSiteKEmpty, jt);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane < 8) {
+            reinterpret_cast<float*>(sm + Ly::kKs)[(jt & 3) * 8 + lane] = ks;
+            reinterpret_cast<float*>(sm + Ly::kLv)[(jt & 3) * 8 + lane] = fmaxf(log2f(lv), -200.f);
+          }
+          if (lane == 0) reinterpret_cast<int*>(sm + Ly::kClean)[jt & 3] = clean;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(base + Ly::kScales + 8 * (jt & 3));
+            mbar_arrive_expect_tx(base + Ly::kKFull + 8 * st, bytes / D * 128);
+          }
+          __syncwarp();
+          // rows of keys without a block keep what they held: their scores
+          // are masked
+          if (issue)
+            tma_load_3d(base + Ly::kK + st * Ly::kKTile + lane * 16 * 128, &tmK, base + Ly::kKFull + 8 * st, 0, in_block,
+                        static_cast<int>(bh));
+          ok = jt == 0 || wait(Ly::kRawEmpty, jt - 1, kSiteRawEmpty, jt);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(base + Ly::kRawFull, bytes);
+          __syncwarp();
+          if (issue)
+            bulk_load_1d(base + Ly::kRaw + lane * 16 * D, v8 + (bh << a.sh) * D + in_block * D,
+                         static_cast<uint32_t>(unit * D), base + Ly::kRawFull);
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
+      }
+      // no copy outlives the CTA, also where a wait gave up (the K tile then
+      // may be one ahead of V's: a phase that never began ends by its time)
+      if (lane == 0 && jt > 0) {
+        const uint64_t end = globaltimer_ns() + a.timeout_ns;
+        dec::mbar_drain(base + Ly::kRawFull, (jt - 1) & 1, end);
+        for (int t = max(0, jt - 2); t < jt; ++t) dec::mbar_drain(base + Ly::kKFull + 8 * (t & 1), (t >> 1) & 1, end);
+      }
+      if (lane == 0 && !ok) dec::mbar_drain(base + Ly::kKFull + 8 * (jt & 1), (jt >> 1) & 1, globaltimer_ns() + 1000000);
     } else if (warp == 12 && lane == 0) {
       // ------------------------------------------------------- the issuer
-      constexpr uint32_t idS = idesc_f16_f32(kHalf, kKeys, false), idPV = idesc_f16_f32(kHalf, D, true);
+      constexpr uint32_t idS = idesc_e4m3_f32(kHalf, kKeys), idPV = idesc_f16_f32(kHalf, D, true);
       // operand descriptors (sw128_desc) by their low word; the high word,
       // stride 1024 and the swizzle, is the same for all
       constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);
@@ -347,13 +446,13 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       auto low = [](uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); };
       int jt = 0, cnt_a = 0, cnt_b = 0;
       auto issue_s = [&](int x, int st) {
-        const uint32_t q = low(base + Ly::kQ + x * Ly::kQHalf, 16), k = low(base + Ly::kK + st * Ly::kTile, 16);
+        const uint32_t q = low(base + Ly::kQ + x * Ly::kQHalf, 16), k = low(base + Ly::kK + st * Ly::kKTile, 16);
         const uint32_t d = tmem + kColS + x * kHalf;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = static_cast<uint32_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-          mma_ss(d, desc(q + off), desc(k + off), idS, kk > 0 ? 1u : 0u);
-        }
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)  // 32 codes of each row
+            mma_ss_f8(d, desc(q + ((part * Ly::kPart) >> 4) + 2 * kk), desc(k + 2 * kk), idS, part + kk > 0 ? 1u : 0u);
         tc_commit(base + Ly::kSFull + 8 * x);
       };
       for (int ns = 0;; ++ns) {
@@ -376,7 +475,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
               ok = wait(Ly::kPFull + 8 * x, x ? cnt_b++ : cnt_a++, kSiteP, jt);
               if (!ok) break;
               tc_fence_after();
-              const uint32_t v = low(base + Ly::kV + st * Ly::kTile, 16384);
+              const uint32_t v = low(base + Ly::kV + st * Ly::kVTile, 16384);
               const uint32_t d = tmem + kColO + x * kHalf, p = tmem + kColS + x * kHalf;
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
@@ -405,27 +504,46 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
     }
   } else if (warp >= 8) {
     reg_dec<80>();
-    // ------------------------------------------- codes and queries to f16
+    // ----------------------------------------- V's codes to f16, Q in parts
     // A thread turns 16 codes of a row into two 16-byte pieces, of rows kStep
-    // apart.  Eight lanes hold four chunks of two rows: their pieces 0 2 4 6,
-    // XORed with the row's low bits, fall on different banks.
+    // apart.  Eight lanes read 128 bytes in a row.  Their pieces go to the
+    // places 0 2 4 6 of a 128-byte row, XORed with the row's low bits: at
+    // d = 64 of two rows, on different banks; at d = 128 of two column blocks
+    // of one, so the lanes of the upper write their odd pieces first.
     constexpr int kPer = kKeys * D / 16 / 128;      // per thread and tile
     constexpr int kStep = kKeys / kPer;
     const int cw = warp - 8, ct = tid - 256;
-    const int c16 = (lane & 3) + (D == 128 ? 4 * (cw & 1) : 0);
-    const int row_lo = (lane >> 2) + 8 * (D == 128 ? cw >> 1 : cw);
+    const int c16 = ct & (D / 16 - 1), row_lo = ct / (D / 16);
+    const bool odd_first = D == 128 && (c16 & 4);
     const uint32_t piece = static_cast<uint32_t>((c16 >> 2) * 16384 + row_lo * 128 +
-                                                 ((((c16 & 3) * 2) ^ (row_lo & 7)) << 4));
-    const int P1 = (1 << a.sh) - 1;
-    // codes wait in buffers that only the thread that copied them reads
-    const uint32_t raw_k = base + Ly::kRaw + ct * 16, raw_v = raw_k + kKeys * D;
-    auto put = [&](uint32_t to, uint32_t from) {
+                                                 ((((c16 & 3) * 2 + (odd_first ? 1 : 0)) ^ (row_lo & 7)) << 4));
+    const uint32_t raw_at = base + Ly::kRaw + ct * 16;
+    // one tile; loads four at a time, as one after the other each would wait
+    // for its own
+    auto put = [&](int st, int jt, int keys_left) {
+      const uint32_t to0 = base + Ly::kV + st * Ly::kVTile + piece, to1 = to0 ^ 16u;
+      const bool clean = reinterpret_cast<const volatile int*>(sm + Ly::kClean)[jt & 3] != 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        uint4 lo, hi;
-        codes16(dec::lds128(from + i * 2048), lo, hi);
-        sts128(to + piece + i * (kStep * 128), lo);
-        sts128((to + piece + i * (kStep * 128)) ^ 16u, hi);
+      for (int b = 0; b < kPer; b += 4) {
+        uint4 c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = dec::lds128(raw_at + (b + i) * 2048);
+        if (!clean) {  // what no token lies in may be anything, NaN too
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = row_lo + kStep * (b + i);
+            if (row >= keys_left || lds_f32(base + Ly::kKs + (jt & 3) * 32 + 4 * (row >> 4)) < 0.f)
+              c[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 p, q;
+          if (odd_first) c[i] = make_uint4(c[i].z, c[i].w, c[i].x, c[i].y);
+          codes16(c[i], p, q);
+          sts128(to0 + (b + i) * (kStep * 128), p);
+          sts128(to1 + (b + i) * (kStep * 128), q);
+        }
       }
     };
     int jt = 0;
@@ -436,125 +554,69 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       const Seg& s = segs[si];
       const int nt = s.nt;
       if (nt == 0) break;
-      const int h = s.h, len = s.len, t0 = s.t0;
-      const int* table = a.table + static_cast<long long>(s.r) * a.M;
-      // block and head of 16-key group `lane` (< 8) of tile j, -1: none
-      auto blocks_of = [&](int j) {
-        int b = -1;
-        const int key = (t0 + j) * kKeys + lane * 16;
-        if (lane < 8 && j < nt && key < len) {
-          b = table[key >> a.sh];
-          if (b < 0 || b >= a.blocks) {
-            if (cw == 0) record_index_error(a.index_err, kSiteFwdBlock, s.r);
-            b = -1;
-          } else {
-            b = b * a.Hkv + h;
-          }
-        }
-        return b;
-      };
-      // this thread's chunks of tile j, zeros where there is no token
-      auto fetch = [&](uint32_t to, const uint8_t* codes, int ids, int j) {
-        if (j < nt) {
-          const int last = len - (t0 + j) * kKeys - row_lo;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int b = __shfl_sync(0xffffffffu, ids, (row_lo + kStep * i) >> 4);
-            const bool real = b >= 0 && kStep * i < last;
-            const uint8_t* from = codes + c16 * 16 + static_cast<long long>(real ? b : 0) * (D << a.sh) +
-                                  ((row_lo + kStep * i) & P1) * D;
-            copy16(to + i * 2048, from, real);
-          }
-        }
-        copies_group();
-      };
-      int ids = blocks_of(0), ids_next = blocks_of(1);
+      const int h = s.h;
 
-      // Q: the bf16 rows copied to where they go, then, each by the threads
-      // that copied it, divided by a power of two of its own and made f16
-      ok = ns == 0 || wait(Ly::kQEmpty, ns - 1, kSiteQEmpty, ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      // Q, half by half: the bf16 rows to a buffer that only the thread that
+      // copied reads, then in two parts to their places
       {
         constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes per row (8 elements each), rows per warp
-        const int col = lane % kLanes;
-        const uint32_t to = base + Ly::kQ + (col >> 3) * 16384;
-        const int rows = s.nv > kHalf ? kRows : kHalf;
-        auto spot = [&](int row) {
-          return to + (row >> 7) * Ly::kQHalf + (row & 127) * 128 + (((col & 7) ^ (row & 7)) << 4);
-        };
-#pragma unroll 4
-        for (int row = cw * kAt + lane / kLanes; row < rows; row += 4 * kAt) {
-          const int rr = s.row0 + row, tk = rr / a.g;
-          const bool real = row < s.nv;
-          const long long at = (s.c0 + tk) * a.q_stride + static_cast<long long>(h * a.g + rr - tk * a.g) * D + col * 8;
-          copy16(spot(row), a.q + (real ? at : 0), real);
-        }
-        copies_group();
-        fetch(raw_k, k8, ids, 0);
-        fetch(raw_v, v8, ids, 0);
-        copies_done();
+        const int col = lane % kLanes, row_w = cw * kAt + lane / kLanes;
+        const uint32_t staged = base + Ly::kStaged + ct * 16;
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-#pragma unroll 4
-        for (int row = cw * kAt + lane / kLanes; row < rows; row += 4 * kAt) {
-          const uint4 w = dec::lds128(spot(row));
-          uint32_t am = amax2(w.x, amax2(w.y, amax2(w.z, amax2(w.w, 0u))));
+        for (int half = 0; half < (s.nv > kHalf ? 2 : 1); ++half) {
+#pragma unroll 2
+          for (int i = 0; i < kHalf / (4 * kAt); ++i) {
+            const int row = half * kHalf + row_w + i * 4 * kAt, rr = s.row0 + row, tk = rr / a.g;
+            const bool real = row < s.nv;
+            const long long at = (s.c0 + tk) * a.q_stride + static_cast<long long>(h * a.g + rr - tk * a.g) * D + col * 8;
+            copy16(staged + i * 2048, a.q + (real ? at : 0), real);
+          }
+          if (half == 0) {
+            ok = ns == 0 || wait(Ly::kQEmpty, ns - 1, kSiteQEmpty, ns);
+            ok = __all_sync(0xffffffffu, ok);
+          }
+          copies_done();
+          if (!ok) break;
+#pragma unroll 2
+          for (int i = 0; i < kHalf / (4 * kAt); ++i) {
+            const int rl = row_w + i * 4 * kAt;
+            uint4 w = dec::lds128(staged + i * 2048);
+            uint32_t am = amax2(w.x, amax2(w.y, amax2(w.z, amax2(w.w, 0u))));
 #pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-          const int ex = dec::row_exponent(am << 16);
-          const float inv = dec::pow2i(-ex);
-          auto two16 = [&](uint32_t v) {
-            v ^= flip;
-            return dec::pack_f16(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
-          };
-          sts128(spot(row), make_uint4(two16(w.x), two16(w.y), two16(w.z), two16(w.w)));
-          if (col == 0)
-            reinterpret_cast<float*>(sm + Ly::kRowScale)[row] = fmaxf(fabsf(a.scale_log2) * dec::pow2i(ex), kTiny);
+            for (int o = 1; o < kLanes; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+            // the largest element to [2^7, 2^8): E4M3 holds up to 448
+            const int ex = dec::row_exponent(am << 16) - 7;
+            const float inv = dec::pow2i(-ex);
+            uint2 hi, lo;
+            split4(w.x ^ flip, w.y ^ flip, inv, hi.x, lo.x);
+            split4(w.z ^ flip, w.w ^ flip, inv, hi.y, lo.y);
+            const uint32_t to = base + Ly::kQ + half * Ly::kQHalf + rl * 128 + (((col >> 1) ^ (rl & 7)) << 4) + (col & 1) * 8;
+            sts64(to, hi);
+            sts64(to + Ly::kPart, lo);
+            if (col == 0)
+              reinterpret_cast<float*>(sm + Ly::kRowScale)[half * kHalf + rl] =
+                  fmaxf(fabsf(a.scale_log2) * dec::pow2i(ex), kTiny);
+          }
         }
+        if (!ok) break;
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(base + Ly::kQFull);
 
       for (int j = 0; j < nt; ++j, ++jt) {
-        const int st = jt & 1;
-        float ks = -1.f, lv = 0.f;
-        if (cw == 0 && lane < 8 && ids >= 0) {
-          ks = a.ks[ids];
-          lv = log2f(a.vs[ids]);
-        }
-        const int ids_after = blocks_of(j + 2);
-        // K
-        if (jt >= 2) {
-          ok = wait(Ly::kKEmpty + 8 * st, (jt >> 1) - 1, kSiteKEmpty, jt);
-          if (!__all_sync(0xffffffffu, ok)) break;
-        }
-        copies_but_one();
-        put(base + Ly::kK + st * Ly::kTile, raw_k);
-        fetch(raw_k, k8, ids_next, j + 1);
-        if (cw == 0) {
-          if (lane < 8) {
-            reinterpret_cast<float*>(sm + Ly::kKs)[(jt & 3) * 8 + lane] = ks;
-            reinterpret_cast<float*>(sm + Ly::kLv)[(jt & 3) * 8 + lane] = fmaxf(lv, -200.f);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(base + Ly::kScales + 8 * (jt & 3));
-        }
+        const int st = jt & 1, left = s.len - (s.t0 + j) * kKeys;
+        ok = wait(Ly::kRawFull, jt, kSiteRawFull, jt) &&
+             (jt < 2 || wait(Ly::kVEmpty + 8 * st, (jt >> 1) - 1, kSiteVEmpty, jt));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        put(st, jt, left);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(base + Ly::kKFull + 8 * st);
-        // V
-        if (jt >= 2) {
-          ok = wait(Ly::kVEmpty + 8 * st, (jt >> 1) - 1, kSiteVEmpty, jt);
-          if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
+          mbar_arrive(base + Ly::kRawEmpty);
+          mbar_arrive(base + Ly::kVFull + 8 * st);
         }
-        copies_but_one();
-        put(base + Ly::kV + st * Ly::kTile, raw_v);
-        fetch(raw_v, v8, ids_next, j + 1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(base + Ly::kVFull + 8 * st);
-        ids = ids_next;
-        ids_next = ids_after;
       }
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);

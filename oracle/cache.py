@@ -91,9 +91,10 @@ def cache_values(codes, scale, table_row, n):
 def attention_cache(q, k8, v8, k_scale, v_scale, table, seq_lens, cu, scale, causal=True):
     """O [T, Hq, d], L [T, Hq] (float64) and, per row, what the error bounds
     scale with: A = sum_j p_j |v_j| [T, Hq, d], S = the largest
-    |scale| sum_t |q_t k_jt| over its visible keys [T, Hq], and W = the largest
-    p_j times its V scale, times the sum of |V code values| [T, Hq, d].  Rows of
-    no request are NaN."""
+    |scale| sum_t |q_t k_jt| over its visible keys [T, Hq], R = the largest
+    |scale| max |q| sum |k_jt| over the t with |q_t| < 2^-9 max |q| [T, Hq], and
+    W = the largest p_j times its V scale, times the sum of |V code values|
+    [T, Hq, d].  Rows of no request are NaN."""
     q = q.detach().to("cpu", torch.float64).numpy()
     k8, v8 = np.asarray(k8), np.asarray(v8)
     k_scale, v_scale, table = np.asarray(k_scale), np.asarray(v_scale), np.asarray(table)
@@ -101,7 +102,7 @@ def attention_cache(q, k8, v8, k_scale, v_scale, table, seq_lens, cu, scale, cau
     g = Hq // k8.shape[1]
     P = k8.shape[2]
     O, A, W = (np.full((T, Hq, d), np.nan) for _ in range(3))
-    L, S = np.full((T, Hq), np.nan), np.full((T, Hq), np.nan)
+    L, S, R = (np.full((T, Hq), np.nan) for _ in range(3))
     for r, n_keys in enumerate(seq_lens):
         c0, n = cu[r], cu[r + 1] - cu[r]
         k = cache_values(k8, k_scale, table[r], n_keys)
@@ -112,7 +113,8 @@ def attention_cache(q, k8, v8, k_scale, v_scale, table, seq_lens, cu, scale, cau
             seen = max(0, min(n_keys, n_keys - n + i + 1)) if causal else n_keys
             for h in range(Hq):
                 if seen == 0:
-                    O[c0 + i, h], A[c0 + i, h], W[c0 + i, h], L[c0 + i, h], S[c0 + i, h] = 0, 0, 0, -math.inf, 0
+                    O[c0 + i, h], A[c0 + i, h], W[c0 + i, h], L[c0 + i, h] = 0, 0, 0, -math.inf
+                    S[c0 + i, h], R[c0 + i, h] = 0, 0
                     continue
                 x, kh, vh = q[c0 + i, h], k[:seen, h // g], v[:seen, h // g]
                 s = scale * (kh @ x)
@@ -122,5 +124,7 @@ def attention_cache(q, k8, v8, k_scale, v_scale, table, seq_lens, cu, scale, cau
                 p /= p.sum()
                 O[c0 + i, h], A[c0 + i, h] = p @ vh, p @ np.abs(vh)
                 S[c0 + i, h] = abs(scale) * (np.abs(kh) @ np.abs(x)).max()
+                small = np.abs(x) < 2.0 ** -9 * np.abs(x).max()
+                R[c0 + i, h] = abs(scale) * np.abs(x).max() * np.abs(kh[:, small]).sum(1).max()
                 W[c0 + i, h] = (p * v_size[:seen, h // g]).max() * np.abs(v_unit[:seen, h // g]).sum(0)
-    return tuple(torch.from_numpy(a) for a in (O, L, A, S, W))
+    return tuple(torch.from_numpy(a) for a in (O, L, A, S, R, W))

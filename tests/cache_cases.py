@@ -47,7 +47,7 @@ def poison(codes, table, lens):
             codes[b] = 0xFF
 
 
-def forward_bounds(O, L, A, S, W, d):
+def forward_bounds(O, L, A, S, R, W, d):
     """Element-wise bounds of |O - o| and |L - l| (float64 oracle values).
 
     Score of one key, in natural units, with u = 2^-24 (fp32): the fp32 sum of
@@ -56,8 +56,14 @@ def forward_bounds(O, L, A, S, W, d):
     four more roundings, and the reference's subtraction one of the reduced
     score: 6 u S.  Query elements below 2^-17 of the row's largest lose up to
     2^-25 of it each, below 2 u S as the largest itself may meet a key element
-    of zero: counted with d u S.  Together delta = (2 d + 8) u S, and 2^x
-    (relative error 2^-22) makes it eps = delta + 2^-21 of a weight.
+    of zero: counted with d u S.  With many rows the query is two E4M3 numbers
+    an element, its largest in [2^7, 2^8): elements of 2^-2 and more (8
+    significant bits, the lowest of them 2^-9 or more) are exact, 4 bits of
+    them in the first number and the rest, at most 8 steps of the lowest bit,
+    in the second; smaller ones are rounded to 2^-9, off by 2^-10, 2^-17 of the
+    largest: 2^-17 R (R: over the elements below 2^-9 of the largest).
+    Together delta = (2 d + 8) u S + 2^-17 R, and 2^x (relative error 2^-22)
+    makes it eps = delta + 2^-21 of a weight.
     O: weights carry eps in the numerator, eps in the sum, and the f16
     rounding of a weight, half of 2^-10 relative; the sums and divisions below
     2^-18 in all; then bf16, half of 2^-7 of the result.  A weight times its V
@@ -69,7 +75,7 @@ def forward_bounds(O, L, A, S, W, d):
     where the heaviest keys are 0 in a column).
     L: eps, the logarithm's and the last product's rounding."""
     u = 2.0 ** -24
-    eps = (2 * d + 8) * u * S + 2.0 ** -21
+    eps = (2 * d + 8) * u * S + 2.0 ** -17 * R + 2.0 ** -21
     bO = (2 * eps[..., None] + 2.0 ** -11 + 2.0 ** -18) * A + 2.0 ** -35 * W
     bO = bO + 2.0 ** -8 * (O.abs() + bO) + 1e-30
     bL = eps + 2.0 ** -20 + 4 * u * L.abs()
@@ -80,7 +86,7 @@ def assert_forward(o, lse, q, codes, table, lens, cu, scale, causal, what=""):
     """o, lse (any device) against the oracle on the rows of requests; returns
     the worst share of the bounds that was used."""
     k8, v8, ks, vs = codes
-    O, L, A, S, W = oracle.attention_cache(q, k8.numpy(), v8.numpy(), ks.numpy(), vs.numpy(), table.numpy(), lens, cu,
+    O, L, A, S, R, W = oracle.attention_cache(q, k8.numpy(), v8.numpy(), ks.numpy(), vs.numpy(), table.numpy(), lens, cu,
                                         scale, causal)
     o, lse = o.detach().to("cpu", torch.float64), lse.detach().to("cpu", torch.float64)
     real = ~torch.isnan(L)
@@ -88,7 +94,7 @@ def assert_forward(o, lse, q, codes, table, lens, cu, scale, causal, what=""):
     assert torch.equal(lse[empty], L[empty]), f"{what}: L of rows without keys"
     assert (o[empty] == 0).all(), f"{what}: O of rows without keys"
     live = real & ~empty
-    bO, bL = forward_bounds(O, L, A, S, W, q.shape[-1])
+    bO, bL = forward_bounds(O, L, A, S, R, W, q.shape[-1])
     assert torch.isfinite(o[live]).all() and torch.isfinite(lse[live]).all(), f"{what}: not finite"
     if not live.any():
         return 0.0

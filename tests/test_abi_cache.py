@@ -180,11 +180,11 @@ def test_oracle_attention_agrees_with_the_dense_oracle():
     v8, vs = make_codes(blocks, 1, P, d, 2)
     q = torch.randn(n, 1, d, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
     for causal in (False, True):
-        O, L, A, S, W = oracle.attention_cache(q, k8, v8, ks, vs, table, [n], [0, n], 0.125, causal)
+        O, L, A, S, R, W = oracle.attention_cache(q, k8, v8, ks, vs, table, [n], [0, n], 0.125, causal)
         k = torch.from_numpy(oracle.cache_values(k8.numpy(), ks.numpy(), table[0], n))
         v = torch.from_numpy(oracle.cache_values(v8.numpy(), vs.numpy(), table[0], n))
         Oref, Lref = oracle.attention_ref(q.double().transpose(0, 1)[None], k.transpose(0, 1)[None],
                                           v.transpose(0, 1)[None], 0.125, causal)
         assert torch.allclose(O[:, 0], Oref[0, 0], rtol=0, atol=1e-12)
         assert torch.allclose(L[:, 0], Lref[0, 0], rtol=0, atol=1e-12)
-        assert (A >= O.abs() - 1e-12).all() and (W >= 0).all() and (S > 0).all()
+        assert (A >= O.abs() - 1e-12).all() and (W >= 0).all() and (R >= 0).all() and (S > 0).all()
