@@ -21,16 +21,19 @@
 // to a buffer, as the blocks hold them, and these warps write them out in the
 // 128-byte-swizzled layout of an MN-major operand.
 //
-// TMEM (512 columns): S of A [0,128) and B [128,256) in fp32, P over the
-// first 64 columns of each as f16 pairs; O of A [256,384) and B [384,512).
-// One thread issues, for key tile j (after S_A(0), S_B(0)),
-//   PV_A(j), S_A(j+1), PV_B(j), S_B(j+1)
-// so that one half's softmax runs under the other half's products.  S(j+1)
-// overwrites P(j), which PV(j) before it reads: products issued by one thread
-// to the same tensor pipe run in order.
+// TMEM (512 columns): of each half two buffers of scores, fp32 [128][64], A at
+// [0,128) and B at [128,256), P over the first half of each as f16 pairs; O of
+// A [256,384) and of B [384,512).
+// A key tile is two steps of 64 keys.  For each half one thread issues S(0),
+// S(1), then for step i PV(i), S(i+2): the scores of a step lie ready when the
+// softmax has done the one before, so that it never waits for its own weights
+// to be multiplied.  (With steps of 128 keys and one buffer, scores, softmax
+// and weights followed one another: 4100 cycles per tile and half, of which the
+// softmax took 1800.)  S(i+2) overwrites P(i), which PV(i) before it reads:
+// products issued by one thread to the same tensor pipe run in order.
 //
 // Warps: 0-3 softmax and epilogue of A, 4-7 of B, 8-11 codes to f16 (and Q),
-// 12 issues the products, 13 walks the range, 14 loads.
+// 12 and 15 issue A's and B's products, 13 walks the range, 14 loads.
 //
 // Softmax: as in the few-row kernel a row has two references, m for l = sum
 // 2^(s - m) and E for the weights 2^(10 + s - E) v_scale of the product, both
@@ -53,6 +56,7 @@ constexpr int kThreads = 512;
 constexpr int kRows = 256;       // query rows of a unit
 constexpr int kHalf = 128;
 constexpr int kKeys = 128;       // keys of a tile
+constexpr int kStepKeys = 64;    // of a step: scores, softmax, weights
 constexpr int kSegs = 4;
 constexpr int kUnitCost = 3;     // a piece's fixed cost, in tiles
 constexpr int kMinCost = 6;      // least cost of a CTA's range
@@ -92,14 +96,14 @@ struct Layout {
   static constexpr int kKEmpty = kKFull + 16;
   static constexpr int kVFull = kKEmpty + 16;
   static constexpr int kVEmpty = kVFull + 16;
-  static constexpr int kSFull = kVEmpty + 16;     // [2] A, B
-  static constexpr int kPFull = kSFull + 16;
-  static constexpr int kPvDone = kPFull + 16;
+  static constexpr int kSFull = kVEmpty + 16;     // [2] A, B [2] score buffers
+  static constexpr int kPFull = kSFull + 32;      // [2][2]
+  static constexpr int kPvDone = kPFull + 32;     // [2]
   static constexpr int kScales = kPvDone + 16;    // [4]
   static constexpr int kRawFull = kScales + 32;
   static constexpr int kRawEmpty = kRawFull + 8;
   static constexpr int kFin = kRawEmpty + 8;
-  static constexpr int kTmemSlot = kFin + 8;
+  static constexpr int kTmemSlot = kFin + 16;
   static constexpr int kAbort = kTmemSlot + 8;
   static constexpr int kStart = (kAbort + 8 + 15) & ~15;  // int4
   static constexpr int kBytes = kStart + 16;
@@ -130,14 +134,17 @@ __device__ __noinline__ long long floor_sum(long long n, long long m, long long 
   return s;
 }
 
-// Key tiles of row tile rt: up to its last row's position.
-__device__ __forceinline__ int tiles_of(const CacheFwdArgs& a, const dec::Req& q, int rt) {
+// Keys that the last row of row tile rt sees.
+__device__ __forceinline__ int seen_of(const CacheFwdArgs& a, const dec::Req& q, int rt) {
   int seen = q.len;
   if (a.causal && q.n <= q.len) {
     const unsigned last = min(static_cast<unsigned>(rt) * kRows + kRows, static_cast<unsigned>(q.n) * a.g) - 1;
     seen = q.len - q.n + static_cast<int>(last / a.g) + 1;
   }
-  return max(1, (seen + kKeys - 1) / kKeys);
+  return seen;
+}
+__device__ __forceinline__ int tiles_of(const CacheFwdArgs& a, const dec::Req& q, int rt) {
+  return max(1, (seen_of(a, q, rt) + kKeys - 1) / kKeys);
 }
 // Cost of the row tiles before rt (< nrt): all of them full, so tile i sees
 // base + floor((256 (i + 1) - 1) / g) + 1 keys, base = len - n, and has
@@ -159,6 +166,13 @@ __device__ __forceinline__ void reg_inc() {
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N) : "memory");
+}
+
+// True in one thread of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 
 // kind::f16 with f16 A and B (format 0), fp32 D.
@@ -235,23 +249,26 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(base + Ly::kSegFull + 8 * i, 1);
-      mbar_init(base + Ly::kSegEmpty + 8 * i, 14);  // 8 softmax warps, 4 converters, issuer, loader
+      mbar_init(base + Ly::kSegEmpty + 8 * i, 15);  // 8 softmax warps, 4 converters, 2 issuers, loader
     }
     mbar_init(base + Ly::kQFull, 4);
-    mbar_init(base + Ly::kQEmpty, 9);  // the products' reads, and each softmax warp's of the row scales
+    mbar_init(base + Ly::kQEmpty, 10);  // both issuers' products, and each softmax warp's reads of the row scales
     for (int i = 0; i < 2; ++i) {
       mbar_init(base + Ly::kKFull + 8 * i, 1);
-      mbar_init(base + Ly::kKEmpty + 8 * i, 1);
+      mbar_init(base + Ly::kKEmpty + 8 * i, 2);
       mbar_init(base + Ly::kVFull + 8 * i, 4);
-      mbar_init(base + Ly::kVEmpty + 8 * i, 1);
-      mbar_init(base + Ly::kSFull + 8 * i, 1);
-      mbar_init(base + Ly::kPFull + 8 * i, 4);
+      mbar_init(base + Ly::kVEmpty + 8 * i, 2);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(base + Ly::kSFull + 8 * (2 * i + b), 1);
+        mbar_init(base + Ly::kPFull + 8 * (2 * i + b), 4);
+      }
       mbar_init(base + Ly::kPvDone + 8 * i, 1);
     }
     mbar_init(base + Ly::kRawFull, 1);
     mbar_init(base + Ly::kRawEmpty, 4);
     for (int i = 0; i < 4; ++i) mbar_init(base + Ly::kScales + 8 * i, 1);
     mbar_init(base + Ly::kFin, 1);
+    mbar_init(base + Ly::kFin + 8, 1);
     *abort_flag = 0;
     fence_mbar_init();
     a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -303,60 +320,63 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
   };
 
   if (warp >= 12) {
-    reg_dec<64>();
-    if (warp == 13 && lane == 0) {
-      // ------------------------------------------------------- the walker
-      const int4 at = *reinterpret_cast<const int4*>(sm + Ly::kStart);
-      int r = at.x, h = at.y, rt = at.z, y = at.w;
-      long long left = x1 - x0;
-      int nseg = 0;
-      bool ok = true;
-      Req q = dec::request<kRows, kKeys>(a, r);
-      while (left > 0) {
-        if (rt >= q.nrt) {  // the next kv head, the next request with rows
-          rt = 0;
-          if (++h == a.Hkv) {
-            h = 0;
-            do q = dec::request<kRows, kKeys>(a, ++r); while (q.nrt == 0);  // ends: cost is left
+    reg_dec<80>();
+    if (warp == 13) {
+      if (lane == 0) {
+        // ------------------------------------------------------- the walker
+        const int4 at = *reinterpret_cast<const int4*>(sm + Ly::kStart);
+        int r = at.x, h = at.y, rt = at.z, y = at.w;
+        long long left = x1 - x0;
+        int nseg = 0;
+        bool ok = true;
+        Req q = dec::request<kRows, kKeys>(a, r);
+        while (left > 0) {
+          if (rt >= q.nrt) {  // the next kv head, the next request with rows
+            rt = 0;
+            if (++h == a.Hkv) {
+              h = 0;
+              do q = dec::request<kRows, kKeys>(a, ++r); while (q.nrt == 0);  // ends: cost is left
+            }
           }
+          const int kt = tiles_of(a, q, rt);
+          const int take = static_cast<int>(min(static_cast<long long>(kt + kUnitCost - y), left));
+          const int t0 = max(0, y - kUnitCost), t1 = max(0, y + take - kUnitCost);
+          left -= take;
+          if (t1 > t0) {
+            const int si = nseg % kSegs;
+            if (nseg >= kSegs && !wait(Ly::kSegEmpty + 8 * si, nseg / kSegs - 1, kSiteSegEmpty, nseg)) {
+              ok = false;
+              break;
+            }
+            const bool begins = t0 == 0, ends = t1 == kt;
+            Seg* s = segs + si;
+            s->r = r;
+            s->h = h;
+            s->row0 = rt * kRows;
+            s->nv = min(kRows, q.n * a.g - rt * kRows);
+            s->c0 = q.c0;
+            s->n = q.n;
+            s->len = q.len;
+            s->t0 = t0;
+            s->nt = t1 - t0;
+            s->mode = begins && ends ? 0 : 1;
+            s->slot = 2 * blockIdx.x + (begins ? 1 : 0);
+            // steps: without the second half of a last tile that no row sees
+          s->base = max(1, min(2 * (t1 - t0), (seen_of(a, q, rt) - t0 * kKeys + kStepKeys - 1) / kStepKeys));
+            mbar_arrive(base + Ly::kSegFull + 8 * si);
+            if (begins && !ends) a.desc[blockIdx.x] = make_int4(r, h, rt, min(kRows, q.n * a.g - rt * kRows));
+            if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
+            ++nseg;
+          }
+          ++rt;
+          y = 0;
         }
-        const int kt = tiles_of(a, q, rt);
-        const int take = static_cast<int>(min(static_cast<long long>(kt + kUnitCost - y), left));
-        const int t0 = max(0, y - kUnitCost), t1 = max(0, y + take - kUnitCost);
-        left -= take;
-        if (t1 > t0) {
+        if (ok) {
           const int si = nseg % kSegs;
-          if (nseg >= kSegs && !wait(Ly::kSegEmpty + 8 * si, nseg / kSegs - 1, kSiteSegEmpty, nseg)) {
-            ok = false;
-            break;
+          if (nseg < kSegs || wait(Ly::kSegEmpty + 8 * si, nseg / kSegs - 1, kSiteSegEmpty, nseg)) {
+            segs[si].nt = 0;
+            mbar_arrive(base + Ly::kSegFull + 8 * si);
           }
-          const bool begins = t0 == 0, ends = t1 == kt;
-          Seg* s = segs + si;
-          s->r = r;
-          s->h = h;
-          s->row0 = rt * kRows;
-          s->nv = min(kRows, q.n * a.g - rt * kRows);
-          s->c0 = q.c0;
-          s->n = q.n;
-          s->len = q.len;
-          s->t0 = t0;
-          s->nt = t1 - t0;
-          s->mode = begins && ends ? 0 : 1;
-          s->slot = 2 * blockIdx.x + (begins ? 1 : 0);
-          s->base = 0;
-          mbar_arrive(base + Ly::kSegFull + 8 * si);
-          if (begins && !ends) a.desc[blockIdx.x] = make_int4(r, h, rt, min(kRows, q.n * a.g - rt * kRows));
-          if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
-          ++nseg;
-        }
-        ++rt;
-        y = 0;
-      }
-      if (ok) {
-        const int si = nseg % kSegs;
-        if (nseg < kSegs || wait(Ly::kSegEmpty + 8 * si, nseg / kSegs - 1, kSiteSegEmpty, nseg)) {
-          segs[si].nt = 0;
-          mbar_arrive(base + Ly::kSegFull + 8 * si);
         }
       }
     } else if (warp == 14) {
@@ -436,74 +456,92 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         for (int t = max(0, jt - 2); t < jt; ++t) dec::mbar_drain(base + Ly::kKFull + 8 * (t & 1), (t >> 1) & 1, end);
       }
       if (lane == 0 && !ok) dec::mbar_drain(base + Ly::kKFull + 8 * (jt & 1), (jt >> 1) & 1, globaltimer_ns() + 1000000);
-    } else if (warp == 12 && lane == 0) {
-      // ------------------------------------------------------- the issuer
-      constexpr uint32_t idS = idesc_e4m3_f32(kHalf, kKeys), idPV = idesc_f16_f32(kHalf, D, true);
+    } else {
+      // ------------------------------------------------ the issuers, 12 and 15
+      // One for each half: the tensor pipe queues little, so whatever one
+      // thread waits for between its products would be lost (about 120 cycles
+      // a wait).  A whole warp runs along and elects a thread to issue, so
+      // that addresses and descriptors stay in uniform registers: from a
+      // branch of one lane every product moved its descriptors there first,
+      // and a key tile took 3000 cycles to issue against 2048 to run.
+      constexpr uint32_t idS = idesc_e4m3_f32(kHalf, kStepKeys), idPV = idesc_f16_f32(kHalf, D, true);
       // operand descriptors (sw128_desc) by their low word; the high word,
       // stride 1024 and the swizzle, is the same for all
       constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);
       auto desc = [](uint32_t lo) { return (static_cast<uint64_t>(kHi) << 32) | lo; };
       auto low = [](uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); };
-      int jt = 0, cnt_a = 0, cnt_b = 0;
-      auto issue_s = [&](int x, int st) {
-        const uint32_t q = low(base + Ly::kQ + x * Ly::kQHalf, 16), k = low(base + Ly::kK + st * Ly::kKTile, 16);
-        const uint32_t d = tmem + kColS + x * kHalf;
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)  // 32 codes of each row
-            mma_ss_f8(d, desc(q + ((part * Ly::kPart) >> 4) + 2 * kk), desc(k + 2 * kk), idS, part + kk > 0 ? 1u : 0u);
-        tc_commit(base + Ly::kSFull + 8 * x);
+      const int x = __shfl_sync(0xffffffffu, warp == 15 ? 1 : 0, 0);
+      const uint32_t dS = tmem + kColS + x * kHalf, dO = tmem + kColO + x * kHalf;
+      const uint32_t q = low(base + Ly::kQ + x * Ly::kQHalf, 16);
+      auto all_wait = [&](int at, uint32_t parity, unsigned site, int item) {
+        return __all_sync(0xffffffffu, wait(at, parity, site, item)) != 0;
       };
+      int jt = 0, cnt = 0;  // the piece's first tile, this half's steps
       for (int ns = 0;; ++ns) {
         const int si = ns % kSegs;
-        if (!wait(Ly::kSegFull + 8 * si, ns / kSegs, kSiteSegFull, ns)) break;
-        const int nt = segs[si].nt;
-        const int halves = segs[si].nv > kHalf ? 2 : 1;
+        if (!all_wait(Ly::kSegFull + 8 * si, ns / kSegs, kSiteSegFull, ns)) break;
+        const int nt = __shfl_sync(0xffffffffu, segs[si].nt, 0), steps = __shfl_sync(0xffffffffu, segs[si].base, 0);
+        const bool mine = __shfl_sync(0xffffffffu, segs[si].nv, 0) > x * kHalf;  // this half has rows
         if (nt == 0) break;
-        bool ok = wait(Ly::kQFull, ns, kSiteQFull, ns);
-        // j = -1: the first scores only
+        bool ok = all_wait(Ly::kQFull, ns, kSiteQFull, ns);
+        // i < 0: scores only
 #pragma unroll 1
-        for (int j = -1; ok && j < nt; ++j) {
-          const int st = (jt - 1) & 1, nx = jt & 1;  // stages of tile j and of the next, jt
-          const bool more = j + 1 < nt;
-          if (more) ok = wait(Ly::kKFull + 8 * nx, jt >> 1, kSiteKFull, jt);
-          if (ok && j >= 0) ok = wait(Ly::kVFull + 8 * st, (jt - 1) >> 1, kSiteVFull, jt);
-#pragma unroll 1
-          for (int x = 0; ok && x < halves; ++x) {
-            if (j >= 0) {
-              ok = wait(Ly::kPFull + 8 * x, x ? cnt_b++ : cnt_a++, kSiteP, jt);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t v = low(base + Ly::kV + st * Ly::kVTile, 16384);
-              const uint32_t d = tmem + kColO + x * kHalf, p = tmem + kColS + x * kHalf;
-#pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_ts(d, p + 8 * kk, desc(v + static_cast<uint32_t>(kk * 128)), idPV, j == 0 && kk == 0 ? 0u : 1u);
-              tc_commit(base + Ly::kPvDone + 8 * x);
-            }
-            if (more) {
-              tc_fence_after();
-              issue_s(x, nx);
-            }
-          }
+        for (int i = -2; i < steps; ++i) {
+          const int n = i + 2, tv = jt + (i >> 1), tk = jt + (n >> 1);  // tiles of step i and of step n
+          const int buf = cnt & 1;                                      // of both
+          if (ok && n < steps && (n & 1) == 0) ok = all_wait(Ly::kKFull + 8 * (tk & 1), tk >> 1, kSiteKFull, tk);
+          if (ok && i >= 0 && (i & 1) == 0) ok = all_wait(Ly::kVFull + 8 * (tv & 1), tv >> 1, kSiteVFull, tv);
+          if (ok && i >= 0 && mine) ok = all_wait(Ly::kPFull + 8 * (2 * x + buf), (cnt >> 1) - 1, kSiteP, tv);
           if (!ok) break;
-          if (j >= 0) tc_commit(base + Ly::kVEmpty + 8 * st);
-          if (more) {
-            tc_commit(base + Ly::kKEmpty + 8 * nx);
-            if (j + 2 == nt) tc_commit(base + Ly::kQEmpty);  // the last read of Q
-            ++jt;
+          tc_fence_after();
+          if (i >= 0) {
+            const uint32_t v = low(base + Ly::kV + (tv & 1) * Ly::kVTile + (i & 1) * (kStepKeys * 128), 16384);
+            const uint32_t first = i == 0 ? 0u : 1u, p = dS + buf * kStepKeys;
+            if (elect_one()) {
+              if (mine) {
+#pragma unroll
+                for (int kk = 0; kk < kStepKeys / 16; ++kk)
+                  mma_ts(dO, p + 8 * kk, desc(v + static_cast<uint32_t>(kk * 128)), idPV, kk == 0 ? first : 1u);
+                tc_commit(base + Ly::kPvDone + 8 * x);
+              }
+              if ((i & 1) == 1 || i + 1 == steps) tc_commit(base + Ly::kVEmpty + 8 * (tv & 1));
+            }
+            __syncwarp();
           }
+          if (n < steps) {
+            const uint32_t k = low(base + Ly::kK + (tk & 1) * Ly::kKTile + (n & 1) * (kStepKeys * 128), 16);
+            const uint32_t d = dS + buf * kStepKeys;
+            if (elect_one()) {
+              if (mine) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                  for (int kk = 0; kk < D / 32; ++kk)  // 32 codes of each row
+                    mma_ss_f8(d, desc(q + ((part * Ly::kPart) >> 4) + 2 * kk), desc(k + 2 * kk), idS,
+                              part + kk > 0 ? 1u : 0u);
+                tc_commit(base + Ly::kSFull + 8 * (2 * x + buf));
+              }
+              if ((n & 1) == 1 || n + 1 == steps) tc_commit(base + Ly::kKEmpty + 8 * (tk & 1));
+              if (n + 1 == steps) tc_commit(base + Ly::kQEmpty);  // the last read of Q
+            }
+            __syncwarp();
+          }
+          if (mine) ++cnt;
         }
         if (!ok) break;
-        mbar_arrive(base + Ly::kSegEmpty + 8 * si);
+        if (mine) cnt -= 2;
+        jt += nt;
+        if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
       }
       // nothing that reads shared or tensor memory outlives the CTA
-      tc_commit(base + Ly::kFin);
-      dec::mbar_drain(base + Ly::kFin, 0, globaltimer_ns() + a.timeout_ns);
+      if (elect_one()) {
+        tc_commit(base + Ly::kFin + 8 * x);
+        dec::mbar_drain(base + Ly::kFin + 8 * x, 0, globaltimer_ns() + a.timeout_ns);
+      }
+      __syncwarp();
     }
   } else if (warp >= 8) {
-    reg_dec<80>();
+    reg_dec<96>();
     // ----------------------------------------- V's codes to f16, Q in parts
     // A thread turns 16 codes of a row into two 16-byte pieces, of rows kStep
     // apart.  Eight lanes read 128 bytes in a row.  Their pieces go to the
@@ -623,16 +661,16 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
     }
     copies_done();  // none outlives the CTA, also where a wait gave up
   } else {
-    reg_inc<184>();
+    reg_inc<168>();
     // ------------------------------------------------ softmax and epilogue
     const int x = warp >> 2;  // half
     const int row = tid;      // of the unit: 128 x + TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + kColS + x * kHalf, tO = tmem + lane_off + kColO + x * kHalf;
-    constexpr int kGroups = kKeys / GROUP;          // groups of a tile
-    constexpr int kIn = GROUP == 16 ? 2 : 1;        // of a 32-key chunk
-    constexpr int kStepG = 8 / kGroups;             // a group's place among the scales
-    int cnt = 0, jt = 0;  // tiles of this half, tiles of the CTA
+    constexpr int G = GROUP < kStepKeys ? GROUP : kStepKeys;
+    constexpr int kGroups = kStepKeys / G;          // groups of a step
+    constexpr int kStepG = 4 / kGroups;             // a group's place among the scales
+    int cnt = 0, jt = 0;  // steps of this half, the piece's first tile
     for (int ns = 0;; ++ns) {
       const int si = ns % kSegs;
       bool ok = wait(Ly::kSegFull + 8 * si, ns / kSegs, kSiteSegFull, ns);
@@ -657,73 +695,73 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       const int all = __reduce_min_sync(0xffffffffu, lim);
       float m = kInit, e = 0.f, l = 0.f;  // e: the second reference less the first
       bool far = false;
-      for (int j = 0; j < nt; ++j, ++jt, ++cnt) {
+      const int steps = s.base;
+      for (int i = 0; i < steps; ++i, ++cnt) {
+        const int tile = jt + (i >> 1), buf = 2 * x + (cnt & 1);
         // (the scales of a tile are never replaced before its scores are read)
-        ok = wait(Ly::kSFull + 8 * x, cnt, kSiteS, jt) && wait(Ly::kScales + 8 * (jt & 3), jt >> 2, kSiteScales, jt);
+        ok = wait(Ly::kSFull + 8 * buf, cnt >> 1, kSiteS, tile) &&
+             wait(Ly::kScales + 8 * (tile & 3), tile >> 2, kSiteScales, tile);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        uint32_t v[4][32];
-        float mx[4];  // of each 32 keys
-        // scales of 16-key group i
-        const uint32_t tile_scales = base + Ly::kKs + (jt & 3) * 32;
-        auto ks_at = [&](int i) { return lds_f32(tile_scales + 4 * i); };
-        auto lv_at = [&](int i) { return lds_f32(tile_scales + (Ly::kLv - Ly::kKs) + 4 * i); };
-        const int key0 = (s.t0 + j) * kKeys;
-        bool careful = key0 + kKeys > all;
-        // read twice, so that they are not held beside the scores
-        auto k_of = [&](int g) { return fmaxf(c * ks_at(g * kStepG), kTiny); };
-        auto lv_of = [&](int g) { return lv_at(g * kStepG); };
+        const uint32_t tSb = tS + (cnt & 1) * kStepKeys;
+        uint32_t v[2][32];
+        float mx[2];  // of each 32 keys
+        // scales of 16-key group y
+        const uint32_t scales = base + Ly::kKs + (tile & 3) * 32 + (i & 1) * 16;
+        auto ks_at = [&](int y) { return lds_f32(scales + 4 * y); };
+        auto lv_at = [&](int y) { return lds_f32(scales + (Ly::kLv - Ly::kKs) + 4 * y); };
+        const int key0 = s.t0 * kKeys + i * kStepKeys;
+        bool careful = key0 + kStepKeys > all;
+        float fk[kGroups], lv[kGroups];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) careful = careful | (ks_at(g * kStepG) < 0.f);
-        if constexpr (GROUP >= 32) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ldred_max32(tS + 32 * q, v[q], mx[q]);
+        for (int g = 0; g < kGroups; ++g) {
+          const float ks = ks_at(g * kStepG);
+          careful = careful | (ks < 0.f);
+          fk[g] = fmaxf(c * ks, kTiny);
+          lv[g] = lv_at(g * kStepG);
+        }
+        if constexpr (G >= 32) {
+          tmem_ldred_max32(tSb, v[0], mx[0]);
+          tmem_ldred_max32(tSb + 32, v[1], mx[1]);
           tmem_ldred_wait32(v[0], mx[0]);
           tmem_ldred_dep32(v[1], mx[1]);
-          tmem_ldred_dep32(v[2], mx[2]);
-          tmem_ldred_dep32(v[3], mx[3]);
         } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, v[q]);
+          tmem_ld32(tSb, v[0]);
+          tmem_ld32(tSb + 32, v[1]);
           tmem_ld_wait32(v[0]);
           tmem_ld_dep32(v[1]);
-          tmem_ld_dep32(v[2]);
-          tmem_ld_dep32(v[3]);
         }
         if (careful) {
           constexpr uint32_t kNegInf = 0xff800000u;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
+          for (int y = 0; y < 4; ++y) {
             // keys of the group below this are visible
-            const int end = ks_at(q) < 0.f ? 0 : lim - (key0 + 16 * q);
+            const int end = ks_at(y) < 0.f ? 0 : lim - (key0 + 16 * y);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (e >= end) v[q >> 1][(q & 1) * 16 + e] = kNegInf;
+            for (int z = 0; z < 16; ++z)
+              if (z >= end) v[y >> 1][(y & 1) * 16 + z] = kNegInf;
           }
         }
-        // the tile's references, eb relative to mb
+        // the step's references, eb relative to mb
         float mb = kInit, eb = -INFINITY;
         auto see = [&](int g, float top) {
-          const float t = top * k_of(g), m1 = fmaxf(mb, t);
-          eb = fmaxf(eb + (mb - m1), t - m1 + lv_of(g));
+          const float t = top * fk[g], m1 = fmaxf(mb, t);
+          eb = fmaxf(eb + (mb - m1), t - m1 + lv[g]);
           mb = m1;
         };
-        if constexpr (GROUP == 16) {
+        if constexpr (G == 16) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) see(g, max32(v[g >> 1], (g & 1) * 16, (g & 1) * 16 + 16));
+          for (int g = 0; g < 4; ++g) see(g, max32(v[g >> 1], (g & 1) * 16, (g & 1) * 16 + 16));
         } else {
           if (careful) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) mx[q] = max32(v[q], 0, 32);
+            mx[0] = max32(v[0], 0, 32);
+            mx[1] = max32(v[1], 0, 32);
           }
-          if constexpr (GROUP == 32) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) see(g, mx[g]);
-          } else if constexpr (GROUP == 64) {
-            see(0, fmaxf(mx[0], mx[1]));
-            see(1, fmaxf(mx[2], mx[3]));
+          if constexpr (G == 32) {
+            see(0, mx[0]);
+            see(1, mx[1]);
           } else {
-            see(0, fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]));
+            see(0, fmaxf(mx[0], mx[1]));
           }
         }
         const bool bump = mb > m + kLazy || eb + (mb - m) > e + kLazy;
@@ -735,49 +773,31 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           m = m1;
           e = e1;
         }
-        if (__any_sync(0xffffffffu, bump)) {
-          // The exponent is one fused product and sum, whose product is not
-          // rounded as m's was: above 2^17 (log2 units) that difference
-          // counts, and the scores are reduced in two steps instead.
-          far = __any_sync(0xffffffffu, fabsf(m) > 131072.f && m != kInit);
-          if (j > 0) {
-            // (where this wait gives up the loop ends below: leaving it here
-            // costs registers)
-            ok = __all_sync(0xffffffffu, wait(Ly::kPvDone + 8 * x, cnt - 1, kSitePV, jt));
-            tc_fence_after();
-            // a few columns at a time, beside the scores in registers
-#pragma unroll 1
-            for (int q = 0; q < D / 8; ++q) {
-              uint32_t o[8];
-              tmem_ld8(tO + 8 * q, o);
-              tmem_ld_wait8(o);
-#pragma unroll
-              for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * up);
-              tmem_st8(tO + 8 * q, o);
-            }
-          }
-        }
+        const bool moved = __any_sync(0xffffffffu, bump);
+        // The exponent is one fused product and sum, whose product is not
+        // rounded as m's was: above 2^17 (log2 units) that difference counts,
+        // and the scores are reduced in two steps instead.
+        if (moved) far = __any_sync(0xffffffffu, fabsf(m) > 131072.f && m != kInit);
         if (far) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              v[q][i] = __float_as_uint(
-                  __fsub_rn(__fmul_rn(__uint_as_float(v[q][i]), k_of((32 * q + i) / GROUP)), m));
+          for (int y = 0; y < 64; ++y) {
+            uint32_t& w = v[y >> 5][y & 31];
+            w = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(w), fk[y / G]), m));
+          }
         }
         float sums = 0.f;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           // 2^up_g: what the weights of this group carry beside 2^(s - m).
           // Below 2^-60 they are 0 in f16 whatever it is.
-          const float up_g = fminf(fmaxf(lv_of(g) + kBias - e, -60.f), 120.f);
-          const float fk = far ? 1.f : k_of(g), nm = far ? up_g : up_g - m;
-          const uint64_t f2 = f2_pack(fk, fk), n2 = f2_pack(nm, nm);
+          const float up_g = fminf(fmaxf(lv[g] + kBias - e, -60.f), 120.f);
+          const float f = far ? 1.f : fk[g], nm = far ? up_g : up_g - m;
+          const uint64_t f2 = f2_pack(f, f), n2 = f2_pack(nm, nm);
           uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-          for (int q = 0; q < (GROUP + 31) / 32; ++q) {
-            const int ch = g * GROUP / 32 + q, lo = (g * GROUP) % 32;
-            constexpr int n = GROUP < 32 ? GROUP : 32;
+          for (int z = 0; z < (G + 31) / 32; ++z) {
+            const int ch = g * G / 32 + z, lo = (g * G) % 32;
+            constexpr int n = G < 32 ? G : 32;
             uint32_t w[n / 2];
 #pragma unroll
             for (int y = 0; y < n; y += 2) {
@@ -789,20 +809,34 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
               sum[(y >> 1) & 1] = f2_add(sum[(y >> 1) & 1], f2_pack(a0, a1));
               w[y >> 1] = dec::pack_f16(a0, a1);
             }
-            if constexpr (GROUP < 32) tmem_st8(tS + 8 * g, w);
-            else tmem_st16(tS + 16 * ch, w);
+            if constexpr (G < 32) tmem_st8(tSb + 8 * g, w);
+            else tmem_st16(tSb + 16 * ch, w);
           }
           float s0, s1;
           f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
           sums = fmaf(s0 + s1, ex2(-up_g), sums);
         }
         l += sums;
+        if (moved && i > 0) {  // O to the new reference, once it has every weight before
+          ok = __all_sync(0xffffffffu, wait(Ly::kPvDone + 8 * x, cnt - 1, kSitePV, tile));
+          tc_fence_after();
+#pragma unroll 1
+          for (int z = 0; z < D / 32; ++z) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * z, o);
+            tmem_ld_wait32(o);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * up);
+            tmem_st32(tO + 32 * z, o);
+          }
+        }
         tmem_st_wait();
         if (!ok) break;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(base + Ly::kPFull + 8 * x);
+        if (lane == 0) mbar_arrive(base + Ly::kPFull + 8 * buf);
       }
+      jt += nt;
       if (!__all_sync(0xffffffffu, ok)) break;
       ok = wait(Ly::kPvDone + 8 * x, cnt - 1, kSitePV, jt);
       if (!__all_sync(0xffffffffu, ok)) break;
