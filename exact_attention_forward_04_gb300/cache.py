@@ -31,16 +31,27 @@ class CacheE4M3(NamedTuple):
     v_scale: torch.Tensor
 
 
-def _lib():
+_empty = torch.empty
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+_fn = None  # the library's entry points, once it is loaded
+
+
+def _load():
+    global _fn
     from . import load_library
-    return load_library()
+    lib = load_library()
+    _fn = (lib.fa_cache_slots, lib.fa_cache_append_e4m3, lib.fa_cache_fwd_e4m3, lib.fa_cache_fwd_e4m3_workspace_size)
+    return _fn
 
 
-def _done(status, where):
-    if status != 0:
-        from . import _raise
-        _raise(status, where)
+def _failed(status, where):
+    from . import _raise
+    _raise(status, where)
 
+
+# A call on a few rows takes the GPU 3 to 15 us, so its checks are one
+# expression per tensor; only where that fails is the reason looked for.
 
 def _check(name, t, dtype, shape, device):
     """A contiguous CUDA tensor of this type; ``shape`` has None where any size will do."""
@@ -50,7 +61,7 @@ def _check(name, t, dtype, shape, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     s = t.shape
     if len(s) != len(shape) or any(b is not None and a != b for a, b in zip(s, shape)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(s)}")
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(s)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if t.device != device:
@@ -58,41 +69,59 @@ def _check(name, t, dtype, shape, device):
 
 
 def _check_rows(name, t, heads, d, device):
-    """bf16 [T, heads, d], heads and d contiguous, any stride between tokens."""
+    """bf16 [T, heads, d], heads and d contiguous, any stride between tokens.
+    Returns (T, heads, stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != _BF16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
-        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {d}], got {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+    s = t.shape
+    if len(s) != 3 or (heads is not None and s[1] != heads) or s[2] != d:
+        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {d}], got {tuple(s)}")
+    n, h, _ = s
+    st = t.stride()
+    if n and h and (st[2] != 1 or (h > 1 and st[1] != d)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return n, h, st[0] if n > 1 else h * d
 
 
 def _check_cache(cache):
-    k8 = cache.k8
+    k8, v8, ks, vs = cache.k8, cache.v8, cache.k_scale, cache.v_scale
     if not isinstance(k8, torch.Tensor) or k8.dim() != 4:
         raise ValueError("cache.k8 must be a uint8 [blocks, heads, block_tokens, d] tensor")
     if not k8.is_cuda:
         raise ValueError("the cache must be CUDA tensors")
     dev, shape = k8.device, k8.shape
-    _check("cache.k8", k8, _U8, shape, dev)
-    _check("cache.v8", cache.v8, _U8, shape, dev)
-    _check("cache.k_scale", cache.k_scale, _F32, shape[:2], dev)
-    _check("cache.v_scale", cache.v_scale, _F32, shape[:2], dev)
+    two = shape[:2]
+    if not (k8.dtype is _U8 and k8.is_contiguous() and isinstance(v8, torch.Tensor) and v8.dtype is _U8
+            and v8.shape == shape and v8.is_contiguous() and v8.device == dev and isinstance(ks, torch.Tensor)
+            and ks.dtype is _F32 and ks.shape == two and ks.is_contiguous() and ks.device == dev
+            and isinstance(vs, torch.Tensor) and vs.dtype is _F32 and vs.shape == two and vs.is_contiguous()
+            and vs.device == dev):
+        _check("cache.k8", k8, _U8, shape, dev)
+        _check("cache.v8", v8, _U8, shape, dev)
+        _check("cache.k_scale", ks, _F32, two, dev)
+        _check("cache.v_scale", vs, _F32, two, dev)
     return dev, shape
+
+
+def _ints(name, t, shape, device, dtype=_I32):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.device == device):
+        _check(name, t, dtype, shape, device)
 
 
 def _call(device, stream, fn, *args):
     """``fn`` with ``device`` current and on ``stream`` (default: the current
     one), so that what it allocates belongs to that stream."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return fn(torch._C._cuda_getCurrentRawStream(device.index), *args)
+    index = device.index
+    if stream is None and index == _current_device():
+        return fn(_raw_stream(index), *args)
     with torch.cuda.device(device):
         if stream is None:
-            return fn(torch.cuda.current_stream().cuda_stream, *args)
+            return fn(_raw_stream(index), *args)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         if stream.device != device:
@@ -127,26 +156,30 @@ def cache_slots(block_table, seq_lens, new_lens, free_blocks, free_used, block_t
     if dev.type != "cuda":
         raise ValueError("block_table must be a CUDA tensor")
     R, M = block_table.shape
-    _check("block_table", block_table, _I32, (R, M), dev)
-    _check("seq_lens", seq_lens, _I32, (R,), dev)
-    _check("new_lens", new_lens, _I32, (R,), dev)
-    _check("free_blocks", free_blocks, _I32, (None,), dev)
-    _check("free_used", free_used, _I32, (1,), dev)
+    if block_table.dtype is not _I32 or not block_table.is_contiguous():
+        _check("block_table", block_table, _I32, (R, M), dev)
+    _ints("seq_lens", seq_lens, (R,), dev)
+    _ints("new_lens", new_lens, (R,), dev)
+    _ints("free_used", free_used, (1,), dev)
+    if not (isinstance(free_blocks, torch.Tensor) and free_blocks.dtype is _I32 and free_blocks.dim() == 1
+            and free_blocks.is_contiguous() and free_blocks.device == dev):
+        _check("free_blocks", free_blocks, _I32, (None,), dev)
     if num_tokens < 0:
         raise ValueError(f"num_tokens must not be negative, got {num_tokens}")
-    return _call(dev, stream, _slots, block_table, seq_lens, new_lens, free_blocks, free_used, R, M,
-                 int(block_tokens), int(num_tokens))
+    return _call(dev, stream, _slots, dev, block_table, seq_lens, new_lens, free_blocks, free_used, R, M, block_tokens,
+                 num_tokens)
 
 
-def _slots(handle, table, seq_lens, new_lens, free, used, R, M, P, T):
-    dev = table.device
-    cu = torch.empty(R + 1, dtype=_I32, device=dev)
-    slots = torch.empty(T, dtype=_I64, device=dev)
-    lens = torch.empty(R, dtype=_I32, device=dev)
-    gone = torch.empty(1, dtype=_I32, device=dev)
-    _done(_lib().fa_cache_slots(table.data_ptr(), seq_lens.data_ptr(), new_lens.data_ptr(), free.data_ptr(),
-                                used.data_ptr(), cu.data_ptr(), slots.data_ptr(), lens.data_ptr(), gone.data_ptr(),
-                                R, M, free.shape[0], P, T, handle), "fa_cache_slots")
+def _slots(handle, dev, table, seq_lens, new_lens, free, used, R, M, P, T):
+    cu = _empty(R + 1, dtype=_I32, device=dev)
+    slots = _empty(T, dtype=_I64, device=dev)
+    lens = _empty(R, dtype=_I32, device=dev)
+    gone = _empty(1, dtype=_I32, device=dev)
+    st = (_fn or _load())[0](
+        table.data_ptr(), seq_lens.data_ptr(), new_lens.data_ptr(), free.data_ptr(), used.data_ptr(), cu.data_ptr(),
+        slots.data_ptr(), lens.data_ptr(), gone.data_ptr(), R, M, free.shape[0], P, T, handle)
+    if st:
+        _failed(st, "fa_cache_slots")
     return cu, slots, lens, gone
 
 
@@ -155,27 +188,27 @@ def cache_append_e4m3(k, v, cache, slot_map, stream=None):
     into the cache at the slots of ``slot_map`` (int64 [T], -1: skip), each
     run of rows in a block with the block's scale, which grows to fit."""
     dev, (blocks, H, P, d) = _check_cache(cache)
-    _check_rows("k", k, H, d, dev)
-    _check_rows("v", v, H, d, dev)
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError(f"k has {T} rows, v {v.shape[0]}")
-    _check("slot_map", slot_map, _I64, (T,), dev)
+    T, _, k_stride = _check_rows("k", k, H, d, dev)
+    Tv, _, v_stride = _check_rows("v", v, H, d, dev)
+    if Tv != T:
+        raise ValueError(f"k has {T} rows, v {Tv}")
+    _ints("slot_map", slot_map, (T,), dev, _I64)
     if T:
-        _call(dev, stream, _append, k, v, cache, slot_map, T, H, d, blocks, P)
+        _call(dev, stream, _append, k, v, k_stride, v_stride, cache, slot_map, T, H, d, blocks, P)
 
 
-def _append(handle, k, v, cache, slot_map, T, H, d, blocks, P):
-    _done(_lib().fa_cache_append_e4m3(
-        k.data_ptr(), v.data_ptr(), k.stride(0) if T > 1 else H * d, v.stride(0) if T > 1 else H * d,
-        cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
-        slot_map.data_ptr(), T, H, d, blocks, P, handle), "fa_cache_append_e4m3")
+def _append(handle, k, v, k_stride, v_stride, cache, slot_map, T, H, d, blocks, P):
+    st = (_fn or _load())[1](
+        k.data_ptr(), v.data_ptr(), k_stride, v_stride, cache.k8.data_ptr(), cache.v8.data_ptr(),
+        cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), slot_map.data_ptr(), T, H, d, blocks, P, handle)
+    if st:
+        _failed(st, "fa_cache_append_e4m3")
 
 
 def cache_forward_workspace_size(R, T, heads, heads_kv, d) -> int:
     """Workspace bytes of ``cache_forward_e4m3`` on the current device for R
     requests and T query rows (0: none needed, or sizes it does not take)."""
-    return int(_lib().fa_cache_fwd_e4m3_workspace_size(int(R), int(T), int(heads), int(heads_kv), int(d)))
+    return int((_fn or _load())[3](int(R), int(T), int(heads), int(heads_kv), int(d)))
 
 
 def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal=True, workspace=None, stream=None):
@@ -189,31 +222,33 @@ def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal
     ``workspace`` (a CUDA tensor of cache_forward_workspace_size bytes) may be
     passed to reuse memory; calls that may overlap need one each."""
     dev, (blocks, H, P, d) = _check_cache(cache)
-    _check_rows("q", q, None, d, dev)
-    T, Hq, _ = q.shape
+    T, Hq, q_stride = _check_rows("q", q, None, d, dev)
     if Hq == 0 or H == 0 or Hq % H:
         raise ValueError(f"{Hq} query heads do not share {H} kv heads evenly")
-    _check("block_table", block_table, _I32, (None, None), dev)
+    if not (isinstance(block_table, torch.Tensor) and block_table.dtype is _I32 and block_table.dim() == 2
+            and block_table.is_contiguous() and block_table.device == dev):
+        _check("block_table", block_table, _I32, (None, None), dev)
     R, M = block_table.shape
-    _check("seq_lens", seq_lens, _I32, (R,), dev)
-    _check("cu_q", cu_q, _I32, (R + 1,), dev)
+    _ints("seq_lens", seq_lens, (R,), dev)
+    _ints("cu_q", cu_q, (R + 1,), dev)
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    return _call(dev, stream, _forward, q, cache, block_table, seq_lens, cu_q, float(scale), int(bool(causal)),
+    return _call(dev, stream, _forward, dev, q, q_stride, cache, block_table, seq_lens, cu_q, float(scale), bool(causal),
                  workspace, R, T, Hq, H, d, blocks, P, M)
 
 
-def _forward(handle, q, cache, table, seq_lens, cu_q, scale, causal, ws, R, T, Hq, H, d, blocks, P, M):
-    dev = q.device
-    o = torch.empty((T, Hq, d), dtype=_BF16, device=dev)
-    lse = torch.empty((T, Hq), dtype=_F32, device=dev)
+def _forward(handle, dev, q, q_stride, cache, table, seq_lens, cu_q, scale, causal, ws, R, T, Hq, H, d, blocks, P, M):
+    o = _empty(T, Hq, d, dtype=_BF16, device=dev)
+    lse = _empty(T, Hq, dtype=_F32, device=dev)
+    fn = _fn or _load()
     if ws is None:
-        ws = torch.empty(_lib().fa_cache_fwd_e4m3_workspace_size(R, T, Hq, H, d), dtype=_U8, device=dev)
-    _done(_lib().fa_cache_fwd_e4m3(
-        q.data_ptr(), q.stride(0) if T > 1 else Hq * d, cache.k8.data_ptr(), cache.v8.data_ptr(),
-        cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
-        o.data_ptr(), lse.data_ptr(), R, T, Hq, H, d, blocks, P, M, scale, causal, ws.data_ptr(),
-        ws.numel() * ws.element_size(), handle), "fa_cache_fwd_e4m3")
+        ws = _empty(fn[3](R, T, Hq, H, d), dtype=_U8, device=dev)
+    st = fn[2](
+        q.data_ptr(), q_stride, cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(),
+        cache.v_scale.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), o.data_ptr(), lse.data_ptr(),
+        R, T, Hq, H, d, blocks, P, M, scale, causal, ws.data_ptr(), ws.numel() * ws.element_size(), handle)
+    if st:
+        _failed(st, "fa_cache_fwd_e4m3")
     return o, lse

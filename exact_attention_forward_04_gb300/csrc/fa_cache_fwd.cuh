@@ -13,11 +13,15 @@
 // two pieces of units, which it leaves as normalised partials with their
 // logsumexp; a second, dependent kernel merges those per row in CTA order.
 //
-// A CTA.  One producer warp walks the range: it reads block tables and
-// scales, publishes one descriptor per unit piece, and moves the tiles (32
-// keys of K and of V as codes) through a ring of TMA loads.  Eight warps take
-// the tiles in turn, each with a softmax of its own; at the end of a piece
-// they merge through shared memory.  In a warp a tile goes
+// A CTA.  One producer warp walks the range: it publishes a descriptor and the
+// query rows of each unit piece, reads block tables and scales for 32 tiles at
+// a time, of one piece or of many, and moves the tiles (32 keys of K and of V
+// as codes) through a ring of TMA loads.  A piece belongs to 1, 2, 4 or 8 of
+// the eight other warps, a few tiles each while it is short, so that short pieces
+// run side by side; its warps take the tiles in turn, each with a softmax of
+// its own, and merge through shared memory at the end.  (With all eight warps on
+// every piece a short one cost about 4500 cycles, 20 tiles' worth.)  In a warp
+// a tile goes
 //   codes -> f16 (exact) -> S = Q K^T -> P -> O += P V
 // by m16n8k16 f16 products with 16 rows per tile: each warp reads its own
 // keys straight from shared memory in the product's operand layout, which a
@@ -49,10 +53,9 @@ constexpr int kWarps = 8;                    // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);  // and the producer
 constexpr int kRows = 16;                    // query rows of a unit
 constexpr int kKeys = 32;                    // keys of a tile
-constexpr int kSegs = 4;                     // unit pieces in flight
+constexpr int kSegs = 8;                     // unit pieces in flight
 constexpr int kMeta = 64;                    // tiles whose blocks and scales are held
-constexpr int kIssue = 8;                    // lanes that issue loads
-constexpr int kUnitCost = 3;                 // a piece's fixed cost, in tiles
+constexpr int kUnitCost = 5;                 // a piece's fixed cost, in tiles
 constexpr int kMinCost = 12;                 // least cost of a CTA's range
 constexpr float kInit = -1e30f;              // references before the first key
 
@@ -66,6 +69,7 @@ struct Seg {
   int t0, nt;          // first key tile of the piece and their number (0: end)
   int mode;            // 0: the whole unit; 1: leaves a partial in slot
   int slot, base;      // base: ring position of the first tile
+  int w0, nw;          // its warps (few rows per kv head only)
 };
 
 template <int D>
@@ -73,23 +77,26 @@ struct Layout {
   static constexpr int kHalf = kKeys * D;       // codes of K (or V) of a tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kStages = 131072 / kStage;
+  static constexpr int kIssue = kStages / 2;    // lanes that issue loads
   static constexpr int kMerge = kStages * kStage;
-  static constexpr int kStats = kMerge + kWarps * kRows * D * 4;  // float4 [warps][rows]
-  static constexpr int kScales = kStats + kWarps * kRows * 16;    // float4 [meta]
-  static constexpr int kBlk = kScales + kMeta * 16;               // int2 [meta]
-  static constexpr int kSeg = kBlk + kMeta * 8;
+  static constexpr int kQ = kMerge + kWarps * 8 * D * 4;        // bf16 [segs][16][D]
+  static constexpr int kStats = kQ + kSegs * kRows * D * 2;     // float4 [warps][8]
+  static constexpr int kScales = kStats + kWarps * 8 * 16;      // float4 [meta]
+  static constexpr int kBlk = kScales + kMeta * 16;             // int4 [meta]: blocks, row in the block, valid
+  static constexpr int kSeg = kBlk + kMeta * 16;
   static constexpr int kBar = (kSeg + kSegs * static_cast<int>(sizeof(Seg)) + 15) & ~15;
   static constexpr int kFull = kBar;                    // [stages]
   static constexpr int kEmpty = kFull + 8 * kStages;    // [stages]
   static constexpr int kSegFull = kEmpty + 8 * kStages; // [segs]
   static constexpr int kSegEmpty = kSegFull + 8 * kSegs;
-  static constexpr int kMergeW = kSegEmpty + 8 * kSegs;
-  static constexpr int kMergeR = kMergeW + 8;
-  static constexpr int kAbort = kMergeR + 8;
+  static constexpr int kMergeW = kSegEmpty + 8 * kSegs; // [7] four pairs, two fours, all
+  static constexpr int kMergeR = kMergeW + 56;
+  static constexpr int kAbort = kMergeR + 56;
   static constexpr int kScan = kAbort + 8;              // long long [33]
-  static constexpr int kStart = kScan + 33 * 8;         // long long rem, int r
+  static constexpr int kStart = (kScan + 33 * 8 + 15) & ~15;  // int4
   static constexpr int kBytes = kStart + 16;
   static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
 };
 
 // Which key of a 32-key tile is column n (0..7) of score tile j (0..3), and
@@ -122,6 +129,13 @@ __device__ __forceinline__ uint32_t code_at(int t, int c) {
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t end) {
   while (!mbar_try_wait(bar, parity) && globaltimer_ns() < end) {
   }
+}
+
+// True in one thread of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -244,7 +258,7 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Ly::kAbort);
   Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
   float4* s_scales = reinterpret_cast<float4*>(sm + Ly::kScales);
-  int2* s_blk = reinterpret_cast<int2*>(sm + Ly::kBlk);
+  int4* s_blk = reinterpret_cast<int4*>(sm + Ly::kBlk);
   if (tid == 0) {
     for (int i = 0; i < Ly::kStages; ++i) {
       mbar_init(base + Ly::kFull + 8 * i, 1);
@@ -254,8 +268,11 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
       mbar_init(base + Ly::kSegFull + 8 * i, 1);
       mbar_init(base + Ly::kSegEmpty + 8 * i, kWarps);
     }
-    mbar_init(base + Ly::kMergeW, kWarps);
-    mbar_init(base + Ly::kMergeR, kWarps);
+    for (int i = 0; i < 7; ++i) {
+      const int n = i < 4 ? 2 : i < 6 ? 4 : 8;
+      mbar_init(base + Ly::kMergeW + 8 * i, n);
+      mbar_init(base + Ly::kMergeR + 8 * i, n);
+    }
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&tmK);
@@ -286,8 +303,11 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
       if (x0 < x + c) break;  // ends: this thread's requests hold x0
       x += c;
     }
-    *reinterpret_cast<long long*>(sm + Ly::kStart) = x0 - x;
-    *reinterpret_cast<int*>(sm + Ly::kStart + 8) = r;
+    // and the kv head, the row tile and the place in it
+    const Req q = request<kRows, kKeys>(a, r);
+    const int unit = q.kt + kUnitCost;
+    const int u = static_cast<int>((x0 - x) / unit), y = static_cast<int>((x0 - x) - static_cast<long long>(u) * unit);
+    *reinterpret_cast<int4*>(sm + Ly::kStart) = make_int4(r, u / q.nrt, u % q.nrt, y);
   }
   __syncthreads();
   const WaitCtx wc{abort_flag, a.err, a.timeout_ns};
@@ -296,135 +316,206 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
-    long long x = x0, rem = *reinterpret_cast<long long*>(sm + Ly::kStart);
-    int r = *reinterpret_cast<int*>(sm + Ly::kStart + 8);
+    const int4 at = *reinterpret_cast<const int4*>(sm + Ly::kStart);
+    int r = at.x, h = at.y, rt = at.z, y = at.w;  // the walk: unit, and place in its cost
+    long long left = x1 - x0;
+    // tiles that a short piece leaves a warp: as many as the ring holds for
+    // each, or one where there is too little work for all of them
+    const int per_warp = left >= 40 ? Ly::kStages / kWarps : 1;
     int pos = 0, nseg = 0;  // ring positions used, pieces published
     int issued = 0;         // positions up to this lane's last load
+    int next_warp = 0;      // first warp of the next piece
     int held = -1;          // first request of the 32 in the lanes' registers
-    Req mineq{};
+    Req mineq{}, q{};
     const int P = 1 << a.sh;
     const int boxes = P < kKeys ? 2 : 1;
-    bool ok = true;
-    while (ok && x < x1) {
-      if (held < 0 || r >= held + 32) {
-        held = r;
-        if (r + lane < a.R) mineq = request<kRows, kKeys>(a, r + lane);
-      }
-      Req q;
-      q.c0 = __shfl_sync(0xffffffffu, mineq.c0, r - held);
-      q.n = __shfl_sync(0xffffffffu, mineq.n, r - held);
-      q.len = __shfl_sync(0xffffffffu, mineq.len, r - held);
-      q.nrt = __shfl_sync(0xffffffffu, mineq.nrt, r - held);
-      q.kt = __shfl_sync(0xffffffffu, mineq.kt, r - held);
-      const long long cost = cost_of(a, q);
-      const int unit = q.kt + kUnitCost;
-      while (ok && rem < cost && x < x1) {
-        const int u = static_cast<int>(rem / unit);
-        const int y = static_cast<int>(rem - static_cast<long long>(u) * unit);
-        const int take = static_cast<int>(min(static_cast<long long>(unit - y), x1 - x));
-        const int t0 = max(0, y - kUnitCost), t1 = max(0, y + take - kUnitCost);
-        x += take;
-        rem += take;
-        if (t1 <= t0) continue;
-        const int h = u / q.nrt, rt = u - h * q.nrt;
-        // publish the piece
-        const int si = nseg % kSegs;
-        if (nseg >= kSegs)
-          ok = mbar_wait(base + Ly::kSegEmpty + 8 * si, ((nseg / kSegs) - 1) & 1, wc, kSiteSegEmpty, nseg);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        const bool begins = t0 == 0, ends = t1 == q.kt;
-        if (lane == 0) {
-          Seg s;
-          s.r = r;
-          s.h = h;
-          s.row0 = rt * kRows;
-          s.nv = min(kRows, q.n * a.g - s.row0);
-          s.c0 = q.c0;
-          s.n = q.n;
-          s.len = q.len;
-          s.t0 = t0;
-          s.nt = t1 - t0;
-          s.mode = begins && ends ? 0 : 1;
-          s.slot = 2 * blockIdx.x + (begins ? 1 : 0);
-          s.base = pos;
-          segs[si] = s;
-          mbar_arrive(base + Ly::kSegFull + 8 * si);
-          if (begins && !ends) a.desc[blockIdx.x] = make_int4(r, h, rt, s.nv);
-          if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
-        }
-        ++nseg;
-        // its tiles, 32 at a time: a lane fetches one tile's blocks and scales,
-        // then one lane issues the loads.  An entry is reused 64 tiles later:
-        // before the first of these 32 tiles was issued, all but the last
-        // ring's worth (at most 32) had been consumed.
-        const int* row = a.table + static_cast<long long>(r) * a.M;
-        for (int b = t0; ok && b < t1; b += 32) {
-          const int tile = b + lane;
-          int blk[2] = {-1, -1};
-          float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};
-          if (tile < t1) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int key = tile * kKeys + i * 16;
-              if (i < boxes && key < q.len) {
-                blk[i] = row[key >> a.sh];
-                if (blk[i] < 0 || blk[i] >= a.blocks) {
-                  record_index_error(a.index_err, kSiteFwdBlock, r);
-                  blk[i] = -1;
+    // the piece whose tiles are being fetched
+    int pr = 0, ph = 0, plen = 0, pt = 0, pend = 0;
+    bool ok = true, fresh = true;  // fresh: the request's sizes are still to be looked up
+    for (;;) {
+      // 32 tiles: what is left of the piece, and further ones
+      int fill = 0, mr = -1, mh = 0, mlen = 0, mt = 0;
+      while (fill < 32) {
+        if (pt == pend) {
+          if (left <= 0) break;
+          const int si = nseg % kSegs;
+          if (nseg >= kSegs) {
+            // a place for its descriptor; waited for only with no tile at hand,
+            // as the pieces before may need those to end
+            const uint32_t bar = base + Ly::kSegEmpty + 8 * si, ph_ = ((nseg / kSegs) - 1) & 1;
+            if (fill > 0) {
+              if (!__all_sync(0xffffffffu, mbar_test_wait(bar, ph_))) break;
+            } else {
+              ok = __all_sync(0xffffffffu, mbar_wait(bar, ph_, wc, kSiteSegEmpty, nseg));
+              if (!ok) break;
+            }
+          }
+          // the next piece: the walk goes on until one has tiles
+          int t0 = 0, t1 = 0;
+          while (left > 0) {
+            if (fresh || rt >= q.nrt) {
+              if (!fresh) {
+                rt = 0;
+                if (++h == a.Hkv) {
+                  h = 0;
+                  ++r;
+                  fresh = true;
                 }
               }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (blk[i] >= 0) {
-                const long long bh = static_cast<long long>(blk[i]) * a.Hkv + h;
-                ks[i] = a.ks[bh];
-                vs[i] = a.vs[bh];
+              if (fresh) {
+                for (;; ++r) {  // ends: cost is left
+                  if (held < 0 || r >= held + 32) {
+                    held = r;
+                    mineq = Req{};
+                    if (r + lane < a.R) mineq = request<kRows, kKeys>(a, r + lane);
+                  }
+                  q.c0 = __shfl_sync(0xffffffffu, mineq.c0, r - held);
+                  q.n = __shfl_sync(0xffffffffu, mineq.n, r - held);
+                  q.len = __shfl_sync(0xffffffffu, mineq.len, r - held);
+                  q.nrt = __shfl_sync(0xffffffffu, mineq.nrt, r - held);
+                  q.kt = __shfl_sync(0xffffffffu, mineq.kt, r - held);
+                  if (q.nrt > 0) break;
+                }
+                fresh = false;
               }
-            if (boxes == 1) { ks[1] = ks[0]; vs[1] = vs[0]; }
-            const int at = (pos + lane) % kMeta;
-            s_scales[at] = make_float4(ks[0], ks[1], vs[0], vs[1]);
-            s_blk[at] = make_int2(blk[0], boxes == 1 ? blk[0] : blk[1]);
+            }
+            const int take = static_cast<int>(min(static_cast<long long>(q.kt + kUnitCost - y), left));
+            t0 = max(0, y - kUnitCost);
+            t1 = max(0, y + take - kUnitCost);
+            left -= take;
+            y = 0;
+            if (t1 > t0) break;
+            if (left > 0) ++rt;  // a unit's cost is never cut before its first tile but at the end
+          }
+          if (t1 <= t0) break;
+          pr = r;
+          ph = h;
+          plen = q.len;
+          pt = t0;
+          pend = t1;
+          const int nv = min(kRows, q.n * a.g - rt * kRows);
+          if (lane == 0) {
+            const int nt = t1 - t0;
+            const bool begins = t0 == 0, ends = t1 == q.kt;
+            Seg* s = segs + si;
+            int nw = 1;
+            while (nw < kWarps && nw * per_warp < nt) nw *= 2;
+            const int w0 = nw == kWarps ? 0 : ((next_warp + nw - 1) / nw * nw) % kWarps;
+            next_warp = (w0 + nw) % kWarps;
+            s->r = r;
+            s->h = h;
+            s->row0 = rt * kRows;
+            s->nv = nv;
+            s->c0 = q.c0;
+            s->n = q.n;
+            s->len = q.len;
+            s->t0 = t0;
+            s->nt = nt;
+            s->mode = begins && ends ? 0 : 1;
+            s->slot = 2 * blockIdx.x + (begins ? 1 : 0);
+            s->base = pos + fill;
+            s->w0 = w0;
+            s->nw = nw;
+            mbar_arrive_expect_tx(base + Ly::kSegFull + 8 * si, static_cast<uint32_t>(nv * D * 2));
+            if (begins && !ends) a.desc[blockIdx.x] = make_int4(r, h, rt, nv);
+            if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
           }
           __syncwarp();
-          const int cnt = min(32, t1 - b);
-          if (lane < kIssue) {
-            for (int i = lane; i < cnt; i += kIssue) {
-              const int p = pos + i, st = p % Ly::kStages, round = p / Ly::kStages;
-              if (round > 0 && !mbar_wait(empty(st), (round - 1) & 1, wc, kSiteStageEmpty, p)) { ok = false; break; }
-              issued = p + 1;
-              const int2 bl = s_blk[p % kMeta];
-              const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
-              if (boxes == 1) {
-                if (bl.x >= 0) {
-                  const int y = (((b + i) * kKeys) & (P - 1)) * D / 128;
-                  const int bh = bl.x * a.Hkv + h;
-                  mbar_arrive_expect_tx(full(st), Ly::kStage);
-                  tma_load_3d(kb, &tmK, full(st), 0, y, bh);
-                  tma_load_3d(vb, &tmV, full(st), 0, y, bh);
-                } else {
-                  mbar_arrive(full(st));
-                }
-              } else {
-                const uint32_t nbox = (bl.x >= 0 ? 1u : 0u) + (bl.y >= 0 ? 1u : 0u);
-                mbar_arrive_expect_tx(full(st), nbox * Ly::kHalf);
-                if (bl.x >= 0) {
-                  tma_load_3d(kb, &tmK, full(st), 0, 0, bl.x * a.Hkv + h);
-                  tma_load_3d(vb, &tmV, full(st), 0, 0, bl.x * a.Hkv + h);
-                }
-                if (bl.y >= 0) {
-                  tma_load_3d(kb + Ly::kHalf / 2, &tmK, full(st), 0, 0, bl.y * a.Hkv + h);
-                  tma_load_3d(vb + Ly::kHalf / 2, &tmV, full(st), 0, 0, bl.y * a.Hkv + h);
-                }
-              }
+          // its query rows: those of a token lie together
+          if (lane < nv) {
+            const int rr = rt * kRows + lane, tk = rr / a.g, in = rr - tk * a.g;
+            if (lane == 0 || in == 0) {
+              const int n = min(nv - lane, a.g - in);
+              bulk_load_1d(base + Ly::kQ + (si * kRows + lane) * D * 2,
+                           a.q + (q.c0 + tk) * a.q_stride + static_cast<long long>(h * a.g + in) * D,
+                           static_cast<uint32_t>(n * D * 2), base + Ly::kSegFull + 8 * si);
             }
           }
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) pos += cnt;
+          ++nseg;
+          ++rt;
+        }
+        const int take = min(32 - fill, pend - pt);
+        if (lane >= fill && lane < fill + take) {
+          mr = pr;
+          mh = ph;
+          mlen = plen;
+          mt = pt + lane - fill;
+        }
+        fill += take;
+        pt += take;
+      }
+      if (fill == 0) break;
+      // their blocks and scales, a lane each, then the loads, by some lanes.
+      // An entry is reused 64 tiles later: before the first of these tiles was
+      // issued, all but the last ring's worth (at most 32) had been consumed.
+      if (mr >= 0) {
+        int blk[2] = {-1, -1};
+        float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};
+        const int* row = a.table + static_cast<long long>(mr) * a.M;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int key = mt * kKeys + i * 16;
+          if (i < boxes && key < mlen) {
+            blk[i] = row[key >> a.sh];
+            if (blk[i] < 0 || blk[i] >= a.blocks) {
+              record_index_error(a.index_err, kSiteFwdBlock, mr);
+              blk[i] = -1;
+            } else {
+              blk[i] = blk[i] * a.Hkv + mh;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (blk[i] >= 0) {
+            ks[i] = a.ks[blk[i]];
+            vs[i] = a.vs[blk[i]];
+          }
+        if (boxes == 1) {
+          ks[1] = ks[0];
+          vs[1] = vs[0];
+        }
+        const int e = (pos + lane) % kMeta;
+        s_scales[e] = make_float4(ks[0], ks[1], vs[0], vs[1]);
+        const int valid = boxes == 1 ? (blk[0] >= 0 ? 3 : 0) : (blk[0] >= 0 ? 1 : 0) | (blk[1] >= 0 ? 2 : 0);
+        s_blk[e] = make_int4(blk[0], blk[1], ((mt * kKeys) & (P - 1)) * D / 128, valid);
+      }
+      __syncwarp();
+      // Several lanes issue the loads, each on a tile of its own: a load of 2
+      // or 4 KB took 270 cycles from one lane, 105 from eight, and 73 from 32;
+      // half the ring at most, as the lanes go on together.
+      if (lane < Ly::kIssue) {
+        for (int i = lane; i < fill; i += Ly::kIssue) {
+          const int p = pos + i, st = p % Ly::kStages, round = p / Ly::kStages;
+          if (round > 0 && !mbar_wait(empty(st), (round - 1) & 1, wc, kSiteStageEmpty, p)) { ok = false; break; }
+          issued = p + 1;
+          const int4 bl = s_blk[p % kMeta];
+          const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
+          if (boxes == 1) {
+            if (bl.x >= 0) {
+              mbar_arrive_expect_tx(full(st), Ly::kStage);
+              tma_load_3d(kb, &tmK, full(st), 0, bl.z, bl.x);
+              tma_load_3d(vb, &tmV, full(st), 0, bl.z, bl.x);
+            } else {
+              mbar_arrive(full(st));
+            }
+          } else {
+            const uint32_t nbox = (bl.x >= 0 ? 1u : 0u) + (bl.y >= 0 ? 1u : 0u);
+            mbar_arrive_expect_tx(full(st), nbox * Ly::kHalf);
+            if (bl.x >= 0) {
+              tma_load_3d(kb, &tmK, full(st), 0, 0, bl.x);
+              tma_load_3d(vb, &tmV, full(st), 0, 0, bl.x);
+            }
+            if (bl.y >= 0) {
+              tma_load_3d(kb + Ly::kHalf / 2, &tmK, full(st), 0, 0, bl.y);
+              tma_load_3d(vb + Ly::kHalf / 2, &tmV, full(st), 0, 0, bl.y);
+            }
+          }
         }
       }
-      ++r;
-      rem = 0;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      pos += fill;
     }
     // the end, also after a wait that gave up (the others then stop by the flag)
     if (ok) {
@@ -443,6 +534,9 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
       const uint64_t end = globaltimer_ns() + a.timeout_ns;
       for (int p = max(0, issued - Ly::kStages); p < issued; ++p)
         mbar_drain(full(p % Ly::kStages), (p / Ly::kStages) & 1, end);
+      for (int n = max(0, nseg - kSegs); n < nseg; ++n)
+        if (n % kSegs != nseg % kSegs || !ok)  // that one is the end's now
+          mbar_drain(base + Ly::kSegFull + 8 * (n % kSegs), (n / kSegs) & 1, end);
     }
     return;
   }
@@ -453,16 +547,28 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
   constexpr int kN = D / 8;    // output tiles of 8 columns
   float* merge = reinterpret_cast<float*>(sm + Ly::kMerge);
   float4* stats = reinterpret_cast<float4*>(sm + Ly::kStats);
+  int merges2 = 0, merges4 = 0, merges8 = 0;  // of this warp's pair, four and eight
+  // Where output row `row` of piece s goes, as a row of [T][Hq].
+  auto out_row = [&](const Seg& s, int row) {
+    const int rr = s.row0 + row, tk = rr / a.g;
+    return static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
+  };
   for (int ns = 0;; ++ns) {
     const int si = ns % kSegs;
     bool ok = mbar_wait(base + Ly::kSegFull + 8 * si, (ns / kSegs) & 1, wc, kSiteSegFull, ns);
     if (!__all_sync(0xffffffffu, ok)) return;
     const Seg& s = segs[si];
     if (s.nt == 0) return;
+    const int w0 = s.w0, nw = s.nw;
+    if (warp < w0 || warp >= w0 + nw) {  // not this warp's
+      if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
+      continue;
+    }
 
     float o[kN][4];
     float m[2] = {kInit, kInit}, E[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // E: the second reference less m
-    if (warp < s.nt) {
+    const bool busy = warp - w0 < s.nt;
+    if (busy) {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
 #pragma unroll
@@ -474,16 +580,15 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
       int lim[2];     // keys visible to it
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int row = s.row0 + g4 + 8 * y;
         const bool real = g4 + 8 * y < s.nv;
-        const int tk = row / a.g;
-        const __nv_bfloat16* src =
-            a.q + (s.c0 + tk) * a.q_stride + static_cast<long long>(s.h * a.g + row - tk * a.g) * D;
+        const int tk = (s.row0 + g4 + 8 * y) / a.g;
+        const uint32_t src = base + Ly::kQ + (si * kRows + g4 + 8 * y) * D * 2 + t4 * 32;
         uint4 w[D / 32];  // 2 vectors of 8 per chunk
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-          w[e] = real ? __ldg(reinterpret_cast<const uint4*>(src + (t4 + 4 * (e >> 1)) * 16 + (e & 1) * 8))
-                      : make_uint4(0u, 0u, 0u, 0u);
+        for (int e = 0; e < D / 32; ++e) {
+          w[e] = lds128(src + (e >> 1) * 128 + (e & 1) * 16);
+          if (!real) w[e] = make_uint4(0u, 0u, 0u, 0u);
+        }
         uint32_t am = 0;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) am = amax2(w[e].x, amax2(w[e].y, amax2(w[e].z, amax2(w[e].w, am))));
@@ -504,14 +609,13 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
       // keys visible to every real row of the tile
       const int all = a.causal ? min(s.len, s.len - s.n + s.row0 / a.g + 1) : s.len;
 
-      for (int k = warp; k < s.nt; k += kWarps) {
+      for (int k = warp - w0; k < s.nt; k += nw) {
         const int p = s.base + k, st = p % Ly::kStages;
         ok = mbar_wait(full(st), (p / Ly::kStages) & 1, wc, kSiteStageFull, p);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
         const float4 sc = s_scales[p % kMeta];
-        const int2 bl = s_blk[p % kMeta];
-        const int valid = (bl.x >= 0 ? 1 : 0) | (bl.y >= 0 ? 2 : 0);
+        const int valid = s_blk[p % kMeta].w;  // bit i: the tile's 16-key group i has a block
         const int key0 = (s.t0 + k) * kKeys;
         const bool careful = key0 + kKeys > all || valid != 3;
         // scores in log2 units
@@ -651,86 +755,131 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
       }
     }
 
-    // merge of the warps.  The buffer is free once every warp has read the
-    // piece before.
-    if (ns > 0) {
-      ok = mbar_wait(base + Ly::kMergeR, (ns - 1) & 1, wc, kSiteMergeR, ns);
-      if (!__all_sync(0xffffffffu, ok)) return;
-    }
+
     // Lane (g4, t4) holds columns (2 t4 + e) D/8 + i of rows g4 (+ 8) in
-    // o[i][e (+ 2)]; 16-byte chunks are XORed so that the eight lanes of a
-    // store fall on different banks.
-    auto chunk_at = [](int row, int ch) {
-      const int sw = D == 128 ? ((ch >> 3) & 3) | ((row & 1) << 2) : ((ch >> 3) & 1) | ((row & 1) << 1);
-      return ch ^ sw;
-    };
-    if (warp < s.nt) {
-      float* mw = merge + warp * kRows * D;
+    // o[i][e (+ 2)].
+    if (nw == 1) {  // nothing to merge
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int row = g4 + 8 * y;
         if (row < s.nv) {
+          // a row without a visible key: O = 0, L = -inf
+          const float fin = l[y] == 0.f ? 0.f : ex2(E[y] - 14.f) / l[y];
+          const float lg = l[y] == 0.f ? -INFINITY : m[y] + log2f(l[y]);
+          const long long to = s.mode == 0 ? out_row(s, row) : static_cast<long long>(s.slot) * kRows + row;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+          for (int e = 0; e < 2; ++e) {
+            const long long col = to * D + (2 * t4 + e) * (D / 8);
 #pragma unroll
-            for (int i = 0; i < kN; i += 4) {
-              const int ch = ((2 * t4 + e) * (D / 8) + i) >> 2;
-              *reinterpret_cast<float4*>(mw + row * D + 4 * chunk_at(row, ch)) =
-                  make_float4(o[i][2 * y + e], o[i + 1][2 * y + e], o[i + 2][2 * y + e], o[i + 3][2 * y + e]);
+            for (int i = 0; i < kN; i += 8) {
+              float f[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z) f[z] = o[i + z][2 * y + e] * fin;
+              if (s.mode == 0) {
+                *reinterpret_cast<uint4*>(a.o + col + i) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                                      pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+              } else {
+                *reinterpret_cast<float4*>(a.part_o + col + i) = make_float4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<float4*>(a.part_o + col + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+              }
             }
-          if (t4 == 0) stats[warp * kRows + row] = make_float4(m[y], l[y], E[y], 0.f);
+          }
+          if (t4 == 0) {
+            if (s.mode == 0) a.lse[to] = lg * 0.6931471805599453f;
+            else a.part_l[to] = lg;
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
+      continue;
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(base + Ly::kMergeW);
-    ok = mbar_wait(base + Ly::kMergeW, ns & 1, wc, kSiteMergeW, ns);
-    if (!__all_sync(0xffffffffu, ok)) return;
-    const int nw = min(kWarps, s.nt);
-    for (int it = tid; it < s.nv * (D / 4); it += 32 * kWarps) {
-      const int row = it / (D / 4), ch = it % (D / 4);
-      float M = kInit, Em = -INFINITY;
-      for (int w = 0; w < nw; ++w) M = fmaxf(M, stats[w * kRows + row].x);
-      for (int w = 0; w < nw; ++w) {
-        const float4 q = stats[w * kRows + row];
-        Em = fmaxf(Em, q.z + (q.x - M));
+
+    // merge of its warps, eight rows at a time
+    const int bar = 8 * (nw == 2 ? w0 >> 1 : nw == 4 ? 4 + (w0 >> 2) : 6);
+    const int active = min(nw, s.nt);
+    // 16-byte chunks are XORed so that the eight lanes of a store fall on
+    // different banks
+    auto chunk_at = [](int row, int ch) {
+      const int sw = D == 128 ? ((ch >> 3) & 3) | ((row & 1) << 2) : ((ch >> 3) & 1) | ((row & 1) << 1);
+      return ch ^ sw;
+    };
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      if (8 * y >= s.nv) break;
+      const int use = nw == 2 ? merges2++ : nw == 4 ? merges4++ : merges8++;
+      // the buffer is free once every warp has read the merge before
+      if (use > 0) {
+        ok = mbar_wait(base + Ly::kMergeR + bar, (use - 1) & 1, wc, kSiteMergeR, ns);
+        if (!__all_sync(0xffffffffu, ok)) return;
       }
-      float L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < nw; ++w) {
-        const float4 q = stats[w * kRows + row];
-        const float f = ex2(q.z + (q.x - M) - Em);
-        const float4 v = *reinterpret_cast<const float4*>(merge + (w * kRows + row) * D + 4 * chunk_at(row, ch));
-        L += q.y * ex2(q.x - M);
-        acc.x += f * v.x;
-        acc.y += f * v.y;
-        acc.z += f * v.z;
-        acc.w += f * v.w;
+      if (busy && g4 + 8 * y < s.nv) {
+        float* mw = merge + (warp * 8 + g4) * D;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < kN; i += 4) {
+            const int ch = ((2 * t4 + e) * (D / 8) + i) >> 2;
+            *reinterpret_cast<float4*>(mw + 4 * chunk_at(g4, ch)) =
+                make_float4(o[i][2 * y + e], o[i + 1][2 * y + e], o[i + 2][2 * y + e], o[i + 3][2 * y + e]);
+          }
+        if (t4 == 0) stats[warp * 8 + g4] = make_float4(m[y], l[y], E[y], 0.f);
       }
-      // a row without a visible key: O = 0, L = -inf
-      const float fin = L == 0.f ? 0.f : ex2(Em - 14.f) / L;
-      const float lg = L == 0.f ? -INFINITY : M + log2f(L);
-      acc.x *= fin;
-      acc.y *= fin;
-      acc.z *= fin;
-      acc.w *= fin;
-      if (s.mode == 0) {
-        const int rr = s.row0 + row, tk = rr / a.g;
-        const long long at = static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
-        *reinterpret_cast<uint2*>(a.o + at * D + 4 * ch) =
-            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-        if (ch == 0) a.lse[at] = lg * 0.6931471805599453f;
-      } else {
-        const long long at = static_cast<long long>(s.slot) * kRows + row;
-        *reinterpret_cast<float4*>(a.part_o + at * D + 4 * ch) = acc;
-        if (ch == 0) a.part_l[at] = lg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + Ly::kMergeW + bar);
+      ok = mbar_wait(base + Ly::kMergeW + bar, use & 1, wc, kSiteMergeW, ns);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      const int rows = min(8, s.nv - 8 * y);
+      for (int it = (warp - w0) * 32 + lane; it < rows * (D / 4); it += 32 * nw) {
+        const int row = it / (D / 4), ch = it % (D / 4);
+        float4 q[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          q[w] = w < active ? stats[(w0 + w) * 8 + row] : make_float4(kInit, 0.f, 0.f, 0.f);
+        float M = kInit, Em = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, q[w].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          q[w].z = w < active ? q[w].z + (q[w].x - M) : -INFINITY;
+          Em = fmaxf(Em, q[w].z);
+        }
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < active) {
+            const float f = ex2(q[w].z - Em);
+            const float4 v = *reinterpret_cast<const float4*>(merge + ((w0 + w) * 8 + row) * D + 4 * chunk_at(row, ch));
+            L += q[w].y * ex2(q[w].x - M);
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+          }
+        }
+        // a row without a visible key: O = 0, L = -inf
+        const float fin = L == 0.f ? 0.f : ex2(Em - 14.f) / L;
+        const float lg = L == 0.f ? -INFINITY : M + log2f(L);
+        acc.x *= fin;
+        acc.y *= fin;
+        acc.z *= fin;
+        acc.w *= fin;
+        if (s.mode == 0) {
+          const long long to = out_row(s, row + 8 * y);
+          *reinterpret_cast<uint2*>(a.o + to * D + 4 * ch) =
+              make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+          if (ch == 0) a.lse[to] = lg * 0.6931471805599453f;
+        } else {
+          const long long to = static_cast<long long>(s.slot) * kRows + row + 8 * y;
+          *reinterpret_cast<float4*>(a.part_o + to * D + 4 * ch) = acc;
+          if (ch == 0) a.part_l[to] = lg;
+        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + Ly::kMergeR + bar);
     }
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(base + Ly::kMergeR);
-      mbar_arrive(base + Ly::kSegEmpty + 8 * si);
-    }
+    if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
   }
 }
 

@@ -25,12 +25,16 @@
 // [0,128) and B at [128,256), P over the first half of each as f16 pairs; O of
 // A [256,384) and of B [384,512).
 // A key tile is two steps of 64 keys.  For each half one thread issues S(0),
-// S(1), then for step i PV(i), S(i+2): the scores of a step lie ready when the
-// softmax has done the one before, so that it never waits for its own weights
-// to be multiplied.  (With steps of 128 keys and one buffer, scores, softmax
-// and weights followed one another: 4100 cycles per tile and half, of which the
-// softmax took 1800.)  S(i+2) overwrites P(i), which PV(i) before it reads:
-// products issued by one thread to the same tensor pipe run in order.
+// then for step i S(i+1) and PV(i): the scores of a step are made while the
+// softmax does the one before, so that it never waits for its own weights to be
+// multiplied.  (With steps of 128 keys and one buffer, scores, softmax and
+// weights followed one another: 4100 cycles per tile and half, of which the
+// softmax took 1800.)  S(i+1) takes the buffer of P(i-1) and waits until PV(i-1)
+// is done: that the products of a thread run in order is promised for one
+// accumulator only.  What happens once a step (scores made, weights written,
+// weights multiplied) has a barrier for even and one for odd steps: a wait by
+// parity tells one phase from the next, and those who skip some would be two
+// behind on a single one.
 //
 // Warps: 0-3 softmax and epilogue of A, 4-7 of B, 8-11 codes to f16 (and Q),
 // 12 and 15 issue A's and B's products, 13 walks the range, 14 loads.
@@ -98,8 +102,8 @@ struct Layout {
   static constexpr int kVEmpty = kVFull + 16;
   static constexpr int kSFull = kVEmpty + 16;     // [2] A, B [2] score buffers
   static constexpr int kPFull = kSFull + 32;      // [2][2]
-  static constexpr int kPvDone = kPFull + 32;     // [2]
-  static constexpr int kScales = kPvDone + 16;    // [4]
+  static constexpr int kPvDone = kPFull + 32;     // [2][2]
+  static constexpr int kScales = kPvDone + 32;    // [4]
   static constexpr int kRawFull = kScales + 32;
   static constexpr int kRawEmpty = kRawFull + 8;
   static constexpr int kFin = kRawEmpty + 8;
@@ -166,13 +170,6 @@ __device__ __forceinline__ void reg_inc() {
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N) : "memory");
-}
-
-// True in one thread of the (converged) warp, always the same one.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
 }
 
 // kind::f16 with f16 A and B (format 0), fp32 D.
@@ -261,8 +258,8 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       for (int b = 0; b < 2; ++b) {
         mbar_init(base + Ly::kSFull + 8 * (2 * i + b), 1);
         mbar_init(base + Ly::kPFull + 8 * (2 * i + b), 4);
+        mbar_init(base + Ly::kPvDone + 8 * (2 * i + b), 1);
       }
-      mbar_init(base + Ly::kPvDone + 8 * i, 1);
     }
     mbar_init(base + Ly::kRawFull, 1);
     mbar_init(base + Ly::kRawEmpty, 4);
@@ -484,34 +481,21 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         const bool mine = __shfl_sync(0xffffffffu, segs[si].nv, 0) > x * kHalf;  // this half has rows
         if (nt == 0) break;
         bool ok = all_wait(Ly::kQFull, ns, kSiteQFull, ns);
-        // i < 0: scores only
+        if (ok && mine && cnt > 0) ok = all_wait(Ly::kPvDone + 8 * (2 * x + ((cnt - 1) & 1)), (cnt - 1) >> 1, kSitePV, jt);
+        // i = -1: the first scores only
 #pragma unroll 1
-        for (int i = -2; i < steps; ++i) {
-          const int n = i + 2, tv = jt + (i >> 1), tk = jt + (n >> 1);  // tiles of step i and of step n
-          const int buf = cnt & 1;                                      // of both
-          if (ok && n < steps && (n & 1) == 0) ok = all_wait(Ly::kKFull + 8 * (tk & 1), tk >> 1, kSiteKFull, tk);
-          if (ok && i >= 0 && (i & 1) == 0) ok = all_wait(Ly::kVFull + 8 * (tv & 1), tv >> 1, kSiteVFull, tv);
-          if (ok && i >= 0 && mine) ok = all_wait(Ly::kPFull + 8 * (2 * x + buf), (cnt >> 1) - 1, kSiteP, tv);
-          if (!ok) break;
-          tc_fence_after();
-          if (i >= 0) {
-            const uint32_t v = low(base + Ly::kV + (tv & 1) * Ly::kVTile + (i & 1) * (kStepKeys * 128), 16384);
-            const uint32_t first = i == 0 ? 0u : 1u, p = dS + buf * kStepKeys;
-            if (elect_one()) {
-              if (mine) {
-#pragma unroll
-                for (int kk = 0; kk < kStepKeys / 16; ++kk)
-                  mma_ts(dO, p + 8 * kk, desc(v + static_cast<uint32_t>(kk * 128)), idPV, kk == 0 ? first : 1u);
-                tc_commit(base + Ly::kPvDone + 8 * x);
-              }
-              if ((i & 1) == 1 || i + 1 == steps) tc_commit(base + Ly::kVEmpty + 8 * (tv & 1));
-            }
-            __syncwarp();
-          }
+        for (int i = -1; ok && i < steps; ++i) {
+          const int n = i + 1, tv = jt + (i >> 1), tk = jt + (n >> 1);  // tiles of step i and of step n
           if (n < steps) {
+            const int buf = (cnt + n) & 1;
+            if ((n & 1) == 0) ok = all_wait(Ly::kKFull + 8 * (tk & 1), tk >> 1, kSiteKFull, tk);
+            // the buffer's weights, of two steps before, have been multiplied
+            if (ok && mine && i >= 1) ok = all_wait(Ly::kPvDone + 8 * (2 * x + buf), (cnt + i - 1) >> 1, kSitePV, tk);
+            if (!ok) break;
+            tc_fence_after();
             const uint32_t k = low(base + Ly::kK + (tk & 1) * Ly::kKTile + (n & 1) * (kStepKeys * 128), 16);
             const uint32_t d = dS + buf * kStepKeys;
-            if (elect_one()) {
+            if (dec::elect_one()) {
               if (mine) {
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
@@ -526,15 +510,33 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
             }
             __syncwarp();
           }
-          if (mine) ++cnt;
+          if (i >= 0) {
+            const int buf = (cnt + i) & 1;
+            if ((i & 1) == 0) ok = all_wait(Ly::kVFull + 8 * (tv & 1), tv >> 1, kSiteVFull, tv);
+            if (ok && mine) ok = all_wait(Ly::kPFull + 8 * (2 * x + buf), (cnt + i) >> 1, kSiteP, tv);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v = low(base + Ly::kV + (tv & 1) * Ly::kVTile + (i & 1) * (kStepKeys * 128), 16384);
+            const uint32_t first = i == 0 ? 0u : 1u, p = dS + buf * kStepKeys;
+            if (dec::elect_one()) {
+              if (mine) {
+#pragma unroll
+                for (int kk = 0; kk < kStepKeys / 16; ++kk)
+                  mma_ts(dO, p + 8 * kk, desc(v + static_cast<uint32_t>(kk * 128)), idPV, kk == 0 ? first : 1u);
+                tc_commit(base + Ly::kPvDone + 8 * (2 * x + buf));
+              }
+              if ((i & 1) == 1 || i + 1 == steps) tc_commit(base + Ly::kVEmpty + 8 * (tv & 1));
+            }
+            __syncwarp();
+          }
         }
         if (!ok) break;
-        if (mine) cnt -= 2;
+        if (mine) cnt += steps;
         jt += nt;
         if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
       }
       // nothing that reads shared or tensor memory outlives the CTA
-      if (elect_one()) {
+      if (dec::elect_one()) {
         tc_commit(base + Ly::kFin + 8 * x);
         dec::mbar_drain(base + Ly::kFin + 8 * x, 0, globaltimer_ns() + a.timeout_ns);
       }
@@ -818,7 +820,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         }
         l += sums;
         if (moved && i > 0) {  // O to the new reference, once it has every weight before
-          ok = __all_sync(0xffffffffu, wait(Ly::kPvDone + 8 * x, cnt - 1, kSitePV, tile));
+          ok = __all_sync(0xffffffffu, wait(Ly::kPvDone + 8 * (buf ^ 1), (cnt - 1) >> 1, kSitePV, tile));
           tc_fence_after();
 #pragma unroll 1
           for (int z = 0; z < D / 32; ++z) {
@@ -838,7 +840,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       }
       jt += nt;
       if (!__all_sync(0xffffffffu, ok)) break;
-      ok = wait(Ly::kPvDone + 8 * x, cnt - 1, kSitePV, jt);
+      ok = wait(Ly::kPvDone + 8 * (2 * x + ((cnt - 1) & 1)), (cnt - 1) >> 1, kSitePV, jt);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const bool real = row < s.nv;
