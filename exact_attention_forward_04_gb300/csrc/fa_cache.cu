@@ -136,28 +136,33 @@ int cache_append(const void* k, const void* v, long long k_stride, long long v_s
 
 // ----------------------------------------------------------------- forward
 
-// Which kernel: the few-row one while a request has 48 rows per kv head or
-// fewer on average (tokens times the query heads of a kv head): it reads the
-// keys again for every 16 of them, the other pays for 128.  16 requests of 2-5
-// drafted tokens, 8 heads sharing (27 rows): 45 us against 74.
-bool many_rows(int R, int T, int g) {
-  return static_cast<long long>(T) * g > 48ll * R;
+// Query rows of a unit, and with them the kernel, by the average rows a request
+// has per kv head (tokens times the query heads that share it): the few-row
+// kernel with 8 or 16, which reads the keys again for every so many, up to 48,
+// and above the many-row one with 256.
+int unit_rows(int R, int T, int g) {
+  const long long rows = static_cast<long long>(T) * g;
+  return rows <= 8ll * R ? 8 : rows <= 48ll * R ? 16 : prm::kRows;
 }
 
 // Workspace: the CTAs' marks, then two partials of a unit's query rows per CTA.
-constexpr int kMaxGrid = 256;
-size_t marks_bytes(int sms) { return static_cast<size_t>(sms) * 32; }
+constexpr int kMaxGrid = 512;  // the merge's threads look at a CTA each
+int cache_fwd_grid(int sms, int rows, int d) {
+  const int n = sms * dec::ctas_per_sm(d, rows);
+  return n < kMaxGrid ? n : kMaxGrid;
+}
+size_t marks_bytes(int grid) { return static_cast<size_t>(grid) * 32; }
 
 size_t cache_fwd_workspace(int R, int T, int Hq, int Hkv, int d) {
   if ((d != 64 && d != 128) || R <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
   host::Device dev;
   if (host::device(&dev) != FA_OK) return 0;
-  const int rows = many_rows(R, T, Hq / Hkv) ? prm::kRows : dec::kRows;
-  return marks_bytes(dev.sms) + static_cast<size_t>(2) * dev.sms * rows * (d + 1) * 4;
+  const int rows = unit_rows(R, T, Hq / Hkv), grid = cache_fwd_grid(dev.sms, rows, d);
+  return marks_bytes(grid) + static_cast<size_t>(2) * grid * rows * (d + 1) * 4;
 }
 
 std::mutex g_cache_mu;
-bool g_cache_ready[64][2][5] = {};
+bool g_cache_ready[64][2][6] = {};
 
 // Dynamic shared memory of a kernel, set once per device.
 template <typename K>
@@ -176,7 +181,7 @@ template <int D, int ROWS>
 int launch_merge(const CacheFwdArgs& a, int grid, int split, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, split, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(512, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -190,15 +195,14 @@ int launch_merge(const CacheFwdArgs& a, int grid, int split, cudaStream_t s) {
 template <int D>
 int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, char* ws, const host::Device& dev,
                      cudaStream_t s) {
-  const int grid = dev.sms < kMaxGrid ? dev.sms : kMaxGrid;
-  const bool many = many_rows(a.R, a.T, a.g);
+  const int unit = unit_rows(a.R, a.T, a.g), grid = cache_fwd_grid(dev.sms, unit, D);
   a.desc = reinterpret_cast<int4*>(ws);
-  a.cont = reinterpret_cast<int*>(ws + static_cast<size_t>(dev.sms) * 16);
-  a.part_o = reinterpret_cast<float*>(ws + marks_bytes(dev.sms));
-  a.part_l = a.part_o + static_cast<size_t>(2) * grid * (many ? prm::kRows : dec::kRows) * D;
+  a.cont = reinterpret_cast<int*>(ws + static_cast<size_t>(grid) * 16);
+  a.part_o = reinterpret_cast<float*>(ws + marks_bytes(grid));
+  a.part_l = a.part_o + static_cast<size_t>(2) * grid * unit * D;
   bool* set = g_cache_ready[dev.dev][D == 128];
   int st = FA_OK;
-  if (many) {
+  if (unit == prm::kRows) {
     using Ly = prm::Layout<D>;
     // a key per 128-byte row, zeros behind the codes at d = 64
     CUtensorMap mk;
@@ -221,8 +225,6 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
     if (static_cast<long long>(a.M) * P <= prm::kKeys) return FA_OK;
     return launch_merge<D, prm::kRows>(a, grid, 4, s);
   }
-  using Ly = dec::Layout<D>;
-  if ((st = ready(fa_cache_fwd_kernel<D>, Ly::kAlloc, set[0])) != FA_OK) return st;
   CUtensorMap mk, mv;
   const cuuint64_t rows = static_cast<cuuint64_t>(P) * D / 128;
   const cuuint64_t bh = static_cast<cuuint64_t>(a.blocks) * a.Hkv;
@@ -231,11 +233,19 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
   if (st != FA_OK) return st;
   st = host::tensor_map(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, v8, 128, rows, bh, 128, rows * 128, 128, box);
   if (st != FA_OK) return st;
-  fa_cache_fwd_kernel<D><<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
+  if (unit == 8) {
+    using Ly = dec::Layout<D, 8>;
+    if ((st = ready(fa_cache_fwd_kernel<D, 8>, Ly::kAlloc, set[0])) != FA_OK) return st;
+    fa_cache_fwd_kernel<D, 8><<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
+  } else {
+    using Ly = dec::Layout<D, 16>;
+    if ((st = ready(fa_cache_fwd_kernel<D, 16>, Ly::kAlloc, set[5])) != FA_OK) return st;
+    fa_cache_fwd_kernel<D, 16><<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return host::fail(e);
   if (static_cast<long long>(a.M) * P <= dec::kKeys) return FA_OK;
-  return launch_merge<D, dec::kRows>(a, grid, 1, s);
+  return unit == 8 ? launch_merge<D, 8>(a, grid, 1, s) : launch_merge<D, 16>(a, grid, 1, s);
 }
 
 int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8, const float* ks, const float* vs,

@@ -51,16 +51,15 @@ namespace dec {
 
 constexpr int kWarps = 8;                    // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);  // and the producer
-constexpr int kRows = 16;                    // query rows of a unit
 constexpr int kKeys = 32;                    // keys of a tile
-constexpr int kSegs = 8;                     // unit pieces in flight
 constexpr int kMeta = 64;                    // tiles whose blocks and scales are held
 constexpr int kUnitCost = 5;                 // a piece's fixed cost, in tiles
 constexpr int kMinCost = 12;                 // least cost of a CTA's range
+constexpr int kWarpScan = 128;               // requests that one warp sums
 constexpr float kInit = -1e30f;              // references before the first key
 
 enum : unsigned { kSiteStageFull = 501, kSiteStageEmpty = 502, kSiteSegFull = 503, kSiteSegEmpty = 504,
-                  kSiteMergeW = 505, kSiteMergeR = 506 };
+                  kSiteMergeW = 505, kSiteMergeR = 506, kSiteIssued = 507 };
 
 struct Seg {
   int r, h, row0;      // request, kv head, first row of the tile
@@ -72,15 +71,20 @@ struct Seg {
   int w0, nw;          // its warps (few rows per kv head only)
 };
 
-template <int D>
+// ROWS query rows a unit, 16 or 8.  8 rows at d = 64 leave registers and room
+// for two CTAs per SM with half the ring each.
+constexpr int ctas_per_sm(int d, int rows) { return d == 64 && rows == 8 ? 2 : 1; }
+template <int D, int ROWS>
 struct Layout {
-  static constexpr int kHalf = kKeys * D;       // codes of K (or V) of a tile
+  static constexpr int kCtas = ctas_per_sm(D, ROWS);
+  static constexpr int kSegs = 8;                               // unit pieces in flight
+  static constexpr int kHalf = kKeys * D;                       // codes of K (or V) of a tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = 131072 / kStage;
-  static constexpr int kIssue = kStages / 2;    // lanes that issue loads
+  static constexpr int kStages = 131072 / kCtas / kStage;
+  static constexpr int kIssue = kStages / 2;                    // lanes that issue loads
   static constexpr int kMerge = kStages * kStage;
-  static constexpr int kQ = kMerge + kWarps * 8 * D * 4;        // bf16 [segs][16][D]
-  static constexpr int kStats = kQ + kSegs * kRows * D * 2;     // float4 [warps][8]
+  static constexpr int kQ = kMerge + kWarps * 8 * D * 4;        // bf16 [segs][rows][D]
+  static constexpr int kStats = kQ + kSegs * ROWS * D * 2;      // float4 [warps][8]
   static constexpr int kScales = kStats + kWarps * 8 * 16;      // float4 [meta]
   static constexpr int kBlk = kScales + kMeta * 16;             // int4 [meta]: blocks, row in the block, valid
   static constexpr int kSeg = kBlk + kMeta * 16;
@@ -91,12 +95,14 @@ struct Layout {
   static constexpr int kSegEmpty = kSegFull + 8 * kSegs;
   static constexpr int kMergeW = kSegEmpty + 8 * kSegs; // [7] four pairs, two fours, all
   static constexpr int kMergeR = kMergeW + 56;
-  static constexpr int kAbort = kMergeR + 56;
+  static constexpr int kIssued = kMergeR + 56;          // int [stages]: position last issued
+  static constexpr int kAbort = kIssued + 4 * kStages;
   static constexpr int kScan = kAbort + 8;              // long long [33]
+  static_assert(kStages % kWarps == 0 && kAbort % 8 == 0, "stages");
   static constexpr int kStart = (kScan + 33 * 8 + 15) & ~15;  // int4
   static constexpr int kBytes = kStart + 16;
   static constexpr int kAlloc = kBytes + 1024;
-  static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kCtas * (kAlloc + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 // Which key of a 32-key tile is column n (0..7) of score tile j (0..3), and
@@ -129,6 +135,41 @@ __device__ __forceinline__ uint32_t code_at(int t, int c) {
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t end) {
   while (!mbar_try_wait(bar, parity) && globaltimer_ns() < end) {
   }
+}
+
+// Waits until ring position p has been issued.  A barrier's parity tells only
+// the phase before from the one after: a warp that knows of a tile more than
+// one round of the ring before the tile is issued would take the phase of two
+// rounds ago for its own.
+__device__ __forceinline__ bool issue_wait(uint32_t tag, int p, const WaitCtx& w, unsigned site) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    int v;
+    asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(tag) : "memory");
+    if (v == p) return true;
+    if (it == 0) t0 = globaltimer_ns();
+    if ((it & 31u) == 31u) {
+      if (*w.cta_abort) return false;
+      if (globaltimer_ns() - t0 > w.timeout_ns) {
+        if (atomicCAS(&w.err->code, 0u, 1u) == 0u) {
+          w.err->site = site;
+          w.err->block = blockIdx.x;
+          w.err->tile = p;
+          __threadfence();
+        }
+        *w.cta_abort = 1;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ void issue_mark(uint32_t tag, int p) {
+  asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(tag), "r"(p) : "memory");
+}
+
+// Offset of the merge barrier of the 2, 4 or 8 warps that `warp` is one of.
+__device__ __forceinline__ int merge_bar(int warp, int nw) {
+  return 8 * (nw == 2 ? warp >> 1 : nw == 4 ? 4 + (warp >> 2) : 6);
 }
 
 // True in one thread of the (converged) warp, always the same one.
@@ -171,9 +212,26 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+// Largest value over the lanes that hold one row's keys: a quad where the rows
+// come first in the score product, else the eight lanes of equal t4.
+template <bool WIDE>
+__device__ __forceinline__ float row_max(float x) {
+  if constexpr (WIDE) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+  } else {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+  }
+}
+
+// The 8 x 8 matrix of 16-bit elements that a warp holds (lane l: row l / 4,
+// elements 2 (l % 4), + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 // floor(log2 x) of a normal positive x (smaller ones: -127).
@@ -242,12 +300,13 @@ __device__ __forceinline__ long long cost_of(const CacheFwdArgs& a, const Req& q
 
 }  // namespace dec
 
-template <int D>
-__global__ void __launch_bounds__(dec::kThreads, 1)
+template <int D, int ROWS>
+__global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
     fa_cache_fwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ CacheFwdArgs a) {
   using namespace dec;
-  using Ly = Layout<D>;
+  using Ly = Layout<D, ROWS>;
+  constexpr int kRows = ROWS, kSegs = Ly::kSegs;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -259,66 +318,124 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
   Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
   float4* s_scales = reinterpret_cast<float4*>(sm + Ly::kScales);
   int4* s_blk = reinterpret_cast<int4*>(sm + Ly::kBlk);
-  if (tid == 0) {
-    for (int i = 0; i < Ly::kStages; ++i) {
-      mbar_init(base + Ly::kFull + 8 * i, 1);
+  if (warp == kWarps) {
+    for (int i = lane; i < Ly::kStages; i += 32) {
+      mbar_init(base + Ly::kFull + 8 * i, 2);  // its loads, and its scales
       mbar_init(base + Ly::kEmpty + 8 * i, 1);
+      issue_mark(base + Ly::kIssued + 4 * i, -1);
     }
-    for (int i = 0; i < kSegs; ++i) {
-      mbar_init(base + Ly::kSegFull + 8 * i, 1);
-      mbar_init(base + Ly::kSegEmpty + 8 * i, kWarps);
+    if (lane < kSegs) {
+      mbar_init(base + Ly::kSegFull + 8 * lane, 1);
+      mbar_init(base + Ly::kSegEmpty + 8 * lane, kWarps);
     }
-    for (int i = 0; i < 7; ++i) {
-      const int n = i < 4 ? 2 : i < 6 ? 4 : 8;
-      mbar_init(base + Ly::kMergeW + 8 * i, n);
-      mbar_init(base + Ly::kMergeR + 8 * i, n);
+    if (lane < 7) {
+      const int n = lane < 4 ? 2 : lane < 6 ? 4 : 8;
+      mbar_init(base + Ly::kMergeW + 8 * lane, n);
+      mbar_init(base + Ly::kMergeR + 8 * lane, n);
     }
-    *abort_flag = 0;
     fence_mbar_init();
-    prefetch_tensormap(&tmK);
-    prefetch_tensormap(&tmV);
-    a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    a.cont[blockIdx.x] = 0;
+    if (lane == 0) {
+      *abort_flag = 0;
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+      a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      a.cont[blockIdx.x] = 0;
+    }
   }
 
-  // this CTA's range of the total cost, and the request that it starts in
-  const int per = (a.R + kThreads - 1) / kThreads;
-  const int ra = min(a.R, tid * per), rb = min(a.R, ra + per);
-  long long mine = 0, total;
-  for (int r = ra; r < rb; ++r) {
-    mine += cost_of(a, request<kRows, kKeys>(a, r));
-    if (blockIdx.x == 0) check_request(a, r);
-  }
-  const long long before = cta_scan(mine, reinterpret_cast<long long*>(sm + Ly::kScan), total) - mine;
-  const long long want = (total + kMinCost - 1) / kMinCost;
-  const int parts = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, want)));
-  if (static_cast<int>(blockIdx.x) >= parts) return;
-  const long long x0 = total * blockIdx.x / parts, x1 = total * (blockIdx.x + 1) / parts;
-  if (x0 >= x1) return;
-  if (before <= x0 && x0 < before + mine) {
-    long long x = before;
-    int r = ra;
-    for (;; ++r) {
-      const long long c = cost_of(a, request<kRows, kKeys>(a, r));
-      if (x0 < x + c) break;  // ends: this thread's requests hold x0
-      x += c;
-    }
-    // and the kv head, the row tile and the place in it
+  // This CTA's range of the total cost: its length, and the request, kv head,
+  // row tile and place in it that it starts at.  A small batch is summed by the
+  // producer alone, a large one by the whole CTA.
+  long long left = 0;
+  int4 at = make_int4(0, 0, 0, 0);
+  auto range = [&](long long total, long long& x0, long long& len) {
+    const long long want = (total + kMinCost - 1) / kMinCost;
+    const int parts = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, want)));
+    const int c = min(static_cast<int>(blockIdx.x), parts);
+    x0 = total * c / parts;
+    len = c < parts ? total * (c + 1) / parts - x0 : 0;
+  };
+  auto place = [&](int r, long long in) {
     const Req q = request<kRows, kKeys>(a, r);
     const int unit = q.kt + kUnitCost;
-    const int u = static_cast<int>((x0 - x) / unit), y = static_cast<int>((x0 - x) - static_cast<long long>(u) * unit);
-    *reinterpret_cast<int4*>(sm + Ly::kStart) = make_int4(r, u / q.nrt, u % q.nrt, y);
+    const int u = static_cast<int>(in / unit);
+    return make_int4(r, u / q.nrt, u % q.nrt, static_cast<int>(in - static_cast<long long>(u) * unit));
+  };
+  if (a.R <= kWarpScan) {
+    if (warp == kWarps) {
+      long long c[kWarpScan / 32], total = 0;
+#pragma unroll
+      for (int i = 0; i < kWarpScan / 32; ++i) {
+        const int r = i * 32 + lane;
+        c[i] = 0;
+        if (r < a.R) {
+          c[i] = cost_of(a, request<kRows, kKeys>(a, r));
+          if (blockIdx.x == 0) check_request(a, r);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kWarpScan / 32; ++i) total += c[i];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      long long x0;
+      range(total, x0, left);
+      if (left > 0) {
+        long long before = 0;
+        int found = -1;
+        long long in = 0;
+#pragma unroll
+        for (int i = 0; i < kWarpScan / 32; ++i) {
+          if (found < 0 && i * 32 < a.R) {
+            long long incl = c[i];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+              if (lane >= o) incl += v;
+            }
+            incl += before;
+            const uint32_t past = __ballot_sync(0xffffffffu, incl > x0);
+            if (past) {
+              const int l = __ffs(past) - 1;
+              found = i * 32 + l;
+              in = x0 - __shfl_sync(0xffffffffu, incl - c[i], l);
+            }
+            before = __shfl_sync(0xffffffffu, incl, 31);
+          }
+        }
+        at = place(found, in);
+      }
+    }
+    __syncthreads();
+  } else {
+    const int per = (a.R + kThreads - 1) / kThreads;
+    const int ra = min(a.R, tid * per), rb = min(a.R, ra + per);
+    long long mine = 0, total, x0;
+    for (int r = ra; r < rb; ++r) {
+      mine += cost_of(a, request<kRows, kKeys>(a, r));
+      if (blockIdx.x == 0) check_request(a, r);
+    }
+    const long long before = cta_scan(mine, reinterpret_cast<long long*>(sm + Ly::kScan), total) - mine;
+    range(total, x0, left);
+    if (left > 0 && before <= x0 && x0 < before + mine) {
+      long long x = before;
+      int r = ra;
+      for (;; ++r) {
+        const long long c = cost_of(a, request<kRows, kKeys>(a, r));
+        if (x0 < x + c) break;  // ends: this thread's requests hold x0
+        x += c;
+      }
+      *reinterpret_cast<int4*>(sm + Ly::kStart) = place(r, x0 - x);
+    }
+    __syncthreads();
+    at = *reinterpret_cast<const int4*>(sm + Ly::kStart);
   }
-  __syncthreads();
   const WaitCtx wc{abort_flag, a.err, a.timeout_ns};
   auto full = [&](int s) { return base + Ly::kFull + 8 * s; };
   auto empty = [&](int s) { return base + Ly::kEmpty + 8 * s; };
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
-    const int4 at = *reinterpret_cast<const int4*>(sm + Ly::kStart);
     int r = at.x, h = at.y, rt = at.z, y = at.w;  // the walk: unit, and place in its cost
-    long long left = x1 - x0;
     // tiles that a short piece leaves a warp: as many as the ring holds for
     // each, or one where there is too little work for all of them
     const int per_warp = left >= 40 ? Ly::kStages / kWarps : 1;
@@ -448,9 +565,8 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
       // their blocks and scales, a lane each, then the loads, by some lanes.
       // An entry is reused 64 tiles later: before the first of these tiles was
       // issued, all but the last ring's worth (at most 32) had been consumed.
+      int blk[2] = {-1, -1};
       if (mr >= 0) {
-        int blk[2] = {-1, -1};
-        float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};
         const int* row = a.table + static_cast<long long>(mr) * a.M;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -465,53 +581,62 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
             }
           }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (blk[i] >= 0) {
-            ks[i] = a.ks[blk[i]];
-            vs[i] = a.vs[blk[i]];
-          }
-        if (boxes == 1) {
-          ks[1] = ks[0];
-          vs[1] = vs[0];
-        }
-        const int e = (pos + lane) % kMeta;
-        s_scales[e] = make_float4(ks[0], ks[1], vs[0], vs[1]);
         const int valid = boxes == 1 ? (blk[0] >= 0 ? 3 : 0) : (blk[0] >= 0 ? 1 : 0) | (blk[1] >= 0 ? 2 : 0);
-        s_blk[e] = make_int4(blk[0], blk[1], ((mt * kKeys) & (P - 1)) * D / 128, valid);
+        s_blk[(pos + lane) % kMeta] = make_int4(blk[0], blk[1], ((mt * kKeys) & (P - 1)) * D / 128, valid);
       }
+      // on their way while the loads are issued
+      float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (blk[i] >= 0) {
+          ks[i] = __ldg(a.ks + blk[i]);
+          vs[i] = __ldg(a.vs + blk[i]);
+        }
       __syncwarp();
       // Several lanes issue the loads, each on a tile of its own: a load of 2
       // or 4 KB took 270 cycles from one lane, 105 from eight, and 73 from 32;
       // half the ring at most, as the lanes go on together.
-      if (lane < Ly::kIssue) {
-        for (int i = lane; i < fill; i += Ly::kIssue) {
-          const int p = pos + i, st = p % Ly::kStages, round = p / Ly::kStages;
-          if (round > 0 && !mbar_wait(empty(st), (round - 1) & 1, wc, kSiteStageEmpty, p)) { ok = false; break; }
-          issued = p + 1;
-          const int4 bl = s_blk[p % kMeta];
-          const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
-          if (boxes == 1) {
-            if (bl.x >= 0) {
-              mbar_arrive_expect_tx(full(st), Ly::kStage);
-              tma_load_3d(kb, &tmK, full(st), 0, bl.z, bl.x);
-              tma_load_3d(vb, &tmV, full(st), 0, bl.z, bl.x);
+      for (int i0 = 0; i0 < fill; i0 += Ly::kIssue) {
+        const int p = pos + i0 + lane;
+        if (lane < Ly::kIssue && i0 + lane < fill) {
+          const int st = p % Ly::kStages, round = p / Ly::kStages;
+          if (round > 0) ok = mbar_wait(empty(st), (round - 1) & 1, wc, kSiteStageEmpty, p);
+          if (ok) {
+            issued = p + 1;
+            issue_mark(base + Ly::kIssued + 4 * st, p);
+            const int4 bl = s_blk[p % kMeta];
+            const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
+            if (boxes == 1) {
+              if (bl.x >= 0) {
+                mbar_arrive_expect_tx(full(st), Ly::kStage);
+                tma_load_3d(kb, &tmK, full(st), 0, bl.z, bl.x);
+                tma_load_3d(vb, &tmV, full(st), 0, bl.z, bl.x);
+              } else {
+                mbar_arrive(full(st));
+              }
             } else {
-              mbar_arrive(full(st));
-            }
-          } else {
-            const uint32_t nbox = (bl.x >= 0 ? 1u : 0u) + (bl.y >= 0 ? 1u : 0u);
-            mbar_arrive_expect_tx(full(st), nbox * Ly::kHalf);
-            if (bl.x >= 0) {
-              tma_load_3d(kb, &tmK, full(st), 0, 0, bl.x);
-              tma_load_3d(vb, &tmV, full(st), 0, 0, bl.x);
-            }
-            if (bl.y >= 0) {
-              tma_load_3d(kb + Ly::kHalf / 2, &tmK, full(st), 0, 0, bl.y);
-              tma_load_3d(vb + Ly::kHalf / 2, &tmV, full(st), 0, 0, bl.y);
+              const uint32_t nbox = (bl.x >= 0 ? 1u : 0u) + (bl.y >= 0 ? 1u : 0u);
+              mbar_arrive_expect_tx(full(st), nbox * Ly::kHalf);
+              if (bl.x >= 0) {
+                tma_load_3d(kb, &tmK, full(st), 0, 0, bl.x);
+                tma_load_3d(vb, &tmV, full(st), 0, 0, bl.x);
+              }
+              if (bl.y >= 0) {
+                tma_load_3d(kb + Ly::kHalf / 2, &tmK, full(st), 0, 0, bl.y);
+                tma_load_3d(vb + Ly::kHalf / 2, &tmV, full(st), 0, 0, bl.y);
+              }
             }
           }
         }
+        ok = __all_sync(0xffffffffu, ok);
+        // the scales of these tiles, by the lanes that have them
+        if (ok && lane >= i0 && lane < min(fill, i0 + Ly::kIssue)) {
+          const int e = pos + lane;
+          s_scales[e % kMeta] = boxes == 1 ? make_float4(ks[0], ks[0], vs[0], vs[0])
+                                           : make_float4(ks[0], ks[1], vs[0], vs[1]);
+          mbar_arrive(full(e % Ly::kStages));
+        }
+        if (!ok) break;
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -542,12 +667,12 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
   }
 
   // -------------------------------------------------------------- consumers
-  const int g4 = lane >> 2, t4 = lane & 3;
   constexpr int kK = D / 16;   // score products per 8 keys
-  constexpr int kN = D / 8;    // output tiles of 8 columns
   float* merge = reinterpret_cast<float*>(sm + Ly::kMerge);
   float4* stats = reinterpret_cast<float4*>(sm + Ly::kStats);
-  int merges2 = 0, merges4 = 0, merges8 = 0;  // of this warp's pair, four and eight
+  // Merges of this warp's pair, four and eight: bits 0-2 are the phase of the
+  // next; bits 3-5 tell which of the three the last one was, if any.
+  uint32_t merges = 0;
   // Where output row `row` of piece s goes, as a row of [T][Hq].
   auto out_row = [&](const Seg& s, int row) {
     const int rr = s.row0 + row, tk = rr / a.g;
@@ -565,23 +690,36 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
       continue;
     }
 
-    float o[kN][4];
+    // the lane's place in the products; opaque where two CTAs share the
+    // registers, so that offsets made from it are not kept between pieces
+    int ln = lane;
+    if constexpr (Ly::kCtas == 2) asm volatile("" : "+r"(ln));
+    const int g4 = ln >> 2, t4 = ln & 3;
+    // ROWS = 16: S = Q K^T and O = P V with the 16 query rows first; a lane
+    //   holds rows g4, g4 + 8 and columns (2 t4 + e) D/8 + i in o[i][2 y + e].
+    // ROWS = 8: S^T = K Q^T and O^T = V^T P^T, 16 keys or columns first and the
+    //   8 rows second, half the products; a lane holds rows 2 t4 + y and columns
+    //   g4 D/8 + i in o[i / 2][2 (i & 1) + y].
+    constexpr bool kWide = ROWS == 16;
+    constexpr int kO = kWide ? D / 8 : D / 16;
+    float o[kO][4];
     float m[2] = {kInit, kInit}, E[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // E: the second reference less m
     const bool busy = warp - w0 < s.nt;
+    auto row_of = [&](int y) { return kWide ? g4 + 8 * y : 2 * t4 + y; };  // a lane's two rows
     if (busy) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
+      for (int i = 0; i < kO; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-      // Q rows g4 and g4 + 8 in operand layout: product kk takes, in lane t4,
-      // the four elements 4 (kk % 4) .. + 3 of chunk t4 + 4 (kk / 4)
-      uint32_t qa[kK][4];
+      // Q rows g4 (and g4 + 8) in operand layout: product kk takes, in lane
+      // t4, the four elements 4 (kk % 4) .. + 3 of chunk t4 + 4 (kk / 4)
+      constexpr int kY = kWide ? 2 : 1;
+      uint32_t qa[kK][2 * kY];
       float c[2];     // scale of the scores of each row
       int lim[2];     // keys visible to it
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < kY; ++y) {
         const bool real = g4 + 8 * y < s.nv;
-        const int tk = (s.row0 + g4 + 8 * y) / a.g;
         const uint32_t src = base + Ly::kQ + (si * kRows + g4 + 8 * y) * D * 2 + t4 * 32;
         uint4 w[D / 32];  // 2 vectors of 8 per chunk
 #pragma unroll
@@ -597,34 +735,48 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
         const int ex = row_exponent(am << 16);
         const float inv = pow2i(-ex);
         c[y] = a.scale_log2 * pow2i(ex);
-        lim[y] = !real ? 0 : (a.causal ? min(s.len, s.len - s.n + tk + 1) : s.len);
 #pragma unroll
         for (int kk = 0; kk < kK; ++kk) {
           const uint4 v = w[2 * (kk >> 2) + ((kk & 3) >> 1)];
           const uint32_t p0 = (kk & 1) ? v.z : v.x, p1 = (kk & 1) ? v.w : v.y;
           qa[kk][y] = pack_f16(__uint_as_float(p0 << 16) * inv, __uint_as_float(p0 & 0xffff0000u) * inv);
-          qa[kk][2 + y] = pack_f16(__uint_as_float(p1 << 16) * inv, __uint_as_float(p1 & 0xffff0000u) * inv);
+          qa[kk][kY + y] = pack_f16(__uint_as_float(p1 << 16) * inv, __uint_as_float(p1 & 0xffff0000u) * inv);
         }
       }
+      if constexpr (!kWide) {
+        const float mine = c[0];
+        c[0] = __shfl_sync(0xffffffffu, mine, 8 * t4);
+        c[1] = __shfl_sync(0xffffffffu, mine, 8 * t4 + 4);
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        lim[y] = row_of(y) >= s.nv ? 0 : (a.causal ? min(s.len, s.len - s.n + (s.row0 + row_of(y)) / a.g + 1) : s.len);
       // keys visible to every real row of the tile
       const int all = a.causal ? min(s.len, s.len - s.n + s.row0 / a.g + 1) : s.len;
 
       for (int k = warp - w0; k < s.nt; k += nw) {
         const int p = s.base + k, st = p % Ly::kStages;
-        ok = mbar_wait(full(st), (p / Ly::kStages) & 1, wc, kSiteStageFull, p);
+        // the piece's first round: the stage may be further behind than a phase
+        ok = k >= Ly::kStages || issue_wait(base + Ly::kIssued + 4 * st, p, wc, kSiteIssued);
+        ok = ok && mbar_wait(full(st), (p / Ly::kStages) & 1, wc, kSiteStageFull, p);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
         const float4 sc = s_scales[p % kMeta];
         const int valid = s_blk[p % kMeta].w;  // bit i: the tile's 16-key group i has a block
         const int key0 = (s.t0 + k) * kKeys;
         const bool careful = key0 + kKeys > all || valid != 3;
-        // scores in log2 units
-        float x[4][4];
+        // scores in log2 units, x[z][..] of row y: of key column(z, y)'s token
+        // wide: tiles of 8 keys z = 0..3, [2 y + e], key 2 t4 + e of the tile;
+        // else: groups of 16 keys z = 0, 1, [2 e + y], key g4 of tile 2 z + e
+        constexpr int kZ = kWide ? 4 : 2;
+        float x[kZ][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int z = 0; z < kZ; ++z)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[j][e] = 0.f;
-        // two score tiles at a time: two chains of dependent products
+          for (int e = 0; e < 4; ++e) x[z][e] = 0.f;
+        auto at = [](int y, int e) { return kWide ? 2 * y + e : 2 * e + y; };
+        auto token = [&](int z, int e) { return kWide ? tok<D>(z, 2 * t4 + e) : tok<D>(2 * z + e, g4); };
+        // two score tiles at a time: chains of dependent products side by side
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
           uint32_t w[2][D / 16];
@@ -641,45 +793,59 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
             }
           }
 #pragma unroll
-          for (int e = 0; e < kK; ++e)
+          for (int e = 0; e < kK; ++e) {
+            uint32_t b[2][2];
+            e4m3_to_f16(w[0][e], b[0][0], b[0][1]);
+            e4m3_to_f16(w[1][e], b[1][0], b[1][1]);
+            if constexpr (kWide) {
+              mma16816(x[j], qa[e], b[0][0], b[0][1]);
+              mma16816(x[j + 1], qa[e], b[1][0], b[1][1]);
+            } else {
+              const uint32_t ka[4] = {b[0][0], b[1][0], b[0][1], b[1][1]};
+              mma16816(x[j / 2], ka, qa[e][0], qa[e][1]);
+            }
+          }
+        }
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              uint32_t b0, b1;
-              e4m3_to_f16(w[f][e], b0, b1);
-              mma16816(x[j + f], qa[e], b0, b1);
+        for (int z = 0; z < kZ; ++z)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float f = c[y] * (z < kZ / 2 ? sc.x : sc.y);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[z][at(y, e)] *= f;
+          }
+        if (careful) {
+#pragma unroll
+          for (int z = 0; z < kZ; ++z)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int t = token(z, e);
+              const bool there = (valid >> (t >> 4)) & 1;
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (!there || key0 + t >= lim[y]) x[z][at(y, e)] = -INFINITY;
             }
         }
         float gm[2][2];  // largest score of each row in each group of 16 keys
 #pragma unroll
-        for (int gr = 0; gr < 2; ++gr) {
-          const float k2 = gr ? sc.y : sc.x;
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float f = c[y] * k2;
-#pragma unroll
-            for (int j = 2 * gr; j < 2 * gr + 2; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) x[j][2 * y + e] *= f;
-          }
-        }
-        if (careful) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int t = tok<D>(j, 2 * t4 + e);
-              const bool there = (valid >> (t >> 4)) & 1;
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-                if (!there || key0 + t >= lim[y]) x[j][2 * y + e] = -INFINITY;
-            }
-        }
-#pragma unroll
         for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-            gm[gr][y] = quad_max(fmaxf(fmaxf(x[2 * gr][2 * y], x[2 * gr][2 * y + 1]),
-                                       fmaxf(x[2 * gr + 1][2 * y], x[2 * gr + 1][2 * y + 1])));
+          for (int y = 0; y < 2; ++y) {
+            gm[gr][y] = fmaxf(x[gr * (kZ / 2)][at(y, 0)], x[gr * (kZ / 2)][at(y, 1)]);
+            if constexpr (kWide) gm[gr][y] = fmaxf(gm[gr][y], fmaxf(x[2 * gr + 1][at(y, 0)], x[2 * gr + 1][at(y, 1)]));
+          }
+        // over the lanes that hold a row's keys; of both groups together where
+        // they have one scale
+        const bool same = sc.z == sc.w;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          if (same) {
+            gm[0][y] = gm[1][y] = row_max<kWide>(fmaxf(gm[0][y], gm[1][y]));
+          } else {
+            gm[0][y] = row_max<kWide>(gm[0][y]);
+            gm[1][y] = row_max<kWide>(gm[1][y]);
+          }
+        }
         const float lv[2] = {floor_log2(sc.z), floor_log2(sc.w)};
         float wgt[2][2], up[2];
         bool grew = false;
@@ -698,30 +864,43 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
         }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            o[i][0] *= up[0];
-            o[i][1] *= up[0];
-            o[i][2] *= up[1];
-            o[i][3] *= up[1];
-          }
+          for (int i = 0; i < kO; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) o[i][at(y, e)] *= up[y];
         }
+        // weights, as f16 operands of the product with V
         uint32_t pa[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int z = 0; z < kZ; ++z) {
+          float p[2][2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float p0 = ex2(x[j][2 * y] - m[y]), p1 = ex2(x[j][2 * y + 1] - m[y]);
-            l[y] += p0 + p1;
-            pa[j >> 1][2 * (j & 1) + y] = pack_f16(p0 * wgt[j >> 1][y], p1 * wgt[j >> 1][y]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[y][e] = ex2(x[z][at(y, e)] - m[y]);
+            l[y] += p[y][0] + p[y][1];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[y][e] *= wgt[z < kZ / 2 ? 0 : 1][y];
           }
+          if constexpr (kWide) {
+            pa[z >> 1][2 * (z & 1)] = pack_f16(p[0][0], p[0][1]);
+            pa[z >> 1][2 * (z & 1) + 1] = pack_f16(p[1][0], p[1][1]);
+          } else {
+            // key g4, rows 2 t4, 2 t4 + 1 -> row g4, keys 2 t4, 2 t4 + 1
+            pa[z][0] = transpose8(pack_f16(p[0][0], p[1][0]));
+            pa[z][1] = transpose8(pack_f16(p[0][1], p[1][1]));
+          }
+        }
         // O += P V: lane g4 takes output columns g4 D/8 .. of the keys 2 t4, 2 t4 + 1
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          uint32_t w[4][D / 32];  // keys: score tile 2 ks (even, odd column), 2 ks + 1
+          constexpr int kW = D / 32;
+          uint32_t w[4][kW];  // keys: score tile 2 ks (even, odd column), 2 ks + 1
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int t = tok<D>(2 * ks + (e >> 1), 2 * t4 + (e & 1));
-            if constexpr (D == 128) {
+            if constexpr (kW == 4) {
               const uint4 v = lds128(vb + code_at<D>(t, g4));
               w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
             } else {
@@ -731,18 +910,26 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
             // what lies behind the last token may be anything, NaN too
             if (careful && (key0 + t >= s.len || !((valid >> (t >> 4)) & 1))) {
 #pragma unroll
-              for (int f = 0; f < D / 32; ++f) w[e][f] = 0u;
+              for (int f = 0; f < kW; ++f) w[e][f] = 0u;
             }
           }
 #pragma unroll
-          for (int f = 0; f < D / 32; ++f) {
+          for (int f = 0; f < kW; ++f) {
             uint32_t b0[4], b1[4];
             e4m3_to_f16(__byte_perm(w[0][f], w[1][f], 0x5140), b0[0], b0[1]);
             e4m3_to_f16(__byte_perm(w[0][f], w[1][f], 0x7362), b0[2], b0[3]);
             e4m3_to_f16(__byte_perm(w[2][f], w[3][f], 0x5140), b1[0], b1[1]);
             e4m3_to_f16(__byte_perm(w[2][f], w[3][f], 0x7362), b1[2], b1[3]);
+            if constexpr (kWide) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma16816(o[4 * f + e], pa[ks], b0[e], b1[e]);
+              for (int e = 0; e < 4; ++e) mma16816(o[4 * f + e], pa[ks], b0[e], b1[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const uint32_t va[4] = {b0[e], b0[e + 1], b1[e], b1[e + 1]};
+                mma16816(o[2 * f + e / 2], va, pa[ks][0], pa[ks][1]);
+              }
+            }
           }
         }
         __syncwarp();
@@ -750,31 +937,40 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
-        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+        if constexpr (kWide) {
+          l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+          l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+        } else {
+          l[y] += __shfl_xor_sync(0xffffffffu, l[y], 4);
+          l[y] += __shfl_xor_sync(0xffffffffu, l[y], 8);
+          l[y] += __shfl_xor_sync(0xffffffffu, l[y], 16);
+        }
       }
     }
+    // column i of the lane's run `e` (wide: two runs a row) of row y
+    auto out = [&](int y, int e, int i) { return kWide ? o[i % kO][2 * y + e] : o[(i / 2) % kO][2 * (i & 1) + y]; };
+    auto run_at = [&](int e) { return (kWide ? 2 * t4 + e : g4) * (D / 8); };  // its first column
+    constexpr int kRuns = kWide ? 2 : 1;
+    const bool first = kWide ? t4 == 0 : g4 == 0;  // the lane that writes a row's statistics
 
 
-    // Lane (g4, t4) holds columns (2 t4 + e) D/8 + i of rows g4 (+ 8) in
-    // o[i][e (+ 2)].
     if (nw == 1) {  // nothing to merge
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int row = g4 + 8 * y;
+        const int row = row_of(y);
         if (row < s.nv) {
           // a row without a visible key: O = 0, L = -inf
           const float fin = l[y] == 0.f ? 0.f : ex2(E[y] - 14.f) / l[y];
           const float lg = l[y] == 0.f ? -INFINITY : m[y] + log2f(l[y]);
           const long long to = s.mode == 0 ? out_row(s, row) : static_cast<long long>(s.slot) * kRows + row;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const long long col = to * D + (2 * t4 + e) * (D / 8);
+          for (int e = 0; e < kRuns; ++e) {
+            const long long col = to * D + run_at(e);
 #pragma unroll
-            for (int i = 0; i < kN; i += 8) {
+            for (int i = 0; i < D / 8; i += 8) {
               float f[8];
 #pragma unroll
-              for (int z = 0; z < 8; ++z) f[z] = o[i + z][2 * y + e] * fin;
+              for (int z = 0; z < 8; ++z) f[z] = out(y, e, i + z) * fin;
               if (s.mode == 0) {
                 *reinterpret_cast<uint4*>(a.o + col + i) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
                                                                       pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
@@ -784,7 +980,7 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
               }
             }
           }
-          if (t4 == 0) {
+          if (first) {
             if (s.mode == 0) a.lse[to] = lg * 0.6931471805599453f;
             else a.part_l[to] = lg;
           }
@@ -796,38 +992,49 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
     }
 
     // merge of its warps, eight rows at a time
-    const int bar = 8 * (nw == 2 ? w0 >> 1 : nw == 4 ? 4 + (w0 >> 2) : 6);
+    const int bar = merge_bar(warp, nw);
     const int active = min(nw, s.nt);
     // 16-byte chunks are XORed so that the eight lanes of a store fall on
     // different banks
     auto chunk_at = [](int row, int ch) {
-      const int sw = D == 128 ? ((ch >> 3) & 3) | ((row & 1) << 2) : ((ch >> 3) & 1) | ((row & 1) << 1);
+      int sw;
+      if constexpr (kWide) sw = D == 128 ? ((ch >> 3) & 3) | ((row & 1) << 2) : ((ch >> 3) & 1) | ((row & 1) << 1);
+      else sw = D == 128 ? (row >> 1) & 3 : ((row & 2) << 1) | ((row >> 2) & 1);
       return ch ^ sw;
     };
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
+    for (int y = 0; y < ROWS / 8; ++y) {
       if (8 * y >= s.nv) break;
-      const int use = nw == 2 ? merges2++ : nw == 4 ? merges4++ : merges8++;
-      // the buffer is free once every warp has read the merge before
-      if (use > 0) {
-        ok = mbar_wait(base + Ly::kMergeR + bar, (use - 1) & 1, wc, kSiteMergeR, ns);
+      // this warp's buffer is free once the last merge that it was part of,
+      // of whatever size, has been read
+      if (merges >> 3) {
+        const uint32_t last = merges >> 3;  // its phase is the one before that size's next
+        ok = mbar_wait(base + Ly::kMergeR + merge_bar(warp, 2 * last), (merges & last) ? 0 : 1, wc, kSiteMergeR, ns);
         if (!__all_sync(0xffffffffu, ok)) return;
       }
-      if (busy && g4 + 8 * y < s.nv) {
-        float* mw = merge + (warp * 8 + g4) * D;
+      const uint32_t kind = nw >> 1, use = (merges & kind) ? 1 : 0;  // 1, 2, 4
+      merges = ((merges & 7) ^ kind) | kind << 3;
+      if (busy) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int z = 0; z < 2 / (ROWS / 8); ++z) {  // wide: row g4 of this pass, else both rows
+          const int yy = kWide ? y : z, row = kWide ? g4 : 2 * t4 + z;
+          if (8 * y + row < s.nv) {
+            float* mw = merge + (warp * 8 + row) * D;
 #pragma unroll
-          for (int i = 0; i < kN; i += 4) {
-            const int ch = ((2 * t4 + e) * (D / 8) + i) >> 2;
-            *reinterpret_cast<float4*>(mw + 4 * chunk_at(g4, ch)) =
-                make_float4(o[i][2 * y + e], o[i + 1][2 * y + e], o[i + 2][2 * y + e], o[i + 3][2 * y + e]);
+            for (int e = 0; e < kRuns; ++e)
+#pragma unroll
+              for (int i = 0; i < D / 8; i += 4) {
+                const int ch = (run_at(e) + i) >> 2;
+                *reinterpret_cast<float4*>(mw + 4 * chunk_at(row, ch)) =
+                    make_float4(out(yy, e, i), out(yy, e, i + 1), out(yy, e, i + 2), out(yy, e, i + 3));
+              }
+            if (first) stats[warp * 8 + row] = make_float4(m[yy], l[yy], E[yy], 0.f);
           }
-        if (t4 == 0) stats[warp * 8 + g4] = make_float4(m[y], l[y], E[y], 0.f);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(base + Ly::kMergeW + bar);
-      ok = mbar_wait(base + Ly::kMergeW + bar, use & 1, wc, kSiteMergeW, ns);
+      ok = mbar_wait(base + Ly::kMergeW + bar, use, wc, kSiteMergeW, ns);
       if (!__all_sync(0xffffffffu, ok)) return;
       const int rows = min(8, s.nv - 8 * y);
       for (int it = (warp - w0) * 32 + lane; it < rows * (D / 4); it += 32 * nw) {
@@ -888,10 +1095,10 @@ __global__ void __launch_bounds__(dec::kThreads, 1)
 // y, for large units) per CTA of the forward: it takes the unit that one began
 // and did not finish.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) fa_cache_merge_kernel(const __grid_constant__ CacheFwdArgs a, int grid) {
+__global__ void __launch_bounds__(512) fa_cache_merge_kernel(const __grid_constant__ CacheFwdArgs a, int grid) {
   __shared__ int s_end;
   __shared__ int s_n;
-  __shared__ int s_slot[257];
+  __shared__ int s_slot[513];
   griddep_wait();
   const int4 d = a.desc[blockIdx.x];
   if (d.x < 0) return;
@@ -909,18 +1116,18 @@ __global__ void __launch_bounds__(256) fa_cache_merge_kernel(const __grid_consta
   __syncthreads();
   const bool part = mark != 0 && at <= s_end;
   const uint32_t bal = __ballot_sync(0xffffffffu, part);
-  __shared__ int s_cnt[8];
+  __shared__ int s_cnt[16];
   if ((tid & 31) == 0) s_cnt[tid >> 5] = __popc(bal);
   __syncthreads();
   int off = 1;
   for (int w = 0; w < (tid >> 5); ++w) off += s_cnt[w];
   if (part) s_slot[off + __popc(bal & ((1u << (tid & 31)) - 1u))] = 2 * at;
   if (tid == 0) s_slot[0] = 2 * c + 1;
-  if (tid == 255) s_n = off + __popc(bal);
+  if (tid == 511) s_n = off + __popc(bal);
   __syncthreads();
   const int n = s_n;
   const int n0 = max(0, min(a.T, a.cu_q[d.x]));
-  for (int it = blockIdx.y * 256 + tid; it < d.w * (D / 4); it += 256 * gridDim.y) {
+  for (int it = blockIdx.y * 512 + tid; it < d.w * (D / 4); it += 512 * gridDim.y) {
     const int row = it / (D / 4), ch = it % (D / 4);
     float M = -INFINITY;
     for (int i = 0; i < n; ++i) M = fmaxf(M, a.part_l[static_cast<long long>(s_slot[i]) * ROWS + row]);

@@ -280,6 +280,37 @@ def test_forward_many_requests():
     _forward_case(lens, new, 16, 1, 2, 64, seed=4)
 
 
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("g,high", ((1, 1), (4, 2), (12, 2), (12, 30)))
+def test_forward_many_pieces_the_same_every_time(d, g, high):
+    """Many units of very different lengths a CTA, so that short pieces run
+    side by side while longer ones wait for their keys: the same bits from
+    every call, and right."""
+    gen = torch.Generator().manual_seed(g + d)
+    R, H, P = 160, 8, 16
+    lens = (torch.randint(0, 40, (R,), generator=gen) ** 2).tolist()
+    new = [min(n, int(x)) for n, x in zip(lens, torch.randint(0, high + 1, (R,), generator=gen))]
+    table, blocks = make_tables(lens, P, seed=g)
+    codes = make_codes(blocks, H, P, d, 1) + make_codes(blocks, H, P, d, 2)
+    k8, ks, v8, vs = codes
+    poison(k8, table, lens)
+    poison(v8, table, lens)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    q = torch.randn(cu[-1], H * g, d, generator=gen).to(torch.bfloat16)
+    args = (q.to(DEV), fa.CacheE4M3(*(t.to(DEV) for t in (k8, v8, ks, vs))), table.to(DEV), i32(lens), i32(cu))
+    o, lse = fa.cache_forward_e4m3(*args)
+    for _ in range(40):
+        o2, lse2 = fa.cache_forward_e4m3(*args)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    fa.check_errors()
+    h = 5  # one kv head of the whole batch against the oracle
+    at, of = slice(h * g, h * g + g), slice(h, h + 1)
+    assert_forward(o[:, at], lse[:, at], q[:, at], (k8[:, of], v8[:, of], ks[:, of], vs[:, of]), table, lens, cu,
+                   d ** -0.5, True, f"d={d} g={g}")
+
+
 def test_forward_wide_groups_and_heads():
     _forward_case([130, 50], [1, 1], 64, 1, 40, 128, seed=5)   # more rows than a tile
     _forward_case([70], [1], 32, 24, 1, 64, seed=6)
