@@ -138,11 +138,18 @@ int cache_append(const void* k, const void* v, long long k_stride, long long v_s
 
 // Query rows of a unit, and with them the kernel, by the average rows a request
 // has per kv head (tokens times the query heads that share it): the few-row
-// kernel with 8 or 16, which reads the keys again for every so many, up to 48,
-// and above the many-row one with 256.
-int unit_rows(int R, int T, int g) {
-  const long long rows = static_cast<long long>(T) * g;
-  return rows <= 8ll * R ? 8 : rows <= 48ll * R ? 16 : prm::kRows;
+// kernel with 8 or 16, which reads the keys again for every so many, or the
+// many-row one with 256.  Measured (us; d = 128, lengths evenly up to 4000 for
+// 64 requests of 8 kv heads, of 8000 for one), rows of 8 / 16 / 256 a unit:
+//   rows per kv head      8               16               24               48
+//   64 requests     63 / 71 / 115   109 / 83 / 116   156 / 134 / 116  295 / 212 / 119
+//   one request     18 / 19 / 27     18 / 22 / 28     19 / 21 / 28     25 / 23 / 28
+// so with few units, where the many-row kernel's start counts, the step up to it
+// comes later.
+int unit_rows(int R, int T, int Hq, int Hkv, int sms) {
+  const long long rows = static_cast<long long>(T) * (Hq / Hkv);
+  const bool few = static_cast<long long>(R) * Hkv * 8 <= sms;
+  return rows <= 8ll * R ? 8 : rows <= (few ? 48ll : 16ll) * R ? 16 : prm::kRows;
 }
 
 // Workspace: the CTAs' marks, then two partials of a unit's query rows per CTA.
@@ -157,7 +164,7 @@ size_t cache_fwd_workspace(int R, int T, int Hq, int Hkv, int d) {
   if ((d != 64 && d != 128) || R <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
   host::Device dev;
   if (host::device(&dev) != FA_OK) return 0;
-  const int rows = unit_rows(R, T, Hq / Hkv), grid = cache_fwd_grid(dev.sms, rows, d);
+  const int rows = unit_rows(R, T, Hq, Hkv, dev.sms), grid = cache_fwd_grid(dev.sms, rows, d);
   return marks_bytes(grid) + static_cast<size_t>(2) * grid * rows * (d + 1) * 4;
 }
 
@@ -195,7 +202,7 @@ int launch_merge(const CacheFwdArgs& a, int grid, int split, cudaStream_t s) {
 template <int D>
 int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, char* ws, const host::Device& dev,
                      cudaStream_t s) {
-  const int unit = unit_rows(a.R, a.T, a.g), grid = cache_fwd_grid(dev.sms, unit, D);
+  const int unit = unit_rows(a.R, a.T, a.Hq, a.Hkv, dev.sms), grid = cache_fwd_grid(dev.sms, unit, D);
   a.desc = reinterpret_cast<int4*>(ws);
   a.cont = reinterpret_cast<int*>(ws + static_cast<size_t>(grid) * 16);
   a.part_o = reinterpret_cast<float*>(ws + marks_bytes(grid));

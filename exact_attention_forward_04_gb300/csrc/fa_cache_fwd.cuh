@@ -53,7 +53,7 @@ constexpr int kWarps = 8;                    // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);  // and the producer
 constexpr int kKeys = 32;                    // keys of a tile
 constexpr int kMeta = 64;                    // tiles whose blocks and scales are held
-constexpr int kUnitCost = 5;                 // a piece's fixed cost, in tiles
+constexpr int kUnitCost = 12;                // a piece's fixed cost, in tiles
 constexpr int kMinCost = 12;                 // least cost of a CTA's range
 constexpr int kWarpScan = 128;               // requests that one warp sums
 constexpr float kInit = -1e30f;              // references before the first key
