@@ -75,12 +75,12 @@ int cache_slots(const SlotArgs& a, int P, cudaStream_t s) {
 
 template <int D>
 void launch_append(const AppendArgs& a, dim3 grid, cudaStream_t s) {
-  const int nv = ((1 << a.sh) * D) / (8 * app::kThreads);  // 1 .. 16
-  if (nv == 16) fa_cache_append_kernel<D, 16><<<grid, app::kThreads, 0, s>>>(a);
-  else if (nv == 8) fa_cache_append_kernel<D, 8><<<grid, app::kThreads, 0, s>>>(a);
-  else if (nv == 4) fa_cache_append_kernel<D, 4><<<grid, app::kThreads, 0, s>>>(a);
-  else if (nv == 2) fa_cache_append_kernel<D, 2><<<grid, app::kThreads, 0, s>>>(a);
-  else fa_cache_append_kernel<D, 1><<<grid, app::kThreads, 0, s>>>(a);
+  const int nv = ((1 << a.sh) * D) / (8 * 128);  // 1 .. 16
+  if (nv == 16) fa_cache_append_kernel<D, 8, 256><<<grid, 256, 0, s>>>(a);
+  else if (nv == 8) fa_cache_append_kernel<D, 8, 128><<<grid, 128, 0, s>>>(a);
+  else if (nv == 4) fa_cache_append_kernel<D, 4, 128><<<grid, 128, 0, s>>>(a);
+  else if (nv == 2) fa_cache_append_kernel<D, 2, 128><<<grid, 128, 0, s>>>(a);
+  else fa_cache_append_kernel<D, 1, 128><<<grid, 128, 0, s>>>(a);
 }
 
 int cache_append(const void* k, const void* v, long long k_stride, long long v_stride, void* k8, void* v8,
@@ -126,8 +126,20 @@ int cache_append(const void* k, const void* v, long long k_stride, long long v_s
   a.Hkv = Hkv;
   a.sh = block_shift(P);
   a.err = dev.index_err;
-  const dim3 grid(static_cast<unsigned>((static_cast<long long>(T) + app::kChunk - 1) / app::kChunk),
-                  static_cast<unsigned>(Hkv), 2);
+  // Tokens and rows of a CTA, by the rows there are for each SM: few of both where
+  // latency counts, more of them where a CTA without a run's start, and the wait
+  // for a run's first rows, cost more (us; 8 kv heads, d = 128, P = 64; single
+  // tokens / prompts):
+  //   tokens     4 x 1          16 x 1         64 x 1         64 x 4
+  //     32      2.6 / 3.4      3.7 / 3.4      5.4 / 3.3      16 / 5.5
+  //    512      7.0 / 6.1      4.6 / 4.6      9.1 / 3.6      30 / 5.9
+  //   2048       21 / 14        13 / 7.5       12 / 4.9      30 / 6.1
+  //  32768        - / 190        - / 79         - / 51        - / 39
+  const long long per_sm = 2ll * T * Hkv / dev.sms;
+  a.chunk = per_sm <= 24 ? 4 : per_sm <= 160 ? 16 : app::kMaxChunk;
+  a.group = per_sm <= 600 ? (2 * Hkv > 65535 ? 2 : 1) : 4;
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(T) + a.chunk - 1) / a.chunk),
+                  static_cast<unsigned>((2 * Hkv + a.group - 1) / a.group));
   if (d == 128) launch_append<128>(a, grid, s);
   else launch_append<64>(a, grid, s);
   const cudaError_t e = cudaGetLastError();

@@ -121,6 +121,31 @@ def test_append_prompts(P, d, H):
     _same(cache, ref, f"P={P} d={d}")
 
 
+@pytest.mark.parametrize("T,H", ((300, 3), (900, 5), (2500, 8), (2500, 19), (9000, 9)))
+@pytest.mark.parametrize("P,d", ((16, 64), (64, 128), (128, 128)))
+def test_append_many_tokens(T, H, P, d):
+    """Runs of one token among longer ones, over all the shares of a call that
+    a CTA takes: few tokens of one head to many of several, K's and V's."""
+    gen = torch.Generator().manual_seed(T + P)
+    slots, block = [], 0
+    while len(slots) < T:
+        kind = int(torch.randint(0, 4, (1,), generator=gen))
+        if kind == 3:
+            slots.append(-1)
+            continue
+        n = 1 if kind == 0 else int(torch.randint(2, 3 * P, (1,), generator=gen))
+        at = block * P + int(torch.randint(0, P, (1,), generator=gen))
+        slots += range(at, at + n)
+        block = (at + n + P - 1) // P + 1  # no block is met twice
+    slots = slots[:T]
+    cache = _random_cache(block, H, P, d, seed=T)
+    k, v = _rows(T, H, d, 1), _rows(T, H, d, 2)
+    ref = _append_ref(k, v, cache, slots, P)
+    fa.cache_append_e4m3(k, v, cache, torch.tensor(slots, device=DEV))
+    fa.check_errors()
+    _same(cache, ref, f"T={T} H={H} P={P} d={d}")
+
+
 @pytest.mark.parametrize("P,d", ((16, 128), (128, 64)))
 def test_append_token_by_token(P, d):
     """Two blocks filled one token at a time, magnitudes rising and falling."""
