@@ -72,7 +72,7 @@ constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for B
 
 enum : unsigned { kSiteSegFull = 521, kSiteSegEmpty = 522, kSiteQFull = 523, kSiteQEmpty = 524, kSiteKFull = 525,
                   kSiteKEmpty = 526, kSiteVFull = 527, kSiteVEmpty = 528, kSiteS = 529, kSiteP = 530, kSitePV = 531,
-                  kSiteScales = 532, kSiteRawFull = 533, kSiteRawEmpty = 534 };
+                  kSiteScales = 532, kSiteRawFull = 533, kSiteRawEmpty = 534, kSiteJoin = 535 };
 
 template <int D>
 struct Layout {
@@ -90,7 +90,8 @@ struct Layout {
   static constexpr int kKs = kRowScale + kRows * 4;        // float [4][8]: K scale, -1: no block
   static constexpr int kLv = kKs + 4 * 8 * 4;                 // float [4][8]: log2 of the V scale
   static constexpr int kClean = kLv + 4 * 8 * 4;              // int [4]: every key of the tile is one to see
-  static constexpr int kSeg = kClean + 4 * 4;
+  static constexpr int kStat = kClean + 4 * 4;                // float4 [2][128]: a row's statistics, of either half
+  static constexpr int kSeg = kStat + 2 * kHalf * 16;
   static constexpr int kBar = (kSeg + kSegs * static_cast<int>(sizeof(dec::Seg)) + 15) & ~15;
   static constexpr int kSegFull = kBar;
   static constexpr int kSegEmpty = kSegFull + 8 * kSegs;
@@ -106,7 +107,8 @@ struct Layout {
   static constexpr int kScales = kPvDone + 32;    // [4]
   static constexpr int kRawFull = kScales + 32;
   static constexpr int kRawEmpty = kRawFull + 8;
-  static constexpr int kFin = kRawEmpty + 8;
+  static constexpr int kJoin = kRawEmpty + 8;     // [4] pairs of softmax warps
+  static constexpr int kFin = kJoin + 32;
   static constexpr int kTmemSlot = kFin + 16;
   static constexpr int kAbort = kTmemSlot + 8;
   static constexpr int kStart = (kAbort + 8 + 15) & ~15;  // int4
@@ -263,7 +265,10 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
     }
     mbar_init(base + Ly::kRawFull, 1);
     mbar_init(base + Ly::kRawEmpty, 4);
-    for (int i = 0; i < 4; ++i) mbar_init(base + Ly::kScales + 8 * i, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(base + Ly::kScales + 8 * i, 1);
+      mbar_init(base + Ly::kJoin + 8 * i, 2);
+    }
     mbar_init(base + Ly::kFin, 1);
     mbar_init(base + Ly::kFin + 8, 1);
     *abort_flag = 0;
@@ -469,7 +474,6 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       auto low = [](uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); };
       const int x = __shfl_sync(0xffffffffu, warp == 15 ? 1 : 0, 0);
       const uint32_t dS = tmem + kColS + x * kHalf, dO = tmem + kColO + x * kHalf;
-      const uint32_t q = low(base + Ly::kQ + x * Ly::kQHalf, 16);
       auto all_wait = [&](int at, uint32_t parity, unsigned site, int item) {
         return __all_sync(0xffffffffu, wait(at, parity, site, item)) != 0;
       };
@@ -478,60 +482,70 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         const int si = ns % kSegs;
         if (!all_wait(Ly::kSegFull + 8 * si, ns / kSegs, kSiteSegFull, ns)) break;
         const int nt = __shfl_sync(0xffffffffu, segs[si].nt, 0), steps = __shfl_sync(0xffffffffu, segs[si].base, 0);
-        const bool mine = __shfl_sync(0xffffffffu, segs[si].nv, 0) > x * kHalf;  // this half has rows
+        const bool two = __shfl_sync(0xffffffffu, segs[si].nv, 0) > kHalf;
         if (nt == 0) break;
         bool ok = all_wait(Ly::kQFull, ns, kSiteQFull, ns);
-        if (ok && mine && cnt > 0) ok = all_wait(Ly::kPvDone + 8 * (2 * x + ((cnt - 1) & 1)), (cnt - 1) >> 1, kSitePV, jt);
+        // rows for both halves: each takes every step; else every other one,
+        // with the same rows
+        const int own = two ? steps : (steps + 1 - x) >> 1;
+        const uint32_t q = low(base + Ly::kQ + (two ? x * Ly::kQHalf : 0), 16);
+        auto step_of = [&](int k) { return two ? k : 2 * k + x; };
+        if (ok && own > 0 && cnt > 0) ok = all_wait(Ly::kPvDone + 8 * (2 * x + ((cnt - 1) & 1)), (cnt - 1) >> 1, kSitePV, jt);
         // i = -1: the first scores only
 #pragma unroll 1
-        for (int i = -1; ok && i < steps; ++i) {
-          const int n = i + 1, tv = jt + (i >> 1), tk = jt + (n >> 1);  // tiles of step i and of step n
-          if (n < steps) {
-            const int buf = (cnt + n) & 1;
-            if ((n & 1) == 0) ok = all_wait(Ly::kKFull + 8 * (tk & 1), tk >> 1, kSiteKFull, tk);
+        for (int i = -1; ok && i < own; ++i) {
+          const int n = i + 1;
+          if (n < own) {
+            const int g = step_of(n), tk = jt + (g >> 1), buf = (cnt + n) & 1;
+            if (!two || (g & 1) == 0) ok = all_wait(Ly::kKFull + 8 * (tk & 1), tk >> 1, kSiteKFull, tk);
             // the buffer's weights, of two steps before, have been multiplied
-            if (ok && mine && i >= 1) ok = all_wait(Ly::kPvDone + 8 * (2 * x + buf), (cnt + i - 1) >> 1, kSitePV, tk);
+            if (ok && i >= 1) ok = all_wait(Ly::kPvDone + 8 * (2 * x + buf), (cnt + i - 1) >> 1, kSitePV, tk);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t k = low(base + Ly::kK + (tk & 1) * Ly::kKTile + (n & 1) * (kStepKeys * 128), 16);
+            const uint32_t k = low(base + Ly::kK + (tk & 1) * Ly::kKTile + (g & 1) * (kStepKeys * 128), 16);
             const uint32_t d = dS + buf * kStepKeys;
             if (dec::elect_one()) {
-              if (mine) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-                  for (int kk = 0; kk < D / 32; ++kk)  // 32 codes of each row
-                    mma_ss_f8(d, desc(q + ((part * Ly::kPart) >> 4) + 2 * kk), desc(k + 2 * kk), idS,
-                              part + kk > 0 ? 1u : 0u);
-                tc_commit(base + Ly::kSFull + 8 * (2 * x + buf));
-              }
-              if ((n & 1) == 1 || n + 1 == steps) tc_commit(base + Ly::kKEmpty + 8 * (tk & 1));
-              if (n + 1 == steps) tc_commit(base + Ly::kQEmpty);  // the last read of Q
+                for (int kk = 0; kk < D / 32; ++kk)  // 32 codes of each row
+                  mma_ss_f8(d, desc(q + ((part * Ly::kPart) >> 4) + 2 * kk), desc(k + 2 * kk), idS,
+                            part + kk > 0 ? 1u : 0u);
+              tc_commit(base + Ly::kSFull + 8 * (2 * x + buf));
+              if (!two || (g & 1) == 1 || g + 1 == steps) tc_commit(base + Ly::kKEmpty + 8 * (tk & 1));
+              if (n + 1 == own) tc_commit(base + Ly::kQEmpty);  // the last read of Q
             }
             __syncwarp();
           }
           if (i >= 0) {
-            const int buf = (cnt + i) & 1;
-            if ((i & 1) == 0) ok = all_wait(Ly::kVFull + 8 * (tv & 1), tv >> 1, kSiteVFull, tv);
-            if (ok && mine) ok = all_wait(Ly::kPFull + 8 * (2 * x + buf), (cnt + i) >> 1, kSiteP, tv);
+            const int g = step_of(i), tv = jt + (g >> 1), buf = (cnt + i) & 1;
+            if (!two || (g & 1) == 0) ok = all_wait(Ly::kVFull + 8 * (tv & 1), tv >> 1, kSiteVFull, tv);
+            if (ok) ok = all_wait(Ly::kPFull + 8 * (2 * x + buf), (cnt + i) >> 1, kSiteP, tv);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t v = low(base + Ly::kV + (tv & 1) * Ly::kVTile + (i & 1) * (kStepKeys * 128), 16384);
+            const uint32_t v = low(base + Ly::kV + (tv & 1) * Ly::kVTile + (g & 1) * (kStepKeys * 128), 16384);
             const uint32_t first = i == 0 ? 0u : 1u, p = dS + buf * kStepKeys;
             if (dec::elect_one()) {
-              if (mine) {
 #pragma unroll
-                for (int kk = 0; kk < kStepKeys / 16; ++kk)
-                  mma_ts(dO, p + 8 * kk, desc(v + static_cast<uint32_t>(kk * 128)), idPV, kk == 0 ? first : 1u);
-                tc_commit(base + Ly::kPvDone + 8 * (2 * x + buf));
-              }
-              if ((i & 1) == 1 || i + 1 == steps) tc_commit(base + Ly::kVEmpty + 8 * (tv & 1));
+              for (int kk = 0; kk < kStepKeys / 16; ++kk)
+                mma_ts(dO, p + 8 * kk, desc(v + static_cast<uint32_t>(kk * 128)), idPV, kk == 0 ? first : 1u);
+              tc_commit(base + Ly::kPvDone + 8 * (2 * x + buf));
+              if (!two || (g & 1) == 1 || g + 1 == steps) tc_commit(base + Ly::kVEmpty + 8 * (tv & 1));
             }
             __syncwarp();
           }
         }
+        if (ok && !two && x == 1 && (steps & 1)) {
+          // a last tile without a step of this half, freed in its own phase
+          const int t = jt + (steps >> 1);
+          ok = all_wait(Ly::kKFull + 8 * (t & 1), t >> 1, kSiteKFull, t);
+          if (ok && lane == 0) mbar_arrive(base + Ly::kKEmpty + 8 * (t & 1));
+          if (ok && lane == 0 && own == 0) mbar_arrive(base + Ly::kQEmpty);
+          ok = ok && all_wait(Ly::kVFull + 8 * (t & 1), t >> 1, kSiteVFull, t);
+          if (ok && lane == 0) mbar_arrive(base + Ly::kVEmpty + 8 * (t & 1));
+        }
         if (!ok) break;
-        if (mine) cnt += steps;
+        cnt += own;
         jt += nt;
         if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
       }
@@ -666,7 +680,6 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
     reg_inc<168>();
     // ------------------------------------------------ softmax and epilogue
     const int x = warp >> 2;  // half
-    const int row = tid;      // of the unit: 128 x + TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + kColS + x * kHalf, tO = tmem + lane_off + kColO + x * kHalf;
     constexpr int G = GROUP < kStepKeys ? GROUP : kStepKeys;
@@ -680,14 +693,20 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       const Seg& s = segs[si];
       const int nt = s.nt;
       if (nt == 0) break;
-      // no wait is left out for a piece without rows in this half: a phase
+      // Rows for both halves: each takes every step, of its own rows.  Else
+      // both have the same rows, A the even steps and B the odd ones, and join
+      // at the end.
+      const bool two = s.nv > kHalf;
+      const int own = two ? s.base : (s.base + 1 - x) >> 1;
+      const int row = two ? tid : tid & (kHalf - 1);  // of the unit
+      // no wait is left out for a piece without a step of this half: a phase
       // that a warp never saw could pass for a later one of the same parity
       ok = wait(Ly::kQFull, ns, kSiteQFull, ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       const float c = lds_f32(base + Ly::kRowScale + 4 * row);
       __syncwarp();
       if (lane == 0) mbar_arrive(base + Ly::kQEmpty);
-      if (x == 1 && s.nv <= kHalf) {
+      if (own == 0) {
         jt += nt;
         if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
         continue;
@@ -697,9 +716,8 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       const int all = __reduce_min_sync(0xffffffffu, lim);
       float m = kInit, e = 0.f, l = 0.f;  // e: the second reference less the first
       bool far = false;
-      const int steps = s.base;
-      for (int i = 0; i < steps; ++i, ++cnt) {
-        const int tile = jt + (i >> 1), buf = 2 * x + (cnt & 1);
+      for (int i = 0; i < own; ++i, ++cnt) {
+        const int step = two ? i : 2 * i + x, tile = jt + (step >> 1), buf = 2 * x + (cnt & 1);
         // (the scales of a tile are never replaced before its scores are read)
         ok = wait(Ly::kSFull + 8 * buf, cnt >> 1, kSiteS, tile) &&
              wait(Ly::kScales + 8 * (tile & 3), tile >> 2, kSiteScales, tile);
@@ -709,10 +727,10 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         uint32_t v[2][32];
         float mx[2];  // of each 32 keys
         // scales of 16-key group y
-        const uint32_t scales = base + Ly::kKs + (tile & 3) * 32 + (i & 1) * 16;
+        const uint32_t scales = base + Ly::kKs + (tile & 3) * 32 + (step & 1) * 16;
         auto ks_at = [&](int y) { return lds_f32(scales + 4 * y); };
         auto lv_at = [&](int y) { return lds_f32(scales + (Ly::kLv - Ly::kKs) + 4 * y); };
-        const int key0 = s.t0 * kKeys + i * kStepKeys;
+        const int key0 = s.t0 * kKeys + step * kStepKeys;
         bool careful = key0 + kStepKeys > all;
         float fk[kGroups], lv[kGroups];
 #pragma unroll
@@ -844,41 +862,80 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const bool real = row < s.nv;
+      // The halves' statistics, through shared memory; then each of the two
+      // warps that have a row combines and writes one half of its columns.
+      const bool join = !two && s.base > 1;
+      float f = 1.f, f2 = 0.f;  // what this half's sums and the other's count
+      if (join) {
+        const uint32_t bar = base + Ly::kJoin + 8 * (warp & 3);
+        float4* stat = reinterpret_cast<float4*>(sm + Ly::kStat);
+        stat[x * kHalf + row] = make_float4(m, e, l, 0.f);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+        ok = wait(Ly::kJoin + 8 * (warp & 3), 0, kSiteJoin, jt);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const float4 b = stat[(1 - x) * kHalf + row];
+        const float m1 = fmaxf(m, b.x), e0 = e + (m - m1), eb = b.y + (b.x - m1), e1 = fmaxf(e0, eb);
+        l = l * ex2(m - m1) + b.z * ex2(b.x - m1);
+        f = ex2(e0 - e1);
+        f2 = ex2(eb - e1);
+        m = m1;
+        e = e1;
+      }
       const float inv = l == 0.f ? 0.f : ex2(e - kBias) / l;
       const float lg = l == 0.f ? -INFINITY : m + log2f(l);
+      f *= inv;
+      f2 *= inv;
       const int rr = s.row0 + row, tk = rr / a.g;
       const long long at = static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
       const long long pat = static_cast<long long>(s.slot) * kRows + row;
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
+      for (int q = join ? x * (D / 64) : 0; q < (join && x == 0 ? D / 64 : D / 32); ++q) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * q, o);
         tmem_ld_wait32(o);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+        if (join) {
+          uint32_t o2[32];
+          tmem_ld32(tO + (kHalf - 2 * x * kHalf) + 32 * q, o2);
+          tmem_ld_wait32(o2);
+#pragma unroll
+          for (int y = 0; y < 32; ++y)
+            o[y] = __float_as_uint(fmaf(__uint_as_float(o2[y]), f2, __uint_as_float(o[y])));
+        }
         if (real) {
           if (s.mode == 0) {
             uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + 32 * q);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               dst[e] = make_uint4(
-                  pack_bf16(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv),
-                  pack_bf16(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv),
-                  pack_bf16(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv),
-                  pack_bf16(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv));
+                  pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
+                  pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
+                  pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
+                  pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
           } else {
             float4* dst = reinterpret_cast<float4*>(a.part_o + pat * D + 32 * q);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                   __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+              dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
           }
         }
       }
-      if (real) {
+      if (real && (two || x == 0)) {
         if (s.mode == 0) a.lse[at] = lg * 0.6931471805599453f;
         else a.part_l[pat] = lg;
       }
       tc_fence_before();  // O has been read: the next piece's first product may overwrite it
       __syncwarp();
+      if (join) {  // by the other warp, too
+        if (lane == 0) mbar_arrive(base + Ly::kJoin + 8 * (warp & 3));
+        ok = wait(Ly::kJoin + 8 * (warp & 3), 1, kSiteJoin, jt);
+        if (!__all_sync(0xffffffffu, ok)) break;
+      }
       if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
     }
   }
