@@ -83,10 +83,12 @@ struct Layout {
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kQHalf;          // [2]
   static constexpr int kV = kK + 2 * kKTile;     // [2]
-  static constexpr int kStaged = kV + 2 * kVTile;             // bf16 rows of one half of Q
-  static constexpr int kRaw = kStaged + kHalf * D * 2;        // codes of the next tile of V
-  static constexpr int kScan = kRaw;                          // before the first: long long [33]
-  static constexpr int kRowScale = kRaw + kKeys * D;          // float [256]
+  static constexpr int kRawTile = kKeys * D;                  // codes of a tile of V, as they lie
+  static constexpr int kRaw = kV + 2 * kVTile;                // [3]
+  static constexpr int kStaged = kRaw;                        // over two of them: bf16 rows of one half of Q
+  static constexpr int kScan = kRaw + 2 * kRawTile;           // before the first: long long [33]
+  static constexpr int kRowScale = kRaw + 3 * kRawTile;       // float [256]
+  static_assert(kHalf * D * 2 == 2 * kRawTile, "the staged rows' place");
   static constexpr int kKs = kRowScale + kRows * 4;        // float [4][8]: K scale, -1: no block
   static constexpr int kLv = kKs + 4 * 8 * 4;                 // float [4][8]: log2 of the V scale
   static constexpr int kClean = kLv + 4 * 8 * 4;              // int [4]: every key of the tile is one to see
@@ -106,8 +108,8 @@ struct Layout {
   static constexpr int kPvDone = kPFull + 32;     // [2][2]
   static constexpr int kScales = kPvDone + 32;    // [4]
   static constexpr int kRawFull = kScales + 32;
-  static constexpr int kRawEmpty = kRawFull + 8;
-  static constexpr int kJoin = kRawEmpty + 8;     // [4] pairs of softmax warps
+  static constexpr int kRawEmpty = kRawFull + 24;
+  static constexpr int kJoin = kRawEmpty + 24;    // [4] pairs of softmax warps
   static constexpr int kFin = kJoin + 32;
   static constexpr int kTmemSlot = kFin + 16;
   static constexpr int kAbort = kTmemSlot + 8;
@@ -192,6 +194,9 @@ __device__ __forceinline__ void codes16(uint4 c, uint4& lo, uint4& hi) {
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Those before the last copies_end, or all.
+__device__ __forceinline__ void copies_but_last() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
@@ -263,8 +268,10 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         mbar_init(base + Ly::kPvDone + 8 * (2 * i + b), 1);
       }
     }
-    mbar_init(base + Ly::kRawFull, 1);
-    mbar_init(base + Ly::kRawEmpty, 4);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(base + Ly::kRawFull + 8 * i, 1);
+      mbar_init(base + Ly::kRawEmpty + 8 * i, 4);
+    }
     for (int i = 0; i < 4; ++i) {
       mbar_init(base + Ly::kScales + 8 * i, 1);
       mbar_init(base + Ly::kJoin + 8 * i, 2);
@@ -383,12 +390,15 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       }
     } else if (warp == 14) {
       // ------------------------------------------------------- the loader
-      // Codes of a tile's blocks, as they lie, into the raw buffers; its
-      // scales, fetched while the tile before is converted.
+      // Codes of a tile's blocks, K's to their place, V's as they lie into a
+      // raw buffer; its scales, fetched while the tile before is loaded.  A
+      // piece's tiles take raw buffers 2, 0, 1, 2, ...; 0 and 1 once its
+      // queries, which are staged there, have been read.
       const int unit = min(1 << a.sh, kKeys);  // tokens that lie together
       fence_proxy_async_smem();  // the scan's use of the raw buffer
       if (lane == 0) prefetch_tensormap(&tmK);
       int jt = 0;
+      uint32_t turn = 0;  // bit i: phase of raw buffer i's next use
       bool ok = true;
       for (int ns = 0;; ++ns) {
         const int si = ns % kSegs;
@@ -396,6 +406,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         if (!ok) break;
         const Seg& s = segs[si];
         const int nt = s.nt, h = s.h, len = s.len, t0 = s.t0;
+        const bool two = s.nv > kHalf;
         if (nt == 0) break;
         const int* table = a.table + static_cast<long long>(s.r) * a.M;
         // block of this lane's 16 keys (8 lanes) in tile j; -1: none, -2: no keys
@@ -438,14 +449,24 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           if (issue)
             tma_load_3d(base + Ly::kK + st * Ly::kKTile + lane * 16 * 128, &tmK, base + Ly::kKFull + 8 * st, 0, in_block,
                         static_cast<int>(bh));
-          ok = jt == 0 || wait(Ly::kRawEmpty, jt - 1, kSiteRawEmpty, jt);
+          const int rb = (j + 2) % 3, prev = (j + 1) % 3;
+          // Two tiles ahead, but one with rows for both halves: the
+          // conversions then fall between the softmax's steps (1212 us for
+          // prompts of 3 requests, else 1268; for drafts of 16 44.1 and 40.5).
+          // (A piece of one tile leaves out the wait for its queries.  The next
+          // one's cannot mistake the phase: buffer 2, used in between, was
+          // freed after them.)
+          ok = wait(Ly::kRawEmpty + 8 * rb, (turn >> rb) ^ 1, kSiteRawEmpty, jt) &&
+               (j != 1 || wait(Ly::kQFull, ns, kSiteQFull, ns)) &&
+               (!two || j == 0 || wait(Ly::kRawEmpty + 8 * prev, (turn >> prev) ^ 1, kSiteRawEmpty, jt));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(base + Ly::kRawFull, bytes);
+          if (lane == 0) mbar_arrive_expect_tx(base + Ly::kRawFull + 8 * rb, bytes);
           __syncwarp();
           if (issue)
-            bulk_load_1d(base + Ly::kRaw + lane * 16 * D, v8 + (bh << a.sh) * D + in_block * D,
-                         static_cast<uint32_t>(unit * D), base + Ly::kRawFull);
+            bulk_load_1d(base + Ly::kRaw + rb * Ly::kRawTile + lane * 16 * D, v8 + (bh << a.sh) * D + in_block * D,
+                         static_cast<uint32_t>(unit * D), base + Ly::kRawFull + 8 * rb);
+          turn ^= 1u << rb;
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
@@ -454,7 +475,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       // may be one ahead of V's: a phase that never began ends by its time)
       if (lane == 0 && jt > 0) {
         const uint64_t end = globaltimer_ns() + a.timeout_ns;
-        dec::mbar_drain(base + Ly::kRawFull, (jt - 1) & 1, end);
+        for (int i = 0; i < 3; ++i) dec::mbar_drain(base + Ly::kRawFull + 8 * i, ((turn >> i) ^ 1) & 1, end);
         for (int t = max(0, jt - 2); t < jt; ++t) dec::mbar_drain(base + Ly::kKFull + 8 * (t & 1), (t >> 1) & 1, end);
       }
       if (lane == 0 && !ok) dec::mbar_drain(base + Ly::kKFull + 8 * (jt & 1), (jt >> 1) & 1, globaltimer_ns() + 1000000);
@@ -571,10 +592,9 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
     const bool odd_first = D == 128 && (c16 & 4);
     const uint32_t piece = static_cast<uint32_t>((c16 >> 2) * 16384 + row_lo * 128 +
                                                  ((((c16 & 3) * 2 + (odd_first ? 1 : 0)) ^ (row_lo & 7)) << 4));
-    const uint32_t raw_at = base + Ly::kRaw + ct * 16;
     // one tile; loads four at a time, as one after the other each would wait
     // for its own
-    auto put = [&](int st, int jt, int keys_left) {
+    auto put = [&](int st, int jt, int keys_left, uint32_t raw_at) {
       const uint32_t to0 = base + Ly::kV + st * Ly::kVTile + piece, to1 = to0 ^ 16u;
       const bool clean = reinterpret_cast<const volatile int*>(sm + Ly::kClean)[jt & 3] != 0;
 #pragma unroll
@@ -601,6 +621,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       }
     };
     int jt = 0;
+    uint32_t turn = 0;  // bit i: phase of raw buffer i's next use
     for (int ns = 0;; ++ns) {
       const int si = ns % kSegs;
       bool ok = wait(Ly::kSegFull + 8 * si, ns / kSegs, kSiteSegFull, ns);
@@ -610,47 +631,82 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       if (nt == 0) break;
       const int h = s.h;
 
-      // Q, half by half: the bf16 rows to a buffer that only the thread that
-      // copied reads, then in two parts to their places
+      // Q, 64 rows at a time: the bf16 rows to raw buffers 0 and 1, once every
+      // warp has read those, each to where only the thread that copied it
+      // reads; then in two parts to their places, with the next 64 on their way.
+      // (128 at a time and without the second copies ahead, two or three rows
+      // of a warp at once: 23000 cycles for 256 rows, a sixth of a piece.)
+      ok = wait(Ly::kRawEmpty, turn ^ 1, kSiteRawEmpty, jt) && wait(Ly::kRawEmpty + 8, (turn >> 1) ^ 1, kSiteRawEmpty, jt);
+      if (!__all_sync(0xffffffffu, ok)) break;
       {
         constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes per row (8 elements each), rows per warp
+        constexpr int kEach = 64 / (4 * kAt);             // rows of a lane
         const int col = lane % kLanes, row_w = cw * kAt + lane / kLanes;
-        const uint32_t staged = base + Ly::kStaged + ct * 16;
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-        for (int half = 0; half < (s.nv > kHalf ? 2 : 1); ++half) {
-#pragma unroll 2
-          for (int i = 0; i < kHalf / (4 * kAt); ++i) {
-            const int row = half * kHalf + row_w + i * 4 * kAt, rr = s.row0 + row, tk = rr / a.g;
-            const bool real = row < s.nv;
-            const long long at = (s.c0 + tk) * a.q_stride + static_cast<long long>(h * a.g + rr - tk * a.g) * D + col * 8;
-            copy16(staged + i * 2048, a.q + (real ? at : 0), real);
+        const int nv = s.nv, chunks = nv > kHalf ? 4 : 2;
+        const int tk0 = s.row0 / a.g, in0 = s.row0 - tk0 * a.g;
+        const float per_g = 1.f / static_cast<float>(a.g);
+        const __nv_bfloat16* q0 = a.q + (s.c0 + tk0) * a.q_stride + static_cast<long long>(h * a.g) * D + col * 8;
+        auto copy = [&](int c) {
+          if (c < chunks) {
+#pragma unroll 4
+            for (int i = 0; i < kEach; ++i) {
+              const int row = c * 64 + row_w + i * 4 * kAt, y = in0 + row;
+              // y / g, of y < g + 256
+              const int tk = a.g > 256 ? (y >= a.g ? 1 : 0) : static_cast<int>((static_cast<float>(y) + 0.5f) * per_g);
+              const bool real = row < nv;
+              const long long at = real ? tk * a.q_stride + static_cast<long long>(y - tk * a.g) * D : 0;
+              copy16(base + Ly::kStaged + (c & 1) * (64 * D * 2) + ct * 16 + i * 2048, q0 + at, real);
+            }
           }
-          if (half == 0) {
-            ok = ns == 0 || wait(Ly::kQEmpty, ns - 1, kSiteQEmpty, ns);
-            ok = __all_sync(0xffffffffu, ok);
-          }
-          copies_done();
-          if (!ok) break;
-#pragma unroll 2
-          for (int i = 0; i < kHalf / (4 * kAt); ++i) {
-            const int rl = row_w + i * 4 * kAt;
-            uint4 w = dec::lds128(staged + i * 2048);
-            uint32_t am = amax2(w.x, amax2(w.y, amax2(w.z, amax2(w.w, 0u))));
+          copies_end();
+        };
+        copy(0);
+        copy(1);
+        ok = ns == 0 || wait(Ly::kQEmpty, ns - 1, kSiteQEmpty, ns);
+        ok = __all_sync(0xffffffffu, ok);
+        for (int c = 0; ok && c < chunks; ++c) {
+          copies_but_last();
+          const uint32_t from = base + Ly::kStaged + (c & 1) * (64 * D * 2) + ct * 16;
+          const uint32_t to = base + Ly::kQ + (c >> 1) * Ly::kQHalf + (c & 1) * (64 * 128) + row_w * 128 +
+                              (((col >> 1) ^ (row_w & 7)) << 4) + (col & 1) * 8;
+          float* row_scale = reinterpret_cast<float*>(sm + Ly::kRowScale) + c * 64 + row_w;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kEach; i0 += 4) {
+            const uint32_t to4 = to + i0 * (4 * kAt * 128);
+            uint4 w[4];
+            uint32_t am[4];
+            if (c * 64 + cw * kAt + i0 * 4 * kAt >= nv) {  // none of the warp's rows exists
 #pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-            // the largest element to [2^7, 2^8): E4M3 holds up to 448
-            const int ex = dec::row_exponent(am << 16) - 7;
-            const float inv = dec::pow2i(-ex);
-            uint2 hi, lo;
-            split4(w.x ^ flip, w.y ^ flip, inv, hi.x, lo.x);
-            split4(w.z ^ flip, w.w ^ flip, inv, hi.y, lo.y);
-            const uint32_t to = base + Ly::kQ + half * Ly::kQHalf + rl * 128 + (((col >> 1) ^ (rl & 7)) << 4) + (col & 1) * 8;
-            sts64(to, hi);
-            sts64(to + Ly::kPart, lo);
-            if (col == 0)
-              reinterpret_cast<float*>(sm + Ly::kRowScale)[half * kHalf + rl] =
-                  fmaxf(fabsf(a.scale_log2) * dec::pow2i(ex), kTiny);
+              for (int i = 0; i < 4; ++i) {
+                sts64(to4 + 4 * kAt * 128 * i, make_uint2(0u, 0u));
+                sts64(to4 + 4 * kAt * 128 * i + Ly::kPart, make_uint2(0u, 0u));
+                if (col == 0) row_scale[(i0 + i) * 4 * kAt] = kTiny;
+              }
+              continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = dec::lds128(from + (i0 + i) * 2048);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) am[i] = amax2(w[i].x, amax2(w[i].y, amax2(w[i].z, amax2(w[i].w, 0u))));
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) am[i] = max(am[i], __shfl_xor_sync(0xffffffffu, am[i], o));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // the largest element to [2^7, 2^8): E4M3 holds up to 448
+              const int ex = dec::row_exponent(am[i] << 16) - 7;
+              const float inv = dec::pow2i(-ex);
+              uint2 hi, lo;
+              split4(w[i].x ^ flip, w[i].y ^ flip, inv, hi.x, lo.x);
+              split4(w[i].z ^ flip, w[i].w ^ flip, inv, hi.y, lo.y);
+              sts64(to4 + 4 * kAt * 128 * i, hi);
+              sts64(to4 + 4 * kAt * 128 * i + Ly::kPart, lo);
+              if (col == 0) row_scale[(i0 + i) * 4 * kAt] = fmaxf(fabsf(a.scale_log2) * dec::pow2i(ex), kTiny);
+            }
           }
+          copy(c + 2);
         }
         if (!ok) break;
       }
@@ -660,17 +716,19 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
 
       for (int j = 0; j < nt; ++j, ++jt) {
         const int st = jt & 1, left = s.len - (s.t0 + j) * kKeys;
-        ok = wait(Ly::kRawFull, jt, kSiteRawFull, jt) &&
+        const int rb = (j + 2) % 3;
+        ok = wait(Ly::kRawFull + 8 * rb, turn >> rb, kSiteRawFull, jt) &&
              (jt < 2 || wait(Ly::kVEmpty + 8 * st, (jt >> 1) - 1, kSiteVEmpty, jt));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        put(st, jt, left);
+        put(st, jt, left, base + Ly::kRaw + rb * Ly::kRawTile + ct * 16);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(base + Ly::kRawEmpty);
+          mbar_arrive(base + Ly::kRawEmpty + 8 * rb);
           mbar_arrive(base + Ly::kVFull + 8 * st);
         }
+        turn ^= 1u << rb;
       }
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
