@@ -154,8 +154,8 @@ int cache_append(const void* k, const void* v, long long k_stride, long long v_s
 // many-row one with 256.  Measured (us; d = 128, lengths evenly up to 4000 for
 // 64 requests of 8 kv heads, of 8000 for one), rows of 8 / 16 / 256 a unit:
 //   rows per kv head      8               16               24               48
-//   64 requests     63 / 71 / 115   109 / 83 / 116   156 / 134 / 116  295 / 212 / 119
-//   one request     18 / 19 / 27     18 / 22 / 28     19 / 21 / 28     25 / 23 / 28
+//   64 requests     63 / 71 / 104   108 / 83 / 104   156 / 134 / 105  295 / 212 / 108
+//   one request     18 / 19 / 23     18 / 22 / 24     19 / 21 / 24     25 / 23 / 25
 // so with few units, where the many-row kernel's start counts, the step up to it
 // comes later.
 int unit_rows(int R, int T, int Hq, int Hkv, int sms) {
@@ -170,7 +170,7 @@ int cache_fwd_grid(int sms, int rows, int d) {
   const int n = sms * dec::ctas_per_sm(d, rows);
   return n < kMaxGrid ? n : kMaxGrid;
 }
-size_t marks_bytes(int grid) { return static_cast<size_t>(grid) * 32; }
+size_t marks_bytes(int grid) { return static_cast<size_t>(grid) * 32 + 16; }  // and to the next 32 bytes
 
 size_t cache_fwd_workspace(int R, int T, int Hq, int Hkv, int d) {
   if ((d != 64 && d != 128) || R <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
@@ -217,7 +217,8 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
   const int unit = unit_rows(a.R, a.T, a.Hq, a.Hkv, dev.sms), grid = cache_fwd_grid(dev.sms, unit, D);
   a.desc = reinterpret_cast<int4*>(ws);
   a.cont = reinterpret_cast<int*>(ws + static_cast<size_t>(grid) * 16);
-  a.part_o = reinterpret_cast<float*>(ws + marks_bytes(grid));
+  // 32-byte stores; ws is aligned to 16
+  a.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + marks_bytes(grid)) & ~static_cast<uintptr_t>(31));
   a.part_l = a.part_o + static_cast<size_t>(2) * grid * unit * D;
   bool* set = g_cache_ready[dev.dev][D == 128];
   int st = FA_OK;

@@ -119,27 +119,37 @@ struct Layout {
   static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
 };
 
-// sum of floor((a i + b) / m) over i < n, all >= 0 (the Euclid-like sum).
-__device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum of floor((a i + b) / m) over i < n, all >= 0 (the Euclid-like sum).  T
+// holds a n + b of every step, at most the first's plus m.
+template <typename T>
+__device__ __forceinline__ long long floor_sum_in(T n, T m, T a, T b) {
   long long s = 0;
   while (n > 0) {
     if (a >= m) {
-      s += n * (n - 1) / 2 * (a / m);
+      s += static_cast<long long>(n) * (n - 1) / 2 * (a / m);
       a %= m;
     }
     if (b >= m) {
-      s += n * (b / m);
+      s += static_cast<long long>(n) * (b / m);
       b %= m;
     }
-    const long long y = a * n + b;
+    const T y = a * n + b;
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const long long t = m;
+    const T t = m;
     m = a;
     a = t;
   }
   return s;
+}
+__device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  // divisions of 64 bits take several times as long: a third of what a CTA
+  // does before its first load
+  if (a * n + b + m < (1ll << 31))
+    return floor_sum_in<unsigned>(static_cast<unsigned>(n), static_cast<unsigned>(m), static_cast<unsigned>(a),
+                                  static_cast<unsigned>(b));
+  return floor_sum_in<long long>(n, m, a, b);
 }
 
 // Keys that the last row of row tile rt sees.
@@ -205,6 +215,13 @@ __device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
 
 __device__ __forceinline__ void sts64(uint32_t at, uint2 v) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(v.x), "r"(v.y) : "memory");
+}
+
+// 32 bytes to global memory, aligned.
+__device__ __forceinline__ void stg256(float* at, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Four bf16 times `inv` as the sum of two E4M3 numbers each.
@@ -975,11 +992,9 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
                   pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
                   pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
           } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + pat * D + 32 * q);
+            // a row a lane: 32 bytes a store, as every row takes a pass of its own
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            for (int e = 0; e < 32; e += 8) stg256(a.part_o + pat * D + 32 * q + e, o + e);
           }
         }
       }
