@@ -62,7 +62,7 @@ constexpr int kHalf = 128;
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kStepKeys = 64;    // of a step: scores, softmax, weights
 constexpr int kSegs = 4;
-constexpr int kUnitCost = 3;     // a piece's fixed cost, in tiles
+constexpr int kUnitCost = 5;     // a piece's fixed cost, in tiles
 constexpr int kMinCost = 6;      // least cost of a CTA's range
 constexpr float kLazy = 4.f;     // log2 a reference may be exceeded by
 constexpr float kBias = 10.f;    // log2 the weights are scaled by
