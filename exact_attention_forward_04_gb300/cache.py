@@ -235,8 +235,8 @@ def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    return _call(dev, stream, _forward, dev, q, q_stride, cache, block_table, seq_lens, cu_q, float(scale), bool(causal),
-                 workspace, R, T, Hq, H, d, blocks, P, M)
+    return _call(dev, stream, _forward, dev, q, q_stride, cache, block_table, seq_lens, cu_q, float(scale),
+                 bool(causal), workspace, R, T, Hq, H, d, blocks, P, M)
 
 
 def _forward(handle, dev, q, q_stride, cache, table, seq_lens, cu_q, scale, causal, ws, R, T, Hq, H, d, blocks, P, M):

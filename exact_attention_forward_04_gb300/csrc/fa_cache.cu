@@ -218,7 +218,8 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
   a.desc = reinterpret_cast<int4*>(ws);
   a.cont = reinterpret_cast<int*>(ws + static_cast<size_t>(grid) * 16);
   // 32-byte stores; ws is aligned to 16
-  a.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + marks_bytes(grid)) & ~static_cast<uintptr_t>(31));
+  const uintptr_t parts = reinterpret_cast<uintptr_t>(ws) + marks_bytes(grid);
+  a.part_o = reinterpret_cast<float*>(parts & ~static_cast<uintptr_t>(31));
   a.part_l = a.part_o + static_cast<size_t>(2) * grid * unit * D;
   bool* set = g_cache_ready[dev.dev][D == 128];
   int st = FA_OK;

@@ -5,11 +5,12 @@
 //
 // over the visible keys j of query i.  The rows of one (request, kv head) are
 // its new tokens times the Hq / Hkv query heads that share the kv head, in
-// tiles of 16; a work unit is one such tile over all of the request's keys.
+// tiles of ROWS, 8 or 16; a work unit is one such tile over all of the request's
+// keys.
 //
 // Work.  The keys of every unit are cut into tiles of 32, and the tiles of
-// all units, in order, into one equal range per CTA (one CTA per SM), so any
-// mix of lengths fills the GPU evenly.  A CTA covers whole units and at most
+// all units, in order and with a fixed cost for each piece, into one equal range
+// per CTA, so any mix of lengths fills the GPU evenly.  A CTA covers whole units and at most
 // two pieces of units, which it leaves as normalised partials with their
 // logsumexp; a second, dependent kernel merges those per row in CTA order.
 //
@@ -19,16 +20,21 @@
 // as codes) through a ring of TMA loads.  A piece belongs to 1, 2, 4 or 8 of
 // the eight other warps, a few tiles each while it is short, so that short pieces
 // run side by side; its warps take the tiles in turn, each with a softmax of
-// its own, and merge through shared memory at the end.  (With all eight warps on
-// every piece a short one cost about 4500 cycles, 20 tiles' worth.)  In a warp
-// a tile goes
+// its own, and merge through shared memory at the end.  In a warp a tile goes
 //   codes -> f16 (exact) -> S = Q K^T -> P -> O += P V
-// by m16n8k16 f16 products with 16 rows per tile: each warp reads its own
+// by m16n8k16 f16 products, with 8 rows S^T = K Q^T and O^T = V^T P^T, half as
+// many (64 requests of 100 to 8192 tokens, 4 rows per kv head: 123 us with 16
+// rows, 113 with 8): each warp reads its own
 // keys straight from shared memory in the product's operand layout, which a
 // choice of which key and which head-dim index each lane takes makes 16-byte
 // reads without bank conflicts (Tok below).  tcgen05 would need the codes
 // converted in shared memory first: twice the traffic of the conversion for
 // rows that fill an eighth of its 128.
+//
+// What bounds it.  DRAM for long keys: 24 requests of 20000 to 32768 tokens, 8
+// kv heads of 128, in 209 us, 6.1 TB/s; the pieces' starts and ends and the
+// last CTA for shorter ones: 64 requests of 30 to 8192 in 104 us (5.3 TB/s).
+// Latency for little work: one request of 1000 in 12 us, two launches.
 //
 // Numbers.  A query row is divided by the power of two of its largest element
 // and held in f16, three bits more than its bf16 has: exact but for elements
@@ -53,7 +59,7 @@ constexpr int kWarps = 8;                    // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);  // and the producer
 constexpr int kKeys = 32;                    // keys of a tile
 constexpr int kMeta = 64;                    // tiles whose blocks and scales are held
-constexpr int kUnitCost = 12;                // a piece's fixed cost, in tiles
+constexpr int kUnitCost = 12;                // a piece's fixed cost, in tiles (5: 114 us for 104)
 constexpr int kMinCost = 12;                 // least cost of a CTA's range
 constexpr int kWarpScan = 128;               // requests that one warp sums
 constexpr float kInit = -1e30f;              // references before the first key

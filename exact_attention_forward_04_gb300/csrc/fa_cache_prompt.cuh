@@ -17,8 +17,8 @@
 // costs what one f16 product would, and K goes from the cache to the tensor
 // cores as it is.  P stays f16, as two parts of it would cost the softmax more
 // than they save; tcgen05 has no product of f16 with E4M3, so four warps turn
-// V's codes into f16 (exact) on their way: bulk copies bring the next tile's
-// to a buffer, as the blocks hold them, and these warps write them out in the
+// V's codes into f16 (exact) on their way: bulk copies bring the next tiles'
+// to buffers, as the blocks hold them, and these warps write them out in the
 // 128-byte-swizzled layout of an MN-major operand.
 //
 // TMEM (512 columns): of each half two buffers of scores, fp32 [128][64], A at
@@ -35,6 +35,16 @@
 // weights multiplied) has a barrier for even and one for odd steps: a wait by
 // parity tells one phase from the next, and those who skip some would be two
 // behind on a single one.
+//
+// A unit with rows for A only (a few tokens, a prompt's end) gives both halves
+// the same rows and alternate steps; at its end they join their sums, each warp
+// reading both accumulators (drafts of 16 requests: 48.5 us with B idle, 44.2).
+//
+// What bounds it: the products' time.  Prompts of 1500 to 4096 tokens of 3
+// requests behind up to 10000, 32 heads on 8 of 128, take 1124 us, 1.33 PFLOP/s
+// of bf16's 1.92; a step's two halves take 1690 cycles, near what its products
+// take alone, as 128 x 64 ones in 8 bits read their A operand for 70 to 90
+// cycles where the sums need 32.
 //
 // Warps: 0-3 softmax and epilogue of A, 4-7 of B, 8-11 codes to f16 (and Q),
 // 12 and 15 issue A's and B's products, 13 walks the range, 14 loads.
@@ -62,7 +72,7 @@ constexpr int kHalf = 128;
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kStepKeys = 64;    // of a step: scores, softmax, weights
 constexpr int kSegs = 4;
-constexpr int kUnitCost = 5;     // a piece's fixed cost, in tiles
+constexpr int kUnitCost = 5;     // a piece's fixed cost, in tiles (3: 1140 us for prompts of 3 requests, 5: 1124)
 constexpr int kMinCost = 6;      // least cost of a CTA's range
 constexpr float kLazy = 4.f;     // log2 a reference may be exceeded by
 constexpr float kBias = 10.f;    // log2 the weights are scaled by
@@ -388,7 +398,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
             s->mode = begins && ends ? 0 : 1;
             s->slot = 2 * blockIdx.x + (begins ? 1 : 0);
             // steps: without the second half of a last tile that no row sees
-          s->base = max(1, min(2 * (t1 - t0), (seen_of(a, q, rt) - t0 * kKeys + kStepKeys - 1) / kStepKeys));
+            s->base = max(1, min(2 * (t1 - t0), (seen_of(a, q, rt) - t0 * kKeys + kStepKeys - 1) / kStepKeys));
             mbar_arrive(base + Ly::kSegFull + 8 * si);
             if (begins && !ends) a.desc[blockIdx.x] = make_int4(r, h, rt, min(kRows, q.n * a.g - rt * kRows));
             if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
@@ -464,8 +474,8 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           // rows of keys without a block keep what they held: their scores
           // are masked
           if (issue)
-            tma_load_3d(base + Ly::kK + st * Ly::kKTile + lane * 16 * 128, &tmK, base + Ly::kKFull + 8 * st, 0, in_block,
-                        static_cast<int>(bh));
+            tma_load_3d(base + Ly::kK + st * Ly::kKTile + lane * 16 * 128, &tmK, base + Ly::kKFull + 8 * st, 0,
+                        in_block, static_cast<int>(bh));
           const int rb = (j + 2) % 3, prev = (j + 1) % 3;
           // Two tiles ahead, but one with rows for both halves: the
           // conversions then fall between the softmax's steps (1212 us for
@@ -495,7 +505,8 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         for (int i = 0; i < 3; ++i) dec::mbar_drain(base + Ly::kRawFull + 8 * i, ((turn >> i) ^ 1) & 1, end);
         for (int t = max(0, jt - 2); t < jt; ++t) dec::mbar_drain(base + Ly::kKFull + 8 * (t & 1), (t >> 1) & 1, end);
       }
-      if (lane == 0 && !ok) dec::mbar_drain(base + Ly::kKFull + 8 * (jt & 1), (jt >> 1) & 1, globaltimer_ns() + 1000000);
+      if (lane == 0 && !ok)
+        dec::mbar_drain(base + Ly::kKFull + 8 * (jt & 1), (jt >> 1) & 1, globaltimer_ns() + 1000000);
     } else {
       // ------------------------------------------------ the issuers, 12 and 15
       // One for each half: the tensor pipe queues little, so whatever one
@@ -528,7 +539,8 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         const int own = two ? steps : (steps + 1 - x) >> 1;
         const uint32_t q = low(base + Ly::kQ + (two ? x * Ly::kQHalf : 0), 16);
         auto step_of = [&](int k) { return two ? k : 2 * k + x; };
-        if (ok && own > 0 && cnt > 0) ok = all_wait(Ly::kPvDone + 8 * (2 * x + ((cnt - 1) & 1)), (cnt - 1) >> 1, kSitePV, jt);
+        if (ok && own > 0 && cnt > 0)
+          ok = all_wait(Ly::kPvDone + 8 * (2 * x + ((cnt - 1) & 1)), (cnt - 1) >> 1, kSitePV, jt);
         // i = -1: the first scores only
 #pragma unroll 1
         for (int i = -1; ok && i < own; ++i) {
@@ -653,7 +665,8 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       // reads; then in two parts to their places, with the next 64 on their way.
       // (128 at a time and without the second copies ahead, two or three rows
       // of a warp at once: 23000 cycles for 256 rows, a sixth of a piece.)
-      ok = wait(Ly::kRawEmpty, turn ^ 1, kSiteRawEmpty, jt) && wait(Ly::kRawEmpty + 8, (turn >> 1) ^ 1, kSiteRawEmpty, jt);
+      ok = wait(Ly::kRawEmpty, turn ^ 1, kSiteRawEmpty, jt) &&
+           wait(Ly::kRawEmpty + 8, (turn >> 1) ^ 1, kSiteRawEmpty, jt);
       if (!__all_sync(0xffffffffu, ok)) break;
       {
         constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes per row (8 elements each), rows per warp

@@ -446,10 +446,13 @@ int fa_cache_append_e4m3(const void* k, const void* v, long long k_stride, long 
  *          bytes, 16-byte aligned.  Contents on entry are ignored.  Calls that may run at
  *          the same time need one each.
  * O and L are those of the exact attention over the cached values, up to the
- * rounding of the softmax weights to f16 in the product with V.  Results do
- * not depend on the order in which blocks run, and are the same from call to
- * call.  Errors as above, and Hq % Hkv != 0, a missing or short workspace, or
- * an output that overlaps an input or another output: FA_ERR_INVALID_ARG.
+ * rounding of the softmax weights to f16 in the product with V, and of query
+ * elements far below their row's largest: by up to 2^-17 of that one, where
+ * requests have more than 16 rows per kv head on average.  Results do not
+ * depend on the order in which blocks run, and are the same from call to call;
+ * those of one request may differ in their last bits from batch to batch.
+ * Errors as above, and Hq % Hkv != 0, a missing or short workspace, or an
+ * output that overlaps an input or another output: FA_ERR_INVALID_ARG.
  * Enqueues one kernel, and a second that merges the parts of requests whose
  * keys were split (launched as a programmatic dependent of the first).
  */
@@ -460,7 +463,7 @@ int fa_cache_fwd_e4m3(const void* q, long long q_stride, const void* k8, const v
                       int causal, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of fa_cache_fwd_e4m3 on the current device for these sizes
- * (about 2.5 MB, 40 MB for batches of prompts); 0 for sizes it has no work for
+ * (about 2.5 MB, 40 MB where requests have many rows); 0 for sizes it has no work for
  * or does not take. */
 size_t fa_cache_fwd_e4m3_workspace_size(int R, int T, int Hq, int Hkv, int d);
 
