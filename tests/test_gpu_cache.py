@@ -397,6 +397,26 @@ def test_forward_query_magnitudes(g):
     assert_forward(o, lse, q, (k8, v8, ks, vs), table, lens, [0, 1, 2, 3, 4], scales, True)
 
 
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("g", (2, 5, 12, 34))
+def test_forward_rows_that_are_not_finite(d, g):
+    """A query row of NaNs and one of infinities leave the others as they are."""
+    lens, P = [100, 300], 32
+    table, blocks = make_tables(lens, P, seed=1)
+    k8, ks = make_codes(blocks, 1, P, d, 2)
+    v8, vs = make_codes(blocks, 1, P, d, 3)
+    cache = fa.CacheE4M3(*(t.to(DEV) for t in (k8, v8, ks, vs)))
+    q = torch.randn(2, g, d, generator=torch.Generator().manual_seed(g)).to(torch.bfloat16)
+    bad = q.clone()
+    bad[0, 0], bad[1, 1] = math.nan, math.inf
+    o, lse = fa.cache_forward_e4m3(bad.to(DEV), cache, table.to(DEV), i32(lens), i32([0, 1, 2]))
+    fa.check_errors()
+    keep = [[h for h in range(g) if h != r] for r in (0, 1)]
+    for r in (0, 1):
+        assert_forward(o[r:r + 1, keep[r]], lse[r:r + 1, keep[r]], q[r:r + 1, keep[r]], (k8, v8, ks, vs),
+                       table[r:r + 1], lens[r:r + 1], [0, 1], d ** -0.5, True, f"row {r}")
+
+
 def test_forward_strided_queries_untouched_rows_and_repeatability():
     lens, new, P, d = [200, 31, 0], [2, 1, 0], 32, 128
     table, blocks = make_tables(lens, P, seed=1)
@@ -540,3 +560,98 @@ def test_other_streams():
         got = fa.cache_forward_e4m3(q, cache, t, sl, cu, stream=stream)
         fa.check_errors(s)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("new", (1, 40))
+def test_cache_of_more_than_4_gib(new):
+    """Blocks whose codes lie beyond 32-bit offsets: the same codes, scales and
+    results as in a small cache, with both kernels of the forward."""
+    H, P, d, g = 8, 128, 128, 4
+    blocks = (1 << 32) // (H * P * d) + 9
+    lens = [150, 300, 40]
+    table, few = make_tables(lens, P, seed=new)
+    far = torch.where(table >= 0, table + blocks - few, table)
+    far[1, 0] = 1  # and one at the start
+    T, cu = 3 * new, [0, new, 2 * new, 3 * new]
+    k, v = _rows(sum(lens), H, d, 1), _rows(sum(lens), H, d, 2)
+    q = _rows(T, H * g, d, 3, -2, 0)
+    out = []
+    for n, tab in ((few, table), (blocks, far)):
+        cache = fa.cache_alloc_e4m3(n, H, P, d)
+        slots = [int(tab[r, i // P]) * P + i % P for r, m in enumerate(lens) for i in range(m)]
+        fa.cache_append_e4m3(k, v, cache, torch.tensor(slots, device=DEV))
+        o, lse = fa.cache_forward_e4m3(q, cache, tab.to(DEV), i32(lens), i32(cu))
+        used = tab[tab >= 0].long().to(DEV)
+        out.append([o, lse] + [t[used] for t in cache])
+    fa.check_errors()
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
+def test_calls_at_once_on_two_streams():
+    """Calls that run side by side, each with a workspace of its own."""
+    jobs = []
+    for i, (lens, new, d) in enumerate((([3000, 900, 50] * 8, 1, 128), ([700, 1200], 150, 64))):
+        table, blocks = make_tables(lens, 32, seed=i)
+        codes = make_codes(blocks, 4, 32, d, i) + make_codes(blocks, 4, 32, d, 9 + i)
+        cache = fa.CacheE4M3(*(codes[j].to(DEV) for j in (0, 2, 1, 3)))
+        cu = [new * r for r in range(len(lens) + 1)]
+        jobs.append((_rows(cu[-1], 8, d, i, -1, 1), cache, table.to(DEV), i32(lens), i32(cu)))
+    want = [fa.cache_forward_e4m3(*job) for job in jobs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(20):
+        for job, s, w in zip(jobs, streams, want):
+            got.append((fa.cache_forward_e4m3(*job, stream=s), w))
+    torch.cuda.synchronize()
+    fa.check_errors()
+    for (o, lse), (ow, lw) in got:
+        assert torch.equal(o, ow) and torch.equal(lse, lw)
+
+
+@pytest.mark.parametrize("d,rows", ((64, 3), (64, 50), (128, 3), (128, 50)))
+def test_queries_as_a_slice_of_a_projection(d, rows):
+    """Queries, keys and values of one tensor, as strided slices; the same as copies."""
+    lens, P, H, g = [rows, rows, rows], 32, 2, 4
+    table, blocks = make_tables(lens, P, seed=d)
+    qkv = _rows(3 * rows, H * (g + 2) + 1, d, rows, -1, 1)
+    q, k, v = qkv[:, :H * g], qkv[:, H * g:H * (g + 1)], qkv[:, H * (g + 1):-1]
+    slots = torch.tensor([int(table[r, i // P]) * P + i % P for r in range(3) for i in range(rows)], device=DEV)
+    cu, out = i32([0, rows, 2 * rows, 3 * rows]), []
+    for x, y, z in ((q, k, v), (q.contiguous(), k.contiguous(), v.contiguous())):
+        cache = fa.cache_alloc_e4m3(blocks, H, P, d)
+        fa.cache_append_e4m3(y, z, cache, slots)
+        out.append((*cache, *fa.cache_forward_e4m3(x, cache, table.to(DEV), i32(lens), cu)))
+    fa.check_errors()
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    codes = [t.cpu() for t in out[0][:4]]
+    assert_forward(out[0][4], out[0][5], q.cpu().contiguous(), codes, table, lens, [0, rows, 2 * rows, 3 * rows],
+                   d ** -0.5, True)
+
+
+def test_captured_prompts_replay_on_other_lengths():
+    """The many-row kernel in a graph: tables, lengths and rows of later batches,
+    shorter ones and padded ones, as eager calls give them."""
+    P, H, g, d, T, R = 64, 2, 4, 128, 200, 3
+    batches = [([500, 30, 90], [100, 10, 90]), ([7, 0, 0], [7, 0, 0]), ([640, 600, 64], [64, 72, 64]),
+               ([130, 129, 1], [130, 0, 1])]
+    gen = torch.Generator().manual_seed(3)
+    cache = fa.CacheE4M3(*(t.to(DEV) for t in (make_codes(40, H, P, d, 1)[0], make_codes(40, H, P, d, 2)[0],
+                                               make_codes(40, H, P, d, 1)[1], make_codes(40, H, P, d, 2)[1])))
+    table, lens, cu = i32([[0] * 10] * R), i32([0] * R), i32([0] * (R + 1))
+    q = torch.zeros(T, H * g, d, dtype=torch.bfloat16, device=DEV)
+    fa.cache_forward_e4m3(q, cache, table, lens, cu)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = fa.cache_forward_e4m3(q, cache, table, lens, cu)
+    for n, new in batches:
+        table.copy_(torch.randperm(40, generator=gen)[:30].reshape(R, 10).to(torch.int32))
+        lens.copy_(i32(n))
+        cu.copy_(i32([0, new[0], new[0] + new[1], sum(new)]))
+        q.copy_(torch.randn(T, H * g, d, generator=gen).to(torch.bfloat16))
+        ow, lw = fa.cache_forward_e4m3(q, cache, table, lens, cu)
+        graph.replay()
+        rows = sum(new)
+        assert torch.equal(o[:rows], ow[:rows]) and torch.equal(lse[:rows], lw[:rows])
+    fa.check_errors()
