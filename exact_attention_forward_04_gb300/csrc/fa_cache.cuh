@@ -266,10 +266,11 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
 // NV: 16-byte vectors per thread of the longest run, P * D / 8 / THREADS.
 //
 // Bound by memory for prompts: 24 of 1 to 4096 tokens, 8 kv heads of 128 in
-// blocks of 64, in 62 us, 5.1 TB/s (152 us with one head a CTA and 16 tokens).
+// blocks of 64, in 58.5 us, 5.4 TB/s (152 us with one head a CTA and 16 tokens;
+// 62 with four CTAs per SM instead of five).
 // By latency for single tokens: 32 of them in 2.3 us, 500 of 16 heads in 5.7 us.
 template <int D, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS) fa_cache_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(THREADS, 640 / THREADS) fa_cache_append_kernel(AppendArgs a) {
   constexpr int kWarps = THREADS / 32;
   __shared__ long long s_slot[app::kMaxChunk + 2];
   __shared__ uint32_t s_max[2][kWarps];
