@@ -165,11 +165,7 @@ int unit_rows(int R, int T, int Hq, int Hkv, int sms) {
 }
 
 // Workspace: the CTAs' marks, then two partials of a unit's query rows per CTA.
-constexpr int kMaxGrid = 512;  // the merge's threads look at a CTA each
-int cache_fwd_grid(int sms, int rows, int d) {
-  const int n = sms * dec::ctas_per_sm(d, rows);
-  return n < kMaxGrid ? n : kMaxGrid;
-}
+int cache_fwd_grid(int sms, int rows, int d) { return sms * dec::ctas_per_sm(d, rows); }
 size_t marks_bytes(int grid) { return static_cast<size_t>(grid) * 32 + 16; }  // and to the next 32 bytes
 
 size_t cache_fwd_workspace(int R, int T, int Hq, int Hkv, int d) {

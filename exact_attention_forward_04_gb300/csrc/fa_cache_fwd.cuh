@@ -267,7 +267,8 @@ struct CacheFwdArgs {
   float* lse;              // [T][Hq]
   float* part_o;           // [2 grid][rows][D]
   float* part_l;           // [2 grid][rows], log2 units
-  int4* desc;              // [grid]: the unit begun and not finished by each CTA
+  int4* desc;              // [grid]: the unit begun and not finished by each CTA: its request's
+                           // first query row (-1: none), kv head, row tile, rows
   int* cont;               // [grid]: 1, 2: holds (the end of) a unit begun before it
   int R, T, Hq, Hkv, g, sh, M, blocks, causal;
   float scale_log2;        // scale * log2(e)
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
             s->w0 = w0;
             s->nw = nw;
             mbar_arrive_expect_tx(base + Ly::kSegFull + 8 * si, static_cast<uint32_t>(nv * D * 2));
-            if (begins && !ends) a.desc[blockIdx.x] = make_int4(r, h, rt, nv);
+            if (begins && !ends) a.desc[blockIdx.x] = make_int4(q.c0, h, rt, nv);
             if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
           }
           __syncwarp();
@@ -1099,60 +1100,76 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
 // Merges the partials of each unit that more than one CTA worked on, in CTA
 // order: L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s.  One CTA (or more, in
 // y, for large units) per CTA of the forward: it takes the unit that one began
-// and did not finish.
+// and did not finish.  Each warp looks up the parts itself, 32 CTAs at a time,
+// and four parts are loaded together: two rounds of loads behind the wait, where
+// a list in shared memory took five and 1.5 to 2 us more.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(512) fa_cache_merge_kernel(const __grid_constant__ CacheFwdArgs a, int grid) {
-  __shared__ int s_end;
-  __shared__ int s_n;
-  __shared__ int s_slot[513];
+  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   griddep_wait();
-  const int4 d = a.desc[blockIdx.x];
+  const int4 d = a.desc[c];
+  const int mark0 = c + 1 + lane < grid ? a.cont[c + 1 + lane] : 0;
   if (d.x < 0) return;
-  const int c = blockIdx.x, tid = threadIdx.x;
-  if (tid == 0) {
-    s_end = grid;
-    s_n = 0;
-  }
-  __syncthreads();
-  // the unit ends in the first CTA behind this one that says so; CTAs in
-  // between may have had nothing to do
-  const int at = c + 1 + tid;
-  const int mark = at < grid ? a.cont[at] : 0;
-  if (mark == 2) atomicMin(&s_end, at);
-  __syncthreads();
-  const bool part = mark != 0 && at <= s_end;
-  const uint32_t bal = __ballot_sync(0xffffffffu, part);
-  __shared__ int s_cnt[16];
-  if ((tid & 31) == 0) s_cnt[tid >> 5] = __popc(bal);
-  __syncthreads();
-  int off = 1;
-  for (int w = 0; w < (tid >> 5); ++w) off += s_cnt[w];
-  if (part) s_slot[off + __popc(bal & ((1u << (tid & 31)) - 1u))] = 2 * at;
-  if (tid == 0) s_slot[0] = 2 * c + 1;
-  if (tid == 511) s_n = off + __popc(bal);
-  __syncthreads();
-  const int n = s_n;
-  const int n0 = max(0, min(a.T, a.cu_q[d.x]));
-  for (int it = blockIdx.y * 512 + tid; it < d.w * (D / 4); it += 512 * gridDim.y) {
+  for (int it0 = blockIdx.y * 512 + (tid & ~31); it0 < d.w * (D / 4); it0 += 512 * gridDim.y) {
+    const int it = min(it0 + lane, d.w * (D / 4) - 1);  // (a warp's last lanes may do its last item again)
     const int row = it / (D / 4), ch = it % (D / 4);
-    float M = -INFINITY;
-    for (int i = 0; i < n; ++i) M = fmaxf(M, a.part_l[static_cast<long long>(s_slot[i]) * ROWS + row]);
-    float L = 0.f;
+    float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
-      const long long p = static_cast<long long>(s_slot[i]) * ROWS + row;
-      const float l = a.part_l[p];
-      const float f = l == -INFINITY ? 0.f : ex2(l - M);
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + p * D + 4 * ch);
-      L += f;
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
+    // the part that was begun here, then those behind up to the one that ends:
+    // CTAs in between may have had nothing to do
+    int first = c, mark = mark0;
+    uint32_t own = 1u;
+    for (bool more = true; more;) {
+      const uint32_t end = __ballot_sync(0xffffffffu, mark == 2);
+      uint32_t parts = __ballot_sync(0xffffffffu, mark != 0);
+      if (end) parts &= (end & (0u - end)) * 2u - 1u;  // up to the first that ends
+      more = end == 0u && first + 33 < grid;
+      while (own | parts) {
+        float l[4];
+        float4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          l[i] = -INFINITY;
+          v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          int slot = -1;
+          if (own) {
+            slot = 2 * c + 1;
+            own = 0u;
+          } else if (parts) {
+            slot = 2 * (first + __ffs(parts));
+            parts &= parts - 1u;
+          }
+          if (slot >= 0) {
+            const long long p = static_cast<long long>(slot) * ROWS + row;
+            l[i] = a.part_l[p];
+            v[i] = *reinterpret_cast<const float4*>(a.part_o + p * D + 4 * ch);
+          }
+        }
+        const float m = fmaxf(fmaxf(M, fmaxf(l[0], l[1])), fmaxf(l[2], l[3]));
+        if (m == -INFINITY) continue;  // rows without a visible key so far
+        const float f = ex2(M - m);
+        M = m;
+        L *= f;
+        acc.x *= f;
+        acc.y *= f;
+        acc.z *= f;
+        acc.w *= f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float g = ex2(l[i] - m);
+          L += g;
+          acc.x += g * v[i].x;
+          acc.y += g * v[i].y;
+          acc.z += g * v[i].z;
+          acc.w += g * v[i].w;
+        }
+      }
+      first += 32;
+      mark = more && first + 1 + lane < grid ? a.cont[first + 1 + lane] : 0;
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const int rr = d.z * ROWS + row, tk = rr / a.g;
-    const long long to = static_cast<long long>(n0 + tk) * a.Hq + d.y * a.g + (rr - tk * a.g);
+    const long long to = static_cast<long long>(d.x + tk) * a.Hq + d.y * a.g + (rr - tk * a.g);
     *reinterpret_cast<uint2*>(a.o + to * D + 4 * ch) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     if (ch == 0) a.lse[to] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;

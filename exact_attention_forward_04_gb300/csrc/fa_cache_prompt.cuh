@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
             // steps: without the second half of a last tile that no row sees
             s->base = max(1, min(2 * (t1 - t0), (seen_of(a, q, rt) - t0 * kKeys + kStepKeys - 1) / kStepKeys));
             mbar_arrive(base + Ly::kSegFull + 8 * si);
-            if (begins && !ends) a.desc[blockIdx.x] = make_int4(r, h, rt, min(kRows, q.n * a.g - rt * kRows));
+            if (begins && !ends) a.desc[blockIdx.x] = make_int4(q.c0, h, rt, min(kRows, q.n * a.g - rt * kRows));
             if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
             ++nseg;
           }
