@@ -332,17 +332,12 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       if (x0 < x + c) break;  // ends: this thread's requests hold x0
       x += c;
     }
-    // and the kv head, the row tile and the place in it
-    const Req q = dec::request<kRows, kKeys>(a, r);
-    const long long per_head = head_cost(a, q);
+    // and the kv head; the walker finds the row tile
+    const long long per_head = head_cost(a, dec::request<kRows, kKeys>(a, r));
     const int h = static_cast<int>((x0 - x) / per_head);
     const long long y = x0 - x - h * per_head;
-    int lo = 0, hi = q.nrt;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cost_before(a, q, mid) <= y) lo = mid; else hi = mid;
-    }
-    *reinterpret_cast<int4*>(sm + Ly::kStart) = make_int4(r, h, lo, static_cast<int>(y - cost_before(a, q, lo)));
+    *reinterpret_cast<int4*>(sm + Ly::kStart) =
+        make_int4(r, h, static_cast<int>(y & 0xffffffffll), static_cast<int>(y >> 32));
   }
   if (warp == 12) {
     tmem_alloc(base + Ly::kTmemSlot, 512);
@@ -358,14 +353,23 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
   if (warp >= 12) {
     reg_dec<80>();
     if (warp == 13) {
+      // --------------------------------------------------------- the walker
+      const int4 at = *reinterpret_cast<const int4*>(sm + Ly::kStart);
+      int r = at.x, h = at.y, rt = 0;
+      Req q = dec::request<kRows, kKeys>(a, r);
+      long long into = static_cast<long long>(at.w) << 32 | static_cast<unsigned>(at.z);
+      // the last row tile whose cost begins at or before it, 32 at a time
+      for (int end = q.nrt; end - rt > 1;) {
+        const int each = (end - rt + 31) / 32, mine = rt + lane * each;
+        const bool before = lane == 0 || (mine < end && cost_before(a, q, mine) <= into);
+        rt += (31 - __clz(__ballot_sync(0xffffffffu, before))) * each;
+        end = min(end, rt + each);
+      }
       if (lane == 0) {
-        // ------------------------------------------------------- the walker
-        const int4 at = *reinterpret_cast<const int4*>(sm + Ly::kStart);
-        int r = at.x, h = at.y, rt = at.z, y = at.w;
+        int y = static_cast<int>(into - cost_before(a, q, rt));
         long long left = x1 - x0;
         int nseg = 0;
         bool ok = true;
-        Req q = dec::request<kRows, kKeys>(a, r);
         while (left > 0) {
           if (rt >= q.nrt) {  // the next kv head, the next request with rows
             rt = 0;
