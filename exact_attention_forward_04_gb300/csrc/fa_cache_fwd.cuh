@@ -32,9 +32,9 @@
 // rows that fill an eighth of its 128.
 //
 // What bounds it.  DRAM for long keys: 24 requests of 20000 to 32768 tokens, 8
-// kv heads of 128, in 209 us, 6.1 TB/s; the pieces' starts and ends and the
-// last CTA for shorter ones: 64 requests of 30 to 8192 in 104 us (5.3 TB/s).
-// Latency for little work: one request of 1000 in 12 us, two launches.
+// kv heads of 128, in 208 us, 6.1 TB/s; the pieces' starts and ends and the
+// last CTA for shorter ones: 64 requests of 30 to 8192 in 102 us (5.4 TB/s).
+// Latency for little work: one request of 1000 in 10.8 us, two launches.
 //
 // Numbers.  A query row is divided by the power of two of its largest element
 // and held in f16, three bits more than its bf16 has: exact but for elements

@@ -40,11 +40,11 @@
 // the same rows and alternate steps; at its end they join their sums, each warp
 // reading both accumulators (drafts of 16 requests: 48.5 us with B idle, 44.2).
 //
-// What bounds it: the products' time.  Prompts of 1500 to 4096 tokens of 3
-// requests behind up to 10000, 32 heads on 8 of 128, take 1124 us, 1.33 PFLOP/s
-// of bf16's 1.92; a step's two halves take 1690 cycles, near what its products
-// take alone, as 128 x 64 ones in 8 bits read their A operand for 70 to 90
-// cycles where the sums need 32.
+// What bounds it: shared memory.  Prompts of 1500 to 4096 tokens of 3 requests
+// behind up to 10000, 32 heads on 8 of 128, take 1116 us, 1.34 PFLOP/s of bf16's
+// 1.92.  A step of both halves takes 1690 cycles; its products compute for 1024
+// and read 128 KB, a 128 x 64 x 32 one in 8 bits 6 KB for 32 cycles of sums, and
+// bringing K and V there is another 40 KB: 1340 cycles at 128 bytes a cycle.
 //
 // Warps: 0-3 softmax and epilogue of A, 4-7 of B, 8-11 codes to f16 (and Q),
 // 12 and 15 issue A's and B's products, 13 walks the range, 14 loads.
