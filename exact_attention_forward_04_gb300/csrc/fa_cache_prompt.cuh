@@ -40,11 +40,15 @@
 // the same rows and alternate steps; at its end they join their sums, each warp
 // reading both accumulators (drafts of 16 requests: 48.5 us with B idle, 44.2).
 //
-// What bounds it: shared memory.  Prompts of 1500 to 4096 tokens of 3 requests
-// behind up to 10000, 32 heads on 8 of 128, take 1116 us, 1.34 PFLOP/s of bf16's
-// 1.92.  A step of both halves takes 1690 cycles; its products compute for 1024
-// and read 128 KB, a 128 x 64 x 32 one in 8 bits 6 KB for 32 cycles of sums, and
-// bringing K and V there is another 40 KB: 1340 cycles at 128 bytes a cycle.
+// What bounds it: the loop from weights to the scores that take their buffer.
+// Prompts of 1500 to 4096 tokens of 3 requests behind up to 10000, 32 heads on 8
+// of 128, take 1116 us, 1.34 PFLOP/s of bf16's 1.92: 1690 cycles a step of 64
+// keys.  The products of both halves take 1260 by themselves (S 48 cycles each,
+// the time to read 6 KB of shared memory, where the sums take 32; PV 64), the
+// softmax 1150 while both run.  But S(i+2) waits for PV(i): 512 cycles for both
+// halves' PV, 270 to learn of it, 770 for both S and 100 to learn of that are
+// 1650.  A third score buffer does not fit tensor memory; halves kept half a step
+// apart, or taking turns at the softmax, were slower (1140 and 1300 us).
 //
 // Warps: 0-3 softmax and epilogue of A, 4-7 of B, 8-11 codes to f16 (and Q),
 // 12 and 15 issue A's and B's products, 13 walks the range, 14 loads.
