@@ -10,9 +10,9 @@
 //
 // Work.  The keys of every unit are cut into tiles of 32, and the tiles of
 // all units, in order and with a fixed cost for each piece, into one equal range
-// per CTA, so any mix of lengths fills the GPU evenly.  A CTA covers whole units and at most
-// two pieces of units, which it leaves as normalised partials with their
-// logsumexp; a second, dependent kernel merges those per row in CTA order.
+// per CTA, so any mix of lengths fills the GPU evenly.  A CTA covers whole units
+// and at most two pieces of units, which it leaves as normalised partials with
+// their logsumexp; a second, dependent kernel merges those per row in CTA order.
 //
 // A CTA.  One producer warp walks the range: it publishes a descriptor and the
 // query rows of each unit piece, reads block tables and scales for 32 tiles at
@@ -23,11 +23,11 @@
 // its own, and merge through shared memory at the end.  In a warp a tile goes
 //   codes -> f16 (exact) -> S = Q K^T -> P -> O += P V
 // by m16n8k16 f16 products, with 8 rows S^T = K Q^T and O^T = V^T P^T, half as
-// many (64 requests of 100 to 8192 tokens, 4 rows per kv head: 123 us with 16
-// rows, 113 with 8): each warp reads its own
+// many (64 requests of 30 to 8192 tokens, 4 rows per kv head: 123 us with 16
+// rows, 113 with 8, before the pieces' cost was set): each warp reads its own
 // keys straight from shared memory in the product's operand layout, which a
 // choice of which key and which head-dim index each lane takes makes 16-byte
-// reads without bank conflicts (Tok below).  tcgen05 would need the codes
+// reads without bank conflicts (tok() below).  tcgen05 would need the codes
 // converted in shared memory first: twice the traffic of the conversion for
 // rows that fill an eighth of its 128.
 //
