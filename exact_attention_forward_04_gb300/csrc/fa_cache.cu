@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -324,7 +325,15 @@ int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8,
   a.M = M;
   a.blocks = blocks;
   a.causal = causal;
+  // A score's factor is a row's power of two (2^-124 to 2^120) times the scale,
+  // times the K scale (2^-100 to 2^120): the scale is brought to [1/4, 1/2) and
+  // the rest of it goes to the K scale, so that both parts stay normal.
   a.scale_log2 = scale * 1.4426950408889634f;
+  int exponent = 0;
+  std::frexp(a.scale_log2, &exponent);
+  const int shift = std::min(26, std::max(-7, -1 - exponent));
+  a.scale_log2 = std::ldexp(a.scale_log2, shift);
+  a.k_unit = std::ldexp(1.f, -shift);
   a.err = dev.err;
   a.index_err = dev.index_err;
   a.timeout_ns = 2000ull * 1000 * 1000;

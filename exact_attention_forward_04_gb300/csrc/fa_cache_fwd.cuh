@@ -271,7 +271,8 @@ struct CacheFwdArgs {
                            // first query row (-1: none), kv head, row tile, rows
   int* cont;               // [grid]: 1, 2: holds (the end of) a unit begun before it
   int R, T, Hq, Hkv, g, sh, M, blocks, causal;
-  float scale_log2;        // scale * log2(e)
+  float scale_log2;        // scale * log2(e) / k_unit
+  float k_unit;            // a power of two that K's scales are multiplied by
   DevError* err;
   DevError* index_err;
   unsigned long long timeout_ns;
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (blk[i] >= 0) {
-          ks[i] = __ldg(a.ks + blk[i]);
+          ks[i] = __ldg(a.ks + blk[i]) * a.k_unit;
           vs[i] = __ldg(a.vs + blk[i]);
         }
       __syncwarp();

@@ -239,6 +239,15 @@ __device__ __forceinline__ void stg256(float* at, const uint32_t* v) {
                : "memory");
 }
 
+// The power of two that a row is divided by, given its largest |element| as
+// bf16 bits.  It takes that one to [2^7, 2^8), as E4M3 holds up to 448; for the
+// smallest rows it stays at 2^-124, so that it and the row's scale are normal:
+// their elements, multiples of 2^-133, are then multiples of 2^-9 with 8 bits at
+// most, which two E4M3 numbers hold exactly.
+__device__ __forceinline__ int split_exponent(uint32_t bf16_abs) {
+  return max(static_cast<int>(bf16_abs >> 7) - 127 - 7, -124);
+}
+
 // Four bf16 times `inv` as the sum of two E4M3 numbers each.
 __device__ __forceinline__ void split4(uint32_t w0, uint32_t w1, float inv, uint32_t& hi, uint32_t& lo) {
   const float f[4] = {__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xffff0000u) * inv,
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane < 8) {
-            reinterpret_cast<float*>(sm + Ly::kKs)[(jt & 3) * 8 + lane] = ks;
+            reinterpret_cast<float*>(sm + Ly::kKs)[(jt & 3) * 8 + lane] = ks * a.k_unit;
             reinterpret_cast<float*>(sm + Ly::kLv)[(jt & 3) * 8 + lane] = fmaxf(log2f(lv), -200.f);
           }
           if (lane == 0) reinterpret_cast<int*>(sm + Ly::kClean)[jt & 3] = clean;
@@ -720,7 +729,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
               for (int i = 0; i < 4; ++i) {
                 sts64(to4 + 4 * kAt * 128 * i, make_uint2(0u, 0u));
                 sts64(to4 + 4 * kAt * 128 * i + Ly::kPart, make_uint2(0u, 0u));
-                if (col == 0) row_scale[(i0 + i) * 4 * kAt] = kTiny;
+                if (col == 0) row_scale[(i0 + i) * 4 * kAt] = 0.f;
               }
               continue;
             }
@@ -734,15 +743,14 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
               for (int i = 0; i < 4; ++i) am[i] = max(am[i], __shfl_xor_sync(0xffffffffu, am[i], o));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              // the largest element to [2^7, 2^8): E4M3 holds up to 448
-              const int ex = dec::row_exponent(am[i] << 16) - 7;
+              const int ex = split_exponent(am[i]);
               const float inv = dec::pow2i(-ex);
               uint2 hi, lo;
               split4(w[i].x ^ flip, w[i].y ^ flip, inv, hi.x, lo.x);
               split4(w[i].z ^ flip, w[i].w ^ flip, inv, hi.y, lo.y);
               sts64(to4 + 4 * kAt * 128 * i, hi);
               sts64(to4 + 4 * kAt * 128 * i + Ly::kPart, lo);
-              if (col == 0) row_scale[(i0 + i) * 4 * kAt] = fmaxf(fabsf(a.scale_log2) * dec::pow2i(ex), kTiny);
+              if (col == 0) row_scale[(i0 + i) * 4 * kAt] = fabsf(a.scale_log2) * dec::pow2i(ex);
             }
           }
           copy(c + 2);

@@ -1,0 +1,111 @@
+"""The 8-bit cache's forward at the ends of its ranges, with the kernel that
+each case takes asserted: query rows, scales and scores of any magnitude, V
+scales far apart, what is out of range, and batches of every kind for the
+many-row kernel.  Against the float64 oracle, within
+``cache_cases.forward_bounds`` where nothing else is said."""
+import math
+
+import pytest
+import torch
+
+import exact_attention_forward_04_gb300 as fa
+import oracle
+from tests.cache_cases import assert_forward, make_codes, make_tables, poison
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+# (query heads per kv head, new tokens of a request) of one request on one kv
+# head, for the three forms: 8 rows a unit, 16, and the many-row kernel
+FORMS = {"few8": (2, 3), "few16": (5, 3), "many": (17, 3)}
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def assert_takes(form, R, T, Hq, H, d):
+    """The form follows from the partials' size: two of a unit's rows per CTA."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = {"few8": 8, "few16": 16, "many": 256}[form]
+    ctas = sms * (2 if form == "few8" and d == 64 else 1)
+    assert fa.cache_forward_workspace_size(R, T, Hq, H, d) == 32 * ctas + 16 + 2 * ctas * rows * (d + 1) * 4
+
+
+def attend(form, q, codes, table, lens, new, scale=None, causal=True, raises=None, **kw):
+    """(o, lse) of the kernel that ``form`` names, cu; ``raises``: the site it reports."""
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    T, Hq, d = q.shape
+    assert_takes(form, len(lens), T, Hq, codes[0].shape[1], d)
+    cache = fa.CacheE4M3(*(t.to(DEV) for t in codes))
+    o, lse = fa.cache_forward_e4m3(q.to(DEV), cache, table.to(DEV), i32(lens), i32(cu), scale=scale, causal=causal,
+                                   **kw)
+    if raises is None:
+        fa.check_errors()
+    else:
+        with pytest.raises(fa.FAError) as e:
+            fa.check_errors()
+        assert e.value.status == -6 and f"site={raises}" in str(e.value)
+    return o, lse, cu
+
+
+def check(form, q, codes, table, lens, new, scale, causal=True, what=""):
+    o, lse, cu = attend(form, q, codes, table, lens, new, scale, causal)
+    return assert_forward(o, lse, q, codes, table, lens, cu, scale, causal, f"{form} {what}")
+
+
+def one_head(blocks, P, d, seed, k_exp=0, v_exp=0):
+    """Random codes of one kv head, scales 2^k_exp and 2^v_exp."""
+    k8, ks = make_codes(blocks, 1, P, d, seed, k_exp + 4, k_exp + 4)
+    v8, vs = make_codes(blocks, 1, P, d, seed + 1, v_exp + 4, v_exp + 4)
+    return k8, v8, ks, vs
+
+
+# ------------------------------------------------- query rows of any magnitude
+
+@pytest.mark.parametrize("m", (127, 126, 123, 122, 121, -118, -119, -120, -123, -126, -130))
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("form", FORMS)
+def test_query_rows_of_any_magnitude(form, d, m):
+    """Rows whose largest element lies in [2^m, 2^(m+1)), m the largest of bf16
+    and below the smallest normal one, beside keys and a scale that bring the
+    scores to a few units; and a row of zeros."""
+    g, n = FORMS[form]
+    lens, P = [70], 32
+    table, blocks = make_tables(lens, P, seed=1)
+    k_exp = -98 if m > 0 else 112
+    codes = one_head(blocks, P, d, 2, k_exp)
+    q = torch.randn(n, g, d, generator=torch.Generator().manual_seed(4), dtype=torch.float64)
+    q = q / q.abs().amax(-1, keepdim=True) * 1.5 * 2.0 ** m
+    q[1, 0] = 0
+    check(form, q.to(torch.bfloat16), codes, table, lens, [n], 2.0 ** -(m + k_exp + 6), what=f"m={m}")
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_a_scale_of_zero_beside_the_largest_keys(form):
+    """Scores of 0 whatever the keys are: the mean of the visible values."""
+    g, n = FORMS[form]
+    lens, P, d = [70], 32, 64
+    table, blocks = make_tables(lens, P, seed=1)
+    codes = one_head(blocks, P, d, 2, 118)
+    q = torch.randn(n, g, d, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    check(form, q, codes, table, lens, [n], 0.0)
+
+
+@pytest.mark.parametrize("d", (64, 128))
+def test_many_rows_of_mixed_magnitude(d):
+    """Rows of tiny, ordinary and huge elements, zeros, and elements far below
+    their row's largest, in one unit."""
+    lens, new, P, g = [90], [30], 32, 2
+    table, blocks = make_tables(lens, P, seed=1)
+    codes = one_head(blocks, P, d, 2, -12)
+    q = torch.randn(30, g, d, generator=torch.Generator().manual_seed(4))
+    q[0] *= 2.0 ** -130
+    q[1] = 0
+    q[2] *= torch.exp2(-torch.arange(d).float())
+    q[3, 1] *= 2.0 ** 100
+    q[4, 0] *= 2.0 ** 126 / q[4, 0].abs().max()
+    check("many", q.to(torch.bfloat16), codes, table, lens, new, 1.0)
