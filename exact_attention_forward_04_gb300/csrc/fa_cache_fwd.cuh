@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
         }
         const float lv[2] = {floor_log2(sc.z), floor_log2(sc.w)};
         float wgt[2][2], up[2];
-        bool grew = false;
+        bool grew = false, apart = false;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const float m1 = fmaxf(m[y], fmaxf(gm[0][y], gm[1][y])), dm = m[y] - m1;
@@ -866,11 +866,13 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
           grew = grew || up[y] != 1.f;
           m[y] = m1;
           E[y] = E1;
-          const float f = ex2(fminf(14.f - E1, 120.f));
+          apart = apart || E1 < fmaxf(fmaxf(lv[0], lv[1]) - 86.f, -106.f);
+          const float f = ex2(14.f - E1);
           wgt[0][y] = f * sc.z;
           wgt[1][y] = f * sc.w;
         }
-        if (__any_sync(0xffffffffu, grew)) {
+        if (__any_sync(0xffffffffu, grew || apart)) {
+          apart = __any_sync(0xffffffffu, apart);
 #pragma unroll
           for (int i = 0; i < kO; ++i)
 #pragma unroll
@@ -880,25 +882,52 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
         }
         // weights, as f16 operands of the product with V
         uint32_t pa[2][4];
+        auto weigh = [&](auto value) {  // of scores x[z] of row y: 2^(x - m), and what it counts in l
 #pragma unroll
-        for (int z = 0; z < kZ; ++z) {
-          float p[2][2];
+          for (int z = 0; z < kZ; ++z) {
+            float p[2][2];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < 2; ++y) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) p[y][e] = ex2(x[z][at(y, e)] - m[y]);
-            l[y] += p[y][0] + p[y][1];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) p[y][e] *= wgt[z < kZ / 2 ? 0 : 1][y];
+              for (int e = 0; e < 2; ++e) p[y][e] = x[z][at(y, e)] - m[y];
+              l[y] += value(z < kZ / 2 ? 0 : 1, y, p[y]);
+            }
+            if constexpr (kWide) {
+              pa[z >> 1][2 * (z & 1)] = pack_f16(p[0][0], p[0][1]);
+              pa[z >> 1][2 * (z & 1) + 1] = pack_f16(p[1][0], p[1][1]);
+            } else {
+              // key g4, rows 2 t4, 2 t4 + 1 -> row g4, keys 2 t4, 2 t4 + 1
+              pa[z][0] = transpose8(pack_f16(p[0][0], p[1][0]));
+              pa[z][1] = transpose8(pack_f16(p[0][1], p[1][1]));
+            }
           }
-          if constexpr (kWide) {
-            pa[z >> 1][2 * (z & 1)] = pack_f16(p[0][0], p[0][1]);
-            pa[z >> 1][2 * (z & 1) + 1] = pack_f16(p[1][0], p[1][1]);
-          } else {
-            // key g4, rows 2 t4, 2 t4 + 1 -> row g4, keys 2 t4, 2 t4 + 1
-            pa[z][0] = transpose8(pack_f16(p[0][0], p[1][0]));
-            pa[z][1] = transpose8(pack_f16(p[0][1], p[1][1]));
-          }
+        };
+        if (!apart) {
+          weigh([&](int gr, int y, float (&p)[2]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[e] = ex2(p[e]);
+            const float sum = p[0] + p[1];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[e] *= wgt[gr][y];
+            return sum;
+          });
+        } else {
+          // A group whose V scale is 2^86 or more above 2^E: its weights' factor
+          // may leave fp32's range, and so may the exponentials, which only
+          // together are below 2^15.  What the factor has above 2^100 goes into
+          // their arguments.
+          weigh([&](int gr, int y, float (&p)[2]) {
+            const float size = gr == 0 ? sc.z : sc.w, a = 14.f - E[y] + lv[gr], over = fmaxf(a - 100.f, 0.f);
+            // size / 2^lv; lv is -127 for 0 and what lies below the normal numbers
+            const float w = ex2(a - over) * (lv[gr] == -127.f ? size * 0x1p127f
+                                                              : __uint_as_float((__float_as_uint(size) & 0x7fffffu) | 0x3f800000u));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[e] = ex2(p[e] + over);
+            const float sum = (p[0] + p[1]) * ex2(-over);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[e] *= w;
+            return sum;
+          });
         }
         // O += P V: lane g4 takes output columns g4 D/8 .. of the keys 2 t4, 2 t4 + 1
 #pragma unroll

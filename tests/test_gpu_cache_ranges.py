@@ -109,3 +109,53 @@ def test_many_rows_of_mixed_magnitude(d):
     q[3, 1] *= 2.0 ** 100
     q[4, 0] *= 2.0 ** 126 / q[4, 0].abs().max()
     check("many", q.to(torch.bfloat16), codes, table, lens, new, 1.0)
+
+
+# ------------------------------------------------------- V scales far apart
+
+def _apart(P, d, n_blocks, zero_scale, big_exp, seed=1):
+    """Codes and table of one request: of three blocks two hold V of zeros (of
+    scale ``zero_scale``) under the best keys, and one V of scale 2^big_exp
+    under keys whose scores are about 132 (log2 units) below, for queries of
+    ones and a scale of 1 / sqrt(d)."""
+    table, blocks = make_tables([n_blocks * P], P, seed=seed)
+    k8, v8, ks, vs = one_head(blocks, P, d, seed)
+    gen = torch.Generator().manual_seed(seed)
+    k8 = torch.randint(0x38, 0x40, k8.shape, generator=gen).to(torch.uint8)  # values 1 .. 1.875
+    ks[:] = 4.0 * 8.0 / math.sqrt(d)
+    for j in range(n_blocks):
+        b = int(table[0, j])
+        if j % 3 == 1:
+            k8[b] |= 0x80
+            v8[b] &= 0xEF  # magnitudes below 2^7
+            vs[b] = 2.0 ** big_exp
+        else:
+            v8[b], vs[b] = 0, zero_scale
+    return (k8, v8, ks, vs), table
+
+
+@pytest.mark.parametrize("P,n_blocks", ((16, 2), (16, 50), (32, 2), (32, 40), (128, 12)))
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("zero_scale,big_exp", ((2.0 ** -100, 14), (2.0 ** -100, 40), (2.0 ** -100, 100),
+                                                (2.0 ** -100, 120), (0.0, 8), (0.0, 90), (1.0, 120)))
+@pytest.mark.parametrize("form", ("few8", "few16"))
+def test_values_of_very_different_scale(form, zero_scale, big_exp, d, P, n_blocks):
+    """Blocks of zeros under the best keys beside blocks of large values far
+    below in score, which make up the whole result."""
+    g, n = FORMS[form]
+    codes, table = _apart(P, d, n_blocks, zero_scale, big_exp)
+    q = torch.ones(n, g, d, dtype=torch.bfloat16)
+    check(form, q, codes, table, [n_blocks * P], [n], 1 / math.sqrt(d), what=f"2^{big_exp}")
+
+
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("zero_scale,big_exp", ((2.0 ** -100, 14), (2.0 ** -100, 110), (0.0, 8)))
+@pytest.mark.parametrize("form", ("few8", "few16"))
+def test_masked_values_of_very_different_scale(form, zero_scale, big_exp, d):
+    """Rows that see a block of zeros only, beside rows that see a key of a
+    block of large values in the same tile as well."""
+    g, n = FORMS[form]
+    P = 16
+    codes, table = _apart(P, d, 2, zero_scale, big_exp)
+    q = torch.ones(n, g, d, dtype=torch.bfloat16)
+    check(form, q, codes, table, [P + n - 2], [n], 1 / math.sqrt(d), what=f"2^{big_exp}")
