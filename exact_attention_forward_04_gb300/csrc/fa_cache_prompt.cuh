@@ -914,8 +914,10 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           // 2^up_g: what the weights of this group carry beside 2^(s - m).
-          // Below 2^-60 they are 0 in f16 whatever it is.
-          const float up_g = fminf(fmaxf(lv[g] + kBias - e, -60.f), 120.f);
+          // Below 2^-60 they are 0 in f16 whatever it is.  It has no upper
+          // bound: together with s - m it is at most kBias + kLazy, and a group
+          // beyond 2^126 counts nothing in l, as its s - m are below -112.
+          const float up_g = fmaxf(lv[g] + kBias - e, -60.f);
           const float f = far ? 1.f : fk[g], nm = far ? up_g : up_g - m;
           const uint64_t f2 = f2_pack(f, f), n2 = f2_pack(nm, nm);
           uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};

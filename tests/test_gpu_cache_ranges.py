@@ -138,7 +138,7 @@ def _apart(P, d, n_blocks, zero_scale, big_exp, seed=1):
 @pytest.mark.parametrize("d", (64, 128))
 @pytest.mark.parametrize("zero_scale,big_exp", ((2.0 ** -100, 14), (2.0 ** -100, 40), (2.0 ** -100, 100),
                                                 (2.0 ** -100, 120), (0.0, 8), (0.0, 90), (1.0, 120)))
-@pytest.mark.parametrize("form", ("few8", "few16"))
+@pytest.mark.parametrize("form", FORMS)
 def test_values_of_very_different_scale(form, zero_scale, big_exp, d, P, n_blocks):
     """Blocks of zeros under the best keys beside blocks of large values far
     below in score, which make up the whole result."""
@@ -150,7 +150,7 @@ def test_values_of_very_different_scale(form, zero_scale, big_exp, d, P, n_block
 
 @pytest.mark.parametrize("d", (64, 128))
 @pytest.mark.parametrize("zero_scale,big_exp", ((2.0 ** -100, 14), (2.0 ** -100, 110), (0.0, 8)))
-@pytest.mark.parametrize("form", ("few8", "few16"))
+@pytest.mark.parametrize("form", FORMS)
 def test_masked_values_of_very_different_scale(form, zero_scale, big_exp, d):
     """Rows that see a block of zeros only, beside rows that see a key of a
     block of large values in the same tile as well."""
