@@ -62,7 +62,10 @@ constexpr int kMeta = 64;                    // tiles whose blocks and scales ar
 constexpr int kUnitCost = 12;                // a piece's fixed cost, in tiles (5: 114 us for 104)
 constexpr int kMinCost = 12;                 // least cost of a CTA's range
 constexpr int kWarpScan = 128;               // requests that one warp sums
-constexpr float kInit = -1e30f;              // references before the first key
+// References before the first key: -FLT_MAX, as scores may lie anywhere above.
+// What is subtracted from it or from a score may then be -inf, which ends as a
+// weight of 0; it is never added to +inf.
+constexpr float kInit = -3.402823466e38f;
 
 enum : unsigned { kSiteStageFull = 501, kSiteStageEmpty = 502, kSiteSegFull = 503, kSiteSegEmpty = 504,
                   kSiteMergeW = 505, kSiteMergeR = 506, kSiteIssued = 507 };

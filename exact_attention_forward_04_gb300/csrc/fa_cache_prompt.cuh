@@ -81,7 +81,7 @@ constexpr int kUnitCost = 5;     // a piece's fixed cost, in tiles (3: 1140 us f
 constexpr int kMinCost = 6;      // least cost of a CTA's range
 constexpr float kLazy = 4.f;     // log2 a reference may be exceeded by
 constexpr float kBias = 10.f;    // log2 the weights are scaled by
-constexpr float kInit = -1e30f;
+using dec::kInit;
 constexpr float kTiny = 1.17549435e-38f;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for B
 

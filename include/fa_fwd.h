@@ -433,8 +433,9 @@ int fa_cache_append_e4m3(const void* k, const void* v, long long k_stride, long 
  * and L = -inf; rows from cu_q[R] on are left as they were.
  *   q    : bf16, row t of head h at q + t * q_stride + h * d (elements),
  *          16-byte aligned, q_stride a multiple of 8 and at least Hq * d (of
- *          no matter for T = 1).  A NaN or infinity leaves its row's results
- *          unspecified, and no other's.
+ *          no matter for T = 1).  A NaN or infinity, a score of 2^126 or more
+ *          either way, or |scale| * |x| * (K scale) of that size leaves its
+ *          row's results unspecified, and no other's.
  *   o    : bf16 [T][Hq][d], 16-byte aligned.  lse: fp32 [T][Hq].
  *   cu_q : int32 [R + 1], ascending from 0 on; R, T >= 0 (0: nothing to do).
  *   Hq a multiple of Hkv; T * Hq and max_blocks * P below 2^31.

@@ -159,3 +159,32 @@ def test_masked_values_of_very_different_scale(form, zero_scale, big_exp, d):
     codes, table = _apart(P, d, 2, zero_scale, big_exp)
     q = torch.ones(n, g, d, dtype=torch.bfloat16)
     check(form, q, codes, table, [P + n - 2], [n], 1 / math.sqrt(d), what=f"2^{big_exp}")
+
+
+# --------------------------------------------- scores near the ends of fp32's
+
+@pytest.mark.parametrize("exp", (101, 110, 124))
+@pytest.mark.parametrize("sign", (-1, 1))
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("form", FORMS)
+def test_scores_of_any_size(form, d, sign, exp):
+    """One key, or equal ones, with a score of +-2^exp: L is that score (plus
+    ln n) and O their values' mean.  All weights are equal, so O is off by
+    their rounding to f16, the sums (2^-18) and bf16's rounding only."""
+    g, n = FORMS[form]
+    P = 32
+    lens, new = [1, 1, 5, 70], [1, 0, n, n]
+    table, blocks = make_tables(lens, P, seed=1)
+    k8, v8, ks, vs = one_head(blocks, P, d, 2)
+    k8[:] = 0x38  # 1.0
+    T, g = sum(new), 30 if form == "many" else g  # (rows of four requests)
+    q = torch.full((T, g, d), sign * 2.0 ** (exp - 6), dtype=torch.bfloat16)
+    scale = 64.0 / d / float(ks[0, 0])
+    o, lse, cu = attend(form, q, (k8, v8, ks, vs), table, lens, new, scale)
+    O, L, A, _, _, _ = oracle.attention_cache(q, k8.numpy(), v8.numpy(), ks.numpy(), vs.numpy(), table.numpy(), lens, cu,
+                                              scale, True)
+    o, lse = o.cpu().double(), lse.cpu().double()
+    # the score: 64 equal terms of a power of two, times log2 e and back, each rounded
+    assert ((lse - L).abs() <= 2.0 ** -21 * L.abs()).all()
+    bound = (2.0 ** -11 + 2.0 ** -18) * A
+    assert ((o - O).abs() <= bound + 2.0 ** -8 * (O.abs() + bound)).all()
