@@ -24,7 +24,7 @@ _I32, _I64, _F32, _U8, _BF16 = torch.int32, torch.int64, torch.float32, torch.ui
 
 class CacheE4M3(NamedTuple):
     """A pool of cache blocks: codes uint8 [blocks, Hkv, P, d], scales fp32
-    [blocks, Hkv], of K and of V."""
+    [blocks, Hkv], finite and not negative, of K and of V."""
     k8: torch.Tensor
     v8: torch.Tensor
     k_scale: torch.Tensor

@@ -26,7 +26,8 @@ __device__ __forceinline__ void record_index_error(DevError* err, unsigned site,
   }
 }
 
-enum : unsigned { kSiteAppendSlot = 601, kSiteFwdBlock = 611, kSiteFwdLen = 612, kSiteFwdRows = 613 };
+enum : unsigned { kSiteAppendSlot = 601, kSiteFwdBlock = 611, kSiteFwdLen = 612, kSiteFwdRows = 613,
+                  kSiteFwdScale = 614 };
 
 // ------------------------------------------------------------------- slots
 

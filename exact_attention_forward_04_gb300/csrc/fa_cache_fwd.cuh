@@ -283,6 +283,12 @@ struct CacheFwdArgs {
 
 namespace dec {
 
+// A block's scales are finite and not negative: the two kernels would take others
+// differently.  Infinity, NaN and what has a sign are the larger bit patterns (0
+// with a sign is made one without).
+constexpr uint32_t kBadScale = 0x7f800000u;
+__device__ __forceinline__ uint32_t scale_bits(float x) { return __float_as_uint(x + 0.f); }
+
 struct Req {
   int c0, n, len, nrt, kt;
 };
@@ -643,6 +649,15 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
         // the scales of these tiles, by the lanes that have them
         if (ok && lane >= i0 && lane < min(fill, i0 + Ly::kIssue)) {
           const int e = pos + lane;
+          if (max(max(scale_bits(ks[0]), scale_bits(vs[0])), max(scale_bits(ks[1]), scale_bits(vs[1]))) >= kBadScale) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (max(scale_bits(ks[i]), scale_bits(vs[i])) >= kBadScale) {  // as if it had no block
+                record_index_error(a.index_err, kSiteFwdScale, mr);
+                ks[i] = vs[i] = 0.f;
+                s_blk[e % kMeta].w &= boxes == 1 ? 0 : ~(1 << i);
+              }
+          }
           s_scales[e % kMeta] = boxes == 1 ? make_float4(ks[0], ks[0], vs[0], vs[0])
                                            : make_float4(ks[0], ks[1], vs[0], vs[1]);
           mbar_arrive(full(e % Ly::kStages));

@@ -463,7 +463,6 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         for (int j = 0; j < nt; ++j, ++jt) {
           const int b = next;
           const bool real = b >= 0 && b < a.blocks;
-          if (b != -2 && !real) record_index_error(a.index_err, kSiteFwdBlock, s.r);
           const long long bh = static_cast<long long>(b) * a.Hkv + h;
           float ks = -1.f, lv = 0.f;
           if (real) {
@@ -473,27 +472,31 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
           next = block_of(j + 1);
           const bool issue = real && ((lane * 16) & (unit - 1)) == 0;
           const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, issue)) * unit * D);
-          const bool clean = __popc(__ballot_sync(0xffffffffu, real)) == 8 && (t0 + j + 1) * kKeys <= len;
           const int st = jt & 1, in_block = ((t0 + j) * kKeys + lane * 16) & ((1 << a.sh) - 1);
           ok = jt < 2 || wait(Ly::kKEmpty + 8 * st, (jt >> 1) - 1, kSiteKEmpty, jt);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane < 8) {
-            reinterpret_cast<float*>(sm + Ly::kKs)[(jt & 3) * 8 + lane] = ks * a.k_unit;
-            reinterpret_cast<float*>(sm + Ly::kLv)[(jt & 3) * 8 + lane] = fmaxf(log2f(lv), -200.f);
-          }
-          if (lane == 0) reinterpret_cast<int*>(sm + Ly::kClean)[jt & 3] = clean;
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(base + Ly::kScales + 8 * (jt & 3));
-            mbar_arrive_expect_tx(base + Ly::kKFull + 8 * st, bytes / D * 128);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(base + Ly::kKFull + 8 * st, bytes / D * 128);
           __syncwarp();
           // rows of keys without a block keep what they held: their scores
           // are masked
           if (issue)
             tma_load_3d(base + Ly::kK + st * Ly::kKTile + lane * 16 * 128, &tmK, base + Ly::kKFull + 8 * st, 0,
                         in_block, static_cast<int>(bh));
+          if (real && max(dec::scale_bits(ks), dec::scale_bits(lv)) >= dec::kBadScale) {  // as if it had no block
+            ks = -1.f;
+            lv = 0.f;
+          }
+          // (one report for both: a second one's code took prompts from 1122 to 1285 us)
+          if (b != -2 && ks < 0.f) record_index_error(a.index_err, real ? kSiteFwdScale : kSiteFwdBlock, s.r);
+          const bool clean = __popc(__ballot_sync(0xffffffffu, ks >= 0.f)) == 8 && (t0 + j + 1) * kKeys <= len;
+          if (lane < 8) {
+            reinterpret_cast<float*>(sm + Ly::kKs)[(jt & 3) * 8 + lane] = ks * a.k_unit;
+            reinterpret_cast<float*>(sm + Ly::kLv)[(jt & 3) * 8 + lane] = fmaxf(log2f(lv), -200.f);
+          }
+          if (lane == 0) reinterpret_cast<int*>(sm + Ly::kClean)[jt & 3] = clean;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(base + Ly::kScales + 8 * (jt & 3));
           const int rb = (j + 2) % 3, prev = (j + 1) % 3;
           // Two tiles ahead, but one with rows for both halves: the
           // conversions then fall between the softmax's steps (1212 us for

@@ -188,3 +188,25 @@ def test_scores_of_any_size(form, d, sign, exp):
     assert ((lse - L).abs() <= 2.0 ** -21 * L.abs()).all()
     bound = (2.0 ** -11 + 2.0 ** -18) * A
     assert ((o - O).abs() <= bound + 2.0 ** -8 * (O.abs() + bound)).all()
+
+
+# ------------------------------------------------------- what is out of range
+
+@pytest.mark.parametrize("bad", (-1.0, -2.0 ** -90, math.nan, math.inf, -math.inf))
+@pytest.mark.parametrize("which", ("k_scale", "v_scale"))
+@pytest.mark.parametrize("P", (16, 64))
+@pytest.mark.parametrize("form", FORMS)
+def test_scales_out_of_range_hide_their_block(form, P, which, bad):
+    """A scale that is negative or not finite is reported, and its block's
+    tokens are not seen, by either kernel."""
+    g, n = FORMS[form]
+    d, lens = 64, [5 * P + 3]
+    table, blocks = make_tables(lens, P, seed=1)
+    k8, v8, ks, vs = one_head(blocks, P, d, 2, -8)
+    q = torch.randn(n, g, d, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    broken = {"k_scale": ks.clone(), "v_scale": vs.clone()}
+    broken[which][int(table[0, 1])] = bad
+    broken[which][int(table[0, 4])] = bad
+    o, lse, cu = attend(form, q, (k8, v8, broken["k_scale"], broken["v_scale"]), table, lens, [n], 0.125, raises=614)
+    rest = torch.tensor([[int(table[0, j]) for j in (0, 2, 3, 5)]], dtype=torch.int32)
+    assert_forward(o, lse, q, (k8, v8, ks, vs), rest, [lens[0] - 2 * P], cu, 0.125, True, form)
