@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
         // block of this lane's 16 keys (8 lanes) in tile j; -1: none, -2: no keys
         auto block_of = [&](int j) {
           const int key = (t0 + j) * kKeys + lane * 16;
-          return lane < 8 && j < nt && key < len ? table[key >> a.sh] : -2;
+          return lane < 8 && j < nt && key < len ? max(-1, table[key >> a.sh]) : -2;
         };
         int next = block_of(0);
         for (int j = 0; j < nt; ++j, ++jt) {

@@ -210,3 +210,20 @@ def test_scales_out_of_range_hide_their_block(form, P, which, bad):
     o, lse, cu = attend(form, q, (k8, v8, broken["k_scale"], broken["v_scale"]), table, lens, [n], 0.125, raises=614)
     rest = torch.tensor([[int(table[0, j]) for j in (0, 2, 3, 5)]], dtype=torch.int32)
     assert_forward(o, lse, q, (k8, v8, ks, vs), rest, [lens[0] - 2 * P], cu, 0.125, True, form)
+
+
+@pytest.mark.parametrize("entry", (-1, -2, -5, -2 ** 31, 2 ** 31 - 1, None))
+@pytest.mark.parametrize("form", FORMS)
+def test_table_entries_out_of_range_hide_their_block(form, entry):
+    """Any number that is no block's (None: the one behind the last block's),
+    alone in a table, is reported and its tokens are not seen."""
+    g, n = FORMS[form]
+    d, P, lens = 64, 16, [83]
+    table, blocks = make_tables(lens, P, seed=1)
+    codes = one_head(blocks, P, d, 2, -8)
+    q = torch.randn(n, g, d, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    wrong = table.clone()
+    wrong[0, 2] = blocks if entry is None else entry
+    o, lse, cu = attend(form, q, codes, wrong, lens, [n], 0.125, raises=611)
+    rest = table[:, [0, 1, 3, 4, 5]]
+    assert_forward(o, lse, q, codes, rest, [lens[0] - P], cu, 0.125, True, form)
