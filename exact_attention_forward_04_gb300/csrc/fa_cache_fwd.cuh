@@ -933,17 +933,20 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
           // A group whose V scale is 2^86 or more above 2^E: its weights' factor
           // may leave fp32's range, and so may the exponentials, which only
           // together are below 2^15.  What the factor has above 2^100 goes into
-          // their arguments.
-          weigh([&](int gr, int y, float (&p)[2]) {
-            const float size = gr == 0 ? sc.z : sc.w, a = 14.f - E[y] + lv[gr], over = fmaxf(a - 100.f, 0.f);
+          // their arguments.  (The scales are read again: held until here, they
+          // would not fit in the registers of two CTAs.)
+          weigh([&](int gr, int y, float (&v)[2]) {
+            const float4 again = s_scales[p % kMeta];
+            const float size = gr == 0 ? again.z : again.w, lv = floor_log2(size);
+            const float a = 14.f - E[y] + lv, over = fmaxf(a - 100.f, 0.f);
             // size / 2^lv; lv is -127 for 0 and what lies below the normal numbers
-            const float w = ex2(a - over) * (lv[gr] == -127.f ? size * 0x1p127f
-                                                              : __uint_as_float((__float_as_uint(size) & 0x7fffffu) | 0x3f800000u));
+            const uint32_t mantissa = (__float_as_uint(size) & 0x7fffffu) | 0x3f800000u;
+            const float w = ex2(a - over) * (lv == -127.f ? size * 0x1p127f : __uint_as_float(mantissa));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) p[e] = ex2(p[e] + over);
-            const float sum = (p[0] + p[1]) * ex2(-over);
+            for (int e = 0; e < 2; ++e) v[e] = ex2(v[e] + over);
+            const float sum = (v[0] + v[1]) * ex2(-over);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) p[e] *= w;
+            for (int e = 0; e < 2; ++e) v[e] *= w;
             return sum;
           });
         }
