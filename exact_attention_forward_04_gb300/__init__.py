@@ -60,6 +60,8 @@ SYMBOLS = {
                              [_c.c_int] * 5 + [_c.c_void_p]),
     "fa_cache_fwd_e4m3": (_c.c_int, [_c.c_void_p, _c.c_longlong] + [_c.c_void_p] * 9 + [_c.c_int] * 8 +
                           [_c.c_float, _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "fa_cache_fwd_e4m3_slots": (_c.c_int, [_c.c_void_p, _c.c_longlong] + [_c.c_void_p] * 10 + [_c.c_int] * 8 +
+                                [_c.c_float, _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "fa_cache_fwd_e4m3_workspace_size": (_c.c_size_t, [_c.c_int] * 5),
     "fa_check_errors": (_c.c_int, [_c.c_void_p]),
     "fa_selftest_wait_timeout": (_c.c_int, [_c.c_uint, _c.c_void_p]),

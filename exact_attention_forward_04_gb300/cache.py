@@ -5,7 +5,7 @@ synchronisation, so that a step can be captured into a CUDA graph:
 
     cu, slots, lens, used = cache_slots(table, lens, new, free, used, P, T)
     cache_append_e4m3(k, v, cache, slots)             # per layer
-    o, lse = cache_forward_e4m3(q, cache, table, lens, cu)
+    o, lse = cache_forward_e4m3(q, cache, table, lens, cu, slot_map=slots)
 
 ``include/fa_fwd.h`` says what each does with every input.
 """
@@ -41,7 +41,8 @@ def _load():
     global _fn
     from . import load_library
     lib = load_library()
-    _fn = (lib.fa_cache_slots, lib.fa_cache_append_e4m3, lib.fa_cache_fwd_e4m3, lib.fa_cache_fwd_e4m3_workspace_size)
+    _fn = (lib.fa_cache_slots, lib.fa_cache_append_e4m3, lib.fa_cache_fwd_e4m3_slots,
+           lib.fa_cache_fwd_e4m3_workspace_size)
     return _fn
 
 
@@ -149,7 +150,9 @@ def cache_slots(block_table, seq_lens, new_lens, free_blocks, free_used, block_t
     [1]) of them gone, num_tokens the length of the slot map.  Returns
     (cu_new int32 [R + 1], slot_map int64 [num_tokens], seq_lens_out int32
     [R], free_used_out int32 [1]).  A request that cannot be served keeps its
-    length and gets slots of -1; slots behind the last request's are -1."""
+    length and gets slots of -1, its rows their place in cu_new; slots behind
+    the last request's are -1.  Where the free blocks run out, every later
+    request that needs one is refused too."""
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be an int32 [R, max_blocks] tensor")
     dev = block_table.device
@@ -211,7 +214,8 @@ def cache_forward_workspace_size(R, T, heads, heads_kv, d) -> int:
     return int((_fn or _load())[3](int(R), int(T), int(heads), int(heads_kv), int(d)))
 
 
-def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal=True, workspace=None, stream=None):
+def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal=True, workspace=None, stream=None,
+                       slot_map=None):
     """Attention of each request's newest tokens over its cached keys.
 
     q bf16 [T, Hq, d] (any stride between tokens), Hq a multiple of the
@@ -219,6 +223,9 @@ def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal
     [R + 1]), its last ones of seq_lens[r] (int32 [R]) cached tokens, whose
     blocks are block_table[r] (int32 [R, max_blocks]).  Returns (o bf16 [T,
     Hq, d], lse fp32 [T, Hq]); rows behind cu_q[R] are not written.
+    ``slot_map`` (int64 [T], of cache_slots): a request that it refused, whose
+    rows' slots are -1, has no keys (o 0, lse -inf); without it the rows of such
+    a request are taken for the last of its older tokens.
     ``workspace`` (a CUDA tensor of cache_forward_workspace_size bytes) may be
     passed to reuse memory; calls that may overlap need one each."""
     dev, (blocks, H, P, d) = _check_cache(cache)
@@ -231,15 +238,18 @@ def cache_forward_e4m3(q, cache, block_table, seq_lens, cu_q, scale=None, causal
     R, M = block_table.shape
     _ints("seq_lens", seq_lens, (R,), dev)
     _ints("cu_q", cu_q, (R + 1,), dev)
+    if slot_map is not None:
+        _ints("slot_map", slot_map, (T,), dev, _I64)
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    return _call(dev, stream, _forward, dev, q, q_stride, cache, block_table, seq_lens, cu_q, float(scale),
+    return _call(dev, stream, _forward, dev, q, q_stride, cache, block_table, seq_lens, cu_q, slot_map, float(scale),
                  bool(causal), workspace, R, T, Hq, H, d, blocks, P, M)
 
 
-def _forward(handle, dev, q, q_stride, cache, table, seq_lens, cu_q, scale, causal, ws, R, T, Hq, H, d, blocks, P, M):
+def _forward(handle, dev, q, q_stride, cache, table, seq_lens, cu_q, slot_map, scale, causal, ws, R, T, Hq, H, d, blocks,
+             P, M):
     o = _empty(T, Hq, d, dtype=_BF16, device=dev)
     lse = _empty(T, Hq, dtype=_F32, device=dev)
     fn = _fn or _load()
@@ -247,8 +257,9 @@ def _forward(handle, dev, q, q_stride, cache, table, seq_lens, cu_q, scale, caus
         ws = _empty(fn[3](R, T, Hq, H, d), dtype=_U8, device=dev)
     st = fn[2](
         q.data_ptr(), q_stride, cache.k8.data_ptr(), cache.v8.data_ptr(), cache.k_scale.data_ptr(),
-        cache.v_scale.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), o.data_ptr(), lse.data_ptr(),
-        R, T, Hq, H, d, blocks, P, M, scale, causal, ws.data_ptr(), ws.numel() * ws.element_size(), handle)
+        cache.v_scale.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
+        None if slot_map is None else slot_map.data_ptr(), o.data_ptr(), lse.data_ptr(), R, T, Hq, H, d, blocks, P, M,
+        scale, causal, ws.data_ptr(), ws.numel() * ws.element_size(), handle)
     if st:
         _failed(st, "fa_cache_fwd_e4m3")
     return o, lse

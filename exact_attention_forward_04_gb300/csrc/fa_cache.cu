@@ -267,9 +267,9 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
 }
 
 int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8, const float* ks, const float* vs,
-              const int* table, const int* seq_lens, const int* cu_q, void* o, float* lse, int R, int T, int Hq,
-              int Hkv, int d, int blocks, int P, int M, float scale, int causal, void* ws, size_t ws_bytes,
-              cudaStream_t s) {
+              const int* table, const int* seq_lens, const int* cu_q, const long long* slot_map, void* o, float* lse,
+              int R, int T, int Hq, int Hkv, int d, int blocks, int P, int M, float scale, int causal, void* ws,
+              size_t ws_bytes, cudaStream_t s) {
   int st = check_cache(Hkv, d, blocks, P);
   if (st != FA_OK) return st;
   if (R < 0 || T < 0 || Hq <= 0 || M <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
@@ -289,6 +289,7 @@ int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8,
                         static_cast<const void*>(seq_lens), static_cast<const void*>(cu_q),
                         static_cast<const void*>(lse)})
     if (misaligned(p, 4)) return FA_ERR_MISALIGNED;
+  if (misaligned(slot_map, 8)) return FA_ERR_MISALIGNED;
   host::Device dev;
   if ((st = host::device(&dev)) != FA_OK) return st;
   const size_t need = cache_fwd_workspace(R, T, Hq, Hkv, d);
@@ -298,7 +299,8 @@ int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8,
   const size_t nq = (static_cast<size_t>(T - 1) * q_stride + row) * 2, no = static_cast<size_t>(T) * row * 2;
   const Range ins[] = {{q, nq}, {k8, nc}, {v8, nc}, {ks, ns}, {vs, ns},
                        {table, static_cast<size_t>(R) * M * 4}, {seq_lens, static_cast<size_t>(R) * 4},
-                       {cu_q, (static_cast<size_t>(R) + 1) * 4}};
+                       {cu_q, (static_cast<size_t>(R) + 1) * 4},
+                       {slot_map, slot_map ? static_cast<size_t>(T) * 8 : 0}};
   const Range outs[] = {{o, no}, {lse, static_cast<size_t>(T) * Hq * 4}, {ws, need}};
   for (int i = 0; i < 3; ++i) {
     for (const Range& in : ins)
@@ -314,6 +316,7 @@ int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8,
   a.table = table;
   a.seq_lens = seq_lens;
   a.cu_q = cu_q;
+  a.slot_map = slot_map;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   a.R = R;
@@ -370,8 +373,18 @@ int fa_cache_fwd_e4m3(const void* q, long long q_stride, const void* k8, const v
                       float* lse, int R, int T, int Hq, int Hkv, int d, int num_blocks, int block_tokens,
                       int max_blocks, float scale, int causal, void* workspace, size_t workspace_bytes,
                       void* stream) {
-  return fa::cache_fwd(q, q_stride, k8, v8, k_scale, v_scale, block_table, seq_lens, cu_q, o, lse, R, T, Hq, Hkv, d,
-                       num_blocks, block_tokens, max_blocks, scale, causal, workspace, workspace_bytes,
+  return fa::cache_fwd(q, q_stride, k8, v8, k_scale, v_scale, block_table, seq_lens, cu_q, nullptr, o, lse, R, T, Hq,
+                       Hkv, d, num_blocks, block_tokens, max_blocks, scale, causal, workspace, workspace_bytes,
+                       static_cast<cudaStream_t>(stream));
+}
+
+int fa_cache_fwd_e4m3_slots(const void* q, long long q_stride, const void* k8, const void* v8, const float* k_scale,
+                            const float* v_scale, const int* block_table, const int* seq_lens, const int* cu_q,
+                            const long long* slot_map, void* o, float* lse, int R, int T, int Hq, int Hkv, int d,
+                            int num_blocks, int block_tokens, int max_blocks, float scale, int causal,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  return fa::cache_fwd(q, q_stride, k8, v8, k_scale, v_scale, block_table, seq_lens, cu_q, slot_map, o, lse, R, T, Hq,
+                       Hkv, d, num_blocks, block_tokens, max_blocks, scale, causal, workspace, workspace_bytes,
                        static_cast<cudaStream_t>(stream));
 }
 

@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
             s->nv = min(kRows, q.n * a.g - rt * kRows);
             s->c0 = q.c0;
             s->n = q.n;
-            s->len = q.len;
+            s->len = dec::keys_of(a, q);
             s->t0 = t0;
             s->nt = t1 - t0;
             s->mode = begins && ends ? 0 : 1;

@@ -371,7 +371,12 @@ size_t fa_attn_unfused_workspace_size(int B, int H, int N, int d);
  * A request that cannot be served is left as it is: its blocks would exceed
  * max_blocks, its tokens num_tokens, or the free blocks do not last for it.
  * Its slots are -1, its seq_lens_out is seq_lens[r], and it takes no block (a
- * request that needs no block is served even when none are left).  Slots
+ * request that needs no block is served even when none are left).  A request
+ * for which the free blocks do not last counts with all it asked for, so that
+ * later ones that need a block are refused too, smaller ones among them.  The
+ * rows of a refused request keep their place in cu_new: fa_cache_fwd_e4m3 would
+ * take them for the last of its older tokens; fa_cache_fwd_e4m3_slots gives
+ * them no keys.  Slots
  * behind cu_new[R] are -1, and so are those in a held block whose table entry
  * is negative.  Negative lengths count as 0.
  *   free_blocks : int32 [num_free], distinct blocks in use by no request.
@@ -465,6 +470,19 @@ int fa_cache_fwd_e4m3(const void* q, long long q_stride, const void* k8, const v
                       const int* seq_lens, const int* cu_q, void* o, float* lse, int R, int T, int Hq,
                       int Hkv, int d, int num_blocks, int block_tokens, int max_blocks, float scale,
                       int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_cache_fwd_e4m3_slots — the same with the slot map of the rows' appends
+ * (int64 [T], 8-byte aligned; NULL: as fa_cache_fwd_e4m3): a request whose first
+ * row's slot is negative, as fa_cache_slots leaves one that it refused, has no
+ * visible key: O = 0, L = -inf.
+ */
+int fa_cache_fwd_e4m3_slots(const void* q, long long q_stride, const void* k8, const void* v8,
+                            const float* k_scale, const float* v_scale, const int* block_table,
+                            const int* seq_lens, const int* cu_q, const long long* slot_map, void* o,
+                            float* lse, int R, int T, int Hq, int Hkv, int d, int num_blocks,
+                            int block_tokens, int max_blocks, float scale, int causal, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of fa_cache_fwd_e4m3 on the current device for these sizes
  * (about 2.5 MB, 40 MB where requests have many rows); 0 for sizes it has no work for

@@ -227,3 +227,63 @@ def test_table_entries_out_of_range_hide_their_block(form, entry):
     o, lse, cu = attend(form, q, codes, wrong, lens, [n], 0.125, raises=611)
     rest = table[:, [0, 1, 3, 4, 5]]
     assert_forward(o, lse, q, codes, rest, [lens[0] - P], cu, 0.125, True, form)
+
+
+@pytest.mark.parametrize("P", (16, 64))
+@pytest.mark.parametrize("form", ("few", "many"))
+def test_refused_requests_are_not_attended(form, P):
+    """A request that cache_slots refuses keeps its length, and its rows their
+    place: with the slot map the forward gives them no keys, where their
+    positions would be those of older tokens.  The others are as ever."""
+    d, H, g, R = 64, 2, 2, 4
+    # table width; new tokens and the refused requests of each step
+    M, steps = {"few": (2, (([5, 2 * P, 7, 2 * P - 1], []), ([1, 1, 2, 1], [1]), ([2, 3, 1, 1], [1, 3]))),
+                "many": (8, (([65, 60, 7, 60], []), ([1, 8 * P, 2, 1], [1]), ([60, 1, 8 * P, 1], [2])))}[form]
+    cache = fa.cache_alloc_e4m3(20, H, P, d)
+    table = torch.full((R, M), -1, dtype=torch.int32, device=DEV)
+    free = i32(list(range(20)))
+    gen = torch.Generator().manual_seed(P)
+
+    def rows(T, heads):
+        return torch.randn(T, heads, d, generator=gen).to(torch.bfloat16)
+
+    lens, used = i32([0] * R), i32([0])
+    for step, (new, refused) in enumerate(steps):
+        T = sum(new) + 2  # two rows of no request
+        before = lens.tolist()
+        cu, slots, lens, used = fa.cache_slots(table, lens, i32(new), free, used, P, T)
+        assert [r for r in range(R) if lens[r] == before[r]] == refused
+        fa.cache_append_e4m3(rows(T, H).to(DEV), rows(T, H).to(DEV), cache, slots)
+        q = rows(T, H * g)
+        if step > 0:
+            assert_takes("few8" if form == "few" else "many", R, T, H * g, H, d)
+        o, lse = fa.cache_forward_e4m3(q.to(DEV), cache, table, lens, cu, slot_map=slots)
+        fa.check_errors()
+        codes = [cache[i].cpu() for i in range(4)]
+        c = cu.tolist()
+        for r in range(R):
+            at = slice(c[r], c[r + 1])
+            if r in refused:
+                assert (o[at] == 0).all() and (lse[at] == -math.inf).all(), f"step {step} request {r}"
+            else:
+                assert_forward(o[at], lse[at], q[at], codes, table[r:r + 1].cpu(), [int(lens[r])], [0, new[r]],
+                               d ** -0.5, True, f"step {step} request {r}")
+
+
+def test_a_slot_map_of_the_wrong_kind_is_refused():
+    cache = fa.cache_alloc_e4m3(2, 1, 16, 64)
+    q = torch.zeros(3, 1, 64, dtype=torch.bfloat16, device=DEV)
+    args = (q, cache, i32([[0, 1]]), i32([5]), i32([0, 3]))
+    with pytest.raises(TypeError, match="slot_map"):
+        fa.cache_forward_e4m3(*args, slot_map=i32([0, 1, 2]))
+    with pytest.raises(ValueError, match="slot_map"):
+        fa.cache_forward_e4m3(*args, slot_map=torch.zeros(4, dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError, match="slot_map"):
+        fa.cache_forward_e4m3(*args, slot_map=torch.zeros(3, dtype=torch.int64))
+    # results over the slot map, by the C entry
+    slots, lse = torch.zeros(3, dtype=torch.int64, device=DEV), torch.zeros(3, 1, device=DEV)
+    o, ws = torch.zeros_like(q), torch.empty(fa.cache_forward_workspace_size(1, 3, 1, 1, 64), dtype=torch.uint8, device=DEV)
+    for out, l2, work in ((slots, lse, ws), (o, slots, ws), (o, lse, slots)):
+        assert fa.load_library().fa_cache_fwd_e4m3_slots(
+            q.data_ptr(), 64, *(c.data_ptr() for c in cache), *(t.data_ptr() for t in args[2:]), slots.data_ptr(),
+            out.data_ptr(), l2.data_ptr(), 1, 3, 1, 1, 64, 2, 16, 2, 0.125, 1, work.data_ptr(), ws.numel(), None) == -1
