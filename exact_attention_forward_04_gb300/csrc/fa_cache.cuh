@@ -75,8 +75,8 @@ struct SlotArgs {
   int R, M, F, sh, T;     // blocks of 2^sh tokens
 };
 
-// One request: tokens held and new, the blocks it needs and whether it fits
-// its table row and the slot map (a request that does not takes no block).
+// One request: tokens held and new, the blocks it needs and whether it fits its
+// table row, the slot map and an int32 length (one that does not takes no block).
 struct SlotReq {
   long long len, add, held, need;
   bool fits;
@@ -88,7 +88,7 @@ __device__ __forceinline__ SlotReq slot_req(const SlotArgs& a, int r, long long 
   const int up = (1 << a.sh) - 1;
   q.held = (q.len + up) >> a.sh;
   const long long want = (q.len + q.add + up) >> a.sh;
-  q.fits = want <= a.M && cu + q.add <= a.T;
+  q.fits = want <= a.M && cu + q.add <= a.T && q.len + q.add <= 0x7fffffffll;
   q.need = q.fits ? want - q.held : 0;
   return q;
 }

@@ -369,7 +369,8 @@ size_t fa_attn_unfused_workspace_size(int B, int H, int N, int d);
  *   seq_lens_out[r] = seq_lens[r] + new_lens[r]
  *   *free_used_out  = *free_used + the number of blocks granted
  * A request that cannot be served is left as it is: its blocks would exceed
- * max_blocks, its tokens num_tokens, or the free blocks do not last for it.
+ * max_blocks, its tokens num_tokens, its length 2^31 - 1, or the free blocks do
+ * not last for it.
  * Its slots are -1, its seq_lens_out is seq_lens[r], and it takes no block (a
  * request that needs no block is served even when none are left).  A request
  * for which the free blocks do not last counts with all it asked for, so that

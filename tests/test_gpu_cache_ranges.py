@@ -287,3 +287,21 @@ def test_a_slot_map_of_the_wrong_kind_is_refused():
         assert fa.load_library().fa_cache_fwd_e4m3_slots(
             q.data_ptr(), 64, *(c.data_ptr() for c in cache), *(t.data_ptr() for t in args[2:]), slots.data_ptr(),
             out.data_ptr(), l2.data_ptr(), 1, 3, 1, 1, 64, 2, 16, 2, 0.125, 1, work.data_ptr(), ws.numel(), None) == -1
+
+
+# -------------------------------------------------------- slots at the ends
+
+def test_slots_of_lengths_near_2_to_the_31():
+    """A request whose length would pass int32 is refused, one just below is served."""
+    P, M = 128, (1 << 24) + 1
+    for length, new, served in ((2 ** 31 - 15, 10, True), (2 ** 31 - 11, 10, True), (2 ** 31 - 10, 10, False),
+                                (2 ** 31 - 5, 10, False), (2 ** 31 - 1, 1, False), (2 ** 31 - 1, 0, True)):
+        table = torch.zeros(1, M, dtype=torch.int32, device=DEV)
+        table[0, (1 << 24) - 1] = 7
+        cu, slots, lens, used = fa.cache_slots(table, i32([length]), i32([new]), i32([5]), i32([0]), P, 12)
+        fa.check_errors()
+        first = 7 * P + length % P
+        want = [first + i if served and i < new else -1 for i in range(12)]
+        assert slots.tolist() == want and cu.tolist() == [0, new], (length, new)
+        assert lens.item() == length + (new if served else 0) and used.item() == 0, (length, new)
+        assert int(table[0, -1]) == 0
