@@ -167,8 +167,8 @@ def cache_slots(block_table, seq_lens, new_lens, free_blocks, free_used, block_t
     if not (isinstance(free_blocks, torch.Tensor) and free_blocks.dtype is _I32 and free_blocks.dim() == 1
             and free_blocks.is_contiguous() and free_blocks.device == dev):
         _check("free_blocks", free_blocks, _I32, (None,), dev)
-    if num_tokens < 0:
-        raise ValueError(f"num_tokens must not be negative, got {num_tokens}")
+    if not 0 <= num_tokens <= 0x7fffffff:
+        raise ValueError(f"num_tokens must be in 0 .. 2^31 - 1, got {num_tokens}")
     return _call(dev, stream, _slots, dev, block_table, seq_lens, new_lens, free_blocks, free_used, R, M, block_tokens,
                  num_tokens)
 

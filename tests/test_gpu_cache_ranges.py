@@ -305,3 +305,10 @@ def test_slots_of_lengths_near_2_to_the_31():
         assert slots.tolist() == want and cu.tolist() == [0, new], (length, new)
         assert lens.item() == length + (new if served else 0) and used.item() == 0, (length, new)
         assert int(table[0, -1]) == 0
+
+
+def test_slots_refuse_a_map_beyond_int32():
+    args = (torch.zeros(1, 4, dtype=torch.int32, device=DEV), i32([0]), i32([1]), i32([5]), i32([0]), 16)
+    for tokens in (2 ** 31, 2 ** 32 + 5, -1):
+        with pytest.raises(ValueError, match="num_tokens"):
+            fa.cache_slots(*args, tokens)
