@@ -312,3 +312,103 @@ def test_slots_refuse_a_map_beyond_int32():
     for tokens in (2 ** 31, 2 ** 32 + 5, -1):
         with pytest.raises(ValueError, match="num_tokens"):
             fa.cache_slots(*args, tokens)
+
+
+# ------------------------------------------------ the many-row kernel's batches
+
+@pytest.mark.parametrize("d", (64, 128))
+@pytest.mark.parametrize("n", (30, 70))
+def test_many_rows_some_not_finite(d, n):
+    """Query rows of NaNs and of infinities leave the others as they are, with
+    rows for one half of a unit and for both."""
+    lens, P, g = [100, 300], 32, 2
+    table, blocks = make_tables(lens, P, seed=1)
+    codes = one_head(blocks, P, d, 2, -8)
+    q = torch.randn(2 * n, g, d, generator=torch.Generator().manual_seed(g)).to(torch.bfloat16)
+    bad = q.clone()
+    where = [(0, 0), (3, 1), (n - 1, 0), (n + 5, 1), (2 * n - 1, 1)]
+    for i, (t, h) in enumerate(where):
+        bad[t, h] = (math.nan, math.inf, -math.inf)[i % 3]
+    o, lse, cu = attend("many", bad, codes, table, lens, [n, n], 0.125)
+    keep = torch.ones(2 * n, g, dtype=torch.bool)
+    for t, h in where:
+        keep[t, h] = False
+    ref = oracle.attention_cache(q, *(c.numpy() for c in codes), table.numpy(), lens, cu, 0.125, True)
+    good = ref[0].clone().to(o.dtype), ref[1].clone().to(lse.dtype)
+    o, lse = o.cpu(), lse.cpu()
+    o[~keep], lse[~keep] = good[0][~keep], good[1][~keep]
+    assert_forward(o, lse, q, codes, table, lens, cu, 0.125, True, f"d={d} n={n}")
+
+
+@pytest.mark.parametrize("P", (16, 64, 128))
+@pytest.mark.parametrize("d,n", ((64, 30), (128, 70)))
+def test_many_rows_report_what_is_out_of_range(d, n, P):
+    """Blocks outside the cache hide their keys; lengths and rows are cut off."""
+    lens, g = [6 * P + 5, n + 3], 2
+    table, blocks = make_tables(lens, P, seed=1)
+    codes = one_head(blocks, P, d, 2, -8)
+    q = torch.randn(2 * n, g, d, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    q1, t1 = q[n:], table[1:]
+    wrong = table.clone()
+    wrong[0, 2], wrong[0, 5] = blocks, -5
+    o, lse, cu = attend("many", q, codes, wrong, lens, [n, n], 0.125, causal=False, raises=611)
+    rest = torch.tensor([[int(table[0, j]) for j in (0, 1, 3, 4, 6)]], dtype=torch.int32)
+    assert_forward(o[:n], lse[:n], q[:n], codes, rest, [lens[0] - 2 * P], [0, n], 0.125, False)
+    assert_forward(o[n:], lse[n:], q1, codes, t1, lens[1:], [0, n], 0.125, False)
+    o, lse, _ = attend("many", q, codes, table, [-3, lens[1]], [n, n], 0.125, raises=612)
+    assert (o[:n] == 0).all() and (lse[:n] == -math.inf).all()
+    assert_forward(o[n:], lse[n:], q1, codes, t1, lens[1:], [0, n], 0.125, True)
+    M = table.shape[1]
+    full = torch.arange(M, dtype=torch.int32).remainder(blocks)[None]
+    o, lse, _ = attend("many", q[:n], codes, full, [M * P + 5], [n], 0.125, raises=612)
+    assert_forward(o, lse, q[:n], codes, full, [M * P], [0, n], 0.125, True)
+    o, lse, _ = attend("many", q[:n], codes, table[1:], lens[1:], [2 * n], 0.125, causal=False, raises=613)
+    assert_forward(o, lse, q[:n], codes, t1, lens[1:], [0, n], 0.125, False)
+
+
+@pytest.mark.parametrize("R", (513, 1100))
+def test_many_rows_of_more_requests_than_threads(R):
+    """Several requests a thread in the sums, some without rows or keys."""
+    P, d, g = 16, 64, 2
+    gen = torch.Generator().manual_seed(R)
+    new = torch.randint(0, 30, (R,), generator=gen).tolist()
+    lens = [0 if i % 97 == 5 else n + int(x) for i, (n, x) in
+            enumerate(zip(new, torch.randint(0, 20, (R,), generator=gen)))]
+    table, blocks = make_tables(lens, P, seed=1)
+    codes = one_head(blocks, P, d, 2, -8)
+    poison(codes[0], table, lens)
+    poison(codes[1], table, lens)
+    q = torch.randn(sum(new), g, d, generator=gen).to(torch.bfloat16)
+    check("many", q, codes, table, lens, new, 0.125)
+
+
+@pytest.mark.parametrize("P,d", ((16, 64), (64, 128)))
+def test_a_run_of_prompts(P, d):
+    """Prompts, their next chunks, drafts of one request among them, one
+    refused for want of blocks: slots, appends and attention together."""
+    H, g, R, M = 2, 2, 3, 16
+    blocks = -(-600 // P)
+    gen = torch.Generator().manual_seed(P)
+    free = torch.randperm(blocks, generator=gen).tolist()
+    cache = fa.cache_alloc_e4m3(blocks, H, P, d)
+    ref = [t.cpu().numpy() for t in cache]
+    table = torch.full((R, M), -1, dtype=torch.int32, device=DEV)
+    lens, used = i32([0] * R), i32([0])
+    rtable, rlens, rused = table.tolist(), [0] * R, 0
+    for step, new in enumerate(([90, 170, 0], [100, 3, 120], [70, 1, 16 * P], [60, 33, 65])):
+        T = sum(new) + 3
+        cu, slots, lens, used = fa.cache_slots(table, lens, i32(new), i32(free), used, P, T)
+        rtable, rcu, rslots, rlens, rused = oracle.cache_slots(rtable, rlens, new, free, rused, P, T)
+        assert table.tolist() == rtable and slots.tolist() == rslots and lens.tolist() == rlens
+        k, v, q = (torch.randn(T, h, d, generator=gen).to(torch.bfloat16) for h in (H, H, H * g))
+        fa.cache_append_e4m3(k.to(DEV), v.to(DEV), cache, slots)
+        oracle.cache_append(k.float().numpy(), ref[0], ref[2], rslots, P)
+        oracle.cache_append(v.float().numpy(), ref[1], ref[3], rslots, P)
+        assert_takes("many", R, T, H * g, H, d)
+        o, lse = fa.cache_forward_e4m3(q.to(DEV), cache, table, lens, cu, slot_map=slots)
+        fa.check_errors()
+        for a, b in zip(cache, ref):
+            assert torch.equal(a.cpu(), torch.from_numpy(b)), f"step {step}"
+        seen = [n if any(s >= 0 for s in rslots[rcu[r]:rcu[r + 1]]) else 0 for r, n in enumerate(rlens)]
+        assert_forward(o, lse, q, [torch.from_numpy(a) for a in ref], table.cpu(), seen, rcu, d ** -0.5, True,
+                       f"step {step}")
