@@ -134,29 +134,33 @@ struct Layout {
   static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
 };
 
-// sum of floor((a i + b) / m) over i < n, all >= 0 (the Euclid-like sum).  T
-// holds a n + b of every step, at most the first's plus m.
+// F(n, m, a, b) = sum of floor((a i + b) / m) over i < n; n >= 0, m > 0, a, b >= 0.
+// Two steps, taken in turn as in Euclid's algorithm (sums of floors as counts of
+// lattice points: Graham, Knuth, Patashnik, Concrete Mathematics, 3.5):
+//   the whole parts of a / m and b / m: F(n, m, a, b) =
+//     floor(a / m) n (n - 1) / 2 + floor(b / m) n + F(n, m, a mod m, b mod m);
+//   then, a, b < m, K = floor((a (n - 1) + b) / m) the last and largest term: for
+//     each j < K the i with a term of j at most are the first
+//     ceil(((j + 1) m - b) / a), and the others count one each, so that
+//     F(n, m, a, b) = n K - F(K, a, m, a + m - b - 1).
+// K < n and all of a step's values are at most the first's a n + b + m.
 template <typename T>
 __device__ __forceinline__ long long floor_sum_in(T n, T m, T a, T b) {
-  long long s = 0;
-  while (n > 0) {
-    if (a >= m) {
-      s += static_cast<long long>(n) * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      s += static_cast<long long>(n) * (b / m);
-      b %= m;
-    }
-    const T y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const T t = m;
-    m = a;
-    a = t;
+  long long sum = 0;
+  for (bool minus = false; n > 0; minus = !minus) {
+    const long long terms = n, whole = static_cast<long long>(a / m) * (terms * (terms - 1) / 2) + b / m * terms;
+    a %= m;
+    b %= m;
+    const T last = (a * (n - 1) + b) / m;
+    sum += minus ? -(whole + terms * last) : whole + terms * last;
+    if (last == 0) break;
+    const T from = a + m - b - 1, by = a;
+    n = last;
+    a = m;
+    m = by;
+    b = from;
   }
-  return s;
+  return sum;
 }
 __device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
   // divisions of 64 bits take several times as long: a third of what a CTA
