@@ -178,7 +178,8 @@ size_t cache_fwd_workspace(int R, int T, int Hq, int Hkv, int d) {
 }
 
 std::mutex g_cache_mu;
-bool g_cache_ready[64][2][6] = {};
+// By device and d (64, 128): 8 rows, many rows with G 16, 32, 64, 16 rows.
+bool g_cache_ready[64][2][5] = {};
 
 // Dynamic shared memory of a kernel, set once per device.
 template <typename K>
@@ -234,8 +235,7 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
     };
     if (P == 16) launch(fa_cache_prompt_kernel<D, 16>, set[1]);
     else if (P == 32) launch(fa_cache_prompt_kernel<D, 32>, set[2]);
-    else if (P == 64) launch(fa_cache_prompt_kernel<D, 64>, set[3]);
-    else launch(fa_cache_prompt_kernel<D, 128>, set[4]);
+    else launch(fa_cache_prompt_kernel<D, 64>, set[3]);
     if (st != FA_OK) return st;
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return host::fail(e);
@@ -257,7 +257,7 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
     fa_cache_fwd_kernel<D, 8><<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
   } else {
     using Ly = dec::Layout<D, 16>;
-    if ((st = ready(fa_cache_fwd_kernel<D, 16>, Ly::kAlloc, set[5])) != FA_OK) return st;
+    if ((st = ready(fa_cache_fwd_kernel<D, 16>, Ly::kAlloc, set[4])) != FA_OK) return st;
     fa_cache_fwd_kernel<D, 16><<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
   }
   const cudaError_t e = cudaGetLastError();

@@ -277,8 +277,8 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32], int lo, int hi) 
 
 }  // namespace prm
 
-// GROUP: tokens of a block, P: keys that share their scales.
-template <int D, int GROUP>
+// G: keys of a step that share their scales, a block's or, of larger ones, all 64.
+template <int D, int G>
 __global__ void __launch_bounds__(prm::kThreads, 1)
     fa_cache_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const uint8_t* __restrict__ v8,
                            const __grid_constant__ CacheFwdArgs a) {
@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
   using dec::Req;
   using dec::Seg;
   using Ly = Layout<D>;
+  static_assert(G == 16 || G == 32 || G == kStepKeys, "keys that share a scale");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -794,7 +795,6 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
     const int x = warp >> 2;  // half
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + kColS + x * kHalf, tO = tmem + lane_off + kColO + x * kHalf;
-    constexpr int G = GROUP < kStepKeys ? GROUP : kStepKeys;
     constexpr int kGroups = kStepKeys / G;          // groups of a step
     constexpr int kStepG = 4 / kGroups;             // a group's place among the scales
     int cnt = 0, jt = 0;  // steps of this half, the piece's first tile
