@@ -12,7 +12,8 @@
 // Products.  S is taken in 8 bits: a query row, divided by a power of two of
 // its own, is the sum of two E4M3 numbers per element, the rounded value and
 // the rest (bf16 has 8 significant bits, E4M3 four: exact down to 2^-9 of the
-// row's largest element, and off by at most 2^-17 of that below), so that
+// row's largest element, and off by at most 2^-17 of that below; exact in rows
+// whose largest is below 2^-116), so that
 //   S = Q_hi K^T + Q_lo K^T
 // costs what one f16 product would, and K goes from the cache to the tensor
 // cores as it is.  P stays f16, as two parts of it would cost the softmax more
@@ -38,16 +39,17 @@
 //
 // A unit with rows for A only (a few tokens, a prompt's end) gives both halves
 // the same rows and alternate steps; at its end they join their sums, each warp
-// reading both accumulators (drafts of 16 requests: 48.5 us with B idle, 44.2).
+// reading both accumulators (drafts of 16 requests: 48.5 us with B idle, then 44.2;
+// 37.5 now.  Times beside a choice are those of the kernel as it then was.)
 //
 // What bounds it: the loop from weights to the scores that take their buffer.
 // Prompts of 1500 to 4096 tokens of 3 requests behind up to 10000, 32 heads on 8
-// of 128, take 1116 us, 1.34 PFLOP/s of bf16's 1.92: 1690 cycles a step of 64
-// keys.  The products of both halves take 1260 by themselves (S 48 cycles each,
-// the time to read 6 KB of shared memory, where the sums take 32; PV 64), the
-// softmax 1150 while both run.  But S(i+2) waits for PV(i): 512 cycles for both
-// halves' PV, 270 to learn of it, 770 for both S and 100 to learn of that are
-// 1650.  A third score buffer does not fit tensor memory; halves kept half a step
+// of 128, take 1131 us, 1.32 PFLOP/s of bf16's 1.92 (978 us with heads of 64).
+// Of 1690 cycles a step of 64 keys, taken at 1116 us, the products of both halves
+// take 1260 by themselves (S 48 cycles each, the time to read 6 KB of shared
+// memory, where the sums take 32; PV 64), the softmax 1150 while both run.  But
+// S(i+2) waits for PV(i): 512 cycles for both halves' PV, 270 to learn of it, 770
+// for both S and 100 to learn of that are 1650.  A third score buffer does not fit tensor memory; halves kept half a step
 // apart, taking turns at the softmax or at issuing, were slower (1140, 1300 and
 // 1305 us).
 //

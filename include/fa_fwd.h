@@ -455,12 +455,15 @@ int fa_cache_append_e4m3(const void* k, const void* v, long long k_stride, long 
  *   workspace: at least fa_cache_fwd_e4m3_workspace_size(R, T, Hq, Hkv, d)
  *          bytes, 16-byte aligned.  Contents on entry are ignored.  Calls that may run at
  *          the same time need one each.
- * O and L are those of the exact attention over the cached values, up to the
- * rounding of the softmax weights to f16 in the product with V, and of query
- * elements far below their row's largest: by up to 2^-17 of that one, where
- * requests have more than 16 rows per kv head on average.  Results do not
- * depend on the order in which blocks run, and are the same from call to call;
- * those of one request may differ in their last bits from batch to batch.
+ * O and L are those of the exact attention over the cached values, up to fp32
+ * sums, the rounding of the softmax weights to f16 in the product with V, and of
+ * query elements far below their row's largest.  Those below 2^-17 of it are off
+ * by up to 2^-25 of it; where requests have more than 16 rows (tokens times
+ * Hq / Hkv) on average, more than 48 where R * Hkv is at most an eighth of the
+ * SMs, those below 2^-9 of it by up to 2^-17 of it.  T counts for that average,
+ * padding included.  Elements of O below 2^-100 may come out as 0.  Results do
+ * not depend on the order in which blocks run, and are the same from call to
+ * call; those of one request may differ by these roundings from batch to batch.
  * Errors as above, and Hq % Hkv != 0, a missing or short workspace, or an
  * output that overlaps an input or another output: FA_ERR_INVALID_ARG.
  * Enqueues one kernel, and a second that merges the parts of requests whose
