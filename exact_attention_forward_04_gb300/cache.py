@@ -24,7 +24,7 @@ _I32, _I64, _F32, _U8, _BF16 = torch.int32, torch.int64, torch.float32, torch.ui
 
 class CacheE4M3(NamedTuple):
     """A pool of cache blocks: codes uint8 [blocks, Hkv, P, d], scales fp32
-    [blocks, Hkv], finite and not negative, of K and of V."""
+    [blocks, Hkv] in 0 .. 2^120, of K and of V."""
     k8: torch.Tensor
     v8: torch.Tensor
     k_scale: torch.Tensor
@@ -261,5 +261,5 @@ def _forward(handle, dev, q, q_stride, cache, table, seq_lens, cu_q, slot_map, s
         None if slot_map is None else slot_map.data_ptr(), o.data_ptr(), lse.data_ptr(), R, T, Hq, H, d, blocks, P, M,
         scale, causal, ws.data_ptr(), ws.numel() * ws.element_size(), handle)
     if st:
-        _failed(st, "fa_cache_fwd_e4m3")
+        _failed(st, "fa_cache_fwd_e4m3_slots")
     return o, lse

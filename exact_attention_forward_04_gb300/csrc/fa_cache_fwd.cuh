@@ -288,10 +288,11 @@ struct CacheFwdArgs {
 
 namespace dec {
 
-// A block's scales are finite and not negative: the two kernels would take others
-// differently.  Infinity, NaN and what has a sign are the larger bit patterns (0
-// with a sign is made one without).
-constexpr uint32_t kBadScale = 0x7f800000u;
+// A block's scales lie in 0 .. 2^120: the two kernels would take others differently,
+// and the K scale times k_unit has to be finite.  What is larger, infinity, NaN and
+// what has a sign are the bit patterns behind 2^120's (0 with a sign is made one
+// without).
+constexpr uint32_t kBadScale = ((120u + 127u) << 23) + 1u;
 __device__ __forceinline__ uint32_t scale_bits(float x) { return __float_as_uint(x + 0.f); }
 
 struct Req {
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (blk[i] >= 0) {
-          ks[i] = __ldg(a.ks + blk[i]) * a.k_unit;
+          ks[i] = __ldg(a.ks + blk[i]);
           vs[i] = __ldg(a.vs + blk[i]);
         }
       __syncwarp();
@@ -669,6 +670,8 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
                 s_blk[e % kMeta].w &= boxes == 1 ? 0 : ~(1 << i);
               }
           }
+          ks[0] *= a.k_unit;
+          ks[1] *= a.k_unit;
           s_scales[e % kMeta] = boxes == 1 ? make_float4(ks[0], ks[0], vs[0], vs[0])
                                            : make_float4(ks[0], ks[1], vs[0], vs[1]);
           mbar_arrive(full(e % Ly::kStages));

@@ -338,8 +338,7 @@ size_t fa_attn_unfused_workspace_size(int B, int H, int N, int d);
  * token.  The cache is a pool of blocks of P tokens, P one of 16, 32, 64, 128:
  *   k8, v8           : E4M3 codes [num_blocks][Hkv][P][d], 16-byte aligned;
  *   k_scale, v_scale : fp32 [num_blocks][Hkv]: the value a code stands for is
- *                      E4M3(code) * scale of its block and head.  Scales are
- *                      finite and not negative.
+ *                      E4M3(code) * scale of its block and head; 0 .. 2^120.
  * d is 64 or 128 and num_blocks * Hkv at most 2^31 - 1.  A request of `len`
  * cached tokens keeps token i in block table[i / P] at offset i % P; the
  * block's number times P plus the offset is the token's slot.  Requests come
@@ -451,7 +450,7 @@ int fa_cache_append_e4m3(const void* k, const void* v, long long k_stride, long 
  *   Lengths above max_blocks * P, negative ones and row offsets outside
  *   [0, T] are cut off to the range and reported (FA_ERR_INDEX); the keys of a
  *   block outside [0, num_blocks), and those of a block and head one of whose
- *   scales is negative or not finite, count as not visible and it is reported.
+ *   scales is no number of [0, 2^120], count as not visible and it is reported.
  *   workspace: at least fa_cache_fwd_e4m3_workspace_size(R, T, Hq, Hkv, d)
  *          bytes, 16-byte aligned.  Contents on entry are ignored.  Calls that may run at
  *          the same time need one each.

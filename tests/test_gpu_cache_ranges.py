@@ -192,13 +192,13 @@ def test_scores_of_any_size(form, d, sign, exp):
 
 # ------------------------------------------------------- what is out of range
 
-@pytest.mark.parametrize("bad", (-1.0, -2.0 ** -90, math.nan, math.inf, -math.inf))
+@pytest.mark.parametrize("bad", (-1.0, -2.0 ** -90, math.nan, math.inf, -math.inf, 2.0 ** 121, 3.4e38))
 @pytest.mark.parametrize("which", ("k_scale", "v_scale"))
 @pytest.mark.parametrize("P", (16, 64))
 @pytest.mark.parametrize("form", FORMS)
 def test_scales_out_of_range_hide_their_block(form, P, which, bad):
-    """A scale that is negative or not finite is reported, and its block's
-    tokens are not seen, by either kernel."""
+    """A scale that is negative, not finite or above 2^120 is reported, and its
+    block's tokens are not seen, by either kernel."""
     g, n = FORMS[form]
     d, lens = 64, [5 * P + 3]
     table, blocks = make_tables(lens, P, seed=1)
