@@ -32,9 +32,9 @@
 // rows that fill an eighth of its 128.
 //
 // What bounds it.  DRAM for long keys: 24 requests of 20000 to 32768 tokens, 8
-// kv heads of 128, in 210 us, 6.1 TB/s; the pieces' starts and ends and the
-// last CTA for shorter ones: 64 requests of 30 to 8192 in 103 us (5.4 TB/s).
-// Latency for little work: one request of 1000 in 10.9 us, two launches.
+// kv heads of 128, in 200 us, 6.3 TB/s; the pieces' starts and ends and the
+// last CTA for shorter ones: 64 requests of 30 to 8192 in 101 us (5.5 TB/s).
+// Latency for little work: one request of 1000 in 10.7 us, two launches.
 // (Times beside a choice are those of the kernel as it then was, with and
 // without it.)
 //
@@ -47,7 +47,7 @@
 // rounded to f16 (11 bits), so that neither a block of small values nor one
 // of zeros costs the others precision.  Where a block's scale lies far above 2^E
 // the two factors of such a weight leave fp32's range; those tiles take a branch
-// of their own (0.5 to 1 % of the time of the others, for asking).  E is kept as
+// of their own (up to 2 % of the others' time, for asking).  E is kept as
 // its distance from m: beside a large m a sum with log2 v_scale would be lost.
 #pragma once
 #include <cuda_bf16.h>

@@ -40,11 +40,11 @@
 // A unit with rows for A only (a few tokens, a prompt's end) gives both halves
 // the same rows and alternate steps; at its end they join their sums, each warp
 // reading both accumulators (drafts of 16 requests: 48.5 us with B idle, then 44.2;
-// 37.5 now.  Times beside a choice are those of the kernel as it then was.)
+// 38 now.  Times beside a choice are those of the kernel as it then was.)
 //
 // What bounds it: the loop from weights to the scores that take their buffer.
 // Prompts of 1500 to 4096 tokens of 3 requests behind up to 10000, 32 heads on 8
-// of 128, take 1131 us, 1.32 PFLOP/s of bf16's 1.92 (978 us with heads of 64).
+// of 128, take 1129 us, 1.32 PFLOP/s of bf16's 1.92 (978 us with heads of 64).
 // Of 1690 cycles a step of 64 keys, taken at 1116 us, the products of both halves
 // take 1260 by themselves (S 48 cycles each, the time to read 6 KB of shared
 // memory, where the sums take 32; PV 64), the softmax 1150 while both run.  But
