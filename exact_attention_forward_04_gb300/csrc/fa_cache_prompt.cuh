@@ -49,9 +49,9 @@
 // take 1260 by themselves (S 48 cycles each, the time to read 6 KB of shared
 // memory, where the sums take 32; PV 64), the softmax 1150 while both run.  But
 // S(i+2) waits for PV(i): 512 cycles for both halves' PV, 270 to learn of it, 770
-// for both S and 100 to learn of that are 1650.  A third score buffer does not fit tensor memory; halves kept half a step
-// apart, taking turns at the softmax or at issuing, were slower (1140, 1300 and
-// 1305 us).
+// for both S and 100 to learn of that are 1650.  A third score buffer does not fit
+// tensor memory; halves kept half a step apart, taking turns at the softmax or at
+// issuing, were slower (1140, 1300 and 1305 us).
 //
 // Warps: 0-3 softmax and epilogue of A, 4-7 of B, 8-11 codes to f16 (and Q),
 // 12 and 15 issue A's and B's products, 13 walks the range, 14 loads.
