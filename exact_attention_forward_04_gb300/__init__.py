@@ -23,6 +23,9 @@ __all__ = [
     "unfused_workspace_size", "unfused_intermediates",
     "CacheE4M3", "cache_alloc_e4m3", "cache_slots", "cache_append_e4m3", "cache_forward_e4m3",
     "cache_forward_workspace_size",
+    "rope_table", "rope", "rope_backward",
+    "CacheE2M1", "cache_alloc_e2m1", "cache_append_e2m1", "cache_read_e2m1", "cache_forward_e2m1",
+    "cache_forward_e2m1_workspace_size",
     "check_errors", "status_string", "library_path", "load_library", "SYMBOLS",
 ]
 
@@ -56,6 +59,7 @@ SYMBOLS = {
                         [_c.c_float, _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "fa_attn_unfused_workspace_size": (_c.c_size_t, [_c.c_int] * 4),
     "fa_cache_slots": (_c.c_int, [_c.c_void_p] * 9 + [_c.c_int] * 5 + [_c.c_void_p]),
+    "fa_cache_slots_positions": (_c.c_int, [_c.c_void_p] * 10 + [_c.c_int] * 5 + [_c.c_void_p]),
     "fa_cache_append_e4m3": (_c.c_int, [_c.c_void_p] * 2 + [_c.c_longlong] * 2 + [_c.c_void_p] * 5 +
                              [_c.c_int] * 5 + [_c.c_void_p]),
     "fa_cache_fwd_e4m3": (_c.c_int, [_c.c_void_p, _c.c_longlong] + [_c.c_void_p] * 9 + [_c.c_int] * 8 +
@@ -63,6 +67,14 @@ SYMBOLS = {
     "fa_cache_fwd_e4m3_slots": (_c.c_int, [_c.c_void_p, _c.c_longlong] + [_c.c_void_p] * 10 + [_c.c_int] * 8 +
                                 [_c.c_float, _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "fa_cache_fwd_e4m3_workspace_size": (_c.c_size_t, [_c.c_int] * 5),
+    "fa_rope": (_c.c_int, [_c.c_void_p] * 5 + [_c.c_longlong, _c.c_void_p] + [_c.c_int] * 8 + [_c.c_void_p]),
+    "fa_cache_append_e2m1": (_c.c_int, [_c.c_void_p] * 2 + [_c.c_longlong] * 2 + [_c.c_void_p] + [_c.c_float] * 2 +
+                             [_c.c_void_p] * 3 + [_c.c_int] * 8 + [_c.c_void_p]),
+    "fa_cache_read_e2m1": (_c.c_int, [_c.c_void_p] + [_c.c_float] * 2 + [_c.c_void_p] * 3 + [_c.c_int] * 5 +
+                           [_c.c_void_p]),
+    "fa_cache_fwd_e2m1": (_c.c_int, [_c.c_void_p, _c.c_longlong, _c.c_void_p] + [_c.c_float] * 2 + [_c.c_void_p] * 6 +
+                          [_c.c_int] * 8 + [_c.c_float, _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    "fa_cache_fwd_e2m1_workspace_size": (_c.c_size_t, [_c.c_int] * 5),
     "fa_check_errors": (_c.c_int, [_c.c_void_p]),
     "fa_selftest_wait_timeout": (_c.c_int, [_c.c_uint, _c.c_void_p]),
     "fa_status_string": (_c.c_char_p, [_c.c_int]),
@@ -478,3 +490,6 @@ def forward_host(q, k, v, scale=None, causal=False, stream=None, staging=None, o
 
 from .cache import (CacheE4M3, cache_alloc_e4m3, cache_append_e4m3, cache_forward_e4m3,  # noqa: E402
                     cache_forward_workspace_size, cache_slots)
+from .cache_e2m1 import (CacheE2M1, cache_alloc_e2m1, cache_append_e2m1, cache_forward_e2m1,  # noqa: E402
+                         cache_forward_e2m1_workspace_size, cache_read_e2m1)
+from .rope import rope, rope_backward, rope_table  # noqa: E402

@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(OUT_DIR, "libfa_fwd.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
-UNITS = ("fa_fwd.cu", "fa_cache.cu")
+UNITS = ("fa_fwd.cu", "fa_cache.cu", "fa_cache4.cu", "fa_rope.cu")
 
 
 def _sources():

@@ -42,7 +42,7 @@ def _load():
     from . import load_library
     lib = load_library()
     _fn = (lib.fa_cache_slots, lib.fa_cache_append_e4m3, lib.fa_cache_fwd_e4m3_slots,
-           lib.fa_cache_fwd_e4m3_workspace_size)
+           lib.fa_cache_fwd_e4m3_workspace_size, lib.fa_cache_slots_positions)
     return _fn
 
 
@@ -142,7 +142,8 @@ def cache_alloc_e4m3(num_blocks, heads_kv, block_tokens, d, device=None):
                      torch.zeros(shape[:2], dtype=_F32, device=device))
 
 
-def cache_slots(block_table, seq_lens, new_lens, free_blocks, free_used, block_tokens, num_tokens, stream=None):
+def cache_slots(block_table, seq_lens, new_lens, free_blocks, free_used, block_tokens, num_tokens, stream=None,
+                positions=False):
     """Grant blocks for each request's new tokens and map them to slots.
 
     block_table int32 [R, max_blocks] (written in place), seq_lens and
@@ -152,7 +153,9 @@ def cache_slots(block_table, seq_lens, new_lens, free_blocks, free_used, block_t
     [R], free_used_out int32 [1]).  A request that cannot be served keeps its
     length and gets slots of -1, its rows their place in cu_new; slots behind
     the last request's are -1.  Where the free blocks run out, every later
-    request that needs one is refused too."""
+    request that needs one is refused too.  ``positions``: a fifth result, each
+    token's position in its request (int32 [num_tokens]; -1: of none that is
+    served), as rope and cache_append_e2m1 take them."""
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be an int32 [R, max_blocks] tensor")
     dev = block_table.device
@@ -170,14 +173,23 @@ def cache_slots(block_table, seq_lens, new_lens, free_blocks, free_used, block_t
     if not 0 <= num_tokens <= 0x7fffffff:
         raise ValueError(f"num_tokens must be in 0 .. 2^31 - 1, got {num_tokens}")
     return _call(dev, stream, _slots, dev, block_table, seq_lens, new_lens, free_blocks, free_used, R, M, block_tokens,
-                 num_tokens)
+                 num_tokens, positions)
 
 
-def _slots(handle, dev, table, seq_lens, new_lens, free, used, R, M, P, T):
+def _slots(handle, dev, table, seq_lens, new_lens, free, used, R, M, P, T, positions):
     cu = _empty(R + 1, dtype=_I32, device=dev)
     slots = _empty(T, dtype=_I64, device=dev)
     lens = _empty(R, dtype=_I32, device=dev)
     gone = _empty(1, dtype=_I32, device=dev)
+    if positions:
+        pos = _empty(T, dtype=_I32, device=dev)
+        st = (_fn or _load())[4](
+            table.data_ptr(), seq_lens.data_ptr(), new_lens.data_ptr(), free.data_ptr(), used.data_ptr(),
+            cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), lens.data_ptr(), gone.data_ptr(), R, M, free.shape[0], P,
+            T, handle)
+        if st:
+            _failed(st, "fa_cache_slots_positions")
+        return cu, slots, lens, gone, pos
     st = (_fn or _load())[0](
         table.data_ptr(), seq_lens.data_ptr(), new_lens.data_ptr(), free.data_ptr(), used.data_ptr(), cu.data_ptr(),
         slots.data_ptr(), lens.data_ptr(), gone.data_ptr(), R, M, free.shape[0], P, T, handle)

@@ -3,39 +3,20 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
-#include <cmath>
 #include <cstdint>
-#include <mutex>
 
 #include "fa_cache.cuh"
 #include "fa_cache_fwd.cuh"
+#include "fa_cache_host.h"
 #include "fa_cache_prompt.cuh"
+#include "fa_cache_slots.cuh"
 #include "fa_fwd.h"
 #include "fa_host.h"
 
 namespace fa {
 namespace {
 
-bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
-
-// log2 of the tokens per block, -1 where it is none of 16, 32, 64, 128.
-int block_shift(int P) { return P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : P == 128 ? 7 : -1; }
-
-// Sizes of a cache that fits 2^31 code rows of 128 bytes (the tensor maps'
-// coordinates are 32-bit).
-int check_cache(int Hkv, int d, int blocks, int P) {
-  if (Hkv <= 0 || blocks <= 0) return FA_ERR_INVALID_ARG;
-  if ((d != 64 && d != 128) || block_shift(P) < 0 || Hkv > 65535) return FA_ERR_UNSUPPORTED;
-  const long long bh = static_cast<long long>(blocks) * Hkv;
-  if (bh > 0x7fffffffLL || static_cast<long long>(blocks) * P > (1ll << 40)) return FA_ERR_UNSUPPORTED;
-  return FA_OK;
-}
-
-struct Range {
-  const void* p;
-  size_t n;
-};
+using namespace cachehost;
 
 // ------------------------------------------------------------------- slots
 
@@ -48,20 +29,17 @@ int cache_slots(const SlotArgs& a, int P, cudaStream_t s) {
   for (const void* p : {static_cast<const void*>(a.table), static_cast<const void*>(a.seq_lens),
                         static_cast<const void*>(a.new_lens), static_cast<const void*>(a.free_blocks),
                         static_cast<const void*>(a.free_used), static_cast<const void*>(a.cu_new),
-                        static_cast<const void*>(a.seq_lens_out), static_cast<const void*>(a.free_used_out)})
+                        static_cast<const void*>(a.seq_lens_out), static_cast<const void*>(a.free_used_out),
+                        static_cast<const void*>(a.positions)})
     if (misaligned(p, 4)) return FA_ERR_MISALIGNED;
   if (misaligned(a.slot_map, 8)) return FA_ERR_MISALIGNED;
   const size_t r = static_cast<size_t>(a.R);
-  const Range ins[] = {{a.seq_lens, 4 * r}, {a.new_lens, 4 * r}, {a.free_blocks, 4 * static_cast<size_t>(a.F)},
+  const std::initializer_list<Range> ins = {{a.seq_lens, 4 * r}, {a.new_lens, 4 * r}, {a.free_blocks, 4 * static_cast<size_t>(a.F)},
                        {a.free_used, 4}};
-  const Range outs[] = {{a.table, 4 * r * a.M}, {a.cu_new, 4 * (r + 1)}, {a.slot_map, 8 * static_cast<size_t>(a.T)},
-                        {a.seq_lens_out, 4 * r}, {a.free_used_out, 4}};
-  for (int i = 0; i < 5; ++i) {
-    for (const Range& in : ins)
-      if (host::overlap(outs[i].p, outs[i].n, in.p, in.n)) return FA_ERR_INVALID_ARG;
-    for (int j = i + 1; j < 5; ++j)
-      if (host::overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return FA_ERR_INVALID_ARG;
-  }
+  const std::initializer_list<Range> outs = {{a.table, 4 * r * a.M}, {a.cu_new, 4 * (r + 1)}, {a.slot_map, 8 * static_cast<size_t>(a.T)},
+                        {a.seq_lens_out, 4 * r}, {a.free_used_out, 4},
+                        {a.positions, a.positions ? 4 * static_cast<size_t>(a.T) : 0}};
+  if (overlapping(outs, ins)) return FA_ERR_INVALID_ARG;
   host::Device dev;
   const int st = host::device(&dev);
   if (st != FA_OK) return st;
@@ -102,14 +80,9 @@ int cache_append(const void* k, const void* v, long long k_stride, long long v_s
   const size_t nx = 2 * static_cast<size_t>(row), nc = static_cast<size_t>(blocks) * P * row;
   const size_t nk = static_cast<size_t>(T - 1) * k_stride * 2 + nx, nv = static_cast<size_t>(T - 1) * v_stride * 2 + nx;
   const size_t ns = static_cast<size_t>(blocks) * Hkv * 4;
-  const Range outs[] = {{k8, nc}, {v8, nc}, {ks, ns}, {vs, ns}};
-  const Range ins[] = {{k, nk}, {v, nv}, {slot_map, 8 * static_cast<size_t>(T)}};
-  for (int i = 0; i < 4; ++i) {
-    for (const Range& in : ins)
-      if (host::overlap(outs[i].p, outs[i].n, in.p, in.n)) return FA_ERR_INVALID_ARG;
-    for (int j = i + 1; j < 4; ++j)
-      if (host::overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return FA_ERR_INVALID_ARG;
-  }
+  const std::initializer_list<Range> outs = {{k8, nc}, {v8, nc}, {ks, ns}, {vs, ns}};
+  const std::initializer_list<Range> ins = {{k, nk}, {v, nv}, {slot_map, 8 * static_cast<size_t>(T)}};
+  if (overlapping(outs, ins)) return FA_ERR_INVALID_ARG;
   host::Device dev;
   if ((st = host::device(&dev)) != FA_OK) return st;
   AppendArgs a{};
@@ -165,60 +138,22 @@ int unit_rows(int R, int T, int Hq, int Hkv, int sms) {
   return rows <= 8ll * R ? 8 : rows <= (few ? 48ll : 16ll) * R ? 16 : prm::kRows;
 }
 
-// Workspace: the CTAs' marks, then two partials of a unit's query rows per CTA.
-int cache_fwd_grid(int sms, int rows, int d) { return sms * dec::ctas_per_sm(d, rows); }
-size_t marks_bytes(int grid) { return static_cast<size_t>(grid) * 32 + 16; }  // and to the next 32 bytes
-
 size_t cache_fwd_workspace(int R, int T, int Hq, int Hkv, int d) {
   if ((d != 64 && d != 128) || R <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
   host::Device dev;
   if (host::device(&dev) != FA_OK) return 0;
-  const int rows = unit_rows(R, T, Hq, Hkv, dev.sms), grid = cache_fwd_grid(dev.sms, rows, d);
-  return marks_bytes(grid) + static_cast<size_t>(2) * grid * rows * (d + 1) * 4;
+  const int rows = unit_rows(R, T, Hq, Hkv, dev.sms);
+  return workspace_bytes(fwd_grid(dev.sms, rows, d), rows, d);
 }
 
-std::mutex g_cache_mu;
 // By device and d (64, 128): 8 rows, many rows with G 16, 32, 64, 16 rows.
 bool g_cache_ready[64][2][5] = {};
-
-// Dynamic shared memory of a kernel, set once per device.
-template <typename K>
-int ready(K kernel, int bytes, bool& done) {
-  std::lock_guard<std::mutex> lock(g_cache_mu);
-  if (!done) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return host::fail(e);
-    done = true;
-  }
-  return FA_OK;
-}
-
-// The merge as a programmatic dependent of the kernel before it.
-template <int D, int ROWS>
-int launch_merge(const CacheFwdArgs& a, int grid, int split, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, split, 1);
-  cfg.blockDim = dim3(512, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_cache_merge_kernel<D, ROWS>, a, grid);
-  return e == cudaSuccess ? FA_OK : host::fail(e);
-}
 
 template <int D>
 int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, char* ws, const host::Device& dev,
                      cudaStream_t s) {
-  const int unit = unit_rows(a.R, a.T, a.Hq, a.Hkv, dev.sms), grid = cache_fwd_grid(dev.sms, unit, D);
-  a.desc = reinterpret_cast<int4*>(ws);
-  a.cont = reinterpret_cast<int*>(ws + static_cast<size_t>(grid) * 16);
-  // 32-byte stores; ws is aligned to 16
-  const uintptr_t parts = reinterpret_cast<uintptr_t>(ws) + marks_bytes(grid);
-  a.part_o = reinterpret_cast<float*>(parts & ~static_cast<uintptr_t>(31));
-  a.part_l = a.part_o + static_cast<size_t>(2) * grid * unit * D;
+  const int unit = unit_rows(a.R, a.T, a.Hq, a.Hkv, dev.sms), grid = fwd_grid(dev.sms, unit, D);
+  set_workspace(a, ws, grid, unit, D);
   bool* set = g_cache_ready[dev.dev][D == 128];
   int st = FA_OK;
   if (unit == prm::kRows) {
@@ -241,107 +176,42 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
     if (e != cudaSuccess) return host::fail(e);
     // a unit of one tile is never split: nothing to merge
     if (static_cast<long long>(a.M) * P <= prm::kKeys) return FA_OK;
-    return launch_merge<D, prm::kRows>(a, grid, 4, s);
+    return launch_merge<D, prm::kRows, E4M3Codes>(a, grid, 4, s);
   }
-  CUtensorMap mk, mv;
+  E4M3Codes::Maps maps;
   const cuuint64_t rows = static_cast<cuuint64_t>(P) * D / 128;
   const cuuint64_t bh = static_cast<cuuint64_t>(a.blocks) * a.Hkv;
   const cuuint32_t box = static_cast<cuuint32_t>((P < dec::kKeys ? P : dec::kKeys) * D / 128);
-  st = host::tensor_map(&mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, k8, 128, rows, bh, 128, rows * 128, 128, box);
+  st = host::tensor_map(&maps.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, k8, 128, rows, bh, 128, rows * 128, 128, box);
   if (st != FA_OK) return st;
-  st = host::tensor_map(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, v8, 128, rows, bh, 128, rows * 128, 128, box);
+  st = host::tensor_map(&maps.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, v8, 128, rows, bh, 128, rows * 128, 128, box);
   if (st != FA_OK) return st;
   if (unit == 8) {
-    using Ly = dec::Layout<D, 8>;
-    if ((st = ready(fa_cache_fwd_kernel<D, 8>, Ly::kAlloc, set[0])) != FA_OK) return st;
-    fa_cache_fwd_kernel<D, 8><<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
+    using Ly = dec::Layout<D, 8, E4M3Codes>;
+    if ((st = ready(fa_cache_fwd_kernel<D, 8, E4M3Codes>, Ly::kAlloc, set[0])) != FA_OK) return st;
+    fa_cache_fwd_kernel<D, 8, E4M3Codes><<<grid, dec::kThreads, Ly::kAlloc, s>>>(maps, a);
   } else {
-    using Ly = dec::Layout<D, 16>;
-    if ((st = ready(fa_cache_fwd_kernel<D, 16>, Ly::kAlloc, set[4])) != FA_OK) return st;
-    fa_cache_fwd_kernel<D, 16><<<grid, dec::kThreads, Ly::kAlloc, s>>>(mk, mv, a);
+    using Ly = dec::Layout<D, 16, E4M3Codes>;
+    if ((st = ready(fa_cache_fwd_kernel<D, 16, E4M3Codes>, Ly::kAlloc, set[4])) != FA_OK) return st;
+    fa_cache_fwd_kernel<D, 16, E4M3Codes><<<grid, dec::kThreads, Ly::kAlloc, s>>>(maps, a);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return host::fail(e);
   if (static_cast<long long>(a.M) * P <= dec::kKeys) return FA_OK;
-  return unit == 8 ? launch_merge<D, 8>(a, grid, 1, s) : launch_merge<D, 16>(a, grid, 1, s);
+  return unit == 8 ? launch_merge<D, 8, E4M3Codes>(a, grid, 1, s)
+                   : launch_merge<D, 16, E4M3Codes>(a, grid, 1, s);
 }
 
-int cache_fwd(const void* q, long long q_stride, const void* k8, const void* v8, const float* ks, const float* vs,
-              const int* table, const int* seq_lens, const int* cu_q, const long long* slot_map, void* o, float* lse,
-              int R, int T, int Hq, int Hkv, int d, int blocks, int P, int M, float scale, int causal, void* ws,
-              size_t ws_bytes, cudaStream_t s) {
-  int st = check_cache(Hkv, d, blocks, P);
-  if (st != FA_OK) return st;
-  if (R < 0 || T < 0 || Hq <= 0 || M <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
-  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
-  if (static_cast<long long>(T) * Hq > 0x7fffffffLL || static_cast<long long>(M) * P > 0x7fffff00LL)
-    return FA_ERR_UNSUPPORTED;
-  if (T == 0 || R == 0) return FA_OK;
-  if (!q || !k8 || !v8 || !ks || !vs || !table || !seq_lens || !cu_q || !o || !lse || !ws) return FA_ERR_INVALID_ARG;
-  const long long row = static_cast<long long>(Hq) * d;
-  if (T > 1 && q_stride < row) return FA_ERR_INVALID_ARG;
-  if (q_stride & 7) return FA_ERR_MISALIGNED;
-  if (q_stride > (1ll << 40)) return FA_ERR_UNSUPPORTED;
-  for (const void* p : {q, k8, v8, static_cast<const void*>(o), static_cast<const void*>(ws)})
-    if (misaligned(p, 16)) return FA_ERR_MISALIGNED;
-  for (const void* p : {static_cast<const void*>(ks), static_cast<const void*>(vs), static_cast<const void*>(table),
-                        static_cast<const void*>(seq_lens), static_cast<const void*>(cu_q),
-                        static_cast<const void*>(lse)})
-    if (misaligned(p, 4)) return FA_ERR_MISALIGNED;
-  if (misaligned(slot_map, 8)) return FA_ERR_MISALIGNED;
+int cache_fwd(const FwdCall& c, const void* k8, const void* v8, const float* ks, const float* vs, cudaStream_t s) {
+  CacheFwdArgs a;
   host::Device dev;
-  if ((st = host::device(&dev)) != FA_OK) return st;
-  const size_t need = cache_fwd_workspace(R, T, Hq, Hkv, d);
-  if (need == 0) return FA_ERR_UNSUPPORTED;
-  if (ws_bytes < need) return FA_ERR_INVALID_ARG;
-  const size_t nc = static_cast<size_t>(blocks) * P * Hkv * d, ns = static_cast<size_t>(blocks) * Hkv * 4;
-  const size_t nq = (static_cast<size_t>(T - 1) * q_stride + row) * 2, no = static_cast<size_t>(T) * row * 2;
-  const Range ins[] = {{q, nq}, {k8, nc}, {v8, nc}, {ks, ns}, {vs, ns},
-                       {table, static_cast<size_t>(R) * M * 4}, {seq_lens, static_cast<size_t>(R) * 4},
-                       {cu_q, (static_cast<size_t>(R) + 1) * 4},
-                       {slot_map, slot_map ? static_cast<size_t>(T) * 8 : 0}};
-  const Range outs[] = {{o, no}, {lse, static_cast<size_t>(T) * Hq * 4}, {ws, need}};
-  for (int i = 0; i < 3; ++i) {
-    for (const Range& in : ins)
-      if (host::overlap(outs[i].p, outs[i].n, in.p, in.n)) return FA_ERR_INVALID_ARG;
-    for (int j = i + 1; j < 3; ++j)
-      if (host::overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return FA_ERR_INVALID_ARG;
-  }
-  CacheFwdArgs a{};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.q_stride = q_stride;
+  const size_t nc = static_cast<size_t>(c.blocks) * c.P * c.Hkv * c.d, ns = static_cast<size_t>(c.blocks) * c.Hkv * 4;
+  const int st = forward_args(c, {{k8, nc, 16}, {v8, nc, 16}, {ks, ns, 4}, {vs, ns, 4}}, cache_fwd_workspace, &a, &dev);
+  if (st != FA_OK || a.T == 0) return st;
   a.ks = ks;
   a.vs = vs;
-  a.table = table;
-  a.seq_lens = seq_lens;
-  a.cu_q = cu_q;
-  a.slot_map = slot_map;
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.lse = lse;
-  a.R = R;
-  a.T = T;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.g = Hq / Hkv;
-  a.sh = block_shift(P);
-  a.M = M;
-  a.blocks = blocks;
-  a.causal = causal;
-  // A score's factor is a row's power of two (2^-124 to 2^120) times the scale,
-  // times the K scale (2^-100 to 2^120): the scale is brought to [1/4, 1/2) and
-  // the rest of it goes to the K scale, so that both parts stay normal.
-  a.scale_log2 = scale * 1.4426950408889634f;
-  int exponent = 0;
-  std::frexp(a.scale_log2, &exponent);
-  const int shift = std::min(26, std::max(-7, -1 - exponent));
-  a.scale_log2 = std::ldexp(a.scale_log2, shift);
-  a.k_unit = std::ldexp(1.f, -shift);
-  a.err = dev.err;
-  a.index_err = dev.index_err;
-  a.timeout_ns = 2000ull * 1000 * 1000;
-  char* w = static_cast<char*>(ws);
-  return d == 128 ? launch_cache_fwd<128>(a, k8, v8, P, w, dev, s) : launch_cache_fwd<64>(a, k8, v8, P, w, dev, s);
+  char* w = static_cast<char*>(c.ws);
+  return c.d == 128 ? launch_cache_fwd<128>(a, k8, v8, c.P, w, dev, s) : launch_cache_fwd<64>(a, k8, v8, c.P, w, dev, s);
 }
 
 }  // namespace
@@ -353,7 +223,17 @@ int fa_cache_slots(int* block_table, const int* seq_lens, const int* new_lens, c
                    const int* free_used, int* cu_new, long long* slot_map, int* seq_lens_out, int* free_used_out,
                    int R, int max_blocks, int num_free, int block_tokens, int num_tokens, void* stream) {
   fa::SlotArgs a{block_table, seq_lens, new_lens, free_blocks, free_used, cu_new, slot_map, seq_lens_out,
-                 free_used_out, R, max_blocks, num_free, fa::block_shift(block_tokens), num_tokens};
+                 free_used_out, nullptr, R, max_blocks, num_free, fa::cachehost::block_shift(block_tokens), num_tokens};
+  return fa::cache_slots(a, block_tokens, static_cast<cudaStream_t>(stream));
+}
+
+int fa_cache_slots_positions(int* block_table, const int* seq_lens, const int* new_lens, const int* free_blocks,
+                             const int* free_used, int* cu_new, long long* slot_map, int* positions,
+                             int* seq_lens_out, int* free_used_out, int R, int max_blocks, int num_free,
+                             int block_tokens, int num_tokens, void* stream) {
+  if (num_tokens > 0 && !positions) return FA_ERR_INVALID_ARG;
+  fa::SlotArgs a{block_table, seq_lens, new_lens, free_blocks, free_used, cu_new, slot_map, seq_lens_out,
+                 free_used_out, positions, R, max_blocks, num_free, fa::cachehost::block_shift(block_tokens), num_tokens};
   return fa::cache_slots(a, block_tokens, static_cast<cudaStream_t>(stream));
 }
 
@@ -373,9 +253,9 @@ int fa_cache_fwd_e4m3(const void* q, long long q_stride, const void* k8, const v
                       float* lse, int R, int T, int Hq, int Hkv, int d, int num_blocks, int block_tokens,
                       int max_blocks, float scale, int causal, void* workspace, size_t workspace_bytes,
                       void* stream) {
-  return fa::cache_fwd(q, q_stride, k8, v8, k_scale, v_scale, block_table, seq_lens, cu_q, nullptr, o, lse, R, T, Hq,
-                       Hkv, d, num_blocks, block_tokens, max_blocks, scale, causal, workspace, workspace_bytes,
-                       static_cast<cudaStream_t>(stream));
+  return fa_cache_fwd_e4m3_slots(q, q_stride, k8, v8, k_scale, v_scale, block_table, seq_lens, cu_q, nullptr, o, lse, R,
+                                 T, Hq, Hkv, d, num_blocks, block_tokens, max_blocks, scale, causal, workspace,
+                                 workspace_bytes, stream);
 }
 
 int fa_cache_fwd_e4m3_slots(const void* q, long long q_stride, const void* k8, const void* v8, const float* k_scale,
@@ -383,9 +263,9 @@ int fa_cache_fwd_e4m3_slots(const void* q, long long q_stride, const void* k8, c
                             const long long* slot_map, void* o, float* lse, int R, int T, int Hq, int Hkv, int d,
                             int num_blocks, int block_tokens, int max_blocks, float scale, int causal,
                             void* workspace, size_t workspace_bytes, void* stream) {
-  return fa::cache_fwd(q, q_stride, k8, v8, k_scale, v_scale, block_table, seq_lens, cu_q, slot_map, o, lse, R, T, Hq,
-                       Hkv, d, num_blocks, block_tokens, max_blocks, scale, causal, workspace, workspace_bytes,
-                       static_cast<cudaStream_t>(stream));
+  const fa::cachehost::FwdCall c{q, q_stride, block_table, seq_lens, cu_q, slot_map, o, lse, R, T, Hq, Hkv, d,
+                                 num_blocks, block_tokens, max_blocks, scale, causal, workspace, workspace_bytes};
+  return fa::cache_fwd(c, k8, v8, k_scale, v_scale, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

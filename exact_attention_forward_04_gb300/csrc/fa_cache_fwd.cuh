@@ -53,16 +53,28 @@
 #include <cuda_bf16.h>
 
 #include "fa_cache.cuh"
+#include "fa_cache4.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
+
+// What a cache holds its rows as.
+struct E4M3Codes {  // a scale per block and head, beside the codes
+  static constexpr bool k4 = false;
+  struct Maps {
+    CUtensorMap k, v;
+  };
+};
+struct E2M1Codes {  // a scale for 16 elements, in granules with the codes
+  static constexpr bool k4 = true;
+  struct Maps {};
+};
 
 namespace dec {
 
 constexpr int kWarps = 8;                    // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);  // and the producer
 constexpr int kKeys = 32;                    // keys of a tile
-constexpr int kMeta = 64;                    // tiles whose blocks and scales are held
 constexpr int kUnitCost = 12;                // a piece's fixed cost, in tiles (5: 114 us for 104)
 constexpr int kMinCost = 12;                 // least cost of a CTA's range
 constexpr int kWarpScan = 128;               // requests that one warp sums
@@ -87,14 +99,19 @@ struct Seg {
 // ROWS query rows a unit, 16 or 8.  8 rows at d = 64 leave registers and room
 // for two CTAs per SM with half the ring each.
 constexpr int ctas_per_sm(int d, int rows) { return d == 64 && rows == 8 ? 2 : 1; }
-template <int D, int ROWS>
+template <int D, int ROWS, class F>
 struct Layout {
   static constexpr int kCtas = ctas_per_sm(D, ROWS);
   static constexpr int kSegs = 8;                               // unit pieces in flight
-  static constexpr int kHalf = kKeys * D;                       // codes of K (or V) of a tile
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = 131072 / kCtas / kStage;
-  static constexpr int kIssue = kStages / 2;                    // lanes that issue loads
+  static constexpr int kHalf = kKeys * D;                       // codes of K (or V) of a tile; 4 bits: unused
+  static constexpr int kStage = F::k4 ? 2 * c4::Granule<D>::kBytes : 2 * kHalf;
+  static constexpr int kStages = 131072 / kCtas / kStage / kWarps * kWarps;
+  static constexpr int kIssue = kStages / 2 < 32 ? kStages / 2 : 32;  // lanes that issue loads
+  // Tiles whose blocks and scales are held.  An entry is reused so many tiles
+  // later: before the first of 32 tiles is looked up, all but the last ring's
+  // worth has been consumed.
+  static constexpr int kMeta = kStages + 32 <= 64 ? 64 : 128;
+  static_assert(kMeta >= kStages + 32, "entries of tiles in flight");
   static constexpr int kMerge = kStages * kStage;
   static constexpr int kQ = kMerge + kWarps * 8 * D * 4;        // bf16 [segs][rows][D]
   static constexpr int kStats = kQ + kSegs * ROWS * D * 2;      // float4 [warps][8]
@@ -197,6 +214,21 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -267,6 +299,7 @@ struct CacheFwdArgs {
   long long q_stride;
   const float* ks;         // [blocks][Hkv]
   const float* vs;
+  const uint8_t* data;     // 4 bits: [blocks][Hkv][P / 16][18 D]
   const int* table;        // [R][M]
   const int* seq_lens;     // [R]
   const int* cu_q;         // [R + 1]
@@ -281,6 +314,7 @@ struct CacheFwdArgs {
   int R, T, Hq, Hkv, g, sh, M, blocks, causal;
   float scale_log2;        // scale * log2(e) / k_unit
   float k_unit;            // a power of two that K's scales are multiplied by
+  float v_unit;            // 4 bits: what V's values are multiplied by
   DevError* err;
   DevError* index_err;
   unsigned long long timeout_ns;
@@ -329,12 +363,11 @@ __device__ __forceinline__ long long cost_of(const CacheFwdArgs& a, const Req& q
 
 }  // namespace dec
 
-template <int D, int ROWS>
+template <int D, int ROWS, class F>
 __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
-    fa_cache_fwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const __grid_constant__ CacheFwdArgs a) {
+    fa_cache_fwd_kernel(const __grid_constant__ typename F::Maps maps, const __grid_constant__ CacheFwdArgs a) {
   using namespace dec;
-  using Ly = Layout<D, ROWS>;
+  using Ly = Layout<D, ROWS, F>;
   constexpr int kRows = ROWS, kSegs = Ly::kSegs;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -349,7 +382,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
   int4* s_blk = reinterpret_cast<int4*>(sm + Ly::kBlk);
   if (warp == kWarps) {
     for (int i = lane; i < Ly::kStages; i += 32) {
-      mbar_init(base + Ly::kFull + 8 * i, 2);  // its loads, and its scales
+      mbar_init(base + Ly::kFull + 8 * i, F::k4 ? 1 : 2);  // its loads, and its scales
       mbar_init(base + Ly::kEmpty + 8 * i, 1);
       issue_mark(base + Ly::kIssued + 4 * i, -1);
     }
@@ -365,8 +398,10 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
     fence_mbar_init();
     if (lane == 0) {
       *abort_flag = 0;
-      prefetch_tensormap(&tmK);
-      prefetch_tensormap(&tmV);
+      if constexpr (!F::k4) {
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+      }
       a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
       a.cont[blockIdx.x] = 0;
     }
@@ -591,9 +626,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
         pt += take;
       }
       if (fill == 0) break;
-      // their blocks and scales, a lane each, then the loads, by some lanes.
-      // An entry is reused 64 tiles later: before the first of these tiles was
-      // issued, all but the last ring's worth (at most 32) had been consumed.
+      // their blocks and scales, a lane each, then the loads, by some lanes
       int blk[2] = {-1, -1};
       if (mr >= 0) {
         const int* row = a.table + static_cast<long long>(mr) * a.M;
@@ -611,13 +644,14 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
           }
         }
         const int valid = boxes == 1 ? (blk[0] >= 0 ? 3 : 0) : (blk[0] >= 0 ? 1 : 0) | (blk[1] >= 0 ? 2 : 0);
-        s_blk[(pos + lane) % kMeta] = make_int4(blk[0], blk[1], ((mt * kKeys) & (P - 1)) * D / 128, valid);
+        const int in = (mt * kKeys) & (P - 1);  // its place in the block: rows of codes, granules
+        s_blk[(pos + lane) % Ly::kMeta] = make_int4(blk[0], blk[1], F::k4 ? in / c4::kTokens : in * D / 128, valid);
       }
       // on their way while the loads are issued
       float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (blk[i] >= 0) {
+        if (!F::k4 && blk[i] >= 0) {
           ks[i] = __ldg(a.ks + blk[i]);
           vs[i] = __ldg(a.vs + blk[i]);
         }
@@ -633,13 +667,22 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
           if (ok) {
             issued = p + 1;
             issue_mark(base + Ly::kIssued + 4 * st, p);
-            const int4 bl = s_blk[p % kMeta];
+            const int4 bl = s_blk[p % Ly::kMeta];
             const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
-            if (boxes == 1) {
+            if constexpr (F::k4) {
+              // a granule of each of two blocks, or two together
+              constexpr uint32_t kBytes = c4::Granule<D>::kBytes;
+              const uint32_t n = boxes == 1 ? (bl.x >= 0 ? 2u : 0u) : (bl.x >= 0 ? 1u : 0u) + (bl.y >= 0 ? 1u : 0u);
+              const long long per = P / c4::kTokens;
+              mbar_arrive_expect_tx(full(st), n * kBytes);
+              if (bl.x >= 0)
+                bulk_load_1d(kb, a.data + (bl.x * per + bl.z) * kBytes, boxes == 1 ? 2 * kBytes : kBytes, full(st));
+              if (boxes == 2 && bl.y >= 0) bulk_load_1d(kb + kBytes, a.data + bl.y * per * kBytes, kBytes, full(st));
+            } else if (boxes == 1) {
               if (bl.x >= 0) {
                 mbar_arrive_expect_tx(full(st), Ly::kStage);
-                tma_load_3d(kb, &tmK, full(st), 0, bl.z, bl.x);
-                tma_load_3d(vb, &tmV, full(st), 0, bl.z, bl.x);
+                tma_load_3d(kb, &maps.k, full(st), 0, bl.z, bl.x);
+                tma_load_3d(vb, &maps.v, full(st), 0, bl.z, bl.x);
               } else {
                 mbar_arrive(full(st));
               }
@@ -647,19 +690,19 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
               const uint32_t nbox = (bl.x >= 0 ? 1u : 0u) + (bl.y >= 0 ? 1u : 0u);
               mbar_arrive_expect_tx(full(st), nbox * Ly::kHalf);
               if (bl.x >= 0) {
-                tma_load_3d(kb, &tmK, full(st), 0, 0, bl.x);
-                tma_load_3d(vb, &tmV, full(st), 0, 0, bl.x);
+                tma_load_3d(kb, &maps.k, full(st), 0, 0, bl.x);
+                tma_load_3d(vb, &maps.v, full(st), 0, 0, bl.x);
               }
               if (bl.y >= 0) {
-                tma_load_3d(kb + Ly::kHalf / 2, &tmK, full(st), 0, 0, bl.y);
-                tma_load_3d(vb + Ly::kHalf / 2, &tmV, full(st), 0, 0, bl.y);
+                tma_load_3d(kb + Ly::kHalf / 2, &maps.k, full(st), 0, 0, bl.y);
+                tma_load_3d(vb + Ly::kHalf / 2, &maps.v, full(st), 0, 0, bl.y);
               }
             }
           }
         }
         ok = __all_sync(0xffffffffu, ok);
         // the scales of these tiles, by the lanes that have them
-        if (ok && lane >= i0 && lane < min(fill, i0 + Ly::kIssue)) {
+        if (!F::k4 && ok && lane >= i0 && lane < min(fill, i0 + Ly::kIssue)) {
           const int e = pos + lane;
           if (max(max(scale_bits(ks[0]), scale_bits(vs[0])), max(scale_bits(ks[1]), scale_bits(vs[1]))) >= kBadScale) {
 #pragma unroll
@@ -667,12 +710,12 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
               if (max(scale_bits(ks[i]), scale_bits(vs[i])) >= kBadScale) {  // as if it had no block
                 record_index_error(a.index_err, kSiteFwdScale, mr);
                 ks[i] = vs[i] = 0.f;
-                s_blk[e % kMeta].w &= boxes == 1 ? 0 : ~(1 << i);
+                s_blk[e % Ly::kMeta].w &= boxes == 1 ? 0 : ~(1 << i);
               }
           }
           ks[0] *= a.k_unit;
           ks[1] *= a.k_unit;
-          s_scales[e % kMeta] = boxes == 1 ? make_float4(ks[0], ks[0], vs[0], vs[0])
+          s_scales[e % Ly::kMeta] = boxes == 1 ? make_float4(ks[0], ks[0], vs[0], vs[0])
                                            : make_float4(ks[0], ks[1], vs[0], vs[1]);
           mbar_arrive(full(e % Ly::kStages));
         }
@@ -713,6 +756,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
   // Merges of this warp's pair, four and eight: bits 0-2 are the phase of the
   // next; bits 3-5 tell which of the three the last one was, if any.
   uint32_t merges = 0;
+  auto unit = [&](float x) { return F::k4 ? x * a.v_unit : x; };
   // Where output row `row` of piece s goes, as a row of [T][Hq].
   auto out_row = [&](const Seg& s, int row) {
     const int rr = s.row0 + row, tk = rr / a.g;
@@ -801,8 +845,8 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
         ok = ok && mbar_wait(full(st), (p / Ly::kStages) & 1, wc, kSiteStageFull, p);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
-        const float4 sc = s_scales[p % kMeta];
-        const int valid = s_blk[p % kMeta].w;  // bit i: the tile's 16-key group i has a block
+        const float4 sc = F::k4 ? make_float4(a.k_unit, a.k_unit, 1.f, 1.f) : s_scales[p % Ly::kMeta];
+        const int valid = s_blk[p % Ly::kMeta].w;  // bit i: the tile's 16-key group i has a block
         const int key0 = (s.t0 + k) * kKeys;
         const bool careful = key0 + kKeys > all || valid != 3;
         // scores in log2 units, x[z][..] of row y: of key column(z, y)'s token
@@ -815,34 +859,77 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[z][e] = 0.f;
         auto at = [](int y, int e) { return kWide ? 2 * y + e : 2 * e + y; };
-        auto token = [&](int z, int e) { return kWide ? tok<D>(z, 2 * t4 + e) : tok<D>(2 * z + e, g4); };
+        // columns of score tiles: of 4 bits, the keys as they come
+        auto key_of = [](int j, int n) { return F::k4 ? 8 * j + n : tok<D>(j, n); };
+        auto token = [&](int z, int e) { return kWide ? key_of(z, 2 * t4 + e) : key_of(2 * z + e, g4); };
         // two score tiles at a time: chains of dependent products side by side
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-          uint32_t w[2][D / 16];
+          if constexpr (F::k4) {
+            using G = c4::Granule<D>;
+            const uint32_t gr = kb + (j >> 1) * G::kBytes;
+            uint32_t w[2][D / 32], f[2][D / 64];  // codes; scales of the lane's groups, twice each
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const int t = tok<D>(j + f, g4);
-#pragma unroll
-            for (int hc = 0; hc < D / 64; ++hc) {
-              const uint4 v = lds128(kb + code_at<D>(t, t4 + 4 * hc));
-              w[f][4 * hc] = v.x;
-              w[f][4 * hc + 1] = v.y;
-              w[f][4 * hc + 2] = v.z;
-              w[f][4 * hc + 3] = v.w;
+            for (int y = 0; y < 2; ++y) {
+              const int t = g4 + 8 * y;
+              if constexpr (D == 128) {
+                const uint4 v = lds128(gr + t * G::kRow + t4 * 16);
+                w[y][0] = v.x; w[y][1] = v.y; w[y][2] = v.z; w[y][3] = v.w;
+                const uint32_t both = c4::e4m3x2_to_f16(lds16(gr + G::kKScales + t * 8 + t4 * 2));
+                f[y][0] = __byte_perm(both, 0u, 0x1010);
+                f[y][1] = __byte_perm(both, 0u, 0x3232);
+              } else {
+                const uint2 v = lds64(gr + t * G::kRow + t4 * 8);
+                w[y][0] = v.x; w[y][1] = v.y;
+                f[y][0] = __byte_perm(c4::e4m3x2_to_f16(lds8(gr + G::kKScales + t * 4 + t4)), 0u, 0x1010);
+              }
             }
-          }
 #pragma unroll
-          for (int e = 0; e < kK; ++e) {
-            uint32_t b[2][2];
-            e4m3_to_f16(w[0][e], b[0][0], b[0][1]);
-            e4m3_to_f16(w[1][e], b[1][0], b[1][1]);
-            if constexpr (kWide) {
-              mma16816(x[j], qa[e], b[0][0], b[0][1]);
-              mma16816(x[j + 1], qa[e], b[1][0], b[1][1]);
-            } else {
-              const uint32_t ka[4] = {b[0][0], b[1][0], b[0][1], b[1][1]};
-              mma16816(x[j / 2], ka, qa[e][0], qa[e][1]);
+            for (int e = 0; e < kK; e += 2) {
+              uint32_t b[2][4];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                c4::e2m1_to_f16(w[y][e / 2], b[y][0], b[y][1], b[y][2], b[y][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[y][i] = c4::mul_f16x2(b[y][i], f[y][e / 4]);
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if constexpr (kWide) {
+                  mma16816(x[j], qa[e + i], b[0][2 * i], b[0][2 * i + 1]);
+                  mma16816(x[j + 1], qa[e + i], b[1][2 * i], b[1][2 * i + 1]);
+                } else {
+                  const uint32_t ka[4] = {b[0][2 * i], b[1][2 * i], b[0][2 * i + 1], b[1][2 * i + 1]};
+                  mma16816(x[j / 2], ka, qa[e + i][0], qa[e + i][1]);
+                }
+              }
+            }
+          } else {
+            uint32_t w[2][D / 16];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const int t = tok<D>(j + f, g4);
+#pragma unroll
+              for (int hc = 0; hc < D / 64; ++hc) {
+                const uint4 v = lds128(kb + code_at<D>(t, t4 + 4 * hc));
+                w[f][4 * hc] = v.x;
+                w[f][4 * hc + 1] = v.y;
+                w[f][4 * hc + 2] = v.z;
+                w[f][4 * hc + 3] = v.w;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < kK; ++e) {
+              uint32_t b[2][2];
+              e4m3_to_f16(w[0][e], b[0][0], b[0][1]);
+              e4m3_to_f16(w[1][e], b[1][0], b[1][1]);
+              if constexpr (kWide) {
+                mma16816(x[j], qa[e], b[0][0], b[0][1]);
+                mma16816(x[j + 1], qa[e], b[1][0], b[1][1]);
+              } else {
+                const uint32_t ka[4] = {b[0][0], b[1][0], b[0][1], b[1][1]};
+                mma16816(x[j / 2], ka, qa[e][0], qa[e][1]);
+              }
             }
           }
         }
@@ -866,52 +953,6 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
                 if (!there || key0 + t >= lim[y]) x[z][at(y, e)] = -INFINITY;
             }
         }
-        float gm[2][2];  // largest score of each row in each group of 16 keys
-#pragma unroll
-        for (int gr = 0; gr < 2; ++gr)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            gm[gr][y] = fmaxf(x[gr * (kZ / 2)][at(y, 0)], x[gr * (kZ / 2)][at(y, 1)]);
-            if constexpr (kWide) gm[gr][y] = fmaxf(gm[gr][y], fmaxf(x[2 * gr + 1][at(y, 0)], x[2 * gr + 1][at(y, 1)]));
-          }
-        // over the lanes that hold a row's keys; of both groups together where
-        // they have one scale
-        const bool same = sc.z == sc.w;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          if (same) {
-            gm[0][y] = gm[1][y] = row_max<kWide>(fmaxf(gm[0][y], gm[1][y]));
-          } else {
-            gm[0][y] = row_max<kWide>(gm[0][y]);
-            gm[1][y] = row_max<kWide>(gm[1][y]);
-          }
-        }
-        const float lv[2] = {floor_log2(sc.z), floor_log2(sc.w)};
-        float wgt[2][2], up[2];
-        bool grew = false, apart = false;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float m1 = fmaxf(m[y], fmaxf(gm[0][y], gm[1][y])), dm = m[y] - m1;
-          const float E1 = fmaxf(E[y] + dm, fmaxf(gm[0][y] - m1 + lv[0], gm[1][y] - m1 + lv[1]));
-          l[y] *= ex2(dm);
-          up[y] = ex2(E[y] + dm - E1);
-          grew = grew || up[y] != 1.f;
-          m[y] = m1;
-          E[y] = E1;
-          apart = apart || E1 < fmaxf(fmaxf(lv[0], lv[1]) - 86.f, -106.f);
-          const float f = ex2(14.f - E1);
-          wgt[0][y] = f * sc.z;
-          wgt[1][y] = f * sc.w;
-        }
-        if (__any_sync(0xffffffffu, grew || apart)) {
-          apart = __any_sync(0xffffffffu, apart);
-#pragma unroll
-          for (int i = 0; i < kO; ++i)
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) o[i][at(y, e)] *= up[y];
-        }
         // weights, as f16 operands of the product with V
         uint32_t pa[2][4];
         auto weigh = [&](auto value) {  // of scores x[z] of row y: 2^(x - m), and what it counts in l
@@ -934,72 +975,200 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
             }
           }
         };
-        if (!apart) {
-          weigh([&](int gr, int y, float (&p)[2]) {
+        if constexpr (F::k4) {
+          // one reference: no value is more than 2^18 times another's step
+          float up[2];
+          bool grew = false;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float top = x[0][at(y, 0)];
+#pragma unroll
+            for (int z = 0; z < kZ; ++z) top = fmax3(top, x[z][at(y, 0)], x[z][at(y, 1)]);
+            const float m1 = fmaxf(m[y], row_max<kWide>(top));
+            up[y] = ex2(m[y] - m1);
+            l[y] *= up[y];
+            grew = grew || up[y] != 1.f;
+            m[y] = m1;
+          }
+          if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int i = 0; i < kO; ++i)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) o[i][at(y, e)] *= up[y];
+          }
+          weigh([&](int, int, float (&p)[2]) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) p[e] = ex2(p[e]);
             const float sum = p[0] + p[1];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) p[e] *= wgt[gr][y];
+            for (int e = 0; e < 2; ++e) p[e] *= 16384.f;
             return sum;
           });
         } else {
-          // A group whose V scale is 2^86 or more above 2^E: its weights' factor
-          // may leave fp32's range, and so may the exponentials, which only
-          // together are below 2^15.  What the factor has above 2^100 goes into
-          // their arguments.  (The scales are read again: held until here, they
-          // would not fit in the registers of two CTAs.)
-          weigh([&](int gr, int y, float (&v)[2]) {
-            const float4 again = s_scales[p % kMeta];
-            const float size = gr == 0 ? again.z : again.w, lv = floor_log2(size);
-            const float a = 14.f - E[y] + lv, over = fmaxf(a - 100.f, 0.f);
-            // size / 2^lv; lv is -127 for 0 and what lies below the normal numbers
-            const uint32_t mantissa = (__float_as_uint(size) & 0x7fffffu) | 0x3f800000u;
-            const float w = ex2(a - over) * (lv == -127.f ? size * 0x1p127f : __uint_as_float(mantissa));
+          float gm[2][2];  // largest score of each row in each group of 16 keys
 #pragma unroll
-            for (int e = 0; e < 2; ++e) v[e] = ex2(v[e] + over);
-            const float sum = (v[0] + v[1]) * ex2(-over);
+          for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) v[e] *= w;
-            return sum;
-          });
+            for (int y = 0; y < 2; ++y) {
+              gm[gr][y] = fmaxf(x[gr * (kZ / 2)][at(y, 0)], x[gr * (kZ / 2)][at(y, 1)]);
+              if constexpr (kWide) gm[gr][y] = fmaxf(gm[gr][y], fmaxf(x[2 * gr + 1][at(y, 0)], x[2 * gr + 1][at(y, 1)]));
+            }
+          // over the lanes that hold a row's keys; of both groups together where
+          // they have one scale
+          const bool same = sc.z == sc.w;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if (same) {
+              gm[0][y] = gm[1][y] = row_max<kWide>(fmaxf(gm[0][y], gm[1][y]));
+            } else {
+              gm[0][y] = row_max<kWide>(gm[0][y]);
+              gm[1][y] = row_max<kWide>(gm[1][y]);
+            }
+          }
+          const float lv[2] = {floor_log2(sc.z), floor_log2(sc.w)};
+          float wgt[2][2], up[2];
+          bool grew = false, apart = false;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float m1 = fmaxf(m[y], fmaxf(gm[0][y], gm[1][y])), dm = m[y] - m1;
+            const float E1 = fmaxf(E[y] + dm, fmaxf(gm[0][y] - m1 + lv[0], gm[1][y] - m1 + lv[1]));
+            l[y] *= ex2(dm);
+            up[y] = ex2(E[y] + dm - E1);
+            grew = grew || up[y] != 1.f;
+            m[y] = m1;
+            E[y] = E1;
+            apart = apart || E1 < fmaxf(fmaxf(lv[0], lv[1]) - 86.f, -106.f);
+            const float f = ex2(14.f - E1);
+            wgt[0][y] = f * sc.z;
+            wgt[1][y] = f * sc.w;
+          }
+          if (__any_sync(0xffffffffu, grew || apart)) {
+            apart = __any_sync(0xffffffffu, apart);
+#pragma unroll
+            for (int i = 0; i < kO; ++i)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) o[i][at(y, e)] *= up[y];
+          }
+          if (!apart) {
+            weigh([&](int gr, int y, float (&p)[2]) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) p[e] = ex2(p[e]);
+              const float sum = p[0] + p[1];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) p[e] *= wgt[gr][y];
+              return sum;
+            });
+          } else {
+            // A group whose V scale is 2^86 or more above 2^E: its weights' factor
+            // may leave fp32's range, and so may the exponentials, which only
+            // together are below 2^15.  What the factor has above 2^100 goes into
+            // their arguments.  (The scales are read again: held until here, they
+            // would not fit in the registers of two CTAs.)
+            weigh([&](int gr, int y, float (&v)[2]) {
+              const float4 again = s_scales[p % Ly::kMeta];
+              const float size = gr == 0 ? again.z : again.w, lv = floor_log2(size);
+              const float a = 14.f - E[y] + lv, over = fmaxf(a - 100.f, 0.f);
+              // size / 2^lv; lv is -127 for 0 and what lies below the normal numbers
+              const uint32_t mantissa = (__float_as_uint(size) & 0x7fffffu) | 0x3f800000u;
+              const float w = ex2(a - over) * (lv == -127.f ? size * 0x1p127f : __uint_as_float(mantissa));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) v[e] = ex2(v[e] + over);
+              const float sum = (v[0] + v[1]) * ex2(-over);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) v[e] *= w;
+              return sum;
+            });
+          }
         }
         // O += P V: lane g4 takes output columns g4 D/8 .. of the keys 2 t4, 2 t4 + 1
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          constexpr int kW = D / 32;
-          uint32_t w[4][kW];  // keys: score tile 2 ks (even, odd column), 2 ks + 1
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = tok<D>(2 * ks + (e >> 1), 2 * t4 + (e & 1));
-            if constexpr (kW == 4) {
-              const uint4 v = lds128(vb + code_at<D>(t, g4));
-              w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
+          if constexpr (F::k4) {
+            using G = c4::Granule<D>;
+            const uint32_t gr = kb + ks * G::kBytes;
+            const int flip = D == 128 ? g4 & 1 : (g4 >> 1) & 1;
+            // piece g4 of tokens 2 t4, 2 t4 + 1 and of those + 8
+            const uint32_t v0 = gr + G::kV + g4 * D + ((t4 * 2) ^ (flip * 8)) * G::kPiece, v1 = v0 ^ (8 * G::kPiece);
+            uint32_t w[4][D / 64 == 2 ? 2 : 1];
+            if constexpr (D == 128) {
+              const uint4 c = lds128(v0), d = lds128(v1);
+              w[0][0] = c.x; w[0][1] = c.y; w[1][0] = c.z; w[1][1] = c.w;
+              w[2][0] = d.x; w[2][1] = d.y; w[3][0] = d.z; w[3][1] = d.w;
             } else {
-              const uint2 v = lds64(vb + code_at<D>(t, g4 >> 1) + (g4 & 1) * 8);
-              w[e][0] = v.x; w[e][1] = v.y;
+              const uint2 c = lds64(v0), d = lds64(v1);
+              w[0][0] = c.x; w[1][0] = c.y; w[2][0] = d.x; w[3][0] = d.y;
             }
-            // what lies behind the last token may be anything, NaN too
-            if (careful && (key0 + t >= s.len || !((valid >> (t >> 4)) & 1))) {
+            uint32_t f = lds32(gr + G::kVScales + (D == 128 ? g4 : g4 >> 1) * 16 + t4 * 4);
+            if (careful) {  // what lies behind the last token may be anything, a scale that is no number too
 #pragma unroll
-              for (int f = 0; f < kW; ++f) w[e][f] = 0u;
+              for (int e = 0; e < 4; ++e)
+                if (key0 + 16 * ks + 2 * t4 + (e & 1) + 8 * (e >> 1) >= s.len || !((valid >> ks) & 1))
+                  f &= ~(0xffu << (8 * e));
             }
-          }
+            const uint32_t f0 = c4::e4m3x2_to_f16(f), f1 = c4::e4m3x2_to_f16(f >> 16);
 #pragma unroll
-          for (int f = 0; f < kW; ++f) {
-            uint32_t b0[4], b1[4];
-            e4m3_to_f16(__byte_perm(w[0][f], w[1][f], 0x5140), b0[0], b0[1]);
-            e4m3_to_f16(__byte_perm(w[0][f], w[1][f], 0x7362), b0[2], b0[3]);
-            e4m3_to_f16(__byte_perm(w[2][f], w[3][f], 0x5140), b1[0], b1[1]);
-            e4m3_to_f16(__byte_perm(w[2][f], w[3][f], 0x7362), b1[2], b1[3]);
-            if constexpr (kWide) {
+            for (int i = 0; i < D / 64; ++i) {
+              // codes of two tokens side by side: even elements, then odd ones
+              constexpr uint32_t kLow = 0x0f0f0f0fu;
+              uint32_t b0[8], b1[8];
+              auto pairs = [&](uint32_t u, uint32_t v, uint32_t f, uint32_t (&b)[8]) {
+                c4::e2m1_to_f16((u & kLow) | ((v << 4) & ~kLow), b[0], b[2], b[4], b[6]);
+                c4::e2m1_to_f16(((u >> 4) & kLow) | (v & ~kLow), b[1], b[3], b[5], b[7]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mma16816(o[4 * f + e], pa[ks], b0[e], b1[e]);
-            } else {
+                for (int e = 0; e < 8; ++e) b[e] = c4::mul_f16x2(b[e], f);
+              };
+              pairs(w[0][i], w[1][i], f0, b0);
+              pairs(w[2][i], w[3][i], f1, b1);
+              if constexpr (kWide) {
 #pragma unroll
-              for (int e = 0; e < 4; e += 2) {
-                const uint32_t va[4] = {b0[e], b0[e + 1], b1[e], b1[e + 1]};
-                mma16816(o[2 * f + e / 2], va, pa[ks][0], pa[ks][1]);
+                for (int e = 0; e < 8; ++e) mma16816(o[8 * i + e], pa[ks], b0[e], b1[e]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                  const uint32_t va[4] = {b0[e], b0[e + 1], b1[e], b1[e + 1]};
+                  mma16816(o[4 * i + e / 2], va, pa[ks][0], pa[ks][1]);
+                }
+              }
+            }
+          } else {
+            constexpr int kW = D / 32;
+            uint32_t w[4][kW];  // keys: score tile 2 ks (even, odd column), 2 ks + 1
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = tok<D>(2 * ks + (e >> 1), 2 * t4 + (e & 1));
+              if constexpr (kW == 4) {
+                const uint4 v = lds128(vb + code_at<D>(t, g4));
+                w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
+              } else {
+                const uint2 v = lds64(vb + code_at<D>(t, g4 >> 1) + (g4 & 1) * 8);
+                w[e][0] = v.x; w[e][1] = v.y;
+              }
+              // what lies behind the last token may be anything, NaN too
+              if (careful && (key0 + t >= s.len || !((valid >> (t >> 4)) & 1))) {
+#pragma unroll
+                for (int f = 0; f < kW; ++f) w[e][f] = 0u;
+              }
+            }
+#pragma unroll
+            for (int f = 0; f < kW; ++f) {
+              uint32_t b0[4], b1[4];
+              e4m3_to_f16(__byte_perm(w[0][f], w[1][f], 0x5140), b0[0], b0[1]);
+              e4m3_to_f16(__byte_perm(w[0][f], w[1][f], 0x7362), b0[2], b0[3]);
+              e4m3_to_f16(__byte_perm(w[2][f], w[3][f], 0x5140), b1[0], b1[1]);
+              e4m3_to_f16(__byte_perm(w[2][f], w[3][f], 0x7362), b1[2], b1[3]);
+              if constexpr (kWide) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma16816(o[4 * f + e], pa[ks], b0[e], b1[e]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                  const uint32_t va[4] = {b0[e], b0[e + 1], b1[e], b1[e + 1]};
+                  mma16816(o[2 * f + e / 2], va, pa[ks][0], pa[ks][1]);
+                }
               }
             }
           }
@@ -1032,7 +1201,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
         const int row = row_of(y);
         if (row < s.nv) {
           // a row without a visible key: O = 0, L = -inf
-          const float fin = l[y] == 0.f ? 0.f : ex2(E[y] - 14.f) / l[y];
+          const float fin = l[y] == 0.f ? 0.f : unit(ex2(E[y] - 14.f) / l[y]);
           const float lg = l[y] == 0.f ? -INFINITY : m[y] + log2f(l[y]);
           const long long to = s.mode == 0 ? out_row(s, row) : static_cast<long long>(s.slot) * kRows + row;
 #pragma unroll
@@ -1138,7 +1307,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
           }
         }
         // a row without a visible key: O = 0, L = -inf
-        const float fin = L == 0.f ? 0.f : ex2(Em - 14.f) / L;
+        const float fin = L == 0.f ? 0.f : unit(ex2(Em - 14.f) / L);
         const float lg = L == 0.f ? -INFINITY : M + log2f(L);
         acc.x *= fin;
         acc.y *= fin;
@@ -1168,7 +1337,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
 // and did not finish.  Each warp looks up the parts itself, 32 CTAs at a time,
 // and four parts are loaded together: two rounds of loads behind the wait, where
 // a list in shared memory took five and 1.5 to 2 us more.
-template <int D, int ROWS>
+template <int D, int ROWS, class F>
 __global__ void __launch_bounds__(512) fa_cache_merge_kernel(const __grid_constant__ CacheFwdArgs a, int grid) {
   const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   griddep_wait();

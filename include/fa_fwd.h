@@ -351,7 +351,8 @@ size_t fa_attn_unfused_workspace_size(int B, int H, int N, int d);
  * said below; where that loses a token, fa_check_errors reports FA_ERR_INDEX
  * and the record's site and work item say which check (601 a slot of an
  * append, item: token; 611 a block, 612 a length, 613 row offsets, 614 a scale
- * of a forward, item: request).
+ * of a forward, item: request; 621 a position of a rotation, 631 a slot of a
+ * read, item: token).
  *
  * Calls take any state of these arrays, so they can be captured into a graph
  * and replayed on new lengths.
@@ -393,6 +394,18 @@ int fa_cache_slots(int* block_table, const int* seq_lens, const int* new_lens, c
                    const int* free_used, int* cu_new, long long* slot_map, int* seq_lens_out,
                    int* free_used_out, int R, int max_blocks, int num_free, int block_tokens,
                    int num_tokens, void* stream);
+
+/*
+ * fa_cache_slots_positions — the same, and every new token's position:
+ *   positions[cu_new[r] + i] = seq_lens[r] + i, and -1 for tokens of a request
+ *     that is not served and behind cu_new[R]  (int32 [num_tokens])
+ * as fa_rope and fa_cache_append_e2m1 take them.
+ */
+int fa_cache_slots_positions(int* block_table, const int* seq_lens, const int* new_lens,
+                             const int* free_blocks, const int* free_used, int* cu_new,
+                             long long* slot_map, int* positions, int* seq_lens_out,
+                             int* free_used_out, int R, int max_blocks, int num_free,
+                             int block_tokens, int num_tokens, void* stream);
 
 /*
  * fa_cache_append_e4m3 — writes T new K and V rows into the cache at their
@@ -491,6 +504,104 @@ int fa_cache_fwd_e4m3_slots(const void* q, long long q_stride, const void* k8, c
  * (about 2.5 MB, 40 MB where requests have many rows); 0 for sizes it has no work for
  * or does not take. */
 size_t fa_cache_fwd_e4m3_workspace_size(int R, int T, int Hq, int Hkv, int d);
+
+/*
+ * Rotary positions.  A row's first `rot` elements are turned in pairs by the
+ * angles of its position, whose (cos, sin) are a row of a table:
+ *   half:        (x_i, x_{i + rot/2}) -> (x_i c_i - x_{i + rot/2} s_i,
+ *                                        x_{i + rot/2} c_i + x_i s_i)
+ *   interleaved: the same of (x_{2i}, x_{2i+1}),       i < rot / 2
+ * and the others pass.  Results are exact for the table's entries and rounded
+ * once to bf16, nearest even (infinities and NaN go through the formula).
+ *
+ * fa_rope — the rotation of x, bf16 [B, H, N] rows of d, into out.
+ *   x_strides, out_strides : elements between batches, heads and tokens, three
+ *          each (host memory); multiples of 8, 0 to 2^31.  No two rows of out
+ *          share memory; those of x may (a stride of 0).  d is contiguous.
+ *   positions : int32, of token n of batch b at positions[b * positions_stride
+ *          + n]; positions_stride 0 (the same for all) or at least N.  A
+ *          negative one: the row is copied; one of `length` or more is reported
+ *          (FA_ERR_INDEX) and the row copied.
+ *   table   : fp32 [length][rot / 2][2], (cos, sin), 16-byte aligned.
+ *   d 64 or 128; rot a multiple of 16, at most d.
+ *   interleaved 0 or 1.  transposed 1: sines negated, which turns the gradient
+ *          of a result into that of x.
+ *   out may be x with the same strides, else it overlaps no input.
+ * B, N >= 0 (0: nothing to do), B * N at most 2^33.  Errors: NULL, sizes, flags,
+ * overlap: FA_ERR_INVALID_ARG; d, rot or strides out of range:
+ * FA_ERR_UNSUPPORTED; x, out or table not 16-byte aligned, strides:
+ * FA_ERR_MISALIGNED.  Enqueues one kernel.
+ */
+int fa_rope(const void* x, const long long* x_strides, void* out, const long long* out_strides,
+            const int* positions, long long positions_stride, const float* table, int length, int B,
+            int H, int N, int d, int rot, int interleaved, int transposed, void* stream);
+
+/*
+ * The 4-bit key/value cache: a pool of blocks as the 8-bit one, with the same
+ * tables, slots and lengths (fa_cache_slots serves both), in one array
+ *   data : uint8 [num_blocks][Hkv][P / 16][18 d], 16-byte aligned.
+ * A row (a token and kv head of K, or of V) is d E2M1 codes and an E4M3 scale
+ * for every 16 of them, and a value is
+ *   E2M1(code) * E4M3(scale) * unit,
+ * k_unit for K and v_unit for V, powers of two of 2^-64 to 2^64.  A code's low
+ * bits are 0 .5 1 1.5 2 3 4 6, its highest the sign.  The 18 d bytes of 16 tokens:
+ *   8 d  K codes: token by token; of a row the 16-element groups in the order
+ *        0 4 1 5 2 6 3 7 (d = 64: 0 1 2 3), element 2 i in the low and 2 i + 1 in
+ *        the high four bits of a byte
+ *   d    K scales: token by token, groups in that order
+ *   8 d  V codes: eight pieces of d / 8 elements; of a piece token by token, with
+ *        tokens 0-7 and 8-15 exchanged in pieces 1 3 5 7 (d = 64: 2 3 6 7)
+ *   d    V scales: group by group (in order), of a group tokens 0 1 8 9 2 3 10 11
+ *        4 5 12 13 6 7 14 15
+ *
+ * fa_cache_append_e2m1 — writes T new K and V rows at their slots; for each 16
+ * elements x of a row
+ *   s = E4M3(max |x| / (6 unit)), to nearest even, at most 448
+ *   code = E2M1(x / (s unit)), to nearest even, at most 6; 0 where s is 0
+ * With `positions` (int32 [T]) K's rows are turned first, by `table` [length]
+ * [rot / 2][2] and rounded to bf16 as fa_rope does, negative positions and those
+ * of `length` or more as there; NULL: K is taken as it is and table, length and
+ * rot are not looked at.
+ *   k, v, slot_map: as for fa_cache_append_e4m3, but that nothing is written for
+ *          other tokens than those of the call, so that slots may come in any
+ *          order; they are distinct (rows of one slot mix).  Infinite elements
+ *          count as 6 * 448 units; NaN leaves its 16 elements unspecified.
+ * Errors as there, and a unit that is no such power of two:
+ * FA_ERR_INVALID_ARG.  Enqueues one kernel.
+ */
+int fa_cache_append_e2m1(const void* k, const void* v, long long k_stride, long long v_stride,
+                         void* data, float k_unit, float v_unit, const long long* slot_map,
+                         const int* positions, const float* table, int length, int rot,
+                         int interleaved, int T, int Hkv, int d, int num_blocks, int block_tokens,
+                         void* stream);
+
+/*
+ * fa_cache_read_e2m1 — the values at the T slots of slot_map as rows of k and v,
+ * bf16 [T][Hkv][d], 16-byte aligned: exact.  A slot of -1 gives zeros, any other
+ * value outside [0, num_blocks * P) too, and is reported (FA_ERR_INDEX).
+ * Enqueues one kernel.
+ */
+int fa_cache_read_e2m1(const void* data, float k_unit, float v_unit, const long long* slot_map,
+                       void* k, void* v, int T, int Hkv, int d, int num_blocks, int block_tokens,
+                       void* stream);
+
+/*
+ * fa_cache_fwd_e2m1 — fa_cache_fwd_e4m3_slots over the 4-bit cache (slot_map may
+ * be NULL).  Scales in the cache that are no number of [0, 448] (bytes above
+ * 0x7E) leave the rows that see them unspecified; what lies at and behind a
+ * request's len, or in blocks of no request, may be anything.
+ * Exact up to fp32 sums, the rounding of the softmax weights to f16 in the
+ * product with V, and query elements below 2^-17 of their row's largest, which
+ * are off by up to 2^-25 of it.
+ */
+int fa_cache_fwd_e2m1(const void* q, long long q_stride, const void* data, float k_unit,
+                      float v_unit, const int* block_table, const int* seq_lens, const int* cu_q,
+                      const long long* slot_map, void* o, float* lse, int R, int T, int Hq, int Hkv,
+                      int d, int num_blocks, int block_tokens, int max_blocks, float scale,
+                      int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fa_cache_fwd_e2m1, as fa_cache_fwd_e4m3_workspace_size. */
+size_t fa_cache_fwd_e2m1_workspace_size(int R, int T, int Hq, int Hkv, int d);
 
 /*
  * fa_check_errors — synchronise `stream`, then report and clear the device

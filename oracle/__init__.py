@@ -42,3 +42,5 @@ from .cache import (  # noqa: F401
     cache_slots,
     cache_values,
 )
+from . import cache_e2m1  # noqa: F401
+from .rope import rope, rotate, round_bf16  # noqa: F401
