@@ -166,7 +166,7 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
     if (st != FA_OK) return st;
     const uint8_t* vc = static_cast<const uint8_t*>(v8);
     auto launch = [&](auto kernel, bool& done) {
-      if ((st = ready(kernel, Ly::kAlloc, done)) == FA_OK) kernel<<<grid, prm::kThreads, Ly::kAlloc, s>>>(mk, vc, a);
+      if ((st = ready(kernel, Ly::kAlloc, done, 128)) == FA_OK) kernel<<<grid, prm::kThreads, Ly::kAlloc, s>>>(mk, vc, a);
     };
     if (P == 16) launch(fa_cache_prompt_kernel<D, 16>, set[1]);
     else if (P == 32) launch(fa_cache_prompt_kernel<D, 32>, set[2]);

@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "fa_cache4.cuh"
+#include "fa_cache4_prompt.cuh"
 #include "fa_cache_fwd.cuh"
 #include "fa_cache_host.h"
 #include "fa_fwd.h"
@@ -134,22 +135,24 @@ int cache4_read(const void* data, float k_unit, float v_unit, const long long* s
 
 // ----------------------------------------------------------------- forward
 
-// Query rows of a unit by the average rows a request has per kv head.
-int unit_rows4(int R, int T, int Hq, int Hkv) {
+// Query rows of a unit, and with them the kernel, by the average rows a request
+// has per kv head, as for the 8-bit cache.
+int unit_rows4(int R, int T, int Hq, int Hkv, int sms) {
   const long long rows = static_cast<long long>(T) * (Hq / Hkv);
-  return rows <= 8ll * R ? 8 : 16;
+  const bool few = static_cast<long long>(R) * Hkv * 8 <= sms;
+  return rows <= 8ll * R ? 8 : rows <= (few ? 48ll : 16ll) * R ? 16 : prm4::kRows;
 }
 
 size_t cache4_workspace(int R, int T, int Hq, int Hkv, int d) {
   if ((d != 64 && d != 128) || R <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
   host::Device dev;
   if (host::device(&dev) != FA_OK) return 0;
-  const int rows = unit_rows4(R, T, Hq, Hkv);
+  const int rows = unit_rows4(R, T, Hq, Hkv, dev.sms);
   return workspace_bytes(fwd_grid(dev.sms, rows, d), rows, d);
 }
 
-// By device and d (64, 128): 8 rows, 16 rows.
-bool g_ready[64][2][2] = {};
+// By device and d (64, 128): 8 rows, 16 rows, many.
+bool g_ready[64][2][3] = {};
 
 template <int D, int ROWS>
 int launch_few(CacheFwdArgs& a, int P, int grid, bool& done, cudaStream_t s) {
@@ -166,9 +169,19 @@ int launch_few(CacheFwdArgs& a, int P, int grid, bool& done, cudaStream_t s) {
 
 template <int D>
 int launch_cache4_fwd(CacheFwdArgs& a, int P, char* ws, const host::Device& dev, cudaStream_t s) {
-  const int unit = unit_rows4(a.R, a.T, a.Hq, a.Hkv), grid = fwd_grid(dev.sms, unit, D);
+  const int unit = unit_rows4(a.R, a.T, a.Hq, a.Hkv, dev.sms), grid = fwd_grid(dev.sms, unit, D);
   set_workspace(a, ws, grid, unit, D);
   bool* set = g_ready[dev.dev][D == 128];
+  if (unit == prm4::kRows) {
+    using Ly = prm4::Layout<D>;
+    const int st = ready(fa_cache4_prompt_kernel<D>, Ly::kAlloc, set[2], 128);
+    if (st != FA_OK) return st;
+    fa_cache4_prompt_kernel<D><<<grid, prm4::kThreads, Ly::kAlloc, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return host::fail(e);
+    if (static_cast<long long>(a.M) * P <= prm4::kKeys) return FA_OK;
+    return launch_merge<D, prm4::kRows, E2M1Codes>(a, grid, 4, s);
+  }
   return unit == 8 ? launch_few<D, 8>(a, P, grid, set[0], s) : launch_few<D, 16>(a, P, grid, set[1], s);
 }
 

@@ -156,12 +156,20 @@ inline void set_workspace(CacheFwdArgs& a, char* ws, int grid, int rows, int d) 
   a.part_l = a.part_o + static_cast<size_t>(2) * grid * rows * d;
 }
 
-// Dynamic shared memory of a kernel, set once per device.
+// Dynamic shared memory of a kernel, set once per device.  `regs`: registers per
+// thread that its warps' later shares (setmaxnreg) add up from, 0: any number; with
+// others an increase would wait for ever.
 template <typename K>
-int ready(K kernel, int bytes, bool& done) {
+int ready(K kernel, int bytes, bool& done, int regs = 0) {
   static std::mutex mu;
   std::lock_guard<std::mutex> lock(mu);
   if (!done) {
+    if (regs > 0) {
+      cudaFuncAttributes attr;
+      const cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
+      if (e != cudaSuccess) return host::fail(e);
+      if (attr.numRegs != regs) return FA_ERR_UNSUPPORTED;
+    }
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return host::fail(e);
     done = true;

@@ -164,7 +164,7 @@ __device__ __forceinline__ long long floor_sum_in(T n, T m, T a, T b) {
   }
   return sum;
 }
-__device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+static __device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
   // divisions of 64 bits take several times as long: a third of what a CTA
   // does before its first load
   if (a * n + b + m < (1ll << 31))
@@ -277,6 +277,196 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32], int lo, int hi) 
   return m;
 }
 
+// This CTA's share [x0, x1) of the total cost, false: none.  The thread whose
+// requests hold x0 writes where the walk begins: request, kv head and the cost
+// into that (64 bits); the walker finds the row tile.
+__device__ __forceinline__ bool range_of(const CacheFwdArgs& a, long long* scan, int4* start, long long& x0,
+                                         long long& x1) {
+  const int tid = threadIdx.x;
+  const int per = (a.R + kThreads - 1) / kThreads;
+  const int ra = min(a.R, tid * per), rb = min(a.R, ra + per);
+  long long mine = 0, total;
+  for (int r = ra; r < rb; ++r) {
+    mine += a.Hkv * head_cost(a, dec::request<kRows, kKeys>(a, r));
+    if (blockIdx.x == 0) dec::check_request(a, r);
+  }
+  const long long before = cta_scan(mine, scan, total) - mine;
+  const long long want = (total + kMinCost - 1) / kMinCost;
+  const int parts = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, want)));
+  if (static_cast<int>(blockIdx.x) >= parts) return false;
+  x0 = total * blockIdx.x / parts;
+  x1 = total * (blockIdx.x + 1) / parts;
+  if (x0 >= x1) return false;
+  if (before <= x0 && x0 < before + mine) {
+    long long x = before;
+    int r = ra;
+    for (;; ++r) {
+      const long long c = a.Hkv * head_cost(a, dec::request<kRows, kKeys>(a, r));
+      if (x0 < x + c) break;  // ends: this thread's requests hold x0
+      x += c;
+    }
+    // and the kv head; the walker finds the row tile
+    const long long per_head = head_cost(a, dec::request<kRows, kKeys>(a, r));
+    const int h = static_cast<int>((x0 - x) / per_head);
+    const long long y = x0 - x - h * per_head;
+    *start = make_int4(r, h, static_cast<int>(y & 0xffffffffll), static_cast<int>(y >> 32));
+  }
+  return true;
+}
+
+// The walker, a warp: the pieces of units that `cost` from `at` on covers, one
+// descriptor each.
+template <typename W>
+__device__ __forceinline__ void walk(const CacheFwdArgs& a, int4 at, long long cost, dec::Seg* segs, uint32_t seg_full,
+                                     uint32_t seg_empty, W&& wait) {
+  const int lane = threadIdx.x & 31;
+  int r = at.x, h = at.y, rt = 0;
+  dec::Req q = dec::request<kRows, kKeys>(a, r);
+  long long into = static_cast<long long>(at.w) << 32 | static_cast<unsigned>(at.z);
+  // the last row tile whose cost begins at or before it, 32 at a time
+  for (int end = q.nrt; end - rt > 1;) {
+    const int each = (end - rt + 31) / 32, mine = rt + lane * each;
+    const bool before = lane == 0 || (mine < end && cost_before(a, q, mine) <= into);
+    rt += (31 - __clz(__ballot_sync(0xffffffffu, before))) * each;
+    end = min(end, rt + each);
+  }
+  if (lane == 0) {
+    int y = static_cast<int>(into - cost_before(a, q, rt));
+    long long left = cost;
+    int nseg = 0;
+    bool ok = true;
+    while (left > 0) {
+      if (rt >= q.nrt) {  // the next kv head, the next request with rows
+        rt = 0;
+        if (++h == a.Hkv) {
+          h = 0;
+          do q = dec::request<kRows, kKeys>(a, ++r); while (q.nrt == 0);  // ends: cost is left
+        }
+      }
+      const int kt = tiles_of(a, q, rt);
+      const int take = static_cast<int>(min(static_cast<long long>(kt + kUnitCost - y), left));
+      const int t0 = max(0, y - kUnitCost), t1 = max(0, y + take - kUnitCost);
+      left -= take;
+      if (t1 > t0) {
+        const int si = nseg % kSegs;
+        if (nseg >= kSegs && !wait(seg_empty + 8 * si, nseg / kSegs - 1, nseg)) {
+          ok = false;
+          break;
+        }
+        const bool begins = t0 == 0, ends = t1 == kt;
+        dec::Seg* s = segs + si;
+        s->r = r;
+        s->h = h;
+        s->row0 = rt * kRows;
+        s->nv = min(kRows, q.n * a.g - rt * kRows);
+        s->c0 = q.c0;
+        s->n = q.n;
+        s->len = dec::keys_of(a, q);
+        s->t0 = t0;
+        s->nt = t1 - t0;
+        s->mode = begins && ends ? 0 : 1;
+        s->slot = 2 * blockIdx.x + (begins ? 1 : 0);
+        // steps: without the second half of a last tile that no row sees
+        s->base = max(1, min(2 * (t1 - t0), (seen_of(a, q, rt) - t0 * kKeys + kStepKeys - 1) / kStepKeys));
+        mbar_arrive(seg_full + 8 * si);
+        if (begins && !ends) a.desc[blockIdx.x] = make_int4(q.c0, h, rt, min(kRows, q.n * a.g - rt * kRows));
+        if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
+        ++nseg;
+      }
+      ++rt;
+      y = 0;
+    }
+    if (ok) {
+      const int si = nseg % kSegs;
+      if (nseg < kSegs || wait(seg_empty + 8 * si, nseg / kSegs - 1, nseg)) {
+        segs[si].nt = 0;
+        mbar_arrive(seg_full + 8 * si);
+      }
+    }
+  }
+}
+
+// A unit's end for a softmax thread and its row: the halves' sums joined where
+// both have the same rows, O and L written, or left as a partial.
+template <int D, bool UNIT, typename W>
+__device__ __forceinline__ bool finish(const CacheFwdArgs& a, const dec::Seg& s, int x, int row, int warp, int lane,
+                                       float m, float e, float l, uint32_t tO, float4* stat, uint32_t joined,
+                                       W&& wait) {
+  const bool two = s.nv > kHalf;
+  const bool real = row < s.nv;
+  // The halves' statistics, through shared memory; then each of the two
+  // warps that have a row combines and writes one half of its columns.
+  const bool join = !two && s.base > 1;
+  float f = 1.f, f2 = 0.f;  // what this half's sums and the other's count
+  if (join) {
+    const uint32_t bar = joined + 8 * (warp & 3);
+    stat[x * kHalf + row] = make_float4(m, e, l, 0.f);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    if (!__all_sync(0xffffffffu, wait(bar, 0))) return false;
+    tc_fence_after();
+    const float4 b = stat[(1 - x) * kHalf + row];
+    const float m1 = fmaxf(m, b.x), e0 = e + (m - m1), eb = b.y + (b.x - m1), e1 = fmaxf(e0, eb);
+    l = l * ex2(m - m1) + b.z * ex2(b.x - m1);
+    f = ex2(e0 - e1);
+    f2 = ex2(eb - e1);
+    m = m1;
+    e = e1;
+  }
+  float inv = l == 0.f ? 0.f : ex2(e - kBias) / l;
+  if (UNIT) inv *= a.v_unit;
+  const float lg = l == 0.f ? -INFINITY : m + log2f(l);
+  f *= inv;
+  f2 *= inv;
+  const int rr = s.row0 + row, tk = rr / a.g;
+  const long long at = static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
+  const long long pat = static_cast<long long>(s.slot) * kRows + row;
+#pragma unroll 1
+  for (int q = join ? x * (D / 64) : 0; q < (join && x == 0 ? D / 64 : D / 32); ++q) {
+    uint32_t o[32];
+    tmem_ld32(tO + 32 * q, o);
+    tmem_ld_wait32(o);
+#pragma unroll
+    for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+    if (join) {
+      uint32_t o2[32];
+      tmem_ld32(tO + (kHalf - 2 * x * kHalf) + 32 * q, o2);
+      tmem_ld_wait32(o2);
+#pragma unroll
+      for (int y = 0; y < 32; ++y)
+        o[y] = __float_as_uint(fmaf(__uint_as_float(o2[y]), f2, __uint_as_float(o[y])));
+    }
+    if (real) {
+      if (s.mode == 0) {
+        uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + 32 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          dst[e] = make_uint4(
+              pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
+              pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
+              pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
+              pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
+      } else {
+        // a row a lane: 32 bytes a store, as every row takes a pass of its own
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) stg256(a.part_o + pat * D + 32 * q + e, o + e);
+      }
+    }
+  }
+  if (real && (two || x == 0)) {
+    if (s.mode == 0) a.lse[at] = lg * 0.6931471805599453f;
+    else a.part_l[pat] = lg;
+  }
+  tc_fence_before();  // O has been read: the next piece's first product may overwrite it
+  __syncwarp();
+  if (join) {  // by the other warp, too
+    if (lane == 0) mbar_arrive(joined + 8 * (warp & 3));
+    if (!__all_sync(0xffffffffu, wait(joined + 8 * (warp & 3), 1))) return false;
+  }
+  return true;
+}
+
 }  // namespace prm
 
 // G: keys of a step that share their scales, a block's or, of larger ones, all 64.
@@ -332,34 +522,9 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
     a.cont[blockIdx.x] = 0;
   }
 
-  const int per = (a.R + kThreads - 1) / kThreads;
-  const int ra = min(a.R, tid * per), rb = min(a.R, ra + per);
-  long long mine = 0, total;
-  for (int r = ra; r < rb; ++r) {
-    mine += a.Hkv * head_cost(a, dec::request<kRows, kKeys>(a, r));
-    if (blockIdx.x == 0) dec::check_request(a, r);
-  }
-  const long long before = cta_scan(mine, reinterpret_cast<long long*>(sm + Ly::kScan), total) - mine;
-  const long long want = (total + kMinCost - 1) / kMinCost;
-  const int parts = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, want)));
-  if (static_cast<int>(blockIdx.x) >= parts) return;
-  const long long x0 = total * blockIdx.x / parts, x1 = total * (blockIdx.x + 1) / parts;
-  if (x0 >= x1) return;
-  if (before <= x0 && x0 < before + mine) {
-    long long x = before;
-    int r = ra;
-    for (;; ++r) {
-      const long long c = a.Hkv * head_cost(a, dec::request<kRows, kKeys>(a, r));
-      if (x0 < x + c) break;  // ends: this thread's requests hold x0
-      x += c;
-    }
-    // and the kv head; the walker finds the row tile
-    const long long per_head = head_cost(a, dec::request<kRows, kKeys>(a, r));
-    const int h = static_cast<int>((x0 - x) / per_head);
-    const long long y = x0 - x - h * per_head;
-    *reinterpret_cast<int4*>(sm + Ly::kStart) =
-        make_int4(r, h, static_cast<int>(y & 0xffffffffll), static_cast<int>(y >> 32));
-  }
+  long long x0, x1;
+  if (!range_of(a, reinterpret_cast<long long*>(sm + Ly::kScan), reinterpret_cast<int4*>(sm + Ly::kStart), x0, x1))
+    return;
   if (warp == 12) {
     tmem_alloc(base + Ly::kTmemSlot, 512);
     tmem_relinquish();
@@ -375,71 +540,8 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
     reg_dec<80>();
     if (warp == 13) {
       // --------------------------------------------------------- the walker
-      const int4 at = *reinterpret_cast<const int4*>(sm + Ly::kStart);
-      int r = at.x, h = at.y, rt = 0;
-      Req q = dec::request<kRows, kKeys>(a, r);
-      long long into = static_cast<long long>(at.w) << 32 | static_cast<unsigned>(at.z);
-      // the last row tile whose cost begins at or before it, 32 at a time
-      for (int end = q.nrt; end - rt > 1;) {
-        const int each = (end - rt + 31) / 32, mine = rt + lane * each;
-        const bool before = lane == 0 || (mine < end && cost_before(a, q, mine) <= into);
-        rt += (31 - __clz(__ballot_sync(0xffffffffu, before))) * each;
-        end = min(end, rt + each);
-      }
-      if (lane == 0) {
-        int y = static_cast<int>(into - cost_before(a, q, rt));
-        long long left = x1 - x0;
-        int nseg = 0;
-        bool ok = true;
-        while (left > 0) {
-          if (rt >= q.nrt) {  // the next kv head, the next request with rows
-            rt = 0;
-            if (++h == a.Hkv) {
-              h = 0;
-              do q = dec::request<kRows, kKeys>(a, ++r); while (q.nrt == 0);  // ends: cost is left
-            }
-          }
-          const int kt = tiles_of(a, q, rt);
-          const int take = static_cast<int>(min(static_cast<long long>(kt + kUnitCost - y), left));
-          const int t0 = max(0, y - kUnitCost), t1 = max(0, y + take - kUnitCost);
-          left -= take;
-          if (t1 > t0) {
-            const int si = nseg % kSegs;
-            if (nseg >= kSegs && !wait(Ly::kSegEmpty + 8 * si, nseg / kSegs - 1, kSiteSegEmpty, nseg)) {
-              ok = false;
-              break;
-            }
-            const bool begins = t0 == 0, ends = t1 == kt;
-            Seg* s = segs + si;
-            s->r = r;
-            s->h = h;
-            s->row0 = rt * kRows;
-            s->nv = min(kRows, q.n * a.g - rt * kRows);
-            s->c0 = q.c0;
-            s->n = q.n;
-            s->len = dec::keys_of(a, q);
-            s->t0 = t0;
-            s->nt = t1 - t0;
-            s->mode = begins && ends ? 0 : 1;
-            s->slot = 2 * blockIdx.x + (begins ? 1 : 0);
-            // steps: without the second half of a last tile that no row sees
-            s->base = max(1, min(2 * (t1 - t0), (seen_of(a, q, rt) - t0 * kKeys + kStepKeys - 1) / kStepKeys));
-            mbar_arrive(base + Ly::kSegFull + 8 * si);
-            if (begins && !ends) a.desc[blockIdx.x] = make_int4(q.c0, h, rt, min(kRows, q.n * a.g - rt * kRows));
-            if (!begins) a.cont[blockIdx.x] = ends ? 2 : 1;
-            ++nseg;
-          }
-          ++rt;
-          y = 0;
-        }
-        if (ok) {
-          const int si = nseg % kSegs;
-          if (nseg < kSegs || wait(Ly::kSegEmpty + 8 * si, nseg / kSegs - 1, kSiteSegEmpty, nseg)) {
-            segs[si].nt = 0;
-            mbar_arrive(base + Ly::kSegFull + 8 * si);
-          }
-        }
-      }
+      walk(a, *reinterpret_cast<const int4*>(sm + Ly::kStart), x1 - x0, segs, base + Ly::kSegFull, base + Ly::kSegEmpty,
+           [&](uint32_t bar, uint32_t parity, int item) { return wait(bar - base, parity, kSiteSegEmpty, item); });
     } else if (warp == 14) {
       // ------------------------------------------------------- the loader
       // Codes of a tile's blocks, K's to their place, V's as they lie into a
@@ -977,79 +1079,9 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       ok = wait(Ly::kPvDone + 8 * (2 * x + ((cnt - 1) & 1)), (cnt - 1) >> 1, kSitePV, jt);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const bool real = row < s.nv;
-      // The halves' statistics, through shared memory; then each of the two
-      // warps that have a row combines and writes one half of its columns.
-      const bool join = !two && s.base > 1;
-      float f = 1.f, f2 = 0.f;  // what this half's sums and the other's count
-      if (join) {
-        const uint32_t bar = base + Ly::kJoin + 8 * (warp & 3);
-        float4* stat = reinterpret_cast<float4*>(sm + Ly::kStat);
-        stat[x * kHalf + row] = make_float4(m, e, l, 0.f);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-        ok = wait(Ly::kJoin + 8 * (warp & 3), 0, kSiteJoin, jt);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_fence_after();
-        const float4 b = stat[(1 - x) * kHalf + row];
-        const float m1 = fmaxf(m, b.x), e0 = e + (m - m1), eb = b.y + (b.x - m1), e1 = fmaxf(e0, eb);
-        l = l * ex2(m - m1) + b.z * ex2(b.x - m1);
-        f = ex2(e0 - e1);
-        f2 = ex2(eb - e1);
-        m = m1;
-        e = e1;
-      }
-      const float inv = l == 0.f ? 0.f : ex2(e - kBias) / l;
-      const float lg = l == 0.f ? -INFINITY : m + log2f(l);
-      f *= inv;
-      f2 *= inv;
-      const int rr = s.row0 + row, tk = rr / a.g;
-      const long long at = static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
-      const long long pat = static_cast<long long>(s.slot) * kRows + row;
-#pragma unroll 1
-      for (int q = join ? x * (D / 64) : 0; q < (join && x == 0 ? D / 64 : D / 32); ++q) {
-        uint32_t o[32];
-        tmem_ld32(tO + 32 * q, o);
-        tmem_ld_wait32(o);
-#pragma unroll
-        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-        if (join) {
-          uint32_t o2[32];
-          tmem_ld32(tO + (kHalf - 2 * x * kHalf) + 32 * q, o2);
-          tmem_ld_wait32(o2);
-#pragma unroll
-          for (int y = 0; y < 32; ++y)
-            o[y] = __float_as_uint(fmaf(__uint_as_float(o2[y]), f2, __uint_as_float(o[y])));
-        }
-        if (real) {
-          if (s.mode == 0) {
-            uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + 32 * q);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(
-                  pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
-                  pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
-                  pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
-                  pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
-          } else {
-            // a row a lane: 32 bytes a store, as every row takes a pass of its own
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) stg256(a.part_o + pat * D + 32 * q + e, o + e);
-          }
-        }
-      }
-      if (real && (two || x == 0)) {
-        if (s.mode == 0) a.lse[at] = lg * 0.6931471805599453f;
-        else a.part_l[pat] = lg;
-      }
-      tc_fence_before();  // O has been read: the next piece's first product may overwrite it
-      __syncwarp();
-      if (join) {  // by the other warp, too
-        if (lane == 0) mbar_arrive(base + Ly::kJoin + 8 * (warp & 3));
-        ok = wait(Ly::kJoin + 8 * (warp & 3), 1, kSiteJoin, jt);
-        if (!__all_sync(0xffffffffu, ok)) break;
-      }
+      ok = finish<D, false>(a, s, x, row, warp, lane, m, e, l, tO, reinterpret_cast<float4*>(sm + Ly::kStat),
+                            base + Ly::kJoin, [&](uint32_t bar, uint32_t parity) { return wait(bar - base, parity, kSiteJoin, jt); });
+      if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
     }
   }
