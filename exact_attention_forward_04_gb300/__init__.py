@@ -67,7 +67,8 @@ SYMBOLS = {
     "fa_cache_fwd_e4m3_slots": (_c.c_int, [_c.c_void_p, _c.c_longlong] + [_c.c_void_p] * 10 + [_c.c_int] * 8 +
                                 [_c.c_float, _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "fa_cache_fwd_e4m3_workspace_size": (_c.c_size_t, [_c.c_int] * 5),
-    "fa_rope": (_c.c_int, [_c.c_void_p] * 5 + [_c.c_longlong, _c.c_void_p] + [_c.c_int] * 8 + [_c.c_void_p]),
+    "fa_rope": (_c.c_int, ([_c.c_void_p] + [_c.c_longlong] * 3) * 2 + [_c.c_void_p, _c.c_longlong, _c.c_void_p] +
+                [_c.c_int] * 8 + [_c.c_void_p]),
     "fa_cache_append_e2m1": (_c.c_int, [_c.c_void_p] * 2 + [_c.c_longlong] * 2 + [_c.c_void_p] + [_c.c_float] * 2 +
                              [_c.c_void_p] * 3 + [_c.c_int] * 8 + [_c.c_void_p]),
     "fa_cache_read_e2m1": (_c.c_int, [_c.c_void_p] + [_c.c_float] * 2 + [_c.c_void_p] * 3 + [_c.c_int] * 5 +
@@ -122,6 +123,23 @@ def load_library(path: str | None = None):
         if path is None:
             _lib = lib
         return lib
+
+
+def _load_torch():
+    """The module of the usual calls from PyTorch tensors, bound to the library."""
+    import importlib.util
+    lib = load_library()
+    path = os.path.join(_PKG, "_lib", "fa_torch.so")
+    if not os.path.exists(path):
+        raise FAError(-4, "load", f"{path} is missing; build it with "
+                                  "`python -m exact_attention_forward_04_gb300._build`")
+    spec = importlib.util.spec_from_file_location("fa_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "fa_rope", "fa_cache_append_e2m1", "fa_cache_read_e2m1", "fa_cache_fwd_e2m1",
+        "fa_cache_fwd_e2m1_workspace_size")))
+    return module
 
 
 def status_string(status: int) -> str:

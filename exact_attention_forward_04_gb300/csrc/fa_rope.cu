@@ -34,17 +34,18 @@ bool rows_apart(const int (&n)[3], const long long* strides, int d) {
   return true;
 }
 
-int rope_run(const void* x, const long long* xs, void* out, const long long* os, const int* positions,
+int rope_run(const void* x, long long (&xs)[3], void* out, long long (&os)[3], const int* positions,
              long long positions_stride, const float* table, int length, int B, int H, int N, int d, int rot,
              int interleaved, int transposed, cudaStream_t s) {
   if (B < 0 || H <= 0 || N < 0 || length <= 0) return FA_ERR_INVALID_ARG;
   if ((interleaved != 0 && interleaved != 1) || (transposed != 0 && transposed != 1)) return FA_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || rot <= 0 || rot > d || rot % 16 != 0) return FA_ERR_UNSUPPORTED;
   if (B == 0 || N == 0) return FA_OK;
-  if (!x || !out || !positions || !table || !xs || !os) return FA_ERR_INVALID_ARG;
+  if (!x || !out || !positions || !table) return FA_ERR_INVALID_ARG;
   if (positions_stride != 0 && positions_stride < N) return FA_ERR_INVALID_ARG;
   const int n[3] = {B, H, N};
   for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) xs[i] = os[i] = 0;  // of no matter
     if (xs[i] < 0 || os[i] < 0) return FA_ERR_INVALID_ARG;
     if ((xs[i] | os[i]) & 7) return FA_ERR_MISALIGNED;
     if (xs[i] > (1ll << 31) || os[i] > (1ll << 31)) return FA_ERR_UNSUPPORTED;
@@ -57,7 +58,7 @@ int rope_run(const void* x, const long long* xs, void* out, const long long* os,
   const size_t no = 2 * static_cast<size_t>(span(B, H, N, d, os[0], os[1], os[2]));
   // in place: the same rows, each read and written by the same threads
   bool same = x == out;
-  for (int i = 0; i < 3; ++i) same = same && (n[i] == 1 || xs[i] == os[i]);
+  for (int i = 0; i < 3; ++i) same = same && xs[i] == os[i];
   if (!same && host::overlap(out, no, x, nx)) return FA_ERR_INVALID_ARG;
   const size_t np = 4 * (static_cast<size_t>(B - 1) * positions_stride + N);
   if (host::overlap(out, no, positions, np)) return FA_ERR_INVALID_ARG;
@@ -104,9 +105,11 @@ int rope_run(const void* x, const long long* xs, void* out, const long long* os,
 }  // namespace
 }  // namespace fa
 
-extern "C" int fa_rope(const void* x, const long long* x_strides, void* out, const long long* out_strides,
-                       const int* positions, long long positions_stride, const float* table, int length, int B, int H,
-                       int N, int d, int rot, int interleaved, int transposed, void* stream) {
-  return fa::rope_run(x, x_strides, out, out_strides, positions, positions_stride, table, length, B, H, N, d, rot,
-                      interleaved, transposed, static_cast<cudaStream_t>(stream));
+extern "C" int fa_rope(const void* x, long long x_batch, long long x_head, long long x_token, void* out,
+                       long long out_batch, long long out_head, long long out_token, const int* positions,
+                       long long positions_stride, const float* table, int length, int B, int H, int N, int d, int rot,
+                       int interleaved, int transposed, void* stream) {
+  long long xs[3] = {x_batch, x_head, x_token}, os[3] = {out_batch, out_head, out_token};
+  return fa::rope_run(x, xs, out, os, positions, positions_stride, table, length, B, H, N, d, rot, interleaved,
+                      transposed, static_cast<cudaStream_t>(stream));
 }

@@ -8,7 +8,6 @@
 """
 from __future__ import annotations
 
-import ctypes
 import math
 
 import torch
@@ -18,8 +17,9 @@ from .cache import _call, _check, _failed
 __all__ = ["rope_table", "rope", "rope_backward"]
 
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
-_Strides = ctypes.c_longlong * 3
+_empty = torch.empty
 _fn = None
+_usual = None  # fa_torch's, for the usual calls; None elsewhere
 
 
 def _load():
@@ -27,6 +27,13 @@ def _load():
     from . import load_library
     _fn = load_library().fa_rope
     return _fn
+
+
+def _load_usual():
+    global _usual
+    from . import _load_torch
+    _usual = _load_torch().rope
+    return _usual
 
 
 def rope_table(length, rot, base=10000.0, factor=1.0, original_length=None, low=1.0, high=32.0, magnitude=1.0,
@@ -61,67 +68,66 @@ def rope_table(length, rot, base=10000.0, factor=1.0, original_length=None, low=
     return torch.stack((angle.cos(), angle.sin()), -1).mul_(magnitude).to(_F32).to(device)
 
 
-def _check_table(table, d, device):
-    if not (isinstance(table, torch.Tensor) and table.dtype is _F32 and table.dim() == 3 and table.shape[2] == 2
-            and table.is_contiguous() and table.device == device):
-        _check("table", table, _F32, (None, None, 2), device)
-    rot = 2 * table.shape[1]
-    if rot == 0 or rot % 16 or rot > d:
-        raise ValueError(f"table: {rot} elements to turn must be a multiple of 16 and at most d = {d}")
-    if table.shape[0] == 0:
-        raise ValueError("table has no positions")
-    return table.shape[0], rot
+def _check_table(table, d, index):
+    """(length, rot) of a table on CUDA device ``index``."""
+    if not (isinstance(table, torch.Tensor) and table.dtype is _F32 and table.dim() == 3 and table.is_contiguous()
+            and table.get_device() == index):
+        _check("table", table, _F32, (None, None, 2), torch.device("cuda", index))
+    length, half, two = table.shape
+    if two != 2 or length == 0 or half == 0 or half % 8 or 2 * half > d:
+        raise ValueError(f"table must be [positions, rot / 2, 2] with rot a multiple of 16 and at most d = {d}, got "
+                         f"{tuple(table.shape)}")
+    return length, 2 * half
 
 
 def _rotate(name, x, positions, table, interleaved, out, stream, transposed):
     if not isinstance(x, torch.Tensor) or x.dtype is not _BF16:
         raise TypeError(f"{name} must be a bfloat16 tensor")
-    if not x.is_cuda:
+    index = x.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev, shape = x.device, x.shape
-    if len(shape) not in (3, 4):
-        raise ValueError(f"{name} must be [T, H, d] or [B, H, N, d], got {tuple(shape)}")
-    d = shape[-1]
-    length, rot = _check_table(table, d, dev)
-    if not (isinstance(positions, torch.Tensor) and positions.dtype is _I32 and positions.is_contiguous()
-            and positions.device == dev):
-        _check("positions", positions, _I32, (None,) * (positions.dim() if isinstance(positions, torch.Tensor) else 1),
-               dev)
-    if len(shape) == 3:
-        B, N, H = 1, shape[0], shape[1]
-        if positions.shape != (N,):
-            raise ValueError(f"positions must be [{N}], got {tuple(positions.shape)}")
-        axes, per_batch = (None, 1, 0), 0
+    shape, st = x.shape, x.stride()
+    axes = len(shape)
+    if axes == 3:
+        N, H, d = shape
+        B, strides, usual = 1, (d, st[1], st[0]), (N,)
+    elif axes == 4:
+        B, H, N, d = shape
+        strides, usual = st[:3], (N,)
     else:
-        B, H, N = shape[0], shape[1], shape[2]
-        if positions.shape != (N,) and positions.shape != (B, N):
-            raise ValueError(f"positions must be [{N}] or [{B}, {N}], got {tuple(positions.shape)}")
-        axes, per_batch = (0, 1, 2), N if positions.dim() == 2 else 0
-    if out is not None:
-        if not (isinstance(out, torch.Tensor) and out.dtype is _BF16 and out.shape == shape and out.device == dev):
-            raise ValueError(f"out must be a bfloat16 {tuple(shape)} tensor on {dev}")
-    if H == 0 or B == 0 or N == 0:
-        return torch.empty(shape, dtype=_BF16, device=dev) if out is None else out
-    for what, t in ((name, x), ("out", out)):
-        if t is not None and t.stride(-1) != 1:
-            raise ValueError(f"{what}: the elements of a row must be contiguous")
-    return _call(dev, stream, _run, dev, x, out, axes, positions, per_batch, table, length, B, H, N, d, rot,
-                 bool(interleaved), transposed)
+        raise ValueError(f"{name} must be [T, H, d] or [B, H, N, d], got {tuple(shape)}")
+    length, rot = _check_table(table, d, index)
+    if not (isinstance(positions, torch.Tensor) and positions.dtype is _I32 and positions.is_contiguous()
+            and positions.get_device() == index):
+        dims = positions.dim() if isinstance(positions, torch.Tensor) else 1
+        _check("positions", positions, _I32, (None,) * dims, x.device)
+    per_batch = 0
+    if positions.shape != usual:
+        if axes == 3 or positions.shape != (B, N):
+            raise ValueError(f"positions must be [{N}]{'' if axes == 3 else f' or [{B}, {N}]'}, got "
+                             f"{tuple(positions.shape)}")
+        per_batch = N
+    if out is not None and not (isinstance(out, torch.Tensor) and out.dtype is _BF16 and out.shape == shape
+                                and out.get_device() == index):
+        raise ValueError(f"out must be a bfloat16 {tuple(shape)} tensor on {x.device}")
+    if B * H * N == 0:
+        return _empty(shape, dtype=_BF16, device=x.device) if out is None else out
+    if st[-1] != 1 or (out is not None and out.stride(-1) != 1):
+        raise ValueError(f"{name if st[-1] != 1 else 'out'}: the elements of a row must be contiguous")
+    return _call(x.device, stream, _run, x, strides, out, axes, positions, per_batch, table, length, B, H, N, d, rot,
+                 interleaved, transposed)
 
 
-def _strides(t, axes, sizes, d):
-    """Of batches, heads and tokens; an axis of one element gets d."""
-    st = t.stride()
-    return _Strides(*(d if n == 1 or i is None else st[i] for i, n in zip(axes, sizes)))
-
-
-def _run(handle, dev, x, out, axes, positions, per_batch, table, length, B, H, N, d, rot, interleaved, transposed):
+def _run(handle, x, strides, out, axes, positions, per_batch, table, length, B, H, N, d, rot, interleaved, transposed):
     if out is None:
-        out = torch.empty(x.shape, dtype=_BF16, device=dev)
-    sizes = (B, H, N)
-    st = (_fn or _load())(
-        x.data_ptr(), _strides(x, axes, sizes, d), out.data_ptr(), _strides(out, axes, sizes, d),
-        positions.data_ptr(), per_batch, table.data_ptr(), length, B, H, N, d, rot, interleaved, transposed, handle)
+        out = _empty(x.shape, dtype=_BF16, device=x.device)
+        ob, oh, on = (d, d, H * d) if axes == 3 else (H * N * d, N * d, d)
+    else:
+        st = out.stride()
+        ob, oh, on = (d, st[1], st[0]) if axes == 3 else st[:3]
+    xb, xh, xn = strides
+    st = (_fn or _load())(x.data_ptr(), xb, xh, xn, out.data_ptr(), ob, oh, on, positions.data_ptr(), per_batch,
+                          table.data_ptr(), length, B, H, N, d, rot, bool(interleaved), transposed, handle)
     if st:
         _failed(st, "fa_rope")
     return out
@@ -133,9 +139,17 @@ def rope(x, positions, table, interleaved=False, out=None, stream=None):
     each row turned by its position's angles, the table's: halves with each
     other, or (``interleaved``) neighbours.  Rows at negative positions are
     copied.  ``out`` may be x itself."""
+    if out is None and stream is None:
+        y = (_usual or _load_usual())(x, positions, table, interleaved, False)
+        if y is not None:
+            return y
     return _rotate("x", x, positions, table, interleaved, out, stream, False)
 
 
 def rope_backward(dout, positions, table, interleaved=False, out=None, stream=None):
     """The gradient of rope's x, given that of its result."""
+    if out is None and stream is None:
+        y = (_usual or _load_usual())(dout, positions, table, interleaved, True)
+        if y is not None:
+            return y
     return _rotate("dout", dout, positions, table, interleaved, out, stream, True)

@@ -515,9 +515,9 @@ size_t fa_cache_fwd_e4m3_workspace_size(int R, int T, int Hq, int Hkv, int d);
  * once to bf16, nearest even (infinities and NaN go through the formula).
  *
  * fa_rope — the rotation of x, bf16 [B, H, N] rows of d, into out.
- *   x_strides, out_strides : elements between batches, heads and tokens, three
- *          each (host memory); multiples of 8, 0 to 2^31.  No two rows of out
- *          share memory; those of x may (a stride of 0).  d is contiguous.
+ *   x_batch .. out_token : elements between batches, heads and tokens, multiples
+ *          of 8 from 0 to 2^31 (of no matter where there is one).  No two rows of
+ *          out share memory; those of x may (a stride of 0).  d is contiguous.
  *   positions : int32, of token n of batch b at positions[b * positions_stride
  *          + n]; positions_stride 0 (the same for all) or at least N.  A
  *          negative one: the row is copied; one of `length` or more is reported
@@ -532,9 +532,10 @@ size_t fa_cache_fwd_e4m3_workspace_size(int R, int T, int Hq, int Hkv, int d);
  * FA_ERR_UNSUPPORTED; x, out or table not 16-byte aligned, strides:
  * FA_ERR_MISALIGNED.  Enqueues one kernel.
  */
-int fa_rope(const void* x, const long long* x_strides, void* out, const long long* out_strides,
-            const int* positions, long long positions_stride, const float* table, int length, int B,
-            int H, int N, int d, int rot, int interleaved, int transposed, void* stream);
+int fa_rope(const void* x, long long x_batch, long long x_head, long long x_token, void* out,
+            long long out_batch, long long out_head, long long out_token, const int* positions,
+            long long positions_stride, const float* table, int length, int B, int H, int N, int d,
+            int rot, int interleaved, int transposed, void* stream);
 
 /*
  * The 4-bit key/value cache: a pool of blocks as the 8-bit one, with the same

@@ -1,7 +1,6 @@
 """Refusals of rotary positions and of the 4-bit key/value cache, on the host:
 fake addresses that are never dereferenced, and CPU tensors.  And the oracle's
 pins."""
-import ctypes
 import math
 
 import numpy as np
@@ -22,17 +21,16 @@ def lib():
 
 
 X, OUT, POS, TAB = (0x10000000 * (i + 1) for i in range(4))
-S3 = ctypes.c_longlong * 3
 
 
 def _rope(lib, x=X, xs=(8192, 1024, 128), out=OUT, os=(8192, 1024, 128), pos=POS, ps=0, tab=TAB, length=100, B=2, H=8,
           N=8, d=128, rot=128, il=0, tr=0):
-    return lib.fa_rope(x, xs and S3(*xs), out, os and S3(*os), pos, ps, tab, length, B, H, N, d, rot, il, tr, None)
+    return lib.fa_rope(x, *xs, out, *os, pos, ps, tab, length, B, H, N, d, rot, il, tr, None)
 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(x=0), INVALID), (dict(out=0), INVALID), (dict(pos=0), INVALID), (dict(tab=0), INVALID),
-    (dict(xs=None), INVALID), (dict(os=None), INVALID), (dict(length=0), INVALID), (dict(B=-1), INVALID),
+    (dict(length=0), INVALID), (dict(B=-1), INVALID),
     (dict(H=0), INVALID), (dict(N=-1), INVALID), (dict(il=2), INVALID), (dict(tr=-1), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(rot=0), UNSUPPORTED), (dict(rot=24), UNSUPPORTED), (dict(rot=144), UNSUPPORTED),
     (dict(d=64, rot=128), UNSUPPORTED), (dict(ps=7), INVALID), (dict(ps=-8), INVALID),

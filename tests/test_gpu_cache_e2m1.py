@@ -622,3 +622,21 @@ def test_captured_prompts_replay_on_other_lengths():
         rows = sum(new)
         assert torch.equal(o[:rows], ow[:rows]) and torch.equal(lse[:rows], lw[:rows])
     fa.check_errors()
+
+
+def test_results_are_freed():
+    """Call after call takes the same memory."""
+    P, d, H, g = 16, 64, 2, 2
+    cache = _cache(40, H, P, d, 1)
+    q, sl = _rows(3, H * g, d, 2), torch.tensor([1, 2, 3], device=DEV)
+    table, lens, cu, angles = i32([[0, 1]] * 3), i32([20, 3, 9]), i32([0, 1, 2, 3]), fa.rope_table(40, d)
+
+    def step():
+        fa.cache_append_e2m1(q[:, :H], q[:, H:], cache, sl, positions=lens, table=angles)
+        return fa.rope(q, lens, angles), fa.cache_read_e2m1(cache, sl), fa.cache_forward_e2m1(q, cache, table, lens, cu)
+
+    step()
+    before = torch.cuda.memory_allocated()
+    for _ in range(20):
+        step()
+    assert torch.cuda.memory_allocated() == before
