@@ -189,11 +189,11 @@ int launch_cache_fwd(CacheFwdArgs& a, const void* k8, const void* v8, int P, cha
   if (unit == 8) {
     using Ly = dec::Layout<D, 8, E4M3Codes>;
     if ((st = ready(fa_cache_fwd_kernel<D, 8, E4M3Codes>, Ly::kAlloc, set[0])) != FA_OK) return st;
-    fa_cache_fwd_kernel<D, 8, E4M3Codes><<<grid, dec::kThreads, Ly::kAlloc, s>>>(maps, a);
+    fa_cache_fwd_kernel<D, 8, E4M3Codes><<<grid, Ly::kThreads, Ly::kAlloc, s>>>(maps, a);
   } else {
     using Ly = dec::Layout<D, 16, E4M3Codes>;
     if ((st = ready(fa_cache_fwd_kernel<D, 16, E4M3Codes>, Ly::kAlloc, set[4])) != FA_OK) return st;
-    fa_cache_fwd_kernel<D, 16, E4M3Codes><<<grid, dec::kThreads, Ly::kAlloc, s>>>(maps, a);
+    fa_cache_fwd_kernel<D, 16, E4M3Codes><<<grid, Ly::kThreads, Ly::kAlloc, s>>>(maps, a);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return host::fail(e);

@@ -159,11 +159,11 @@ int launch_few(CacheFwdArgs& a, int P, int grid, bool& done, cudaStream_t s) {
   using Ly = dec::Layout<D, ROWS, E2M1Codes>;
   const int st = ready(fa_cache_fwd_kernel<D, ROWS, E2M1Codes>, Ly::kAlloc, done);
   if (st != FA_OK) return st;
-  fa_cache_fwd_kernel<D, ROWS, E2M1Codes><<<grid, dec::kThreads, Ly::kAlloc, s>>>(E2M1Codes::Maps{}, a);
+  fa_cache_fwd_kernel<D, ROWS, E2M1Codes><<<grid, Ly::kThreads, Ly::kAlloc, s>>>(E2M1Codes::Maps{}, a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return host::fail(e);
   // a unit of one tile is never split: nothing to merge
-  if (static_cast<long long>(a.M) * P <= dec::kKeys) return FA_OK;
+  if (static_cast<long long>(a.M) * P <= Ly::kTile) return FA_OK;
   return launch_merge<D, ROWS, E2M1Codes>(a, grid, 1, s);
 }
 

@@ -72,11 +72,7 @@ struct E2M1Codes {  // a scale for 16 elements, in granules with the codes
 
 namespace dec {
 
-constexpr int kWarps = 8;                    // consumer warps
-constexpr int kThreads = 32 * (kWarps + 1);  // and the producer
-constexpr int kKeys = 32;                    // keys of a tile
-constexpr int kUnitCost = 12;                // a piece's fixed cost, in tiles (5: 114 us for 104)
-constexpr int kMinCost = 12;                 // least cost of a CTA's range
+constexpr int kKeys = 32;                    // keys of a tile, or part of one, that a warp takes
 constexpr int kWarpScan = 128;               // requests that one warp sums
 // References before the first key: -FLT_MAX, as scores may lie anywhere above.
 // What is subtracted from it or from a score may then be -inf, which ends as a
@@ -102,10 +98,36 @@ constexpr int ctas_per_sm(int d, int rows) { return d == 64 && rows == 8 ? 2 : 1
 template <int D, int ROWS, class F>
 struct Layout {
   static constexpr int kCtas = ctas_per_sm(D, ROWS);
+  // Consumer warps, and the numbers of them that a piece may have: 1, 2, 4 and 8.
+  // Taking 4-bit codes apart is more instructions a byte: 15 warps, a register file
+  // of 128 registers a thread full with the producer (one request of 8 kv heads
+  // over all warps; 24 requests of 20000 to 32768 tokens: 154 us with 8), in
+  // threes or all.
+  static constexpr bool kMany = F::k4 && D == 128 && ROWS == 8;
+  static constexpr int kWarps = kMany ? 15 : 8;
+  static constexpr int kThreads = 32 * (kWarps + 1);            // and the producer
+  static constexpr int kSmall = kMany ? 3 : 2, kMiddle = kMany ? 15 : 4;
+  static constexpr int kSmalls = kWarps / kSmall, kMiddles = kMany ? 0 : 2;
+  static constexpr int kMerges = kSmalls + kMiddles + 1;        // groups that merge
+  __device__ static int next_size(int nw) { return nw == 1 ? kSmall : nw == kSmall ? kMiddle : kWarps; }
+  // 1, 2, 4: a bit for each size above one.
+  __device__ static uint32_t kind_of(int nw) { return nw == kSmall ? 1u : nw == kWarps ? 4u : 2u; }
+  // Offset of the merge barrier of the warps of a group that `warp` is one of.
+  __device__ static int merge_bar(int warp, uint32_t kind) {
+    return 8 * (kind == 1u ? warp / kSmall : kind == 2u ? kSmalls + warp / kMiddle : kMerges - 1);
+  }
   static constexpr int kSegs = 8;                               // unit pieces in flight
+  // Keys of a tile: what one load brings of each of its blocks.  Of 4-bit codes two
+  // warps share one, as the producer takes about 100 cycles a load and 32 keys
+  // arrive every 196 (24 requests of 20000 to 32768 tokens: 143 us with 32 keys).
+  static constexpr int kParts = F::k4 ? 2 : 1;
+  static constexpr int kTile = kParts * kKeys;
+  static constexpr int kUnitCost = F::k4 ? 16 : 12;             // a piece's fixed cost, in tiles (8 bits, 5: 114 us for 104)
+  static constexpr int kMinCost = F::k4 ? 6 : 12;               // least cost of a CTA's range
   static constexpr int kHalf = kKeys * D;                       // codes of K (or V) of a tile; 4 bits: unused
-  static constexpr int kStage = F::k4 ? 2 * c4::Granule<D>::kBytes : 2 * kHalf;
-  static constexpr int kStages = 131072 / kCtas / kStage / kWarps * kWarps;
+  static constexpr int kPart = 2 * c4::Granule<D>::kBytes;      // 4 bits: of a warp's keys
+  static constexpr int kStage = F::k4 ? kParts * kPart : 2 * kHalf;
+  static constexpr int kStages = (kMany ? 139264 : 131072) / kCtas / kStage * kParts / kWarps * kWarps / kParts;
   static constexpr int kIssue = kStages / 2 < 32 ? kStages / 2 : 32;  // lanes that issue loads
   // Tiles whose blocks and scales are held.  An entry is reused so many tiles
   // later: before the first of 32 tiles is looked up, all but the last ring's
@@ -116,19 +138,23 @@ struct Layout {
   static constexpr int kQ = kMerge + kWarps * 8 * D * 4;        // bf16 [segs][rows][D]
   static constexpr int kStats = kQ + kSegs * ROWS * D * 2;      // float4 [warps][8]
   static constexpr int kScales = kStats + kWarps * 8 * 16;      // float4 [meta]
-  static constexpr int kBlk = kScales + kMeta * 16;             // int4 [meta]: blocks, row in the block, valid
+  // int4 [meta]: blocks, row in the block, valid; 4 bits: blocks, and in an int
+  // each in the place of the scales the granule in the block and 16 times valid
+  static constexpr int kBlk = kScales + kMeta * 16;
   static constexpr int kSeg = kBlk + kMeta * 16;
   static constexpr int kBar = (kSeg + kSegs * static_cast<int>(sizeof(Seg)) + 15) & ~15;
   static constexpr int kFull = kBar;                    // [stages]
   static constexpr int kEmpty = kFull + 8 * kStages;    // [stages]
   static constexpr int kSegFull = kEmpty + 8 * kStages; // [segs]
   static constexpr int kSegEmpty = kSegFull + 8 * kSegs;
-  static constexpr int kMergeW = kSegEmpty + 8 * kSegs; // [7] four pairs, two fours, all
-  static constexpr int kMergeR = kMergeW + 56;
-  static constexpr int kIssued = kMergeR + 56;          // int [stages]: position last issued
-  static constexpr int kAbort = kIssued + 4 * kStages;
+  static constexpr int kMergeW = kSegEmpty + 8 * kSegs; // [merges] small groups, middle ones, all
+  static constexpr int kMergeR = kMergeW + 8 * kMerges;
+  static constexpr int kIssued = kMergeR + 8 * kMerges; // int [stages]: position last issued
+  static constexpr int kAbort = (kIssued + 4 * kStages + 7) & ~7;
   static constexpr int kScan = kAbort + 8;              // long long [33]
-  static_assert(kStages % kWarps == 0 && kAbort % 8 == 0, "stages");
+  // (a stage's tiles then belong to one warp of a piece for all: it has seen the
+  // one before land when it waits for the next)
+  static_assert(kStages * kParts % kWarps == 0, "stages");
   static constexpr int kStart = (kScan + 33 * 8 + 15) & ~15;  // int4
   static constexpr int kBytes = kStart + 16;
   static constexpr int kAlloc = kBytes + 1024;
@@ -195,11 +221,6 @@ __device__ __forceinline__ bool issue_wait(uint32_t tag, int p, const WaitCtx& w
 }
 __device__ __forceinline__ void issue_mark(uint32_t tag, int p) {
   asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(tag), "r"(p) : "memory");
-}
-
-// Offset of the merge barrier of the 2, 4 or 8 warps that `warp` is one of.
-__device__ __forceinline__ int merge_bar(int warp, int nw) {
-  return 8 * (nw == 2 ? warp >> 1 : nw == 4 ? 4 + (warp >> 2) : 6);
 }
 
 // True in one thread of the (converged) warp, always the same one.
@@ -357,18 +378,19 @@ __device__ __forceinline__ void check_request(const CacheFwdArgs& a, int r) {
   if (len < 0 || len > (static_cast<long long>(a.M) << a.sh)) record_index_error(a.index_err, kSiteFwdLen, r);
   if (c0 < 0 || c1 < c0 || c1 > a.T) record_index_error(a.index_err, kSiteFwdRows, r);
 }
-__device__ __forceinline__ long long cost_of(const CacheFwdArgs& a, const Req& q) {
-  return static_cast<long long>(a.Hkv) * q.nrt * (q.kt + kUnitCost);
+__device__ __forceinline__ long long cost_of(const CacheFwdArgs& a, const Req& q, int unit_cost) {
+  return static_cast<long long>(a.Hkv) * q.nrt * (q.kt + unit_cost);
 }
 
 }  // namespace dec
 
 template <int D, int ROWS, class F>
-__global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
+__global__ void __launch_bounds__(dec::Layout<D, ROWS, F>::kThreads, dec::ctas_per_sm(D, ROWS))
     fa_cache_fwd_kernel(const __grid_constant__ typename F::Maps maps, const __grid_constant__ CacheFwdArgs a) {
   using namespace dec;
   using Ly = Layout<D, ROWS, F>;
-  constexpr int kRows = ROWS, kSegs = Ly::kSegs;
+  constexpr int kRows = ROWS, kSegs = Ly::kSegs, kWarps = Ly::kWarps, kThreads = Ly::kThreads;
+  constexpr int kTile = Ly::kTile, kParts = Ly::kParts, kUnitCost = Ly::kUnitCost, kMinCost = Ly::kMinCost;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -380,18 +402,19 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
   Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
   float4* s_scales = reinterpret_cast<float4*>(sm + Ly::kScales);
   int4* s_blk = reinterpret_cast<int4*>(sm + Ly::kBlk);
+  int* s_in = reinterpret_cast<int*>(sm + Ly::kScales);  // 4 bits
   if (warp == kWarps) {
     for (int i = lane; i < Ly::kStages; i += 32) {
       mbar_init(base + Ly::kFull + 8 * i, F::k4 ? 1 : 2);  // its loads, and its scales
-      mbar_init(base + Ly::kEmpty + 8 * i, 1);
+      mbar_init(base + Ly::kEmpty + 8 * i, kParts);
       issue_mark(base + Ly::kIssued + 4 * i, -1);
     }
     if (lane < kSegs) {
       mbar_init(base + Ly::kSegFull + 8 * lane, 1);
       mbar_init(base + Ly::kSegEmpty + 8 * lane, kWarps);
     }
-    if (lane < 7) {
-      const int n = lane < 4 ? 2 : lane < 6 ? 4 : 8;
+    if (lane < Ly::kMerges) {
+      const int n = lane < Ly::kSmalls ? Ly::kSmall : lane < Ly::kMerges - 1 ? Ly::kMiddle : kWarps;
       mbar_init(base + Ly::kMergeW + 8 * lane, n);
       mbar_init(base + Ly::kMergeR + 8 * lane, n);
     }
@@ -420,7 +443,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
     len = c < parts ? total * (c + 1) / parts - x0 : 0;
   };
   auto place = [&](int r, long long in) {
-    const Req q = request<kRows, kKeys>(a, r);
+    const Req q = request<kRows, kTile>(a, r);
     const int unit = q.kt + kUnitCost;
     const int u = static_cast<int>(in / unit);
     return make_int4(r, u / q.nrt, u % q.nrt, static_cast<int>(in - static_cast<long long>(u) * unit));
@@ -433,7 +456,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
         const int r = i * 32 + lane;
         c[i] = 0;
         if (r < a.R) {
-          c[i] = cost_of(a, request<kRows, kKeys>(a, r));
+          c[i] = cost_of(a, request<kRows, kTile>(a, r), kUnitCost);
           if (blockIdx.x == 0) check_request(a, r);
         }
       }
@@ -475,7 +498,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
     const int ra = min(a.R, tid * per), rb = min(a.R, ra + per);
     long long mine = 0, total, x0;
     for (int r = ra; r < rb; ++r) {
-      mine += cost_of(a, request<kRows, kKeys>(a, r));
+      mine += cost_of(a, request<kRows, kTile>(a, r), kUnitCost);
       if (blockIdx.x == 0) check_request(a, r);
     }
     const long long before = cta_scan(mine, reinterpret_cast<long long*>(sm + Ly::kScan), total) - mine;
@@ -484,7 +507,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
       long long x = before;
       int r = ra;
       for (;; ++r) {
-        const long long c = cost_of(a, request<kRows, kKeys>(a, r));
+        const long long c = cost_of(a, request<kRows, kTile>(a, r), kUnitCost);
         if (x0 < x + c) break;  // ends: this thread's requests hold x0
         x += c;
       }
@@ -502,14 +525,14 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
     int r = at.x, h = at.y, rt = at.z, y = at.w;  // the walk: unit, and place in its cost
     // tiles that a short piece leaves a warp: as many as the ring holds for
     // each, or one where there is too little work for all of them
-    const int per_warp = left >= 40 ? Ly::kStages / kWarps : 1;
+    const int per_warp = left * kParts >= 40 ? Ly::kStages * kParts / kWarps : 1;
     int pos = 0, nseg = 0;  // ring positions used, pieces published
     int issued = 0;         // positions up to this lane's last load
     int next_warp = 0;      // first warp of the next piece
     int held = -1;          // first request of the 32 in the lanes' registers
     Req mineq{}, q{};
     const int P = 1 << a.sh;
-    const int boxes = P < kKeys ? 2 : 1;
+    const int boxes = P < kTile ? kTile / P : 1;  // blocks of a tile
     // the piece whose tiles are being fetched
     int pr = 0, ph = 0, plen = 0, pt = 0, pend = 0;
     bool ok = true, fresh = true;  // fresh: the request's sizes are still to be looked up
@@ -548,7 +571,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
                   if (held < 0 || r >= held + 32) {
                     held = r;
                     mineq = Req{};
-                    if (r + lane < a.R) mineq = request<kRows, kKeys>(a, r + lane);
+                    if (r + lane < a.R) mineq = request<kRows, kTile>(a, r + lane);
                   }
                   q.c0 = __shfl_sync(0xffffffffu, mineq.c0, r - held);
                   q.n = __shfl_sync(0xffffffffu, mineq.n, r - held);
@@ -580,7 +603,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
             const bool begins = t0 == 0, ends = t1 == q.kt;
             Seg* s = segs + si;
             int nw = 1;
-            while (nw < kWarps && nw * per_warp < nt) nw *= 2;
+            while (nw < kWarps && nw * per_warp < nt * kParts) nw = Ly::next_size(nw);
             const int w0 = nw == kWarps ? 0 : ((next_warp + nw - 1) / nw * nw) % kWarps;
             next_warp = (w0 + nw) % kWarps;
             s->r = r;
@@ -627,12 +650,14 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
       }
       if (fill == 0) break;
       // their blocks and scales, a lane each, then the loads, by some lanes
-      int blk[2] = {-1, -1};
+      int blk[2 * kParts];
+#pragma unroll
+      for (int i = 0; i < 2 * kParts; ++i) blk[i] = -1;
       if (mr >= 0) {
         const int* row = a.table + static_cast<long long>(mr) * a.M;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int key = mt * kKeys + i * 16;
+        for (int i = 0; i < 2 * kParts; ++i) {
+          const int key = mt * kTile + i * (F::k4 ? P : 16);
           if (i < boxes && key < mlen) {
             blk[i] = row[key >> a.sh];
             if (blk[i] < 0 || blk[i] >= a.blocks) {
@@ -643,9 +668,17 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
             }
           }
         }
-        const int valid = boxes == 1 ? (blk[0] >= 0 ? 3 : 0) : (blk[0] >= 0 ? 1 : 0) | (blk[1] >= 0 ? 2 : 0);
-        const int in = (mt * kKeys) & (P - 1);  // its place in the block: rows of codes, granules
-        s_blk[(pos + lane) % Ly::kMeta] = make_int4(blk[0], blk[1], F::k4 ? in / c4::kTokens : in * D / 128, valid);
+        const int in = (mt * kTile) & (P - 1);  // its place in the block
+        if constexpr (F::k4) {
+          int valid = 0;  // of its four granules
+#pragma unroll
+          for (int i = 0; i < 4; ++i) valid |= blk[boxes == 1 ? 0 : boxes == 2 ? i >> 1 : i] >= 0 ? 1 << i : 0;
+          s_blk[(pos + lane) % Ly::kMeta] = make_int4(blk[0], blk[1], blk[2], blk[3]);
+          s_in[(pos + lane) % Ly::kMeta] = in / c4::kTokens + 16 * valid;
+        } else {
+          const int valid = boxes == 1 ? (blk[0] >= 0 ? 3 : 0) : (blk[0] >= 0 ? 1 : 0) | (blk[1] >= 0 ? 2 : 0);
+          s_blk[(pos + lane) % Ly::kMeta] = make_int4(blk[0], blk[1], in * D / 128, valid);
+        }
       }
       // on their way while the loads are issued
       float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};
@@ -670,14 +703,19 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
             const int4 bl = s_blk[p % Ly::kMeta];
             const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
             if constexpr (F::k4) {
-              // a granule of each of two blocks, or two together
-              constexpr uint32_t kBytes = c4::Granule<D>::kBytes;
-              const uint32_t n = boxes == 1 ? (bl.x >= 0 ? 2u : 0u) : (bl.x >= 0 ? 1u : 0u) + (bl.y >= 0 ? 1u : 0u);
+              // four granules: together, or one or two of each of its blocks
+              constexpr int kBytes = c4::Granule<D>::kBytes;
+              const int each = min(P, kTile) / c4::kTokens, in = s_in[p % Ly::kMeta] & 15;
               const long long per = P / c4::kTokens;
-              mbar_arrive_expect_tx(full(st), n * kBytes);
-              if (bl.x >= 0)
-                bulk_load_1d(kb, a.data + (bl.x * per + bl.z) * kBytes, boxes == 1 ? 2 * kBytes : kBytes, full(st));
-              if (boxes == 2 && bl.y >= 0) bulk_load_1d(kb + kBytes, a.data + bl.y * per * kBytes, kBytes, full(st));
+              const int b[4] = {bl.x, bl.y, bl.z, bl.w};
+              uint32_t n = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) n += i < boxes && b[i] >= 0 ? 1 : 0;
+              mbar_arrive_expect_tx(full(st), n * each * kBytes);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (i < boxes && b[i] >= 0)
+                  bulk_load_1d(kb + i * each * kBytes, a.data + (b[i] * per + in) * kBytes, each * kBytes, full(st));
             } else if (boxes == 1) {
               if (bl.x >= 0) {
                 mbar_arrive_expect_tx(full(st), Ly::kStage);
@@ -753,7 +791,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
   constexpr int kK = D / 16;   // score products per 8 keys
   float* merge = reinterpret_cast<float*>(sm + Ly::kMerge);
   float4* stats = reinterpret_cast<float4*>(sm + Ly::kStats);
-  // Merges of this warp's pair, four and eight: bits 0-2 are the phase of the
+  // Merges of this warp's small, middle and whole group: bits 0-2 are the phase of the
   // next; bits 3-5 tell which of the three the last one was, if any.
   uint32_t merges = 0;
   auto unit = [&](float x) { return F::k4 ? x * a.v_unit : x; };
@@ -788,7 +826,7 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
     constexpr int kO = kWide ? D / 8 : D / 16;
     float o[kO][4];
     float m[2] = {kInit, kInit}, E[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // E: the second reference less m
-    const bool busy = warp - w0 < s.nt;
+    const bool busy = warp - w0 < s.nt * kParts;
     auto row_of = [&](int y) { return kWide ? g4 + 8 * y : 2 * t4 + y; };  // a lane's two rows
     if (busy) {
 #pragma unroll
@@ -838,16 +876,21 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
       // keys visible to every real row of the tile
       const int all = a.causal ? min(s.len, s.len - s.n + s.row0 / a.g + 1) : s.len;
 
-      for (int k = warp - w0; k < s.nt; k += nw) {
-        const int p = s.base + k, st = p % Ly::kStages;
+      for (int k = warp - w0; k < s.nt * kParts; k += nw) {
+        const int p = s.base + k / kParts, part = k % kParts, st = p % Ly::kStages;
         // the piece's first round: the stage may be further behind than a phase
-        ok = k >= Ly::kStages || issue_wait(base + Ly::kIssued + 4 * st, p, wc, kSiteIssued);
+        ok = k >= Ly::kStages * kParts || issue_wait(base + Ly::kIssued + 4 * st, p, wc, kSiteIssued);
         ok = ok && mbar_wait(full(st), (p / Ly::kStages) & 1, wc, kSiteStageFull, p);
         if (!__all_sync(0xffffffffu, ok)) break;
-        const uint32_t kb = base + st * Ly::kStage, vb = kb + Ly::kHalf;
+        const int key0 = s.t0 * kTile + k * kKeys;
+        if (F::k4 && key0 >= s.len) {  // none of its keys
+          if (lane == 0) mbar_arrive(empty(st));
+          continue;
+        }
+        const uint32_t kb = base + st * Ly::kStage + part * Ly::kPart, vb = kb + Ly::kHalf;
         const float4 sc = F::k4 ? make_float4(a.k_unit, a.k_unit, 1.f, 1.f) : s_scales[p % Ly::kMeta];
-        const int valid = s_blk[p % Ly::kMeta].w;  // bit i: the tile's 16-key group i has a block
-        const int key0 = (s.t0 + k) * kKeys;
+        // bit i: the 16-key group i has a block
+        const int valid = F::k4 ? (s_in[p % Ly::kMeta] >> (4 + 2 * part)) & 3 : s_blk[p % Ly::kMeta].w;
         const bool careful = key0 + kKeys > all || valid != 3;
         // scores in log2 units, x[z][..] of row y: of key column(z, y)'s token
         // wide: tiles of 8 keys z = 0..3, [2 y + e], key 2 t4 + e of the tile;
@@ -1233,8 +1276,9 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
     }
 
     // merge of its warps, eight rows at a time
-    const int bar = merge_bar(warp, nw);
-    const int active = min(nw, s.nt);
+    const uint32_t kind = Ly::kind_of(nw);
+    const int bar = Ly::merge_bar(warp, kind);
+    const int active = min(nw, s.nt * kParts);
     // 16-byte chunks are XORed so that the eight lanes of a store fall on
     // different banks
     auto chunk_at = [](int row, int ch) {
@@ -1250,10 +1294,10 @@ __global__ void __launch_bounds__(dec::kThreads, dec::ctas_per_sm(D, ROWS))
       // of whatever size, has been read
       if (merges >> 3) {
         const uint32_t last = merges >> 3;  // its phase is the one before that size's next
-        ok = mbar_wait(base + Ly::kMergeR + merge_bar(warp, 2 * last), (merges & last) ? 0 : 1, wc, kSiteMergeR, ns);
+        ok = mbar_wait(base + Ly::kMergeR + Ly::merge_bar(warp, last), (merges & last) ? 0 : 1, wc, kSiteMergeR, ns);
         if (!__all_sync(0xffffffffu, ok)) return;
       }
-      const uint32_t kind = nw >> 1, use = (merges & kind) ? 1 : 0;  // 1, 2, 4
+      const uint32_t use = (merges & kind) ? 1 : 0;
       merges = ((merges & 7) ^ kind) | kind << 3;
       if (busy) {
 #pragma unroll
