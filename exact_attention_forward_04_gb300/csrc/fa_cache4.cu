@@ -76,10 +76,10 @@ int cache4_append(const void* k, const void* v, long long k_stride, long long v_
   a.positions = positions;
   a.table = reinterpret_cast<const float2*>(table);
   a.length = length;
-  a.rot = rot;
+  a.rot = positions ? rot : 0;
   a.err = dev.index_err;
   const long long lanes = static_cast<long long>(T) * (d / 16), per_sm = lanes * 2 * Hkv / dev.sms;
-  a.group = per_sm <= 2048 ? 1 : 4;
+  a.group = per_sm <= 2048 ? 1 : 8;
   while ((2 * Hkv + a.group - 1) / a.group > 65535) a.group *= 2;
   const dim3 grid(static_cast<unsigned>((lanes + c4::kThreads - 1) / c4::kThreads),
                   static_cast<unsigned>((2 * Hkv + a.group - 1) / a.group));
@@ -136,18 +136,27 @@ int cache4_read(const void* data, float k_unit, float v_unit, const long long* s
 // ----------------------------------------------------------------- forward
 
 // Query rows of a unit, and with them the kernel, by the average rows a request
-// has per kv head, as for the 8-bit cache.
-int unit_rows4(int R, int T, int Hq, int Hkv, int sms) {
+// has per kv head: the few-row kernel with 8 or, at d = 128, 16, which reads the keys
+// again for every so many, or the many-row one with 256.  Measured (us; lengths evenly
+// up to 4000 for 64 requests of 8 kv heads, of 8000 for one), rows of 8 / 16 / 256 a
+// unit:
+//   rows per kv head          8               16                24                32                48
+//   64 requests, d = 128  54 / 68 / 111   91 / 75 / 111   130 / 127 / 112   163 / 131 / 112   241 / 187 / 115
+//                d = 64   35 / 52 / 89    56 / 56 / 89     77 / 89 / 89      99 / 94 / 90     142 / 132 / 91
+//   one request, d = 128  17 / 17 / 25    17 / 19 / 25     19 / 21 / 25      19 / 21 / 25      23 / 23 / 26
+//                d = 64   17 / 15 / 22    17 / 17 / 23     17 / 17 / 23      17 / 17 / 23      19 / 19 / 23
+int unit_rows4(int R, int T, int Hq, int Hkv, int d, int sms) {
   const long long rows = static_cast<long long>(T) * (Hq / Hkv);
   const bool few = static_cast<long long>(R) * Hkv * 8 <= sms;
-  return rows <= 8ll * R ? 8 : rows <= (few ? 48ll : 16ll) * R ? 16 : prm4::kRows;
+  if (rows <= (few ? 48ll : d == 64 ? 24ll : 8ll) * R) return 8;
+  return d == 128 && rows <= 16ll * R ? 16 : prm4::kRows;
 }
 
 size_t cache4_workspace(int R, int T, int Hq, int Hkv, int d) {
   if ((d != 64 && d != 128) || R <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
   host::Device dev;
   if (host::device(&dev) != FA_OK) return 0;
-  const int rows = unit_rows4(R, T, Hq, Hkv, dev.sms);
+  const int rows = unit_rows4(R, T, Hq, Hkv, d, dev.sms);
   return workspace_bytes(fwd_grid(dev.sms, rows, d), rows, d);
 }
 
@@ -169,7 +178,7 @@ int launch_few(CacheFwdArgs& a, int P, int grid, bool& done, cudaStream_t s) {
 
 template <int D>
 int launch_cache4_fwd(CacheFwdArgs& a, int P, char* ws, const host::Device& dev, cudaStream_t s) {
-  const int unit = unit_rows4(a.R, a.T, a.Hq, a.Hkv, dev.sms), grid = fwd_grid(dev.sms, unit, D);
+  const int unit = unit_rows4(a.R, a.T, a.Hq, a.Hkv, D, dev.sms), grid = fwd_grid(dev.sms, unit, D);
   set_workspace(a, ws, grid, unit, D);
   bool* set = g_ready[dev.dev][D == 128];
   if (unit == prm4::kRows) {
@@ -182,7 +191,10 @@ int launch_cache4_fwd(CacheFwdArgs& a, int P, char* ws, const host::Device& dev,
     if (static_cast<long long>(a.M) * P <= prm4::kKeys) return FA_OK;
     return launch_merge<D, prm4::kRows, E2M1Codes>(a, grid, 4, s);
   }
-  return unit == 8 ? launch_few<D, 8>(a, P, grid, set[0], s) : launch_few<D, 16>(a, P, grid, set[1], s);
+  if constexpr (D == 128) {
+    if (unit == 16) return launch_few<D, 16>(a, P, grid, set[1], s);
+  }
+  return launch_few<D, 8>(a, P, grid, set[0], s);
 }
 
 int cache4_fwd(const FwdCall& c, const void* data, float k_unit, float v_unit, cudaStream_t s) {

@@ -100,35 +100,43 @@ __device__ __forceinline__ float f16_low(uint32_t w) {
 }
 __device__ __forceinline__ float f16_high(uint32_t w) { return f16_low(w >> 16); }
 
-// Sixteen bf16 to codes and their scale:
+// A group's scale and codes of its elements x:
 //   s = E4M3(max |x| / (6 unit)), nearest even, at most 448;  code = E2M1(x / (s unit)), 0 where s = 0.
-// A quotient is taken as a product with a reciprocal, off by 2^-23 of it, and
-// rounded to 16 bits: x has 8 bits and s times a border between two codes at most
-// 7, so that their quotient is the border itself or 2^-9 of it away, and the
-// product ends on the border exactly where the quotient lies on it.
-__device__ __forceinline__ uint2 quantise16(const uint32_t (&w)[8], float inv_unit, uint32_t& scale) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = amax2(w[i], m);
-  m = min(m, 0x7f80u);  // not a number: as infinity
-  const float want = __fdiv_rn(__uint_as_float(m << 16) * inv_unit, 6.f);
+// Both quotients are taken as products with reciprocals, off by 2^-22 of them, and
+// rounded to multiples of fewer bits: x has 8 bits and 6 or s times a border
+// between two codes or scales at most 7, so that a quotient is the border itself or
+// 2^-9 of it away, and the product ends on the border exactly where the quotient
+// lies on it.
+
+// The scale's code, of the largest |x| as bf16 bits; `inv` is 1 / (s unit) or 0.
+__device__ __forceinline__ uint32_t scale_code(uint32_t amax, float inv_unit, float& inv) {
+  const float x = __uint_as_float(min(amax, 0x7f80u) << 16);  // not a number: as infinity
+  const float want = __uint_as_float((__float_as_uint(x * inv_unit * (1.f / 6.f)) + 0x80u) & 0xffffff00u);
+  uint32_t code;
   asm("{\n\t.reg .b16 a;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %1, %2;\n\tcvt.u32.u16 %0, a;\n}"
-      : "=r"(scale)
+      : "=r"(code)
       : "f"(0.f), "f"(want));
-  const float s = f16_low(e4m3x2_to_f16(scale));
-  const float inv = s > 0.f ? __fdiv_rn(1.f, s) * inv_unit : 0.f;
-  uint32_t r[2];
+  const float s = f16_low(e4m3x2_to_f16(code));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  inv = s > 0.f ? inv * inv_unit : 0.f;
+  return code;
+}
+// Eight elements' codes.  A quotient (about 6 at most, borders from 1/4 on) is rounded
+// to multiples of 2^-13 by adding 1024 and taking it away again, in pairs.
+__device__ __forceinline__ uint32_t codes8(uint4 v, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint64_t inv2 = f2_pack(inv, inv), up = f2_pack(1024.f, 1024.f), down = f2_pack(-1024.f, -1024.f);
+  float f[8];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = (i & 1) ? rope::high(w[4 * e + i / 2]) : rope::low(w[4 * e + i / 2]);
-      f[i] = __uint_as_float((__float_as_uint(x * inv) + 0x80u) & 0xffffff00u);
-    }
-    r[e] = pack_e2m1x8(f);
-  }
-  return make_uint2(r[0], r[1]);
+  for (int i = 0; i < 4; ++i)
+    f2_unpack(f2_add(f2_fma(rope::both(w[i]), inv2, up), down), f[2 * i], f[2 * i + 1]);
+  return pack_e2m1x8(f);
+}
+// The largest |x| of eight, as bf16 bits.
+__device__ __forceinline__ uint32_t amax8(uint4 v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                              __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
 }
 
 constexpr int kThreads = 128;
@@ -151,85 +159,120 @@ struct Append4Args {
   DevError* err;
 };
 
-// New K and V rows into the cache.  A lane takes 16 elements of a row, one group:
-// their scale needs nobody else's.  A warp takes 4 tokens (8 at d = 64) and a run of
-// heads, so that K's bytes are stored 256 and V's 32 in a row and a position's cos
-// and sin are read once for several heads.  Halves to be turned together lie in
-// two lanes; each reads the other's elements from L1.
+// New K and V rows into the cache.  D / 16 lanes take a row, two vectors of eight
+// elements each: of V, and of K's elements that pass, one group of 16; of those that
+// turn the two that turn among themselves, so that a lane keeps eight cos and sin for
+// all heads, and a vector's group has its other half in a lane that a shuffle asks for
+// its largest element.  A warp takes 4 tokens (8 at d = 64) and a run of rows, heads of
+// K, then of V, so that K's bytes are stored 256 and V's 32 in a row; a row's elements
+// are on their way while the one before is written.
 template <int D, bool PAIRS>
-__global__ void __launch_bounds__(c4::kThreads) fa_cache4_append_kernel(Append4Args a) {
+__global__ void __launch_bounds__(c4::kThreads, 7) fa_cache4_append_kernel(Append4Args a) {
   using namespace c4;
   using G = Granule<D>;
   constexpr int kLanes = D / 16;
   const int t = (blockIdx.x * kThreads + threadIdx.x) / kLanes, c = threadIdx.x % kLanes;
   const int g0 = blockIdx.y * a.group, g1 = min(2 * a.Hkv, g0 + a.group);
-  if (t >= a.T) return;
-  const long long slot = a.slot_map[t];
-  if (slot < 0 || slot >= a.slots) {
-    if (slot != -1 && c == 0 && g0 == 0) record_index_error(a.err, kSiteAppendSlot, t);
-    return;
-  }
+  const bool token_there = t < a.T;
+  const int tt = token_there ? t : a.T - 1;
+  // the vectors of K (rot is 0 where nothing turns)
+  const rope::Vectors kv = rope::vectors_of<PAIRS>(c, a.rot);
+  const __nv_bfloat16 *krow = a.k + tt * a.k_stride, *vrow = a.v + tt * a.v_stride;
+  const int k0 = min(g0, a.Hkv), k1 = min(g1, a.Hkv), v0 = max(g0, a.Hkv) - a.Hkv, v1 = max(g1, a.Hkv) - a.Hkv;
+  const uint4* from = reinterpret_cast<const uint4*>(k0 < k1 ? krow + static_cast<long long>(k0) * D
+                                                             : vrow + static_cast<long long>(v0) * D);
+  uint4 x[2];
+  auto load = [&](const uint4* row, int first, int second) {
+    x[0] = __ldg(row + first);
+    x[1] = __ldg(row + second);
+  };
+  if (k0 < k1) load(from, kv.first, kv.second);
+  else load(from, 2 * c, 2 * c + 1);
+  const long long slot = a.slot_map[tt];
+  const bool there = token_there && slot >= 0 && slot < a.slots;
+  if (token_there && !there && slot != -1 && c == 0 && g0 == 0) record_index_error(a.err, kSiteAppendSlot, t);
   const int P = 1 << a.sh, token = static_cast<int>(slot) & 15;
-  uint8_t* block = a.data + (slot >> a.sh) * a.Hkv * (P / 16) * G::kBytes +
+  const long long head = static_cast<long long>(P / 16) * G::kBytes;  // bytes of a block's head
+  uint8_t* block = a.data + (slot >> a.sh) * a.Hkv * head +
                    static_cast<long long>((static_cast<int>(slot) & (P - 1)) >> 4) * G::kBytes;
-  // the angles of this lane's elements: those of vectors 2 c and 2 c + 1
-  float2 cs[2][8];
-  int partner[2] = {-1, -1};  // vector that each turns with; -1: it passes
+  rope::Pair cs[4];
+  bool turns = false;
   if (a.positions && g0 < a.Hkv && 16 * c < a.rot) {
-    const int pos = a.positions[t];
-    if (pos >= a.length && c == 0 && g0 == 0) record_index_error(a.err, kSiteRopePosition, t);
-    if (pos >= 0 && pos < a.length) {
-      const float2* row = a.table + static_cast<long long>(pos) * (a.rot / 2);
+    const int pos = a.positions[tt];
+    if (there && pos >= a.length && c == 0 && g0 == 0) record_index_error(a.err, kSiteRopePosition, t);
+    turns = pos >= 0 && pos < a.length;
+    if (turns) rope::load_angles(a.table + static_cast<long long>(pos) * (a.rot / 2) + 8 * c, 1.f, cs);
+  }
+  // where the other halves of the vectors' groups are: five bits of a lane and one of
+  // which of its two vectors, for each
+  const bool apart = kv.second != kv.first + 1 || (kv.first & 1);
+  int other = 0;
+  if (apart) {
+    const int items = a.rot / 16;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int u = (e ? kv.second : kv.first) ^ 1;
+      const int lane = (threadIdx.x & 31) - c + (u < items ? u : u < 2 * items ? u - items : u >> 1);
+      other |= (lane | (u < items ? 0 : u < 2 * items ? 32 : (u & 1) * 32)) << (8 * e);
+    }
+  }
+  const bool any_apart = !PAIRS && a.rot > 16;
+  uint8_t* gr = block + k0 * head;
+  int at0 = token * G::kRow + k_place<D>(kv.first >> 1) * 8 + (kv.first & 1) * 4;
+  int at1 = token * G::kRow + k_place<D>(kv.second >> 1) * 8 + (kv.second & 1) * 4;
+  // a group's scale by the lane with its first vector
+  int scale0 = kv.first & 1 ? 0 : G::kKScales + token * (D / 16) + k_place<D>(kv.first >> 1);
+  const int scale1 = kv.second & 1 ? 0 : G::kKScales + token * (D / 16) + k_place<D>(kv.second >> 1);
+#pragma unroll 1
+  for (int h = k0; h < k1; ++h, gr += head) {
+    uint4 v[2] = {x[0], x[1]};
+    from += D / 8;
+    if (h + 1 < k1) load(from, kv.first, kv.second);
+    else if (v0 < v1) load(reinterpret_cast<const uint4*>(vrow), 2 * c, 2 * c + 1);
+    if (turns) rope::turn_pairs<PAIRS>(v[0], v[1], cs);
+    uint32_t m0 = amax8(v[0]), m1 = amax8(v[1]);
+    if (any_apart) {
+      uint32_t o[2][2];  // the largest of both vectors of the lanes asked
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int v = 2 * c + e, half = a.rot / 16;
-        if constexpr (PAIRS) {
-          float2 p[4];
-          rope::load_pairs<4>(row + 4 * v, 1.f, p);
-          rope::spread(p, cs[e]);
-          partner[e] = v;
-        } else {
-          const bool first = v < half;
-          rope::load_pairs<8>(row + 8 * (first ? v : v - half), first ? -1.f : 1.f, cs[e]);
-          partner[e] = first ? v + half : v - half;
-        }
+        o[e][0] = __shfl_sync(0xffffffffu, m0, other >> (8 * e));
+        o[e][1] = __shfl_sync(0xffffffffu, m1, other >> (8 * e));
+      }
+      if (apart) {
+        m0 = max(m0, other & 32 ? o[0][1] : o[0][0]);
+        m1 = max(m1, other & (32 << 8) ? o[1][1] : o[1][0]);
       }
     }
+    if (!apart) m0 = m1 = max(m0, m1);
+    if (!there) continue;
+    float i0, i1;
+    const uint32_t s0 = scale_code(m0, a.k_inv, i0), s1 = scale_code(m1, a.k_inv, i1);
+    *reinterpret_cast<uint32_t*>(gr + at0) = codes8(v[0], i0);
+    *reinterpret_cast<uint32_t*>(gr + at1) = codes8(v[1], i1);
+    if (scale0 > 0) gr[scale0] = static_cast<uint8_t>(s0);
+    if (scale1 > 0) gr[scale1] = static_cast<uint8_t>(s1);
   }
-  const bool turns = partner[0] >= 0;
+  from = reinterpret_cast<const uint4*>(vrow + static_cast<long long>(v0) * D);
+  gr = block + v0 * head;
+  at0 = G::kV + v_place<D>(D == 128 ? c : 2 * c, token);
+  at1 = G::kV + v_place<D>(D == 128 ? c : 2 * c + 1, token);
+  scale0 = G::kVScales + c * 16 + scale_place(token);
 #pragma unroll 1
-  for (int g = g0; g < g1; ++g) {
-    const bool is_v = g >= a.Hkv;
-    const int h = is_v ? g - a.Hkv : g;
-    const uint4* row = reinterpret_cast<const uint4*>((is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) +
-                                                      static_cast<long long>(h) * D);
-    uint4 x[2] = {__ldg(row + 2 * c), __ldg(row + 2 * c + 1)};
-    if (!is_v && turns) {
-      if constexpr (PAIRS) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) x[e] = rope::turn8(x[e], rope::swap_pairs(x[e]), cs[e]);
-      } else {
-        const uint4 y[2] = {__ldg(row + partner[0]), __ldg(row + partner[1])};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) x[e] = rope::turn8(x[e], y[e], cs[e]);
-      }
-    }
-    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-    uint32_t scale;
-    const uint2 code = quantise16(w, is_v ? a.v_inv : a.k_inv, scale);
-    uint8_t* gr = block + static_cast<long long>(h) * (P / 16) * G::kBytes;
-    if (!is_v) {
-      *reinterpret_cast<uint2*>(gr + token * G::kRow + k_place<D>(c) * 8) = code;
-      gr[G::kKScales + token * (D / 16) + k_place<D>(c)] = static_cast<uint8_t>(scale);
+  for (int h = v0; h < v1; ++h, gr += head) {
+    uint4 v[2] = {x[0], x[1]};
+    from += D / 8;
+    if (h + 1 < v1) load(from, 2 * c, 2 * c + 1);
+    if (!there) continue;
+    float inv;
+    const uint32_t s = scale_code(max(amax8(v[0]), amax8(v[1])), a.v_inv, inv);
+    const uint32_t c0 = codes8(v[0], inv), c1 = codes8(v[1], inv);
+    if constexpr (D == 128) {
+      *reinterpret_cast<uint2*>(gr + at0) = make_uint2(c0, c1);
     } else {
-      if constexpr (D == 128) {
-        *reinterpret_cast<uint2*>(gr + G::kV + v_place<D>(c, token)) = code;
-      } else {
-        *reinterpret_cast<uint32_t*>(gr + G::kV + v_place<D>(2 * c, token)) = code.x;
-        *reinterpret_cast<uint32_t*>(gr + G::kV + v_place<D>(2 * c + 1, token)) = code.y;
-      }
-      gr[G::kVScales + c * 16 + scale_place(token)] = static_cast<uint8_t>(scale);
+      *reinterpret_cast<uint32_t*>(gr + at0) = c0;
+      *reinterpret_cast<uint32_t*>(gr + at1) = c1;
     }
+    gr[scale0] = static_cast<uint8_t>(s);
   }
 }
 

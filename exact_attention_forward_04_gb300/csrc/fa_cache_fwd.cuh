@@ -122,7 +122,7 @@ struct Layout {
   // arrive every 196 (24 requests of 20000 to 32768 tokens: 143 us with 32 keys).
   static constexpr int kParts = F::k4 ? 2 : 1;
   static constexpr int kTile = kParts * kKeys;
-  static constexpr int kUnitCost = F::k4 ? 16 : 12;             // a piece's fixed cost, in tiles (8 bits, 5: 114 us for 104)
+  static constexpr int kUnitCost = F::k4 ? (D == 64 ? 10 : 16) : 12;             // a piece's fixed cost, in tiles (8 bits, 5: 114 us for 104)
   static constexpr int kMinCost = F::k4 ? 6 : 12;               // least cost of a CTA's range
   static constexpr int kHalf = kKeys * D;                       // codes of K (or V) of a tile; 4 bits: unused
   static constexpr int kPart = 2 * c4::Granule<D>::kBytes;      // 4 bits: of a warp's keys

@@ -88,7 +88,7 @@ int rope_run(const void* x, long long (&xs)[3], void* out, long long (&os)[3], c
   const long long lanes = static_cast<long long>(B) * N * (d / 16);
   const long long gx = (lanes + rope::kThreads - 1) / rope::kThreads;
   const long long per_sm = lanes * H / dev.sms;
-  a.group = per_sm <= 2048 ? 1 : per_sm <= 8192 ? 2 : per_sm <= 32768 ? 4 : 8;
+  a.group = per_sm <= 2048 ? 1 : per_sm <= 8192 ? 2 : per_sm <= 32768 ? 4 : 16;
   while ((H + a.group - 1) / a.group > 65535) a.group *= 2;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((H + a.group - 1) / a.group));
   if (d == 128) {

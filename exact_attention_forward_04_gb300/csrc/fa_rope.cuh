@@ -23,72 +23,153 @@ namespace fa {
 
 namespace rope {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
-// x c + y s to within about one unit in its last place: the product's own error
-// is added, so that cancellation does not raise it.
-__device__ __forceinline__ float turn(float x, float c, float y, float s) {
-  const float p = y * s, e = fmaf(y, s, -p);
-  return fmaf(x, c, p) + e;
-}
-// Too near the middle of two bf16 numbers, or not a number (an infinity's error is none).
-__device__ __forceinline__ bool unsure(float r) {
-  return ((__float_as_uint(r) - 0x7ffeu) & 0xffffu) <= 4u || r != r;
-}
-// The same in 64 bits, as a fp32 number that rounds to bf16 as the exact one
-// does: cut off, its last bit set where bits were lost.
-__device__ __forceinline__ float turn_exactly(float x, float c, float y, float s) {
-  const double v = static_cast<double>(x) * c + static_cast<double>(y) * s;
-  const float f = __double2float_rz(v);
-  return static_cast<double>(f) == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
-}
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Eight elements x with their partners y, cs[i] their (cos, +-sin): x_i c_i + y_i s_i.
-__device__ __forceinline__ uint4 turn8(uint4 x, uint4 y, const float2 (&cs)[8]) {
-  const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-  uint32_t r[4];
-  bool again = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = turn(low(xw[i]), cs[2 * i].x, low(yw[i]), cs[2 * i].y);
-    const float b = turn(high(xw[i]), cs[2 * i + 1].x, high(yw[i]), cs[2 * i + 1].y);
-    again = again || unsure(a) || unsure(b);
-    r[i] = pack_bf16(a, b);
-  }
-  if (again) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[i] = pack_bf16(turn_exactly(low(xw[i]), cs[2 * i].x, low(yw[i]), cs[2 * i].y),
-                       turn_exactly(high(xw[i]), cs[2 * i + 1].x, high(yw[i]), cs[2 * i + 1].y));
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-// Elements exchanged with their neighbours.
-__device__ __forceinline__ uint4 swap_pairs(uint4 x) {
-  return make_uint4(__byte_perm(x.x, 0u, 0x1032), __byte_perm(x.y, 0u, 0x1032), __byte_perm(x.z, 0u, 0x1032),
-                    __byte_perm(x.w, 0u, 0x1032));
-}
-// Four pairs' (cos, sin) as those of eight interleaved elements.
-__device__ __forceinline__ void spread(const float2 (&p)[4], float2 (&cs)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    cs[2 * i] = make_float2(p[i].x, -p[i].y);
-    cs[2 * i + 1] = p[i];
-  }
-}
-// N pairs of a table row.
-template <int N>
-__device__ __forceinline__ void load_pairs(const float2* from, float sign, float2 (&p)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(from + i));
-    p[i] = make_float2(v.x, sign * v.y);
-    p[i + 1] = make_float2(v.z, sign * v.w);
-  }
+// Two (cos, sin), for the two-wide arithmetic.
+struct Pair {
+  uint64_t c, s;
+};
+
+// x c + y s as a fp32 number that rounds to bf16 as the exact one does: cut off, its
+// last bit set where bits were lost.  Products and sum are kept as pairs of fp32
+// numbers, rounded value and rest (the rest of a sum: Knuth, The Art of Computer
+// Programming 2, 4.2.2, theorem B).  (In 64 bits, of which a warp's operation takes an
+// SM 16 cycles, these few values took half of the time: 140 us for 93.)
+__device__ __forceinline__ float turn_exactly(float x, float c, float y, float s) {
+  const float p = __fmul_rn(x, c), q = __fmul_rn(y, s), h = __fadd_rn(p, q);
+  const float pe = fmaf(x, c, -p), qe = fmaf(y, s, -q), z = __fsub_rn(h, p);
+  const float he = __fadd_rn(__fsub_rn(p, __fsub_rn(h, z)), __fsub_rn(q, z));
+  const float rest = __fadd_rn(he, __fadd_rn(pe, qe)), t = __fadd_rn(h, rest);
+  const float left = __fadd_rn(__fsub_rn(h, t), rest);  // the exact value less t
+  uint32_t bits = __float_as_uint(t);
+  if (left != 0.f) bits = (bits - ((left < 0.f) != (t < 0.f) ? 1u : 0u)) | 1u;
+  // where rests may be lost, or are none, the sum itself
+  return fabsf(h) >= 0x1p-90f && fabsf(h) < INFINITY ? __uint_as_float(bits) : fmaf(x, c, q);
 }
 
+// Whether some of the results r is too near a border: of their lower halves, two by
+// two and less 0x7ffd each, `near` is the smallest so far; `sum` their sum.
+struct Doubt {
+  uint32_t near = 0xffffffffu;
+  uint64_t sum = 0;  // two zeros
+
+  __device__ __forceinline__ void see(uint64_t r) {
+    float a, b;
+    f2_unpack(r, a, b);
+    near = __vminu2(near, __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410) - 0x7ffd7ffdu);
+    sum = f2_add(sum, r);
+  }
+  // Lower halves of 0x7ffe to 0x8002 give 1 to 5 (the upper of two perhaps one less,
+  // a borrow of the lower); a result that is no number makes the sum none.
+  __device__ __forceinline__ bool any() const {
+    float a, b;
+    f2_unpack(sum, a, b);
+    return (near & 0xffffu) <= 7u || (near >> 16) <= 7u || a + b != a + b;
+  }
+};
+
+// x c + y s, twice.  The product's own error is added to the sum, so that
+// cancellation does not raise it: it is off by about one unit in its last place.
+__device__ __forceinline__ uint64_t turn2(uint64_t x, uint64_t y, uint64_t c, uint64_t s, Doubt& doubt) {
+  const uint64_t minus = f2_pack(-1.f, -1.f);
+  const uint64_t p = f2_mul(y, s), e = f2_fma(y, f2_mul(s, minus), p);  // the product, less its error
+  const uint64_t r = f2_fma(e, minus, f2_fma(x, c, p));
+  doubt.see(r);
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t r) {
+  float a, b;
+  f2_unpack(r, a, b);
+  return pack_bf16(a, b);
+}
+__device__ __forceinline__ uint64_t both(uint32_t w) { return f2_pack(low(w), high(w)); }
+__device__ __forceinline__ uint32_t negated(uint32_t w) { return w ^ 0x80008000u; }
+
+// The same of four words' elements.  Few come here: a loop over arrays in local
+// memory, as registers would be taken from everyone (112 a thread for 80: rope of
+// 32768 tokens 130 us for 101).
+__device__ __forceinline__ void turn_again(const uint32_t (&x)[4], const uint32_t (&y)[4], const Pair (&cs)[4],
+                                           uint32_t (&r)[4]) {
+  uint32_t w[12];
+  Pair p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = x[i];
+    w[4 + i] = y[i];
+    p[i] = cs[i];
+  }
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    float c0, c1, s0, s1;
+    f2_unpack(p[i].c, c0, c1);
+    f2_unpack(p[i].s, s0, s1);
+    const uint32_t u = w[i], v = w[4 + i];
+    w[8 + i] = pack_bf16(turn_exactly(low(u), c0, low(v), s0), turn_exactly(high(u), c1, high(v), s1));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = w[8 + i];
+}
+
+// Eight pairs, in place: the first elements in p and the second in q or, PAIRS,
+// neighbours; the first become x c - y s, the second y c + x s.
+template <bool PAIRS>
+__device__ __forceinline__ void turn_pairs(uint4& p, uint4& q, const Pair (&cs)[4]) {
+  uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+  uint32_t r[8];
+  // pairs 2 i and 2 i + 1: words i and i + 4, or 2 i and 2 i + 1 with the lower
+  // halves' elements the first
+  auto first = [&](int i) { return PAIRS ? __byte_perm(w[2 * i], w[2 * i + 1], 0x5410) : w[i]; };
+  auto second = [&](int i) { return PAIRS ? __byte_perm(w[2 * i], w[2 * i + 1], 0x7632) : w[i + 4]; };
+  auto put = [&](int i, uint32_t x, uint32_t y) {
+    r[PAIRS ? 2 * i : i] = PAIRS ? __byte_perm(x, y, 0x5410) : x;
+    r[PAIRS ? 2 * i + 1 : i + 4] = PAIRS ? __byte_perm(x, y, 0x7632) : y;
+  };
+  Doubt doubt;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = both(first(i)), y = both(second(i)), ny = both(negated(second(i)));
+    put(i, pack2(turn2(x, ny, cs[i].c, cs[i].s, doubt)), pack2(turn2(y, x, cs[i].c, cs[i].s, doubt)));
+  }
+  if (doubt.any()) {
+    uint32_t x[4], y[4], ny[4], xr[4], yr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = first(i);
+      y[i] = second(i);
+      ny[i] = negated(y[i]);
+    }
+    turn_again(x, ny, cs, xr);
+    turn_again(y, x, cs, yr);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put(i, xr[i], yr[i]);
+  }
+  p = make_uint4(r[0], r[1], r[2], r[3]);
+  q = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// The two vectors of eight elements that lane i of a row takes: i and i + rot / 16 or,
+// where they pass or neighbours are pairs, 2 i and 2 i + 1.  They turn among
+// themselves, by the row's eight (cos, sin) from 8 i on.
+struct Vectors {
+  int first, second;
+};
+template <bool PAIRS>
+__device__ __forceinline__ Vectors vectors_of(int i, int rot) {
+  const int items = rot / 16;
+  return !PAIRS && i < items ? Vectors{i, i + items} : Vectors{2 * i, 2 * i + 1};
+}
+
+// Eight (cos, sin) of a table's row, sines times `sign`.
+__device__ __forceinline__ void load_angles(const float2* from, float sign, Pair (&cs)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(from + 2 * i));
+    cs[i] = {f2_pack(v.x, v.z), f2_pack(sign * v.y, sign * v.w)};
+  }
+}
 }  // namespace rope
 
 struct RopeArgs {
@@ -104,11 +185,11 @@ struct RopeArgs {
   DevError* err;
 };
 
-// D / 16 lanes take a token's row, each two vectors of eight elements that turn
-// among themselves (or pass): i and i + rot / 16, or 2 i and 2 i + 1 where pairs
-// are neighbours.  A lane keeps its pairs' cos and sin for its group of heads.
+// D / 16 lanes take a token's row, each two vectors, and keep their cos and sin for
+// their group of heads.  A head's elements are on their way while the one before is
+// turned, the first ones before the position is known.
 template <int D, bool PAIRS>
-__global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(rope::kThreads, 7) fa_rope_kernel(RopeArgs a) {
   using namespace rope;
   constexpr int kLanes = D / 16;
   const long long at = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
@@ -116,40 +197,29 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(RopeArgs a) {
   const int i = threadIdx.x % kLanes;
   const int b = static_cast<int>(at / a.N), n = static_cast<int>(at - static_cast<long long>(b) * a.N);
   const int h0 = blockIdx.y * a.group, h1 = min(a.H, h0 + a.group);
-  const int pos = a.positions[b * a.pb + n];
-  if (pos >= a.length && i == 0 && h0 == 0) record_index_error(a.err, kSiteRopePosition, n);
-  const int items = a.rot / 16;
-  const bool turns = i < items && pos >= 0 && pos < a.length;
-  const bool apart = !PAIRS && i < items;  // the two vectors do not lie together
-  const int v0 = apart ? i : 2 * i, v1 = apart ? i + items : 2 * i + 1;
-  float2 cs[8];
-  if (turns) load_pairs<8>(a.table + static_cast<long long>(pos) * (a.rot / 2) + 8 * i, a.sign, cs);
+  const Vectors v = vectors_of<PAIRS>(i, a.rot);
   const __nv_bfloat16* x = a.x + b * a.xb + n * a.xn;
   __nv_bfloat16* out = a.out + b * a.ob + n * a.on;
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
+  uint4 p, q;
+  auto load = [&](int h) {
     const uint4* from = reinterpret_cast<const uint4*>(x + h * a.xh);
+    p = from[v.first];
+    q = from[v.second];
+  };
+  load(h0);
+  const int pos = a.positions[b * a.pb + n];
+  if (pos >= a.length && i == 0 && h0 == 0) record_index_error(a.err, kSiteRopePosition, n);
+  const bool turns = 16 * i < a.rot && pos >= 0 && pos < a.length;
+  Pair cs[4];
+  if (turns) load_angles(a.table + static_cast<long long>(pos) * (a.rot / 2) + 8 * i, a.sign, cs);
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    uint4 p0 = p, q0 = q;
+    if (h + 1 < h1) load(h + 1);  // (out may be x: another head's row)
+    if (turns) turn_pairs<PAIRS>(p0, q0, cs);
     uint4* to = reinterpret_cast<uint4*>(out + h * a.oh);
-    uint4 p = from[v0], q = from[v1];
-    if (turns) {
-      if constexpr (PAIRS) {
-        const float2 c0[4] = {cs[0], cs[1], cs[2], cs[3]}, c1[4] = {cs[4], cs[5], cs[6], cs[7]};
-        float2 e[8];
-        spread(c0, e);
-        p = turn8(p, swap_pairs(p), e);
-        spread(c1, e);
-        q = turn8(q, swap_pairs(q), e);
-      } else {
-        float2 e[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = make_float2(cs[k].x, -cs[k].y);
-        const uint4 p1 = turn8(p, q, e);
-        q = turn8(q, p, cs);
-        p = p1;
-      }
-    }
-    to[v0] = p;
-    to[v1] = q;
+    to[v.first] = p0;
+    to[v.second] = q0;
   }
 }
 
