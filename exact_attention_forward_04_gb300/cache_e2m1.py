@@ -160,9 +160,9 @@ def cache_forward_e2m1(q, cache, block_table, seq_lens, cu_q, scale=None, causal
     """Attention of each request's newest tokens over its cached keys: as
     cache_forward_e4m3, over a 4-bit cache."""
     data, k_unit, v_unit = cache
-    if stream is None and workspace is None:
+    if stream is None:
         out = (_usual or _load_usual()).forward(q, data, k_unit, v_unit, block_table, seq_lens, cu_q, scale, causal,
-                                                slot_map)
+                                                workspace, slot_map)
         if out is not None:
             return out
     index, blocks, H, P, d = _check_cache(data)

@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(c4::kThreads, 7) fa_cache4_append_kernel(Appen
   using namespace c4;
   using G = Granule<D>;
   constexpr int kLanes = D / 16;
-  const int t = (blockIdx.x * kThreads + threadIdx.x) / kLanes, c = threadIdx.x % kLanes;
+  const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kLanes);
+  const int c = threadIdx.x % kLanes;
   const int g0 = blockIdx.y * a.group, g1 = min(2 * a.Hkv, g0 + a.group);
   const bool token_there = t < a.T;
   const int tt = token_there ? t : a.T - 1;
@@ -294,7 +295,8 @@ __global__ void __launch_bounds__(c4::kThreads) fa_cache4_read_kernel(Read4Args 
   using namespace c4;
   using G = Granule<D>;
   constexpr int kLanes = D / 16;
-  const int t = (blockIdx.x * kThreads + threadIdx.x) / kLanes, c = threadIdx.x % kLanes;
+  const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kLanes);
+  const int c = threadIdx.x % kLanes;
   const int g0 = blockIdx.y * a.group, g1 = min(2 * a.Hkv, g0 + a.group);
   if (t >= a.T) return;
   const long long slot = a.slot_map[t];

@@ -49,6 +49,7 @@ int rope_run(const void* x, long long (&xs)[3], void* out, long long (&os)[3], c
     if (xs[i] < 0 || os[i] < 0) return FA_ERR_INVALID_ARG;
     if ((xs[i] | os[i]) & 7) return FA_ERR_MISALIGNED;
     if (xs[i] > (1ll << 31) || os[i] > (1ll << 31)) return FA_ERR_UNSUPPORTED;
+    if ((n[i] - 1) * xs[i] > (1ll << 46) || (n[i] - 1) * os[i] > (1ll << 46)) return FA_ERR_UNSUPPORTED;
   }
   if (!rows_apart(n, os, d)) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * N > (1ll << 33)) return FA_ERR_UNSUPPORTED;

@@ -7,12 +7,12 @@
 // with (c_i, s_i) the position's row of a table; elements from rot on pass.  The
 // gradient is the transposed rotation, s_i negated.
 //
-// A result is the exact value, with the table's entries as they are, rounded
-// once to bf16.  Its products have 32 bits, so a fp32 sum is off by about one
-// unit of its last place; where that is too near a border of bf16's rounding
-// to tell (5 values of 65536), it is taken again in 64 bits.  So a key that the
-// cache's append turns on the way is bit for bit one turned before, and its 4-bit
-// code never hangs on how a sum was ordered.
+// A result (of 2^-90 or more) is the exact value, with the table's entries as they
+// are, rounded once to bf16.  Its products have 32 bits, so a fp32 sum is off by about
+// one unit of its last place; where that is too near a border of bf16's rounding
+// to tell (8 values of 65536), it is taken again with the rests of its roundings.  So a
+// key that the cache's append turns on the way is bit for bit one turned before, and
+// its 4-bit code never hangs on how a sum was ordered.
 #pragma once
 #include <cuda_bf16.h>
 

@@ -73,6 +73,11 @@ at::Tensor make(c10::IntArrayRef sizes, at::ScalarType type, c10::DeviceIndex de
 }
 void* stream(c10::DeviceIndex device) { return c10::cuda::getCurrentCUDAStream(device).stream(); }
 
+bool flag(PyObject* o, int& f) {
+  f = PyObject_IsTrue(o);
+  if (f < 0) PyErr_Clear();
+  return f >= 0;
+}
 bool number(PyObject* o, float& f) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) {
@@ -98,23 +103,23 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto device = c10::cuda::current_device();
   const at::Tensor* x = tensor(a[0], at::kBFloat16, device);
   if (!x || (x->dim() != 3 && x->dim() != 4) || x->numel() == 0 || x->stride(x->dim() - 1) != 1) Py_RETURN_NONE;
+  int interleaved, transposed;
+  if (!flag(a[3], interleaved) || !flag(a[4], transposed)) Py_RETURN_NONE;
   const bool tokens = x->dim() == 3;
   const int64_t d = x->size(tokens ? 2 : 3), H = x->size(1), N = x->size(tokens ? 0 : 2), B = tokens ? 1 : x->size(0);
   const at::Tensor* pos = vector(a[1], at::kInt, N, device);
   const at::Tensor* table = angles(a[2], d, device);
-  if (!pos || !table || B > kInt || H > kInt || N > kInt) Py_RETURN_NONE;
+  if (!pos || !table || d > 128 || B > kInt || H > kInt || N > kInt) Py_RETURN_NONE;
   const at::Tensor out = make(x->sizes(), at::kBFloat16, device);
   const int64_t* xs = x->strides().data();
   const int st = tokens ? g_rope(x->data_ptr(), 0, xs[1], xs[0], out.data_ptr(), 0, d, H * d,
                                  static_cast<const int*>(pos->data_ptr()), 0,
                                  static_cast<const float*>(table->data_ptr()), table->size(0), 1, H, N, d,
-                                 2 * table->size(1), PyObject_IsTrue(a[3]) == 1, PyObject_IsTrue(a[4]) == 1,
-                                 stream(device))
+                                 2 * table->size(1), interleaved, transposed, stream(device))
                         : g_rope(x->data_ptr(), xs[0], xs[1], xs[2], out.data_ptr(), H * N * d, N * d, d,
                                  static_cast<const int*>(pos->data_ptr()), 0,
                                  static_cast<const float*>(table->data_ptr()), table->size(0), B, H, N, d,
-                                 2 * table->size(1), PyObject_IsTrue(a[3]) == 1, PyObject_IsTrue(a[4]) == 1,
-                                 stream(device));
+                                 2 * table->size(1), interleaved, transposed, stream(device));
   if (st != FA_OK) Py_RETURN_NONE;
   return THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
@@ -128,7 +133,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Cache c;
   float ku, vu;
   int64_t ks, vs;
-  if (!cache(a[2], device, c) || !number(a[3], ku) || !number(a[4], vu)) Py_RETURN_NONE;
+  int interleaved;
+  if (!cache(a[2], device, c) || !number(a[3], ku) || !number(a[4], vu) || !flag(a[8], interleaved)) Py_RETURN_NONE;
   const at::Tensor* k = rows(a[0], c.H, c.d, device, ks);
   const at::Tensor* v = rows(a[1], c.H, c.d, device, vs);
   if (!k || !v || k->size(0) != v->size(0)) Py_RETURN_NONE;
@@ -143,7 +149,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           static_cast<const long long*>(slots->data_ptr()),
                           turned ? static_cast<const int*>(pos->data_ptr()) : nullptr,
                           turned ? static_cast<const float*>(table->data_ptr()) : nullptr, turned ? table->size(0) : 0,
-                          turned ? 2 * table->size(1) : 0, PyObject_IsTrue(a[8]) == 1, T, c.H, c.d, c.blocks, c.P,
+                          turned ? 2 * table->size(1) : 0, interleaved, T, c.H, c.d, c.blocks, c.P,
                           stream(device));
   if (st != FA_OK) Py_RETURN_NONE;
   Py_RETURN_TRUE;
@@ -170,14 +176,15 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// q, data, k_unit, v_unit, block_table, seq_lens, cu_q, scale, causal, slot_map: (o, lse)
+// q, data, k_unit, v_unit, block_table, seq_lens, cu_q, scale, causal, workspace, slot_map: (o, lse)
 PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 10 || !on_gpu(a[1])) Py_RETURN_NONE;
+  if (n != 11 || !on_gpu(a[1])) Py_RETURN_NONE;
   const auto device = c10::cuda::current_device();
   Cache c;
   float ku, vu, scale;
-  if (!cache(a[1], device, c) || !number(a[2], ku) || !number(a[3], vu)) Py_RETURN_NONE;
+  int causal;
+  if (!cache(a[1], device, c) || !number(a[2], ku) || !number(a[3], vu) || !flag(a[8], causal)) Py_RETURN_NONE;
   const at::Tensor* q = tensor(a[0], at::kBFloat16, device);
   if (!q || q->dim() != 3) Py_RETURN_NONE;
   const int64_t T = q->size(0), Hq = q->size(1);
@@ -190,19 +197,31 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t R = table->size(0), M = table->size(1);
   const at::Tensor* lens = vector(a[5], at::kInt, R, device);
   const at::Tensor* cu = vector(a[6], at::kInt, R + 1, device);
-  const at::Tensor* slots = a[9] != Py_None ? vector(a[9], at::kLong, T, device) : nullptr;
-  if (!lens || !cu || (a[9] != Py_None && !slots)) Py_RETURN_NONE;
+  const at::Tensor* slots = a[10] != Py_None ? vector(a[10], at::kLong, T, device) : nullptr;
+  if (!lens || !cu || (a[10] != Py_None && !slots)) Py_RETURN_NONE;
   if (a[7] == Py_None) scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.d)));
   else if (!number(a[7], scale)) Py_RETURN_NONE;
-  const size_t bytes = g_workspace(R, T, Hq, c.H, c.d);
-  if (bytes == 0) Py_RETURN_NONE;
+  size_t bytes = 0;
+  void* ws = nullptr;
+  at::Tensor mine;
+  if (a[9] == Py_None) {
+    bytes = g_workspace(R, T, Hq, c.H, c.d);
+    if (bytes == 0) Py_RETURN_NONE;
+    mine = make({static_cast<int64_t>(bytes)}, at::kByte, device);
+    ws = mine.data_ptr();
+  } else {
+    if (!on_gpu(a[9])) Py_RETURN_NONE;
+    const at::Tensor& given = THPVariable_Unpack(a[9]);
+    if (given.get_device() != device || !given.is_contiguous()) Py_RETURN_NONE;
+    bytes = given.nbytes();
+    ws = given.data_ptr();
+  }
   const at::Tensor o = make({T, Hq, c.d}, at::kBFloat16, device), lse = make({T, Hq}, at::kFloat, device);
-  const at::Tensor ws = make({static_cast<int64_t>(bytes)}, at::kByte, device);
   const int st = g_forward(q->data_ptr(), stride, c.data->data_ptr(), ku, vu, static_cast<const int*>(table->data_ptr()),
                            static_cast<const int*>(lens->data_ptr()), static_cast<const int*>(cu->data_ptr()),
                            slots ? static_cast<const long long*>(slots->data_ptr()) : nullptr, o.data_ptr(),
                            static_cast<float*>(lse.data_ptr()), R, T, Hq, c.H, c.d, c.blocks, c.P, M, scale,
-                           PyObject_IsTrue(a[8]) == 1, ws.data_ptr(), bytes, stream(device));
+                           causal, ws, bytes, stream(device));
   if (st != FA_OK) Py_RETURN_NONE;
   return pair(o, lse);
   END_HANDLE_TH_ERRORS

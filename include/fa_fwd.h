@@ -512,7 +512,8 @@ size_t fa_cache_fwd_e4m3_workspace_size(int R, int T, int Hq, int Hkv, int d);
  *                                        x_{i + rot/2} c_i + x_i s_i)
  *   interleaved: the same of (x_{2i}, x_{2i+1}),       i < rot / 2
  * and the others pass.  Results are exact for the table's entries and rounded
- * once to bf16, nearest even (infinities and NaN go through the formula).
+ * once to bf16, nearest even; those below 2^-90 are first rounded to fp32.
+ * Infinities, NaN and products beyond fp32 go through the formula in fp32.
  *
  * fa_rope — the rotation of x, bf16 [B, H, N] rows of d, into out.
  *   x_batch .. out_token : elements between batches, heads and tokens, multiples
@@ -545,7 +546,8 @@ int fa_rope(const void* x, long long x_batch, long long x_head, long long x_toke
  * for every 16 of them, and a value is
  *   E2M1(code) * E4M3(scale) * unit,
  * k_unit for K and v_unit for V, powers of two of 2^-64 to 2^64.  A code's low
- * bits are 0 .5 1 1.5 2 3 4 6, its highest the sign.  The 18 d bytes of 16 tokens:
+ * three bits are 0 .5 1 1.5 2 3 4 6, its highest the sign.  The 18 d bytes of 16
+ * tokens:
  *   8 d  K codes: token by token; of a row the 16-element groups in the order
  *        0 4 1 5 2 6 3 7 (d = 64: 0 1 2 3), element 2 i in the low and 2 i + 1 in
  *        the high four bits of a byte
@@ -590,7 +592,9 @@ int fa_cache_read_e2m1(const void* data, float k_unit, float v_unit, const long 
  * fa_cache_fwd_e2m1 — fa_cache_fwd_e4m3_slots over the 4-bit cache (slot_map may
  * be NULL).  Scales in the cache that are no number of [0, 448] (bytes above
  * 0x7E) leave the rows that see them unspecified; what lies at and behind a
- * request's len, or in blocks of no request, may be anything.
+ * request's len, or in blocks of no request, may be anything.  A row's results are
+ * unspecified, and no other's, where |scale| * |x| * k_unit is 2^117 or more (or a
+ * score 2^126).
  * Exact up to fp32 sums, the rounding of the softmax weights to f16 in the
  * product with V, and query elements below 2^-17 of their row's largest, which
  * are off by up to 2^-25 of it.

@@ -640,3 +640,40 @@ def test_results_are_freed():
     for _ in range(20):
         step()
     assert torch.cuda.memory_allocated() == before
+
+
+def test_the_usual_path_and_the_other_agree():
+    """The same bits with a stream given (which takes Python's way to the library)
+    and without, and a workspace of one's own."""
+    P, H, g, d = 32, 2, 4, 128
+    lens, new = [300, 70, 5], [20, 1, 5]
+    table, blocks = make_tables(lens, P, seed=1)
+    cu, T = [0, 20, 21, 26], 26
+    qkv, angles = _rows(T, H * (g + 2), d, 3, -1, 1), fa.rope_table(400, 96)
+    pos = i32([i for n, a in zip(lens, new) for i in range(n - a, n)])
+    sl = torch.tensor([int(table[r, i // P]) * P + i % P for r, (n, a) in enumerate(zip(lens, new))
+                       for i in range(n - a, n)], device=DEV)
+    outs = []
+    for kw in ({}, dict(stream=torch.cuda.current_stream())):
+        cache = _cache(blocks, H, P, d, 2)
+        q = fa.rope(qkv[:, :H * g], pos, angles, interleaved=True, **kw)
+        fa.cache_append_e2m1(qkv[:, H * g:H * (g + 1)], qkv[:, H * (g + 1):], cache, sl, positions=pos, table=angles,
+                             interleaved=True, **kw)
+        ws = torch.empty(fa.cache_forward_e2m1_workspace_size(3, T, H * g, H, d), dtype=torch.uint8, device=DEV)
+        args = (q, cache, table.to(DEV), i32(lens), i32(cu))
+        outs.append([q, fa.rope_backward(q, pos, angles, interleaved=True, **kw), cache.data,
+                     *fa.cache_read_e2m1(cache, sl, **kw), *fa.cache_forward_e2m1(*args, **kw),
+                     *fa.cache_forward_e2m1(*args, slot_map=sl, workspace=ws, causal=False, **kw)])
+    fa.check_errors()
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    with pytest.raises(fa.FAError):
+        fa.cache_forward_e2m1(*args, workspace=ws[:-8])
+    with pytest.raises(fa.FAError):
+        fa.cache_read_e2m1(fa.CacheE2M1(cache.data, 3.0, 1.0), sl)
+    for bad in (dict(q=q.float()), dict(block_table=args[2].long()), dict(seq_lens=args[3][:2]),
+                dict(cu_q=args[4][:3]), dict(slot_map=sl[:3])):
+        a = dict(zip(("q", "cache", "block_table", "seq_lens", "cu_q"), args))
+        a.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            fa.cache_forward_e2m1(**a)
