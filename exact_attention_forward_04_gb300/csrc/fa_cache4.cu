@@ -78,6 +78,8 @@ int cache4_append(const void* k, const void* v, long long k_stride, long long v_
   a.length = length;
   a.rot = positions ? rot : 0;
   a.err = dev.index_err;
+  // Rows of a thread: one where they are few, else eight (24 prompts, 8 kv heads of 128:
+  // 4 rows 78 us, 8 70).
   const long long lanes = static_cast<long long>(T) * (d / 16), per_sm = lanes * 2 * Hkv / dev.sms;
   a.group = per_sm <= 2048 ? 1 : 8;
   while ((2 * Hkv + a.group - 1) / a.group > 65535) a.group *= 2;
@@ -122,6 +124,7 @@ int cache4_read(const void* data, float k_unit, float v_unit, const long long* s
   a.k_unit = k_unit;
   a.v_unit = v_unit;
   a.err = dev.index_err;
+  // as the append (the rows of 24 prompts: 4 rows 49 us, 8 53, 16 59)
   const long long lanes = static_cast<long long>(T) * (d / 16), per_sm = lanes * 2 * Hkv / dev.sms;
   a.group = per_sm <= 2048 ? 1 : 4;
   while ((2 * Hkv + a.group - 1) / a.group > 65535) a.group *= 2;

@@ -166,6 +166,12 @@ struct Append4Args {
 // its largest element.  A warp takes 4 tokens (8 at d = 64) and a run of rows, heads of
 // K, then of V, so that K's bytes are stored 256 and V's 32 in a row; a row's elements
 // are on their way while the one before is written.
+//
+// 24 prompts, 51072 tokens of 8 kv heads of 128 in blocks of 64: 70 us with all of K
+// turned, 3.8 TB/s, 58 without; ALU 53 %, issue slots 61 %, DRAM 56 %: neither alone.
+// Seven CTAs per SM (78 us with six, and 104 with four rows' elements on their way in
+// four; 92 with cos and sin read again for every head).  32 tokens in 2.4 us, 500 of 16
+// heads of 64 in 3.5.
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(c4::kThreads, 7) fa_cache4_append_kernel(Append4Args a) {
   using namespace c4;
@@ -289,7 +295,8 @@ struct Read4Args {
 };
 
 // The rows at some slots as bf16, which holds every value exactly; zeros where
-// there is none.  Lanes as in the append.
+// there is none.  A lane takes one group.  Bound by DRAM: the rows of 24 prompts in
+// 49 us, 5.5 TB/s.
 template <int D>
 __global__ void __launch_bounds__(c4::kThreads) fa_cache4_read_kernel(Read4Args a) {
   using namespace c4;

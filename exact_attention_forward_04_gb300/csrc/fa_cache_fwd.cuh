@@ -49,6 +49,16 @@
 // the two factors of such a weight leave fp32's range; those tiles take a branch
 // of their own (up to 2 % of the others' time, for asking).  E is kept as
 // its distance from m: beside a large m a sum with log2 v_scale would be lost.
+//
+// Four bits (E2M1Codes; fa_cache4.cuh has the layout).  The walk, the ring, the
+// pieces and their merge are the same.  A tile is 64 keys, one bulk copy for each of
+// its blocks with the scales inside, and two warps take half of it each.  In a warp
+//   codes -> f16, times their scales (exact) -> S -> P -> O += P V
+// and as no value's range needs a second reference, E is 0.  It is the taking apart
+// that bounds it: 520 instructions for 32 keys, 128 conversions and 128
+// multiplications among them.  24 requests of 20000 to 32768 tokens, 8 kv heads of
+// 128, take 139 us, 5.1 TB/s (114 us with the loads alone, 121 without either
+// product); 64 of 30 to 8192 80 us; one of 1000 10.4 us.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -99,10 +109,10 @@ template <int D, int ROWS, class F>
 struct Layout {
   static constexpr int kCtas = ctas_per_sm(D, ROWS);
   // Consumer warps, and the numbers of them that a piece may have: 1, 2, 4 and 8.
-  // Taking 4-bit codes apart is more instructions a byte: 15 warps, a register file
-  // of 128 registers a thread full with the producer (one request of 8 kv heads
-  // over all warps; 24 requests of 20000 to 32768 tokens: 154 us with 8), in
-  // threes or all.
+  // Taking 4-bit codes apart is more instructions a byte, whose latencies more warps
+  // hide: 15, with the producer as many as have 128 registers a thread, of which a
+  // piece has 1, 3 or all (24 requests of 20000 to 32768 tokens: 145 us, 154 with 8;
+  // 143 with two CTAs of 8 warps, which have 96 registers and spill).
   static constexpr bool kMany = F::k4 && D == 128 && ROWS == 8;
   static constexpr int kWarps = kMany ? 15 : 8;
   static constexpr int kThreads = 32 * (kWarps + 1);            // and the producer
@@ -122,7 +132,9 @@ struct Layout {
   // arrive every 196 (24 requests of 20000 to 32768 tokens: 143 us with 32 keys).
   static constexpr int kParts = F::k4 ? 2 : 1;
   static constexpr int kTile = kParts * kKeys;
-  static constexpr int kUnitCost = F::k4 ? (D == 64 ? 10 : 16) : 12;             // a piece's fixed cost, in tiles (8 bits, 5: 114 us for 104)
+  // A piece's fixed cost, in tiles (64 requests of 30 to 8192 tokens: 8 bits, 5: 114 us,
+  // 12: 104; 4 bits, 10: 84 us, 16: 80, 24: 82)
+  static constexpr int kUnitCost = F::k4 ? (D == 64 ? 10 : 16) : 12;
   static constexpr int kMinCost = F::k4 ? 6 : 12;               // least cost of a CTA's range
   static constexpr int kHalf = kKeys * D;                       // codes of K (or V) of a tile; 4 bits: unused
   static constexpr int kPart = 2 * c4::Granule<D>::kBytes;      // 4 bits: of a warp's keys

@@ -88,6 +88,9 @@ int rope_run(const void* x, long long (&xs)[3], void* out, long long (&os)[3], c
   a.err = dev.index_err;
   const long long lanes = static_cast<long long>(B) * N * (d / 16);
   const long long gx = (lanes + rope::kThreads - 1) / rope::kThreads;
+  // Heads of a thread: one where rows are few, many where its cos and sin are worth
+  // keeping (gradient of 32768 tokens of 32 heads: 16 heads 97 us, 8 101; 9001 tokens of
+  // 40: 4 heads 37.4 us, 8 38.9).
   const long long per_sm = lanes * H / dev.sms;
   a.group = per_sm <= 2048 ? 1 : per_sm <= 8192 ? 2 : per_sm <= 32768 ? 4 : 16;
   while ((H + a.group - 1) / a.group > 65535) a.group *= 2;
