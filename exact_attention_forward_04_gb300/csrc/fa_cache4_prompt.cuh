@@ -100,6 +100,87 @@ __device__ __forceinline__ uint4 values8(uint32_t w, uint32_t f) {
 __device__ __forceinline__ uint32_t low_twice(uint32_t w) { return __byte_perm(w, 0u, 0x1010); }
 __device__ __forceinline__ uint32_t high_twice(uint32_t w) { return __byte_perm(w, 0u, 0x3232); }
 
+// A unit's end for a softmax thread and its row: the halves' sums joined where
+// both have the same rows, O and L written, or left as a partial.  (Written into
+// the kernel instead, prompts took 1265 us for 1227; the 8-bit kernel the other way
+// about.)
+template <int D, typename W>
+__device__ __forceinline__ bool finish(const CacheFwdArgs& a, const dec::Seg& s, int x, int row, int warp, int lane,
+                                       float m, float l, uint32_t tO, float4* stat, uint32_t joined,
+                                       W&& wait) {
+  const bool two = s.nv > kHalf;
+  const bool real = row < s.nv;
+  // The halves' statistics, through shared memory; then each of the two
+  // warps that have a row combines and writes one half of its columns.
+  const bool join = !two && s.base > 1;
+  float f = 1.f, f2 = 0.f;  // what this half's sums and the other's count
+  if (join) {
+    const uint32_t bar = joined + 8 * (warp & 3);
+    stat[x * kHalf + row] = make_float4(m, l, 0.f, 0.f);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    if (!__all_sync(0xffffffffu, wait(bar, 0))) return false;
+    tc_fence_after();
+    const float4 b = stat[(1 - x) * kHalf + row];
+    const float m1 = fmaxf(m, b.x);
+    f = ex2(m - m1);
+    f2 = ex2(b.x - m1);
+    l = l * f + b.y * f2;
+    m = m1;
+  }
+  const float inv = l == 0.f ? 0.f : ex2(-kBias) / l * a.v_unit;
+  const float lg = l == 0.f ? -INFINITY : m + log2f(l);
+  f *= inv;
+  f2 *= inv;
+  const int rr = s.row0 + row, tk = rr / a.g;
+  const long long at = static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
+  const long long pat = static_cast<long long>(s.slot) * kRows + row;
+#pragma unroll 1
+  for (int q = join ? x * (D / 64) : 0; q < (join && x == 0 ? D / 64 : D / 32); ++q) {
+    uint32_t o[32];
+    tmem_ld32(tO + 32 * q, o);
+    tmem_ld_wait32(o);
+#pragma unroll
+    for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+    if (join) {
+      uint32_t o2[32];
+      tmem_ld32(tO + (kHalf - 2 * x * kHalf) + 32 * q, o2);
+      tmem_ld_wait32(o2);
+#pragma unroll
+      for (int y = 0; y < 32; ++y)
+        o[y] = __float_as_uint(fmaf(__uint_as_float(o2[y]), f2, __uint_as_float(o[y])));
+    }
+    if (real) {
+      if (s.mode == 0) {
+        uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + 32 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          dst[e] = make_uint4(
+              pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
+              pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
+              pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
+              pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
+      } else {
+        // a row a lane: 32 bytes a store, as every row takes a pass of its own
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) prm::stg256(a.part_o + pat * D + 32 * q + e, o + e);
+      }
+    }
+  }
+  if (real && (two || x == 0)) {
+    if (s.mode == 0) a.lse[at] = lg * 0.6931471805599453f;
+    else a.part_l[pat] = lg;
+  }
+  tc_fence_before();  // O has been read: the next piece's first product may overwrite it
+  __syncwarp();
+  if (join) {  // by the other warp, too
+    if (lane == 0) mbar_arrive(joined + 8 * (warp & 3));
+    if (!__all_sync(0xffffffffu, wait(joined + 8 * (warp & 3), 1))) return false;
+  }
+  return true;
+}
+
 }  // namespace prm4
 
 template <int D>
@@ -627,8 +708,8 @@ __global__ void __launch_bounds__(prm4::kThreads, 1) fa_cache4_prompt_kernel(con
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       l *= 1.f / (1 << static_cast<int>(kBias));  // the sum of 2^(s - m)
-      ok = prm::finish<D, true>(
-          a, s, x, row, warp, lane, m, 0.f, l, tO, reinterpret_cast<float4*>(sm + Ly::kStat), base + Ly::kJoin,
+      ok = finish<D>(
+          a, s, x, row, warp, lane, m, l, tO, reinterpret_cast<float4*>(sm + Ly::kStat), base + Ly::kJoin,
           [&](uint32_t bar, uint32_t parity) { return wait(bar - base, parity, kSiteJoin, step0); });
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);

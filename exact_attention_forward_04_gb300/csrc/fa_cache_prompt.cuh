@@ -386,87 +386,6 @@ __device__ __forceinline__ void walk(const CacheFwdArgs& a, int4 at, long long c
   }
 }
 
-// A unit's end for a softmax thread and its row: the halves' sums joined where
-// both have the same rows, O and L written, or left as a partial.
-template <int D, bool UNIT, typename W>
-__device__ __forceinline__ bool finish(const CacheFwdArgs& a, const dec::Seg& s, int x, int row, int warp, int lane,
-                                       float m, float e, float l, uint32_t tO, float4* stat, uint32_t joined,
-                                       W&& wait) {
-  const bool two = s.nv > kHalf;
-  const bool real = row < s.nv;
-  // The halves' statistics, through shared memory; then each of the two
-  // warps that have a row combines and writes one half of its columns.
-  const bool join = !two && s.base > 1;
-  float f = 1.f, f2 = 0.f;  // what this half's sums and the other's count
-  if (join) {
-    const uint32_t bar = joined + 8 * (warp & 3);
-    stat[x * kHalf + row] = make_float4(m, e, l, 0.f);
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-    if (!__all_sync(0xffffffffu, wait(bar, 0))) return false;
-    tc_fence_after();
-    const float4 b = stat[(1 - x) * kHalf + row];
-    const float m1 = fmaxf(m, b.x), e0 = e + (m - m1), eb = b.y + (b.x - m1), e1 = fmaxf(e0, eb);
-    l = l * ex2(m - m1) + b.z * ex2(b.x - m1);
-    f = ex2(e0 - e1);
-    f2 = ex2(eb - e1);
-    m = m1;
-    e = e1;
-  }
-  float inv = l == 0.f ? 0.f : ex2(e - kBias) / l;
-  if (UNIT) inv *= a.v_unit;
-  const float lg = l == 0.f ? -INFINITY : m + log2f(l);
-  f *= inv;
-  f2 *= inv;
-  const int rr = s.row0 + row, tk = rr / a.g;
-  const long long at = static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
-  const long long pat = static_cast<long long>(s.slot) * kRows + row;
-#pragma unroll 1
-  for (int q = join ? x * (D / 64) : 0; q < (join && x == 0 ? D / 64 : D / 32); ++q) {
-    uint32_t o[32];
-    tmem_ld32(tO + 32 * q, o);
-    tmem_ld_wait32(o);
-#pragma unroll
-    for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-    if (join) {
-      uint32_t o2[32];
-      tmem_ld32(tO + (kHalf - 2 * x * kHalf) + 32 * q, o2);
-      tmem_ld_wait32(o2);
-#pragma unroll
-      for (int y = 0; y < 32; ++y)
-        o[y] = __float_as_uint(fmaf(__uint_as_float(o2[y]), f2, __uint_as_float(o[y])));
-    }
-    if (real) {
-      if (s.mode == 0) {
-        uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + 32 * q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          dst[e] = make_uint4(
-              pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
-              pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
-              pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
-              pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
-      } else {
-        // a row a lane: 32 bytes a store, as every row takes a pass of its own
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) stg256(a.part_o + pat * D + 32 * q + e, o + e);
-      }
-    }
-  }
-  if (real && (two || x == 0)) {
-    if (s.mode == 0) a.lse[at] = lg * 0.6931471805599453f;
-    else a.part_l[pat] = lg;
-  }
-  tc_fence_before();  // O has been read: the next piece's first product may overwrite it
-  __syncwarp();
-  if (join) {  // by the other warp, too
-    if (lane == 0) mbar_arrive(joined + 8 * (warp & 3));
-    if (!__all_sync(0xffffffffu, wait(joined + 8 * (warp & 3), 1))) return false;
-  }
-  return true;
-}
-
 }  // namespace prm
 
 // G: keys of a step that share their scales, a block's or, of larger ones, all 64.
@@ -1079,9 +998,81 @@ __global__ void __launch_bounds__(prm::kThreads, 1)
       ok = wait(Ly::kPvDone + 8 * (2 * x + ((cnt - 1) & 1)), (cnt - 1) >> 1, kSitePV, jt);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      ok = finish<D, false>(a, s, x, row, warp, lane, m, e, l, tO, reinterpret_cast<float4*>(sm + Ly::kStat),
-                            base + Ly::kJoin, [&](uint32_t bar, uint32_t parity) { return wait(bar - base, parity, kSiteJoin, jt); });
-      if (!__all_sync(0xffffffffu, ok)) break;
+      // (shared with the 4-bit cache's kernel as a function, this end of a unit made
+      // prompts take 1142 us for 1130)
+      const bool real = row < s.nv;
+      // The halves' statistics, through shared memory; then each of the two
+      // warps that have a row combines and writes one half of its columns.
+      const bool join = !two && s.base > 1;
+      float f = 1.f, f2 = 0.f;  // what this half's sums and the other's count
+      if (join) {
+        const uint32_t bar = base + Ly::kJoin + 8 * (warp & 3);
+        float4* stat = reinterpret_cast<float4*>(sm + Ly::kStat);
+        stat[x * kHalf + row] = make_float4(m, e, l, 0.f);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+        ok = wait(Ly::kJoin + 8 * (warp & 3), 0, kSiteJoin, jt);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const float4 b = stat[(1 - x) * kHalf + row];
+        const float m1 = fmaxf(m, b.x), e0 = e + (m - m1), eb = b.y + (b.x - m1), e1 = fmaxf(e0, eb);
+        l = l * ex2(m - m1) + b.z * ex2(b.x - m1);
+        f = ex2(e0 - e1);
+        f2 = ex2(eb - e1);
+        m = m1;
+        e = e1;
+      }
+      const float inv = l == 0.f ? 0.f : ex2(e - kBias) / l;
+      const float lg = l == 0.f ? -INFINITY : m + log2f(l);
+      f *= inv;
+      f2 *= inv;
+      const int rr = s.row0 + row, tk = rr / a.g;
+      const long long at = static_cast<long long>(s.c0 + tk) * a.Hq + s.h * a.g + (rr - tk * a.g);
+      const long long pat = static_cast<long long>(s.slot) * kRows + row;
+#pragma unroll 1
+      for (int q = join ? x * (D / 64) : 0; q < (join && x == 0 ? D / 64 : D / 32); ++q) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * q, o);
+        tmem_ld_wait32(o);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+        if (join) {
+          uint32_t o2[32];
+          tmem_ld32(tO + (kHalf - 2 * x * kHalf) + 32 * q, o2);
+          tmem_ld_wait32(o2);
+#pragma unroll
+          for (int y = 0; y < 32; ++y)
+            o[y] = __float_as_uint(fmaf(__uint_as_float(o2[y]), f2, __uint_as_float(o[y])));
+        }
+        if (real) {
+          if (s.mode == 0) {
+            uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + 32 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(
+                  pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
+                  pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
+                  pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
+                  pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
+          } else {
+            // a row a lane: 32 bytes a store, as every row takes a pass of its own
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) stg256(a.part_o + pat * D + 32 * q + e, o + e);
+          }
+        }
+      }
+      if (real && (two || x == 0)) {
+        if (s.mode == 0) a.lse[at] = lg * 0.6931471805599453f;
+        else a.part_l[pat] = lg;
+      }
+      tc_fence_before();  // O has been read: the next piece's first product may overwrite it
+      __syncwarp();
+      if (join) {  // by the other warp, too
+        if (lane == 0) mbar_arrive(base + Ly::kJoin + 8 * (warp & 3));
+        ok = wait(Ly::kJoin + 8 * (warp & 3), 1, kSiteJoin, jt);
+        if (!__all_sync(0xffffffffu, ok)) break;
+      }
       if (lane == 0) mbar_arrive(base + Ly::kSegEmpty + 8 * si);
     }
   }

@@ -677,3 +677,30 @@ def test_the_usual_path_and_the_other_agree():
         a.update(bad)
         with pytest.raises((TypeError, ValueError)):
             fa.cache_forward_e2m1(**a)
+
+
+def test_the_same_slot_twice_touches_no_other():
+    """Rows of one slot may mix, group by group; every other byte is as it was."""
+    P, d, H, T = 32, 128, 2, 8
+    k, v = _rows(T, H, d, 1), _rows(T, H, d, 2)
+    slots = [5, 5, 5, 9, 9, 40, 5, 63]
+    cache = _cache(2, H, P, d, 3)
+    ref = cache.data.cpu().numpy().copy()
+    fa.cache_append_e2m1(k, v, cache, torch.tensor(slots, device=DEV))
+    fa.check_errors()
+    got = cache.data.cpu().numpy()
+    mine = np.zeros_like(ref, dtype=bool)
+    for byte, _, scale in oracle.cache_e2m1.places(d):
+        for s in set(slots):
+            for where in (byte, scale):
+                mine[s // P, :, s % P // 16, where[s % 16]] = True
+    assert (got[~mine] == ref[~mine]).all()
+    want = ref.copy()
+    oracle.cache_e2m1.append(want, k.cpu().double().numpy(), v.cpu().double().numpy(), slots, 1.0, 1.0)
+    for s in (40, 63):  # those met once
+        once = np.zeros_like(mine)
+        for byte, _, scale in oracle.cache_e2m1.places(d):
+            for where in (byte, scale):
+                once[s // P, :, s % P // 16, where[s % 16]] = True
+        a, b = np.where(once, got, 0), np.where(once, want, 0)
+        _codes_equal(torch.from_numpy(a), b)
