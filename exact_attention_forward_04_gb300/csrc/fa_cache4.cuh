@@ -170,8 +170,8 @@ struct Append4Args {
 // 24 prompts, 51072 tokens of 8 kv heads of 128 in blocks of 64: 70 us with all of K
 // turned, 3.8 TB/s, 58 without; ALU 53 %, issue slots 61 %, DRAM 56 %: neither alone.
 // Seven CTAs per SM (78 us with six, and 104 with four rows' elements on their way in
-// four; 92 with cos and sin read again for every head).  32 tokens in 2.4 us, 500 of 16
-// heads of 64 in 3.5.
+// four; 92 with cos and sin read again for every head).  32 tokens in 3.1 us, 500 of 16
+// heads of 64 in 3.7, a microsecond of it for position and table one after the other.
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(c4::kThreads, 7) fa_cache4_append_kernel(Append4Args a) {
   using namespace c4;
