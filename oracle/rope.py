@@ -1,7 +1,7 @@
 """Float64 CPU oracle for rotary positions.
 
-TEST INFRASTRUCTURE ONLY, sharing no code with the CUDA library: pair by pair as
-complex numbers, each result rounded once to bf16.
+TEST INFRASTRUCTURE ONLY, sharing no code with the CUDA library: pair by pair, the
+products of bf16 and fp32 numbers exact in 64 bits, each result rounded once to bf16.
 """
 from __future__ import annotations
 
@@ -20,10 +20,22 @@ def round_bf16(x):
     return np.where(np.isfinite(x), y, x)
 
 
+def _sum_to_odd(p, q):
+    """p + q cut off to float64, its last bit set where bits were lost: rounding
+    that to fewer bits is rounding the sum itself, once."""
+    with np.errstate(all="ignore"):
+        h = p + q
+        z = h - p
+        rest = (p - (h - z)) + (q - z)
+        lost = np.isfinite(h) & (rest != 0)
+    bits = h.view(np.int64)
+    return np.where(lost, (bits - ((rest < 0) != (h < 0))) | 1, bits).view(np.float64)
+
+
 def rotate(x, positions, table, interleaved=False, transposed=False):
     """x [..., d] (float64), positions of x's shape without the last axis (or
-    one that broadcasts), table [L, rot / 2, 2]: float64, not rounded.  Rows at
-    positions outside the table pass."""
+    one that broadcasts), table [L, rot / 2, 2]: float64, not rounded
+    to fewer bits.  Rows at positions outside the table pass."""
     x, table = np.asarray(x, dtype=np.float64), np.asarray(table, dtype=np.float64)
     L, half, _ = table.shape
     pos = np.broadcast_to(np.asarray(positions), x.shape[:-1])
@@ -32,10 +44,11 @@ def rotate(x, positions, table, interleaved=False, transposed=False):
         p = int(pos[at])
         if p < 0 or p >= L:
             continue
-        w = table[p, :, 0] + 1j * table[p, :, 1] * (-1 if transposed else 1)
+        c, s = table[p, :, 0], table[p, :, 1] * (-1 if transposed else 1)
         row = x[at]
         a, b = (row[0:2 * half:2], row[1:2 * half:2]) if interleaved else (row[:half], row[half:2 * half])
-        re, im = a * w.real - b * w.imag, b * w.real + a * w.imag
+        with np.errstate(invalid="ignore"):
+            re, im = _sum_to_odd(a * c, -(b * s)), _sum_to_odd(b * c, a * s)
         if interleaved:
             y[at][0:2 * half:2], y[at][1:2 * half:2] = re, im
         else:
