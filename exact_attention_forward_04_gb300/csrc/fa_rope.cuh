@@ -7,12 +7,12 @@
 // with (c_i, s_i) the position's row of a table; elements from rot on pass.  The
 // gradient is the transposed rotation, s_i negated.
 //
-// A result (of 2^-90 or more) is the exact value, with the table's entries as they
-// are, rounded once to bf16.  Its products have 32 bits, so a fp32 sum is off by about
-// one unit of its last place; where that is too near a border of bf16's rounding
-// to tell (8 values of 65536), it is taken again with the rests of its roundings.  So a
-// key that the cache's append turns on the way is bit for bit one turned before, and
-// its 4-bit code never hangs on how a sum was ordered.
+// A result is the exact value, with the table's entries as they are, rounded once to
+// bf16.  Its products have 32 bits, so a fp32 sum is off by about one unit of its last
+// place; where that is too near a border of bf16's rounding to tell (8 values of
+// 65536), it is taken again with the rests of its roundings.  So a key that the cache's
+// append turns on the way is bit for bit one turned before, and its 4-bit code never
+// hangs on how a sum was ordered.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -33,21 +33,44 @@ struct Pair {
   uint64_t c, s;
 };
 
-// x c + y s as a fp32 number that rounds to bf16 as the exact one does: cut off, its
-// last bit set where bits were lost.  Products and sum are kept as pairs of fp32
-// numbers, rounded value and rest (the rest of a sum: Knuth, The Art of Computer
-// Programming 2, 4.2.2, theorem B).  (In 64 bits, of which a warp's operation takes an
-// SM 16 cycles, these few values took half of the time: 140 us for 93.)
+// A fp32 number cut off from t, and whether something (of `left`'s sign, less than t's
+// last bit) is left of it, as a number that rounds to bf16 as both together do: with
+// its last bit set where bits were lost.  t is 0 only with nothing or its sign left.
+__device__ __forceinline__ float with_rest(float t, float left) {
+  uint32_t bits = __float_as_uint(t);
+  if (left != 0.f) bits = (bits - ((bits ^ __float_as_uint(left)) >> 31)) | 1u;
+  return __uint_as_float(bits);
+}
+// Whether a result with this lower half is too near a border (0x8000) to tell.
+__device__ __forceinline__ bool in_doubt(uint32_t half) { return half - 0x7ffdu <= 7u; }
+// Whether a product's rest is a fp32 number: factors of 8 and 24 bits lose none of
+// them from 2^-100 on.
+__device__ __forceinline__ bool kept(float product, float x, float c) {
+  return fabsf(product) >= 0x1p-100f || x == 0.f || c == 0.f;
+}
+// x c + y s as a fp32 number that rounds to bf16 as the exact one does.  Most that
+// come here do so with another value in doubt, and turn2's own result serves (all of
+// them taken again, rope of 9001 tokens took 38.6 us for 35.7).  Of the others products
+// and sums are kept as pairs of fp32 numbers, rounded value and rest (the rest of a
+// sum: Knuth, The Art of Computer Programming 2, 4.2.2, theorem B), where fp32 holds
+// all of them; else they are taken in 64 bits, in which the products are exact.  (All
+// of them in 64 bits, of which a warp's operation takes an SM 16 cycles, took half of
+// the time: 140 us for 93.)
 __device__ __forceinline__ float turn_exactly(float x, float c, float y, float s) {
-  const float p = __fmul_rn(x, c), q = __fmul_rn(y, s), h = __fadd_rn(p, q);
-  const float pe = fmaf(x, c, -p), qe = fmaf(y, s, -q), z = __fsub_rn(h, p);
+  const float p = __fmul_rn(x, c), q = __fmul_rn(y, s), pe = fmaf(x, c, -p), qe = fmaf(y, s, -q);
+  const float fast = __fadd_rn(fmaf(x, c, q), qe);
+  if (!in_doubt(__float_as_uint(fast) & 0xffffu) && fast == fast) return fast;
+  const float h = __fadd_rn(p, q), z = __fsub_rn(h, p);
   const float he = __fadd_rn(__fsub_rn(p, __fsub_rn(h, z)), __fsub_rn(q, z));
   const float rest = __fadd_rn(he, __fadd_rn(pe, qe)), t = __fadd_rn(h, rest);
-  const float left = __fadd_rn(__fsub_rn(h, t), rest);  // the exact value less t
-  uint32_t bits = __float_as_uint(t);
-  if (left != 0.f) bits = (bits - ((left < 0.f) != (t < 0.f) ? 1u : 0u)) | 1u;
-  // where rests may be lost, or are none, the sum itself
-  return fabsf(h) >= 0x1p-90f && fabsf(h) < INFINITY ? __uint_as_float(bits) : fmaf(x, c, q);
+  if (fabsf(t) < INFINITY && kept(p, x, c) && kept(q, y, s))
+    return with_rest(t, __fadd_rn(__fsub_rn(h, t), rest));  // and the exact value less t
+  const double P = static_cast<double>(x) * c, Q = static_cast<double>(y) * s, H = P + Q, Z = H - P;
+  if (!(fabs(H) < INFINITY)) return static_cast<float>(H);  // of no finite factors
+  const double E = (P - (H - Z)) + (Q - Z);
+  const float T = __double2float_rz(H);
+  // what is cut off has H's sign, and E less than its last bit
+  return with_rest(T, H != T ? copysignf(1.f, T) : E < 0 ? -1.f : E > 0 ? 1.f : 0.f);
 }
 
 // Whether some of the results r is too near a border: of their lower halves, two by
