@@ -28,6 +28,18 @@ constexpr int kThreads = 128;
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Products and sums of two, subnormals as they are (in sm103_ptx.cuh they count as 0).
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Two (cos, sin), for the two-wide arithmetic.
 struct Pair {
   uint64_t c, s;
@@ -95,11 +107,13 @@ struct Doubt {
 };
 
 // x c + y s, twice.  The product's own error is added to the sum, so that
-// cancellation does not raise it: it is off by about one unit in its last place.
+// cancellation does not raise it: it is off by less than two units in its last place
+// (a half by either sum, in the larger sum's units, and 2^-150 where the product's
+// error lies below fp32).
 __device__ __forceinline__ uint64_t turn2(uint64_t x, uint64_t y, uint64_t c, uint64_t s, Doubt& doubt) {
   const uint64_t minus = f2_pack(-1.f, -1.f);
-  const uint64_t p = f2_mul(y, s), e = f2_fma(y, f2_mul(s, minus), p);  // the product, less its error
-  const uint64_t r = f2_fma(e, minus, f2_fma(x, c, p));
+  const uint64_t p = mul2(y, s), e = fma2(y, mul2(s, minus), p);  // the product, less its error
+  const uint64_t r = fma2(e, minus, fma2(x, c, p));
   doubt.see(r);
   return r;
 }

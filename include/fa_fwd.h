@@ -511,9 +511,9 @@ size_t fa_cache_fwd_e4m3_workspace_size(int R, int T, int Hq, int Hkv, int d);
  *   half:        (x_i, x_{i + rot/2}) -> (x_i c_i - x_{i + rot/2} s_i,
  *                                        x_{i + rot/2} c_i + x_i s_i)
  *   interleaved: the same of (x_{2i}, x_{2i+1}),       i < rot / 2
- * and the others pass.  Results are exact for the table's entries and rounded
- * once to bf16, nearest even; those below 2^-90 are first rounded to fp32.
- * Infinities, NaN and products beyond fp32 go through the formula in fp32.
+ * and the others pass.  Results are exact for the table's entries, whatever
+ * their size, and rounded once to bf16, nearest even.  Infinities and NaN go
+ * through the formula.
  *
  * fa_rope — the rotation of x, bf16 [B, H, N] rows of d, into out.
  *   x_batch .. out_token : elements between batches, heads and tokens, multiples

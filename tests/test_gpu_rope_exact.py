@@ -129,3 +129,33 @@ def test_append_turns_cancelling_pairs_to_the_same_bits():
         fa.check_errors()
         assert torch.equal(one.data, two.data)
         assert (fa.cache_read_e2m1(one, slots)[0] != 0).float().mean() > 0.2
+
+
+@pytest.mark.parametrize("d", (64, 128))
+def test_rows_of_small_numbers(d):
+    """Subnormals of bf16 and what lies just above, alone in their rows: at position
+    0, where they come back as they are, and turned; and beside pairs taken again."""
+    g = np.random.default_rng(7)
+    n, T = d // 2, 240
+    table = fa.rope_table(4000, d, device="cpu")
+    low = np.repeat(np.arange(-133, -85), 5)[:, None]                       # a row's smallest step
+    a, b = (g.integers(-255, 256, (T, n)) * 2.0 ** np.maximum(low, -133) for _ in range(2))
+    check(a, b, table, [0] * T, d)
+    same(fa.rope(laid(a, b, d, False).to(DEV), torch.zeros(T, dtype=torch.int32, device=DEV), table.to(DEV)),
+         laid(a, b, d, False))
+    check(a, b, table, g.integers(0, 4000, T), d)
+    table = table.clone()
+    table[::2, ::8] = torch.tensor([257 / 256, 0.0])
+    a[:, ::8], b[:, ::8] = 1.0, 0.0
+    check(a, b, table, g.integers(0, 4000, T), d)
+
+
+def test_small_table_entries():
+    """Products far below their factors, down to below fp32."""
+    g = np.random.default_rng(8)
+    T, n = 200, 64
+    a, b = (mantissas(g, T, n) * 2.0 ** g.integers(-60, 3, (T, n)) for _ in range(2))
+    table = (g.uniform(-1, 1, (T, n, 2)) * 2.0 ** g.integers(-149, 1, (T, n, 1))).astype(F)
+    a[1::2, ::8], b[1::2, ::8] = 1.0, 0.0                     # a tie in every lane of every other row
+    table[1::2, ::8] = 257 / 256, 0.5
+    check(a, b, table)
