@@ -45,6 +45,12 @@ struct Pair {
   uint64_t c, s;
 };
 
+// a + b, and what its rounding left.
+__device__ __forceinline__ float add_rest(float a, float b, float& rest) {
+  const float h = __fadd_rn(a, b), z = __fsub_rn(h, a);
+  rest = __fadd_rn(__fsub_rn(a, __fsub_rn(h, z)), __fsub_rn(b, z));
+  return h;
+}
 // A fp32 number cut off from t, and whether something (of `left`'s sign, less than t's
 // last bit) is left of it, as a number that rounds to bf16 as both together do: with
 // its last bit set where bits were lost.  t is 0 only with nothing or its sign left.
@@ -64,19 +70,17 @@ __device__ __forceinline__ bool kept(float product, float x, float c) {
 // come here do so with another value in doubt, and turn2's own result serves (all of
 // them taken again, rope of 9001 tokens took 38.6 us for 35.7).  Of the others products
 // and sums are kept as pairs of fp32 numbers, rounded value and rest (the rest of a
-// sum: Knuth, The Art of Computer Programming 2, 4.2.2, theorem B), where fp32 holds
-// all of them; else they are taken in 64 bits, in which the products are exact.  (All
+// sum: Knuth, The Art of Computer Programming 2, 4.2.2, theorem B), where two of them
+// hold all; else they are taken in 64 bits, in which the products are exact.  (All
 // of them in 64 bits, of which a warp's operation takes an SM 16 cycles, took half of
 // the time: 140 us for 93.)
 __device__ __forceinline__ float turn_exactly(float x, float c, float y, float s) {
   const float p = __fmul_rn(x, c), q = __fmul_rn(y, s), pe = fmaf(x, c, -p), qe = fmaf(y, s, -q);
   const float fast = __fadd_rn(fmaf(x, c, q), qe);
   if (!in_doubt(__float_as_uint(fast) & 0xffffu) && fast == fast) return fast;
-  const float h = __fadd_rn(p, q), z = __fsub_rn(h, p);
-  const float he = __fadd_rn(__fsub_rn(p, __fsub_rn(h, z)), __fsub_rn(q, z));
-  const float rest = __fadd_rn(he, __fadd_rn(pe, qe)), t = __fadd_rn(h, rest);
-  if (fabsf(t) < INFINITY && kept(p, x, c) && kept(q, y, s))
-    return with_rest(t, __fadd_rn(__fsub_rn(h, t), rest));  // and the exact value less t
+  float he, ue, ve, left;
+  const float h = add_rest(p, q, he), u = add_rest(pe, qe, ue), v = add_rest(he, u, ve), t = add_rest(h, v, left);
+  if (fabsf(t) < INFINITY && ue == 0.f && ve == 0.f && kept(p, x, c) && kept(q, y, s)) return with_rest(t, left);
   const double P = static_cast<double>(x) * c, Q = static_cast<double>(y) * s, H = P + Q, Z = H - P;
   if (!(fabs(H) < INFINITY)) return static_cast<float>(H);  // of no finite factors
   const double E = (P - (H - Z)) + (Q - Z);

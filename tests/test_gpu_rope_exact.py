@@ -159,3 +159,39 @@ def test_small_table_entries():
     a[1::2, ::8], b[1::2, ::8] = 1.0, 0.0                     # a tie in every lane of every other row
     table[1::2, ::8] = 257 / 256, 0.5
     check(a, b, table)
+
+
+TIES = ((1.265625, 0.75390625, 0.89197528362, 4.200120073960534e-08),
+        (1.0, 2.0 ** -100, 257 / 256, 2.0 ** -60))
+
+
+@pytest.mark.parametrize("x,y,c,s", TIES)
+def test_a_tie_and_a_term_far_below(x, y, c, s):
+    a, b, table = np.zeros((8, 8)), np.zeros((8, 8)), np.zeros((8, 8, 2), F)
+    rows = [(sx * p, sy * q) for p, q in ((x, y), (y, x)) for sx in (1, -1) for sy in (1, -1)]
+    for r, (p, q) in enumerate(rows):
+        a[r, r], b[r, r] = p, q
+        table[r, r] = (c, s) if r < 4 else (s, c)
+    check(a, b, table, d=64)
+
+
+def test_ties_that_the_other_term_decides():
+    """The first product is a tie of bf16, or fp32 rounds it to one, and the other is
+    anything from a step of bf16 to nothing that fp32 holds, or takes back what that
+    rounding lost, but for its last bits."""
+    g = np.random.default_rng(9)
+    T, n = 300, 64
+    a = mantissas(g, T, n)
+    tie = (2 * g.integers(128, 256, (T, n)) + 1) / 256.0
+    a[: T // 3] = 1.0
+    c = (tie / a).astype(F)
+    b = mantissas(g, T, n) * np.where(g.random((T, n)) < 0.5, -1, 1)
+    size = 2.0 ** -g.integers(8, 250, (T, n)).astype(float)
+    lost = a * c.astype(float) - (a.astype(F) * c)
+    back = (np.arange(T)[:, None] % 2 == 1) & (lost != 0)
+    size_b = np.where(back, 1.0, np.maximum(size, 2.0 ** -120))
+    b = b * size_b
+    s = np.where(back, lost / b, np.minimum(size / size_b, 1.0)).astype(F)
+    assert back.mean() > 0.2 and ((a.astype(F) * c).astype(float) == tie).mean() > 0.5
+    check(a, b, np.stack((c, s), -1))
+    check(-a, b, np.stack((c, s), -1))
