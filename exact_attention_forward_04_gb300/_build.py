@@ -2,9 +2,10 @@
 
     python -m exact_attention_forward_04_gb300._build [--force]
 
-Output: exact_attention_forward_04_gb300/_lib/libfa_fwd.so (git-ignored) and
-fa_torch.so, a Python module that takes PyTorch tensors to some of its entry
-points, and the ptxas resource report (registers, spills, shared memory) beside them.
+Output: exact_attention_forward_04_gb300/_lib/libfa_fwd.so (git-ignored), the ptxas
+resource report (registers, spills, shared memory) beside it and, where g++, Python's
+and PyTorch's headers are there, fa_torch.so, a Python module that takes PyTorch
+tensors to some of its entry points with less time on the host.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -44,11 +46,16 @@ def _nvcc():
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build the library")
 
 
+def _older(path, sources):
+    return not os.path.exists(path) or any(os.path.getmtime(f) > os.path.getmtime(path) for f in sources)
+
+
 def needs_build() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(TORCH_PATH)):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_PATH))
-    return any(os.path.getmtime(f) > t for f in _sources())
+    return _older(LIB_PATH, [f for f in _sources() if not f.endswith(".cpp")]) or _older(TORCH_PATH, _torch_sources())
+
+
+def _torch_sources():
+    return [os.path.join(CSRC, "fa_torch.cpp"), os.path.join(INCLUDE, "fa_fwd.h")]
 
 
 def _torch_command(out):
@@ -63,27 +70,64 @@ def _torch_command(out):
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def _start(cmd):
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _start_torch():
+    """The compiler of fa_torch.so at work, and where it writes; None with the
+    reason where there is none."""
+    tmp = TORCH_PATH + f".tmp{os.getpid()}"
+    try:
+        return _start(_torch_command(tmp)), tmp
+    except (ImportError, OSError, RuntimeError) as e:
+        return None, str(e)
+
+
+def _finish_torch(proc, tmp) -> str:
+    """Puts fa_torch.so in its place; the compiler's output.  Where it cannot be
+    built, the calls it serves go through Python: a warning, no error."""
+    out = proc.communicate()[0] if proc else tmp
+    if proc and proc.returncode == 0:
+        os.replace(tmp, TORCH_PATH)
+    else:
+        warnings.warn("fa_torch.so was not built, calls from PyTorch go through Python:\n" + out, stacklevel=3)
+        if proc and os.path.exists(tmp):
+            os.remove(tmp)
+    return out
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libfa_fwd.so if it is missing or older than its sources."""
-    if not force and not needs_build():
-        return LIB_PATH
+    """Compile libfa_fwd.so, and fa_torch.so, where missing or older than their sources."""
     os.makedirs(OUT_DIR, exist_ok=True)
+    module = _start_torch() if force or _older(TORCH_PATH, _torch_sources()) else None
+    try:
+        if force or _older(LIB_PATH, [f for f in _sources() if not f.endswith(".cpp")]):
+            report = _build_library()
+            if verbose:
+                print(report)
+    finally:
+        if module:
+            report = _finish_torch(*module)
+            if verbose:
+                print(report)
+    return LIB_PATH
+
+
+def _build_library() -> str:
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     flags = [ARCH, "-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
-    jobs = []  # one compiler per translation unit, at the same time
-    torch_tmp = TORCH_PATH + f".tmp{os.getpid()}"
-    cmd = _torch_command(torch_tmp)
-    jobs.append((cmd, None, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    jobs = []  # one nvcc per translation unit, at the same time
     for unit in UNITS:
         obj = os.path.join(OUT_DIR, f"{unit}.{os.getpid()}.o")
         cmd = [_nvcc(), *flags, "-Xptxas", "-v", "-c", "-o", obj, os.path.join(CSRC, unit)]
-        jobs.append((cmd, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+        jobs.append((cmd, obj, _start(cmd)))
     report, failed = "", False
     for cmd, _, proc in jobs:
         out = proc.communicate()[0]
         report += " ".join(cmd) + "\n" + out
         failed = failed or proc.returncode != 0
-    objs = [obj for _, obj, _ in jobs if obj]
+    objs = [obj for _, obj, _ in jobs]
     if not failed:
         cmd = [_nvcc(), ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
         res = subprocess.run(cmd, capture_output=True, text=True)
@@ -95,12 +139,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with open(os.path.join(OUT_DIR, "ptxas_report.txt"), "w") as f:
         f.write(report)
     if failed:
-        raise RuntimeError("the build failed:\n" + report)
-    os.replace(torch_tmp, TORCH_PATH)
+        if os.path.exists(tmp):
+            os.remove(tmp)
+        raise RuntimeError("nvcc failed:\n" + report)
     os.replace(tmp, LIB_PATH)
-    if verbose:
-        print(report)
-    return LIB_PATH
+    return report
 
 
 if __name__ == "__main__":
