@@ -125,17 +125,35 @@ def load_library(path: str | None = None):
         return lib
 
 
+class _NoModule:
+    """In the place of fa_torch.so: None, its answer to what it does not take, to every
+    call, so that the Python functions make them all."""
+
+    @staticmethod
+    def rope(*args):
+        return None
+
+    append = read = forward = rope
+
+
 def _load_torch():
-    """The module of the usual calls from PyTorch tensors, bound to the library."""
+    """The module of the usual calls from PyTorch tensors, bound to the library.  One
+    that was built for another PyTorch or Python is not loaded."""
     import importlib.util
+    from . import _build
     lib = load_library()
-    path = os.path.join(_PKG, "_lib", "fa_torch.so")
-    if not os.path.exists(path):
-        raise FAError(-4, "load", f"{path} is missing; build it with "
-                                  "`python -m exact_attention_forward_04_gb300._build`")
-    spec = importlib.util.spec_from_file_location("fa_torch", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    path, made, here = _build.TORCH_PATH, _build.torch_built_for(), _build.torch_key()
+    try:
+        if made != here:
+            raise ImportError(f"built for {made or 'nothing that is noted'}, not for {here}")
+        spec = importlib.util.spec_from_file_location("fa_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        import warnings
+        warnings.warn(f"{path} cannot be used ({e}): calls go through Python. Build it with "
+                      "`python -m exact_attention_forward_04_gb300._build`", RuntimeWarning, stacklevel=3)
+        return _NoModule
     module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
         "fa_rope", "fa_cache_append_e2m1", "fa_cache_read_e2m1", "fa_cache_fwd_e2m1",
         "fa_cache_fwd_e2m1_workspace_size")))

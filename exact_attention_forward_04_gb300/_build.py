@@ -23,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(OUT_DIR, "libfa_fwd.so")
 TORCH_PATH = os.path.join(OUT_DIR, "fa_torch.so")
+TORCH_FLAGS = ("-O2", "-std=c++17", "-fPIC", "-shared")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 UNITS = ("fa_fwd.cu", "fa_cache.cu", "fa_cache4.cu", "fa_rope.cu")
 
@@ -51,11 +52,31 @@ def _older(path, sources):
 
 
 def needs_build() -> bool:
-    return _older(LIB_PATH, [f for f in _sources() if not f.endswith(".cpp")]) or _older(TORCH_PATH, _torch_sources())
+    return _older(LIB_PATH, [f for f in _sources() if not f.endswith(".cpp")]) or _torch_stale()
 
 
-def _torch_sources():
-    return [os.path.join(CSRC, "fa_torch.cpp"), os.path.join(INCLUDE, "fa_fwd.h")]
+def torch_key() -> str:
+    """What fa_torch.so depends on beside its sources: PyTorch's C++ interface and
+    Python's, and the compiler's flags."""
+    import torch
+    return f"PyTorch {torch.__version__}, {sysconfig.get_config_var('SOABI')}, {' '.join(TORCH_FLAGS)}"
+
+
+def torch_built_for() -> str:
+    """The torch_key that fa_torch.so was built for, as noted beside it."""
+    try:
+        with open(TORCH_PATH[:-3] + ".txt") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def _torch_stale() -> bool:
+    sources = [os.path.join(CSRC, "fa_torch.cpp"), os.path.join(INCLUDE, "fa_fwd.h")]
+    try:
+        return _older(TORCH_PATH, sources) or torch_built_for() != torch_key()
+    except ImportError:
+        return True
 
 
 def _torch_command(out):
@@ -65,7 +86,7 @@ def _torch_command(out):
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     include = [INCLUDE, os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    return ["g++", *TORCH_FLAGS, f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *(f"-I{p}" for p in include), os.path.join(CSRC, "fa_torch.cpp"), "-o", out, "-L" + os.path.join(at, "lib"),
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
@@ -89,7 +110,13 @@ def _finish_torch(proc, tmp) -> str:
     built, the calls it serves go through Python: a warning, no error."""
     out = proc.communicate()[0] if proc else tmp
     if proc and proc.returncode == 0:
+        note = TORCH_PATH[:-3] + ".txt"
+        if os.path.exists(note):  # never beside a module that it is not about
+            os.remove(note)
         os.replace(tmp, TORCH_PATH)
+        with open(tmp, "w") as f:
+            f.write(torch_key())
+        os.replace(tmp, note)
     else:
         warnings.warn("fa_torch.so was not built, calls from PyTorch go through Python:\n" + out, stacklevel=3)
         if proc and os.path.exists(tmp):
@@ -98,9 +125,10 @@ def _finish_torch(proc, tmp) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libfa_fwd.so, and fa_torch.so, where missing or older than their sources."""
+    """Compile libfa_fwd.so and fa_torch.so, where missing or older than their
+    sources; fa_torch.so also where it is another PyTorch's or Python's."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    module = _start_torch() if force or _older(TORCH_PATH, _torch_sources()) else None
+    module = _start_torch() if force or _torch_stale() else None
     try:
         if force or _older(LIB_PATH, [f for f in _sources() if not f.endswith(".cpp")]):
             report = _build_library()
