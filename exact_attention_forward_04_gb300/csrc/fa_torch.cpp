@@ -88,6 +88,17 @@ bool number(PyObject* o, float& f) {
   return true;
 }
 
+// `f` while other Python threads run: a launch waits while the GPU's queue is full, for
+// as long as the work in front of it takes, and memory may have to be asked for.
+template <typename F>
+auto unlocked(F&& f) {
+  struct Unlock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlock() { PyEval_RestoreThread(state); }
+  } unlock;
+  return f();
+}
+
 PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
   PyObject* t = PyTuple_New(2);
   if (!t) return nullptr;
@@ -110,16 +121,17 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* pos = vector(a[1], at::kInt, N, device);
   const at::Tensor* table = angles(a[2], d, device);
   if (!pos || !table || d > 128 || B > kInt || H > kInt || N > kInt) Py_RETURN_NONE;
-  const at::Tensor out = make(x->sizes(), at::kBFloat16, device);
-  const int64_t* xs = x->strides().data();
-  const int st = tokens ? g_rope(x->data_ptr(), 0, xs[1], xs[0], out.data_ptr(), 0, d, H * d,
-                                 static_cast<const int*>(pos->data_ptr()), 0,
-                                 static_cast<const float*>(table->data_ptr()), table->size(0), 1, H, N, d,
-                                 2 * table->size(1), interleaved, transposed, stream(device))
-                        : g_rope(x->data_ptr(), xs[0], xs[1], xs[2], out.data_ptr(), H * N * d, N * d, d,
-                                 static_cast<const int*>(pos->data_ptr()), 0,
-                                 static_cast<const float*>(table->data_ptr()), table->size(0), B, H, N, d,
-                                 2 * table->size(1), interleaved, transposed, stream(device));
+  at::Tensor out;
+  const int st = unlocked([&] {
+    out = make(x->sizes(), at::kBFloat16, device);
+    const int64_t* xs = x->strides().data();
+    return tokens ? g_rope(x->data_ptr(), 0, xs[1], xs[0], out.data_ptr(), 0, d, H * d,
+                           static_cast<const int*>(pos->data_ptr()), 0, static_cast<const float*>(table->data_ptr()),
+                           table->size(0), 1, H, N, d, 2 * table->size(1), interleaved, transposed, stream(device))
+                  : g_rope(x->data_ptr(), xs[0], xs[1], xs[2], out.data_ptr(), H * N * d, N * d, d,
+                           static_cast<const int*>(pos->data_ptr()), 0, static_cast<const float*>(table->data_ptr()),
+                           table->size(0), B, H, N, d, 2 * table->size(1), interleaved, transposed, stream(device));
+  });
   if (st != FA_OK) Py_RETURN_NONE;
   return THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
@@ -145,12 +157,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* pos = turned ? vector(a[6], at::kInt, T, device) : nullptr;
   const at::Tensor* table = turned ? angles(a[7], c.d, device) : nullptr;
   if (turned && (!pos || !table)) Py_RETURN_NONE;
-  const int st = g_append(k->data_ptr(), v->data_ptr(), ks, vs, c.data->data_ptr(), ku, vu,
-                          static_cast<const long long*>(slots->data_ptr()),
-                          turned ? static_cast<const int*>(pos->data_ptr()) : nullptr,
-                          turned ? static_cast<const float*>(table->data_ptr()) : nullptr, turned ? table->size(0) : 0,
-                          turned ? 2 * table->size(1) : 0, interleaved, T, c.H, c.d, c.blocks, c.P,
-                          stream(device));
+  const int st = unlocked([&] {
+    return g_append(k->data_ptr(), v->data_ptr(), ks, vs, c.data->data_ptr(), ku, vu,
+                    static_cast<const long long*>(slots->data_ptr()),
+                    turned ? static_cast<const int*>(pos->data_ptr()) : nullptr,
+                    turned ? static_cast<const float*>(table->data_ptr()) : nullptr, turned ? table->size(0) : 0,
+                    turned ? 2 * table->size(1) : 0, interleaved, T, c.H, c.d, c.blocks, c.P, stream(device));
+  });
   if (st != FA_OK) Py_RETURN_NONE;
   Py_RETURN_TRUE;
   END_HANDLE_TH_ERRORS
@@ -168,9 +181,13 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!slots || slots->dim() != 1 || !slots->is_contiguous() || slots->size(0) == 0 || slots->size(0) > kInt)
     Py_RETURN_NONE;
   const int64_t T = slots->size(0);
-  const at::Tensor k = make({T, c.H, c.d}, at::kBFloat16, device), v = make({T, c.H, c.d}, at::kBFloat16, device);
-  const int st = g_read(c.data->data_ptr(), ku, vu, static_cast<const long long*>(slots->data_ptr()), k.data_ptr(),
-                        v.data_ptr(), T, c.H, c.d, c.blocks, c.P, stream(device));
+  at::Tensor k, v;
+  const int st = unlocked([&] {
+    k = make({T, c.H, c.d}, at::kBFloat16, device);
+    v = make({T, c.H, c.d}, at::kBFloat16, device);
+    return g_read(c.data->data_ptr(), ku, vu, static_cast<const long long*>(slots->data_ptr()), k.data_ptr(),
+                  v.data_ptr(), T, c.H, c.d, c.blocks, c.P, stream(device));
+  });
   if (st != FA_OK) Py_RETURN_NONE;
   return pair(k, v);
   END_HANDLE_TH_ERRORS
@@ -203,12 +220,9 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   else if (!number(a[7], scale)) Py_RETURN_NONE;
   size_t bytes = 0;
   void* ws = nullptr;
-  at::Tensor mine;
   if (a[9] == Py_None) {
     bytes = g_workspace(R, T, Hq, c.H, c.d);
     if (bytes == 0) Py_RETURN_NONE;
-    mine = make({static_cast<int64_t>(bytes)}, at::kByte, device);
-    ws = mine.data_ptr();
   } else {
     if (!on_gpu(a[9])) Py_RETURN_NONE;
     const at::Tensor& given = THPVariable_Unpack(a[9]);
@@ -216,12 +230,21 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     bytes = given.nbytes();
     ws = given.data_ptr();
   }
-  const at::Tensor o = make({T, Hq, c.d}, at::kBFloat16, device), lse = make({T, Hq}, at::kFloat, device);
-  const int st = g_forward(q->data_ptr(), stride, c.data->data_ptr(), ku, vu, static_cast<const int*>(table->data_ptr()),
-                           static_cast<const int*>(lens->data_ptr()), static_cast<const int*>(cu->data_ptr()),
-                           slots ? static_cast<const long long*>(slots->data_ptr()) : nullptr, o.data_ptr(),
-                           static_cast<float*>(lse.data_ptr()), R, T, Hq, c.H, c.d, c.blocks, c.P, M, scale,
-                           causal, ws, bytes, stream(device));
+  at::Tensor o, lse;
+  const int st = unlocked([&] {
+    at::Tensor mine;
+    if (a[9] == Py_None) {
+      mine = make({static_cast<int64_t>(bytes)}, at::kByte, device);
+      ws = mine.data_ptr();
+    }
+    o = make({T, Hq, c.d}, at::kBFloat16, device);
+    lse = make({T, Hq}, at::kFloat, device);
+    return g_forward(q->data_ptr(), stride, c.data->data_ptr(), ku, vu, static_cast<const int*>(table->data_ptr()),
+                     static_cast<const int*>(lens->data_ptr()), static_cast<const int*>(cu->data_ptr()),
+                     slots ? static_cast<const long long*>(slots->data_ptr()) : nullptr, o.data_ptr(),
+                     static_cast<float*>(lse.data_ptr()), R, T, Hq, c.H, c.d, c.blocks, c.P, M, scale, causal, ws,
+                     bytes, stream(device));
+  });
   if (st != FA_OK) Py_RETURN_NONE;
   return pair(o, lse);
   END_HANDLE_TH_ERRORS
