@@ -78,10 +78,13 @@ int cache4_append(const void* k, const void* v, long long k_stride, long long v_
   a.length = length;
   a.rot = positions ? rot : 0;
   a.err = dev.index_err;
-  // Rows of a thread: one where they are few, else eight (24 prompts, 8 kv heads of 128:
-  // 4 rows 78 us, 8 70).
+  // Rows of a thread, by the lanes that one each would give an SM.  Measured (us, K
+  // turned; tokens of 8 kv heads of 128, as many of 16 of 64 within 5 %), rows 1 / 2 / 4 / 8 / 16:
+  //   1000 (842)      4.4 / 5.4 / 6.5 / 8.6 / 10.2     8000 (6736)    18.9 / 15.1 / 13.9 / 14.9 / 18.8
+  //   2000 (1684)     6.1 / 6.3 / 7.2 / 9.3 / 13.2     16000 (13473)  34.9 / 27.2 / 24.4 / 23.7 / 26.1
+  //   4000 (3368)    10.9 / 9.1 / 9.5 / 12.1 / 16.4    51000 (42947)  106.7 / 81.9 / 71.8 / 67.1 / 67.6
   const long long lanes = static_cast<long long>(T) * (d / 16), per_sm = lanes * 2 * Hkv / dev.sms;
-  a.group = per_sm <= 2048 ? 1 : 8;
+  a.group = per_sm <= 2048 ? 1 : per_sm <= 8192 ? 4 : 8;
   while ((2 * Hkv + a.group - 1) / a.group > 65535) a.group *= 2;
   const dim3 grid(static_cast<unsigned>((lanes + c4::kThreads - 1) / c4::kThreads),
                   static_cast<unsigned>((2 * Hkv + a.group - 1) / a.group));
@@ -124,9 +127,11 @@ int cache4_read(const void* data, float k_unit, float v_unit, const long long* s
   a.k_unit = k_unit;
   a.v_unit = v_unit;
   a.err = dev.index_err;
-  // as the append (the rows of 24 prompts: 4 rows 49 us, 8 53, 16 59)
+  // as the append:
+  //   2000 (1684)     3.8 / 3.9 / 3.9 / 5.1 / 7.3      16000 (13473)  16.7 / 16.1 / 17.6 / 19.6 / 17.3
+  //   8000 (6736)     9.4 / 9.5 / 10.5 / 9.9 / 13.5    51000 (42947)  51.7 / 47.1 / 47.4 / 50.7 / 58.0
   const long long lanes = static_cast<long long>(T) * (d / 16), per_sm = lanes * 2 * Hkv / dev.sms;
-  a.group = per_sm <= 2048 ? 1 : 4;
+  a.group = per_sm <= 8192 ? 1 : 2;
   while ((2 * Hkv + a.group - 1) / a.group > 65535) a.group *= 2;
   const dim3 grid(static_cast<unsigned>((lanes + c4::kThreads - 1) / c4::kThreads),
                   static_cast<unsigned>((2 * Hkv + a.group - 1) / a.group));

@@ -132,8 +132,13 @@ struct Layout {
   // arrive every 196 (24 requests of 20000 to 32768 tokens: 143 us with 32 keys).
   static constexpr int kParts = F::k4 ? 2 : 1;
   static constexpr int kTile = kParts * kKeys;
-  // A piece's fixed cost, in tiles (64 requests of 30 to 8192 tokens: 8 bits, 5: 114 us,
-  // 12: 104; 4 bits, 10: 84 us, 16: 80, 24: 82)
+  // A piece's fixed cost, in tiles (64 requests of 30 to 8192 tokens, 8 bits, 5: 114 us,
+  // 12: 104).  4 bits, us with 8 / 12 / 16 / 20 / 28 (8 kv heads of 128, then of 64):
+  //   64 requests of 30 to 8192 tokens    84.0 / 80.5 / 77.9 / 77.5 / 79.5   51.4 / 50.0 / 50.1 / 50.7 / 52.0
+  //   200 of 30 to 2000                   94.3 / 94.8 / 95.2 / 98.9 / 102    55.8 / 55.4 / 57.0 / 58.2 / 60.3
+  //   24 of 20000 to 32768                137 within 0.4                     87.8 / 87.9 / 88.2 / 88.4 / 90.1
+  //   32 of 4000, 4 kv heads; 16 of 1 to 1024, 32
+  //                                       30.6 / 30.4 / 29.3 / 29.5 / 29.0   19.9 / 19.4 / 19.5 / 20.1 / 20.9
   static constexpr int kUnitCost = F::k4 ? (D == 64 ? 10 : 16) : 12;
   static constexpr int kMinCost = F::k4 ? 6 : 12;               // least cost of a CTA's range
   static constexpr int kHalf = kKeys * D;                       // codes of K (or V) of a tile; 4 bits: unused

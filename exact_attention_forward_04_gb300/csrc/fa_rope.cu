@@ -88,9 +88,13 @@ int rope_run(const void* x, long long (&xs)[3], void* out, long long (&os)[3], c
   a.err = dev.index_err;
   const long long lanes = static_cast<long long>(B) * N * (d / 16);
   const long long gx = (lanes + rope::kThreads - 1) / rope::kThreads;
-  // Heads of a thread: one where rows are few, many where its cos and sin are worth
-  // keeping (gradient of 32768 tokens of 32 heads: 16 heads 97 us, 8 101; 9001 tokens of
-  // 40: 4 heads 37.4 us, 8 38.9).
+  // Heads of a thread, by the lanes that one each would give an SM: one where rows are
+  // few, many where its cos and sin are worth keeping.  Measured (us; tokens x heads of
+  // 128, of 64 alike), heads 1 / 2 / 4 / 8 / 16:
+  //   500 x 40 (1052)   5.9 / 5.6 / 6.5 / 9.1 / 14.2        4000 x 40 (8421)   22.5 / 19.1 / 18.7 / 20.9 / 20.4
+  //   1000 x 40 (2105)  8.4 / 7.7 / 7.6 / 9.9 / 14.8        8000 x 40 (16842)  41.4 / 34.9 / 33.0 / 34.2 / 33.8
+  //   2000 x 40 (4210)  13.0 / 11.4 / 12.3 / 11.8 / 16.4    16000 x 40 (33684) 79.1 / 66.9 / 63.1 / 62.7 / 61.5
+  //   16000 x 8 (6736)  18.5 / 16.0 / 15.4 / 15.4           32000 x 40 (67368) 156 / 133 / 130 / 125 / 120
   const long long per_sm = lanes * H / dev.sms;
   a.group = per_sm <= 2048 ? 1 : per_sm <= 8192 ? 2 : per_sm <= 32768 ? 4 : 16;
   while ((H + a.group - 1) / a.group > 65535) a.group *= 2;
