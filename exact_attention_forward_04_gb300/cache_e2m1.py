@@ -1,4 +1,4 @@
-"""The 4-bit key/value cache: half the bytes of the 8-bit one, the same calls.
+"""The 4-bit key/value cache: 9/16 of the bytes of the 8-bit one, the same calls.
 
     cu, slots, lens, used, pos = cache_slots(table, lens, new, free, used, P, T, positions=True)
     q = rope(q, pos, angles)                                                   # per layer

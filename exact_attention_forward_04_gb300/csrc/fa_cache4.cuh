@@ -167,11 +167,13 @@ struct Append4Args {
 // K, then of V, so that K's bytes are stored 256 and V's 32 in a row; a row's elements
 // are on their way while the one before is written.
 //
-// 24 prompts, 51072 tokens of 8 kv heads of 128 in blocks of 64: 70 us with all of K
-// turned, 3.8 TB/s, 58 without; ALU 53 %, issue slots 61 %, DRAM 56 %: neither alone.
-// Seven CTAs per SM (78 us with six, and 104 with four rows' elements on their way in
-// four; 92 with cos and sin read again for every head).  32 tokens in 3.1 us, 500 of 16
-// heads of 64 in 3.7, a microsecond of it for position and table one after the other.
+// 24 prompts, 51072 tokens of 8 kv heads of 128 in blocks of 64: 67 us with all of K
+// turned, 4.0 TB/s, 55 without; ALU 54 %, issue slots 61 %, DRAM 57 %.  What it takes
+// beyond 40 us of bytes: where halves turn, two scale codes a lane in place of one and
+// four shuffles for their maxima, and stores of 1 to 8 bytes.  Seven CTAs per SM (78 us
+// with six, and 104 with four rows' elements on their way in four; 92 with cos and sin
+// read again for every head).  32 tokens in 3.3 us, 500 of 16 heads of 64 in 3.7, a
+// microsecond of it for position and table one after the other.
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(c4::kThreads, 7) fa_cache4_append_kernel(Append4Args a) {
   using namespace c4;
@@ -296,7 +298,7 @@ struct Read4Args {
 
 // The rows at some slots as bf16, which holds every value exactly; zeros where
 // there is none.  A lane takes one group.  Bound by DRAM: the rows of 24 prompts in
-// 49 us, 5.5 TB/s.
+// 47 us, 5.7 TB/s.
 template <int D>
 __global__ void __launch_bounds__(c4::kThreads) fa_cache4_read_kernel(Read4Args a) {
   using namespace c4;

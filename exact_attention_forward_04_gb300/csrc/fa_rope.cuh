@@ -233,7 +233,7 @@ struct RopeArgs {
 // Bound by DRAM: 32768 rows of 32 heads of 128 (the gradient's) in 96 us, 5.7 TB/s;
 // 9001 tokens of 40 heads, half of each in neighbours, in 38 us.  Seven CTAs per SM:
 // with four heads' elements on their way a thread had 112 registers, and the first
-// took 130 us.  Latency for few: 64 tokens in 3.1 us, with the position, then its row
+// took 130 us.  Latency for few: 64 tokens in 2.9 us, with the position, then its row
 // of the table to wait for.
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(rope::kThreads, 7) fa_rope_kernel(RopeArgs a) {

@@ -1,10 +1,10 @@
 // The usual calls of the 4-bit cache and of rotary positions from PyTorch
 // tensors to the C ABI: CUDA tensors of the current device, on its current
 // stream.  A step of single tokens takes the GPU 3 to 10 us a call, and a call
-// through Python's checks and ctypes takes the host 9 to 25; through here 4 to 9.
+// through Python's checks and ctypes takes the host 9 to 25; through here 4 to 10.
 //
-// Whatever is not usual (other types, shapes, devices, a status other than
-// FA_OK) gives None and nothing is enqueued: the Python function behind then makes
+// Whatever is not usual (other types, shapes, positions [B, N], devices, a status other
+// than FA_OK) gives None and nothing is enqueued: the Python function behind then makes
 // the call itself and says what is wrong.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
