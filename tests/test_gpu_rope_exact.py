@@ -161,6 +161,25 @@ def test_small_table_entries():
     check(a, b, table)
 
 
+def test_products_beyond_fp32():
+    """Of the largest numbers, with entries above 1: results that fp32 holds again, results
+    that nothing does, and ties, exact all of them."""
+    g = np.random.default_rng(10)
+    T, n = 200, 64
+    a, b = (mantissas(g, T, n) * 2.0 ** g.integers(124, 128, (T, n)) * np.where(g.random((T, n)) < 0.5, -1, 1)
+            for _ in range(2))
+    table = g.uniform(-4, 4, (T, n, 2)).astype(F)
+    near = np.arange(n) % 2 == 0                                   # a c and b s nearly the same
+    table[:, near, 0] = (b * table[..., 1] / a * (1 + g.uniform(-0.1, 0.1, (T, n))))[:, near]
+    table = np.clip(table, -30, 30)
+    a[1::2, ::8], b[1::2, ::8] = 1.0, 0.0
+    table[1::2, ::8] = 257 / 256, 0.5
+    first = a * table[..., 0].astype(float) - b * table[..., 1].astype(float)
+    top = np.abs(a * table[..., 0].astype(float)) > 2.0 ** 128
+    assert (top & (np.abs(first) < 2.0 ** 127)).mean() > 0.1 and (np.abs(first) > 2.0 ** 128).mean() > 0.1
+    check(a, b, table)
+
+
 TIES = ((1.265625, 0.75390625, 0.89197528362, 4.200120073960534e-08),
         (1.0, 2.0 ** -100, 257 / 256, 2.0 ** -60))
 
