@@ -89,11 +89,11 @@ def test_turned_attended_and_turned_back(B, H, N, d, rot, interleaved, causal, p
     dqr, dkr, _ = fa.backward(qr, kr, v.to(DEV), o, lse, g.to(DEV), causal=causal)
     got = [fa.rope_backward(x, p, t, interleaved=interleaved).cpu().double() for x in (dqr, dkr)]
     fa.check_errors()
-    judge(got, references(q, k, v, g, qr.cpu(), kr.cpu(), o.cpu(), lse.cpu(), cs, interleaved, scale, causal),
+    compare(got, references(q, k, v, g, qr.cpu(), kr.cpu(), o.cpu(), lse.cpu(), cs, interleaved, scale, causal),
           (q, k), cs, interleaved)
 
 
-def judge(got, refs, before, cs, interleaved):
+def compare(got, refs, before, cs, interleaved):
     want, of_turned, bounds, loss = refs
     for which, (x, w, r, b) in enumerate(zip(got, want, of_turned, bounds)):
         over = ((x - w).abs() / b).max().item()
